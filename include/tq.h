@@ -58,7 +58,9 @@ typedef enum {
                          /* sizes whose byte counts overflow int64              */
     TQ_ERR_GROUP = -3,   /* G not in {64, 128}                                  */
     TQ_ERR_ALIGN = -4,   /* a pointer is not aligned as its call requires       */
-    TQ_ERR_LAUNCH = -5   /* the HIP runtime reported an error at launch         */
+    TQ_ERR_LAUNCH = -5,  /* the HIP runtime reported an error at launch         */
+    TQ_ERR_WORKSPACE = -6, /* a workspace is smaller than its call asks for      */
+    TQ_ERR_ACT = -7      /* act is not a tq_act value                           */
 } tq_status;
 
 /* Device status bits. */
@@ -67,9 +69,17 @@ enum {
                                /* (tq_dequantize) is Inf or NaN                    */
     TQ_DEV_SCALE_OVERFLOW = 2, /* a group mean rounds to >= 65520 (tq_quantize_pack)*/
     TQ_DEV_INVALID_BYTE = 4,   /* a packed byte is >= 243 (unpack, gemv, gemm)     */
-    TQ_DEV_BAD_PADDING = 8     /* a padding trit is not code 0 (tq_unpack,         */
+    TQ_DEV_BAD_PADDING = 8,    /* a padding trit is not code 0 (tq_unpack,         */
                                /* tq_dequantize)                                   */
+    TQ_DEV_BAD_ADAPTER = 16    /* an adapter id is below -1 or >= adapters         */
+                               /* (tq_lora_matmul)                                 */
 };
+
+/* Gate activations of the gated feed-forward calls. */
+typedef enum {
+    TQ_ACT_SILU = 0, /* g / (1 + e^-g)                                          */
+    TQ_ACT_GELU = 1  /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2         */
+} tq_act;
 
 /* Human-readable name of a tq_status value. */
 const char *tq_status_string(int status);
@@ -533,6 +543,103 @@ int tq_w4a16_gemv_grouped(int count, const uint16_t *const *xs, const uint32_t *
                           const uint16_t *const *scales, const uint16_t *const *biases,
                           uint16_t *const *ys, const int64_t *Ns, const int64_t *Ks, int G,
                           void *stream);
+
+/*
+ * Gated feed-forward block on packed ternary weights (serving), any M >= 0:
+ *   h[m,n] = bf16_rne(act(g[m,n]) * u[m,n]),
+ *   g = x Wg_hat^T, u = x Wu_hat^T, both accumulated in fp32 and never stored
+ * -- the gate and up projections, the activation and the product of one
+ * decoder feed-forward block; h is the x of the down projection.
+ *   x                        [M,K] bf16, 16-byte aligned
+ *   gate_packed, up_packed   [N, K/G, ceil(G/5)] bytes (any alignment)
+ *   gate_scales, up_scales   [N, K/G] fp16, 2-byte aligned
+ *   h                        [M,N] bf16, 2-byte aligned, overwritten
+ *   act                      a tq_act
+ *   workspace                device memory, 16-byte aligned, at least
+ *                            tq_glu_workspace(M, N, K, G) bytes (may be NULL
+ *                            when that is 0); its contents on entry are
+ *                            ignored and on return unspecified.  Calls in
+ *                            flight at the same time need separate ones.
+ * M = 0 enqueues nothing.  K is at most 4194304 (2^22).  A row of x that
+ * holds an Inf or NaN gives unspecified (Inf or NaN where the formula has
+ * them) values in that row of h and in no other.  Invalid packed bytes set
+ * TQ_DEV_INVALID_BYTE; their contribution is then unspecified.
+ * Deterministic: a fixed summation order for given shapes.
+ */
+int tq_glu(const uint16_t *x, const uint8_t *gate_packed, const uint16_t *gate_scales,
+           const uint8_t *up_packed, const uint16_t *up_scales, int64_t M, int64_t N, int64_t K,
+           int G, int act, uint16_t *h, void *workspace, int64_t workspace_bytes,
+           int32_t *d_status, void *stream);
+
+/* Workspace bytes of tq_glu; 0 also on bad arguments (host-only helper). */
+int64_t tq_glu_workspace(int64_t M, int64_t N, int64_t K, int G);
+
+/*
+ * Packed ternary projection shared by the rows of many requests, beside each
+ * row's own low-rank adapter, any M >= 0:
+ *   y[m,n] = sum_k x[m,k] w_hat[n,k]
+ *            + scaling[a] * sum_r B[a,n,r] * (sum_k A[a,r,k] x[m,k]),  a = ids[m]
+ * ids[m] = -1 adds nothing.  Everything is accumulated in fp32; the inner
+ * sums of an adapter are kept to at least 24 bits.
+ *   x         [M,K] bf16, 16-byte aligned
+ *   packed    [N, K/G, ceil(G/5)] bytes (any alignment)
+ *   scales    [N, K/G] fp16, 2-byte aligned
+ *   ids       [M] int32, 4-byte aligned, in any order
+ *   A         [adapters,R,K] bf16, 16-byte aligned
+ *   B         [adapters,N,R] bf16, 16-byte aligned
+ *   scaling   [adapters] fp32, 4-byte aligned
+ *             (A, B, scaling may be NULL when adapters is 0)
+ *   R         a multiple of 8, 8 <= R <= 256 (a lower rank is padded with
+ *             zero rows of A and zero columns of B)
+ *   y         [M,N] fp32, 4-byte aligned, overwritten
+ *   workspace as tq_glu, at least tq_lora_workspace(M, N, K, G, R) bytes
+ * An id below -1 or >= adapters sets TQ_DEV_BAD_ADAPTER and counts as -1.
+ * M = 0 enqueues nothing.  K, Inf and NaN, invalid bytes and determinism as
+ * tq_glu.  Only the adapters that rows name are read.
+ */
+int tq_lora_matmul(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
+                   const int32_t *ids, const uint16_t *A, const uint16_t *B,
+                   const float *scaling, int64_t M, int64_t N, int64_t K, int G,
+                   int64_t adapters, int64_t R, float *y, void *workspace,
+                   int64_t workspace_bytes, int32_t *d_status, void *stream);
+
+/* Workspace bytes of tq_lora_matmul; 0 also on bad arguments (host-only helper). */
+int64_t tq_lora_workspace(int64_t M, int64_t N, int64_t K, int G, int64_t R);
+
+/*
+ * Gated feed-forward block on bf16 weights (training), forward:
+ *   g = x Wg^T, u = x Wu^T (fp32), h = act(g) * u, each rounded once to bf16
+ * with Wg, Wu the w_hat that tq_fake_quantize makes of the latent weights.
+ *   x        [M,K] bf16, 16-byte aligned;  K % 64 == 0, K <= 2^22
+ *   wg, wu   [N,K] bf16, 16-byte aligned
+ *   h        [M,N] bf16, 16-byte aligned, overwritten
+ *   g, u     [M,N] bf16, 16-byte aligned, overwritten: what the backward call
+ *            reads; both NULL when no gradient is needed
+ * M = 0 enqueues nothing.  Deterministic.
+ */
+int tq_glu_forward(const uint16_t *x, const uint16_t *wg, const uint16_t *wu, int64_t M,
+                   int64_t N, int64_t K, int act, uint16_t *h, uint16_t *g, uint16_t *u,
+                   void *stream);
+
+/*
+ * Gradients of tq_glu_forward given dh, the gradient of h:
+ *   dg = dh * u * act'(g), du = dh * act(g)   (rounded to bf16 for the products)
+ *   dx = dg Wg + du Wu, dwg = dg^T x, dwu = du^T x
+ * accumulated in fp32, each rounded once to bf16.  dwg and dwu are also the
+ * gradients of the latent weights (straight-through).
+ *   dh, g, u   [M,N] bf16, 16-byte aligned
+ *   x, wg, wu  as tq_glu_forward
+ *   dx [M,K], dwg, dwu [N,K]   bf16, 16-byte aligned, overwritten
+ *   workspace  as tq_glu, at least tq_glu_backward_workspace(M, N, K) bytes
+ * M = 0 sets dwg and dwu to 0.  Deterministic.
+ */
+int tq_glu_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *wg,
+                    const uint16_t *wu, const uint16_t *g, const uint16_t *u, int64_t M,
+                    int64_t N, int64_t K, int act, uint16_t *dx, uint16_t *dwg, uint16_t *dwu,
+                    void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Workspace bytes of tq_glu_backward; 0 also on bad arguments (host-only helper). */
+int64_t tq_glu_backward_workspace(int64_t M, int64_t N, int64_t K);
 
 #ifdef __cplusplus
 }

@@ -21,6 +21,11 @@ package only marshals torch tensors to that ABI:
     y              = gemm(x_bf16, packed, scales, N, K, G)   # any M
     ys             = gemm_batched(xs, packeds, scales, N, K, G)  # many same-shaped
     ys             = gemm_grouped(xs, packeds, scales, Ns, Ks, G)  # one M, mixed shapes
+    h              = glu(x_bf16, (packed, scales), (packed, scales), N, K, G)  # gated block
+    y              = lora_matmul(x_bf16, packed, scales, ids, a, b, scaling, N, K, G)
+    h, g, u        = glu_forward(x_bf16, w_hat, w_hat)       # gated block on bf16 weights
+    dx, dwg, dwu   = glu_backward(dh, x_bf16, w_hat, w_hat, g, u)
+    h              = GLU.apply(x_bf16, w_hat, w_hat)         # both, for autograd
 
 `ternary_weight_only_amd.package` writes and reads the per-tensor package
 (codes + fp16 scales + sha256 hashes) and decodes it to bf16 on the device.
@@ -31,7 +36,9 @@ missing build raises immediately; there is no CPU fallback.
 """
 from .binding import (  # noqa: F401
     FakeQuantize,
+    GLU,
     TQError,
+    DEV_BAD_ADAPTER,
     DEV_BAD_PADDING,
     DEV_INVALID_BYTE,
     DEV_NONFINITE,
@@ -59,7 +66,14 @@ from .binding import (  # noqa: F401
     w4a16_gemv_grouped,
     w4a16_gemm,
     w4a16_gemm_batched,
+    glu,
+    glu_backward,
+    glu_backward_workspace,
+    glu_forward,
+    glu_workspace,
     lib,
+    lora_matmul,
+    lora_workspace,
     new_status,
     packed_bytes,
     packed_row_bytes,

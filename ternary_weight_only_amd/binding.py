@@ -19,6 +19,9 @@ DEV_NONFINITE = 1
 DEV_SCALE_OVERFLOW = 2
 DEV_INVALID_BYTE = 4
 DEV_BAD_PADDING = 8
+DEV_BAD_ADAPTER = 16
+
+ACTS = {"silu": 0, "gelu": 1}
 
 # Every symbol include/tq.h declares.
 SYMBOLS = ("tq_status_string", "tq_packed_row_bytes", "tq_packed_bytes", "tq_quantize_pack",
@@ -27,7 +30,9 @@ SYMBOLS = ("tq_status_string", "tq_packed_row_bytes", "tq_packed_bytes", "tq_qua
            "tq_unpack_batched", "tq_dequantize", "tq_dequantize_batched", "tq_quantize_pack2",
            "tq_quantize_pack2_batched", "tq_unpack2", "tq_gemv2", "tq_gemv2_batched",
            "tq_gemv2_grouped", "tq_gemm2", "tq_gemm2_batched", "tq_w4a16_gemv", "tq_w4a16_gemv_batched", "tq_w4a16_gemv_grouped",
-           "tq_w4a16_gemm", "tq_w4a16_gemm_batched", "tq_gemv", "tq_gemv_batched", "tq_gemv_grouped", "tq_gemm", "tq_gemm_batched", "tq_gemm_grouped")
+           "tq_w4a16_gemm", "tq_w4a16_gemm_batched", "tq_gemv", "tq_gemv_batched", "tq_gemv_grouped", "tq_gemm", "tq_gemm_batched", "tq_gemm_grouped",
+           "tq_glu", "tq_glu_workspace", "tq_lora_matmul", "tq_lora_workspace", "tq_glu_forward",
+           "tq_glu_backward", "tq_glu_backward_workspace")
 # Every symbol include/tq_probe.h declares (measurement probes).
 PROBE_SYMBOLS = ("tq_probe_lds_table", "tq_probe_mfma_bf16", "tq_probe_read_stream",
                  "tq_probe_valu")
@@ -116,6 +121,21 @@ def lib() -> ctypes.CDLL:
         l.tq_gemv_grouped.restype = i32
         l.tq_gemm_grouped.argtypes = [i32, p, p, p, p, i64, p, p, i32, p, p]
         l.tq_gemm_grouped.restype = i32
+        l.tq_glu.argtypes = [p, p, p, p, p, i64, i64, i64, i32, i32, p, p, i64, p, p]
+        l.tq_glu.restype = i32
+        l.tq_glu_workspace.argtypes = [i64, i64, i64, i32]
+        l.tq_glu_workspace.restype = i64
+        l.tq_lora_matmul.argtypes = [p, p, p, p, p, p, p, i64, i64, i64, i32, i64, i64, p, p, i64,
+                                     p, p]
+        l.tq_lora_matmul.restype = i32
+        l.tq_lora_workspace.argtypes = [i64, i64, i64, i32, i64]
+        l.tq_lora_workspace.restype = i64
+        l.tq_glu_forward.argtypes = [p, p, p, i64, i64, i64, i32, p, p, p, p]
+        l.tq_glu_forward.restype = i32
+        l.tq_glu_backward.argtypes = [p, p, p, p, p, p, i64, i64, i64, i32, p, p, p, p, i64, p]
+        l.tq_glu_backward.restype = i32
+        l.tq_glu_backward_workspace.argtypes = [i64, i64, i64]
+        l.tq_glu_backward_workspace.restype = i64
         # measurement probes (include/tq_probe.h)
         l.tq_probe_read_stream.argtypes = [p, i64, i32, p, p]
         l.tq_probe_read_stream.restype = i32
@@ -775,3 +795,169 @@ def w4a16_gemv_grouped(xs, packeds, scales_list, biases_list, Ns, Ks, G: int, ou
                                     _ptrs(biases_list), _ptrs(outs), _i64s(Ns), _i64s(Ks), G,
                                     _stream()), "tq_w4a16_gemv_grouped")
     return outs
+
+
+# ---------------------------------------------------------------------------
+# the gated feed-forward block and low-rank adapters
+# ---------------------------------------------------------------------------
+
+I32 = (torch.int32,)
+
+
+def _act(act) -> int:
+    if act not in ACTS:
+        raise TQError("act must be one of %s, not %r" % (sorted(ACTS), act))
+    return ACTS[act]
+
+
+def _shaped(t, name: str, shape, dtypes, device):
+    """An input of exactly `shape`, as _dev."""
+    _dev(t, name, dtypes, None, device)
+    if tuple(t.shape) != tuple(shape):
+        raise TQError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    return t
+
+
+def _workspace(ws, need: int, device):
+    """(address, bytes) of a call's workspace: the caller's uint8 tensor, or
+    one allocated here.  The tensor is returned too, to keep it alive until
+    the call is enqueued (torch's allocator reuses it in stream order)."""
+    if ws is None:
+        if need == 0:
+            return None, 0, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+    else:
+        _dev(ws, "workspace", U8, None, device)
+        if ws.numel() < need:
+            raise TQError("workspace has %d bytes, expected at least %d" % (ws.numel(), need))
+    return ws, ws.data_ptr(), ws.numel()
+
+
+def glu_workspace(M: int, N: int, K: int, G: int) -> int:
+    """Workspace bytes of glu; 0 for invalid arguments."""
+    return int(lib().tq_glu_workspace(M, N, K, G))
+
+
+def glu(x, gate, up, N: int, K: int, G: int, act="silu", status=None, out=None, workspace=None):
+    """Gated feed-forward block on packed ternary weights, any M:
+    x [M,K] bf16, gate and up (packed, scales) pairs of [N,K] weights ->
+    h bf16 [M,N] = act(x Wg^T) * (x Wu^T).  act is "silu" or "gelu" (tanh
+    form).  `workspace`, if given, is a uint8 tensor of at least
+    glu_workspace(M, N, K, G) bytes that no other call in flight uses."""
+    _dev(x, "x", BF16, 2)
+    dev, M = x.device, x.shape[0]
+    if x.shape[1] != K:
+        raise TQError("x has K=%d, expected %d" % (x.shape[1], K))
+    a = _act(act)
+    (gp, gs), (up_, us) = gate, up
+    _check_packed(gp, gs, N, K, G, dev, "tq_glu gate")
+    _check_packed(up_, us, N, K, G, dev, "tq_glu up")
+    h = _out(out, "h", (M, N), torch.bfloat16, BF16, dev)
+    ws, wp, wn = _workspace(workspace, glu_workspace(M, N, K, G), dev)
+    _rc(lib().tq_glu(x.data_ptr(), gp.data_ptr(), gs.data_ptr(), up_.data_ptr(), us.data_ptr(), M,
+                     N, K, G, a, h.data_ptr(), wp, wn, _st(status, dev), _stream()), "tq_glu")
+    return h
+
+
+def lora_workspace(M: int, N: int, K: int, G: int, R: int) -> int:
+    """Workspace bytes of lora_matmul; 0 for invalid arguments."""
+    return int(lib().tq_lora_workspace(M, N, K, G, R))
+
+
+def lora_matmul(x, packed, scales, ids, a, b, scaling, N: int, K: int, G: int, status=None,
+                out=None, workspace=None):
+    """A packed ternary projection shared by many requests' rows, beside each
+    row's own low-rank adapter, any M:
+    x [M,K] bf16, ids [M] int32 (-1: no adapter), a [adapters,R,K] bf16,
+    b [adapters,N,R] bf16, scaling [adapters] fp32 ->
+    y fp32 [M,N] = x W_hat^T + scaling[id] * (x a[id]^T) b[id]^T.
+    R is a multiple of 8 up to 256.  `workspace` as for glu, of
+    lora_workspace(M, N, K, G, R) bytes."""
+    _dev(x, "x", BF16, 2)
+    dev, M = x.device, x.shape[0]
+    if x.shape[1] != K:
+        raise TQError("x has K=%d, expected %d" % (x.shape[1], K))
+    _check_packed(packed, scales, N, K, G, dev, "tq_lora_matmul")
+    _shaped(ids, "ids", (M,), I32, dev)
+    _dev(a, "a", BF16, 3, dev)
+    n, R = a.shape[0], a.shape[1]
+    _shaped(a, "a", (n, R, K), BF16, dev)
+    _shaped(b, "b", (n, N, R), BF16, dev)
+    _shaped(scaling, "scaling", (n,), F32, dev)
+    y = _out(out, "y", (M, N), torch.float32, F32, dev)
+    ws, wp, wn = _workspace(workspace, lora_workspace(M, N, K, G, R), dev)
+    _rc(lib().tq_lora_matmul(x.data_ptr(), packed.data_ptr(), scales.data_ptr(), ids.data_ptr(),
+                             a.data_ptr(), b.data_ptr(), scaling.data_ptr(), M, N, K, G, n, R,
+                             y.data_ptr(), wp, wn, _st(status, dev), _stream()), "tq_lora_matmul")
+    return y
+
+
+def _train_inputs(x, wg, wu):
+    _dev(x, "x", BF16, 2)
+    _dev(wg, "wg", BF16, 2, x.device)
+    M, K = x.shape
+    N = wg.shape[0]
+    _shaped(wg, "wg", (N, K), BF16, x.device)
+    _shaped(wu, "wu", (N, K), BF16, x.device)
+    return x.device, M, N, K
+
+
+def glu_forward(x, wg, wu, act="silu", save: bool = True, out=None):
+    """Gated feed-forward block on bf16 weights (training): x [M,K], wg and wu
+    [N,K] bf16 -> (h, g, u) bf16 [M,N] with h = act(g) u, g = x wg^T,
+    u = x wu^T; with save=False h alone (g and u are never written).
+    `out`, if given, is (h, g, u) or, with save=False, h.  K % 64 == 0."""
+    dev, M, N, K = _train_inputs(x, wg, wu)
+    a = _act(act)
+    h, g, u = (None, None, None) if out is None else out if save else (out, None, None)
+    h = _out(h, "h", (M, N), torch.bfloat16, BF16, dev)
+    if save:
+        g = _out(g, "g", (M, N), torch.bfloat16, BF16, dev)
+        u = _out(u, "u", (M, N), torch.bfloat16, BF16, dev)
+    _rc(lib().tq_glu_forward(x.data_ptr(), wg.data_ptr(), wu.data_ptr(), M, N, K, a, h.data_ptr(),
+                             g.data_ptr() if save else 0, u.data_ptr() if save else 0, _stream()),
+        "tq_glu_forward")
+    return (h, g, u) if save else h
+
+
+def glu_backward_workspace(M: int, N: int, K: int) -> int:
+    """Workspace bytes of glu_backward; 0 for invalid arguments."""
+    return int(lib().tq_glu_backward_workspace(M, N, K))
+
+
+def glu_backward(dh, x, wg, wu, g, u, act="silu", out=None, workspace=None):
+    """Gradients of glu_forward: dh, g, u [M,N] bf16 -> (dx [M,K], dwg [N,K],
+    dwu [N,K]) bf16.  `out`, if given, is that triple; `workspace` as for glu,
+    of glu_backward_workspace(M, N, K) bytes."""
+    dev, M, N, K = _train_inputs(x, wg, wu)
+    a = _act(act)
+    for t, name in ((dh, "dh"), (g, "g"), (u, "u")):
+        _shaped(t, name, (M, N), BF16, dev)
+    dx, dwg, dwu = (None, None, None) if out is None else out
+    dx = _out(dx, "dx", (M, K), torch.bfloat16, BF16, dev)
+    dwg = _out(dwg, "dwg", (N, K), torch.bfloat16, BF16, dev)
+    dwu = _out(dwu, "dwu", (N, K), torch.bfloat16, BF16, dev)
+    ws, wp, wn = _workspace(workspace, glu_backward_workspace(M, N, K), dev)
+    _rc(lib().tq_glu_backward(dh.data_ptr(), x.data_ptr(), wg.data_ptr(), wu.data_ptr(),
+                              g.data_ptr(), u.data_ptr(), M, N, K, a, dx.data_ptr(),
+                              dwg.data_ptr(), dwu.data_ptr(), wp, wn, _stream()),
+        "tq_glu_backward")
+    return dx, dwg, dwu
+
+
+class GLU(torch.autograd.Function):
+    """h = act(x wg^T) * (x wu^T) with gradients for x, wg and wu; after
+    FakeQuantize the gradients of wg and wu reach the latent weights
+    unchanged.  Gradients that are not needed are still computed."""
+
+    @staticmethod
+    def forward(ctx, x, wg, wu, act="silu"):
+        h, g, u = glu_forward(x, wg, wu, act)
+        ctx.save_for_backward(x, wg, wu, g, u)
+        ctx.act = act
+        return h
+
+    @staticmethod
+    def backward(ctx, dh):
+        x, wg, wu, g, u = ctx.saved_tensors
+        return (*glu_backward(dh.contiguous(), x, wg, wu, g, u, ctx.act), None)

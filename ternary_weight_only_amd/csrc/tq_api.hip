@@ -44,6 +44,8 @@ const char *tq_status_string(int status) {
     case TQ_ERR_GROUP: return "TQ_ERR_GROUP: G must be 64 or 128";
     case TQ_ERR_ALIGN: return "TQ_ERR_ALIGN: pointer not aligned as required";
     case TQ_ERR_LAUNCH: return "TQ_ERR_LAUNCH: HIP launch failed";
+    case TQ_ERR_WORKSPACE: return "TQ_ERR_WORKSPACE: workspace too small";
+    case TQ_ERR_ACT: return "TQ_ERR_ACT: act is not a tq_act value";
     default: return "unknown tq status";
   }
 }

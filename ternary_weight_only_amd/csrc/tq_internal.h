@@ -12,6 +12,7 @@ constexpr int kDevNonfinite = 1;
 constexpr int kDevScaleOverflow = 2;
 constexpr int kDevInvalidByte = 4;
 constexpr int kDevBadPadding = 8;
+constexpr int kDevBadAdapter = 16;
 
 constexpr int bytes_per_group(int G) { return (G + 4) / 5; }
 
@@ -157,5 +158,26 @@ void launch_gemm_grouped(int count, const uint16_t *const *xs, const uint8_t *co
                          const uint16_t *const *scales, float *const *ys, int64_t M,
                          const int64_t *Ns, const int64_t *Ks, int G, int32_t *d_status,
                          hipStream_t stream);
+
+// Gated feed-forward and adapters on packed ternary weights (tq_glu.hip).
+void launch_glu(const uint16_t *x, const uint8_t *pg, const uint16_t *sg, const uint8_t *pu,
+                const uint16_t *su, int64_t M, int64_t N, int64_t K, int G, int act, uint16_t *h,
+                void *workspace, int32_t *d_status, hipStream_t stream);
+int64_t glu_workspace(int64_t M, int64_t N, int64_t K, int G);
+void launch_lora(const uint16_t *x, const uint8_t *packed, const uint16_t *scales, int64_t M,
+                 int64_t N, int64_t K, int G, const int32_t *ids, const uint16_t *a,
+                 const uint16_t *b, const float *scaling, int adapters, int R, float *y,
+                 void *workspace, int32_t *d_status, hipStream_t stream);
+int64_t lora_workspace(int64_t M, int64_t N, int64_t K, int G, int R);
+
+// Gated feed-forward on bf16 weights, forward and backward (tq_glu_train.hip).
+void launch_glu_forward(const uint16_t *x, const uint16_t *wg, const uint16_t *wu, int64_t M,
+                        int64_t N, int64_t K, int act, uint16_t *h, uint16_t *g, uint16_t *u,
+                        hipStream_t stream);
+void launch_glu_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *wg,
+                         const uint16_t *wu, const uint16_t *g, const uint16_t *u, int64_t M,
+                         int64_t N, int64_t K, int act, uint16_t *dx, uint16_t *dwg, uint16_t *dwu,
+                         void *workspace, hipStream_t stream);
+int64_t glu_backward_workspace(int64_t M, int64_t N, int64_t K);
 
 }  // namespace tq
