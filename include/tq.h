@@ -560,7 +560,7 @@ int tq_w4a16_gemv_grouped(int count, const uint16_t *const *xs, const uint32_t *
  *                            when that is 0); its contents on entry are
  *                            ignored and on return unspecified.  Calls in
  *                            flight at the same time need separate ones.
- * M = 0 enqueues nothing.  K is at most 4194304 (2^22).  A row of x that
+ * M = 0 enqueues nothing.  K is at most 2097152 (2^21).  A row of x that
  * holds an Inf or NaN gives unspecified (Inf or NaN where the formula has
  * them) values in that row of h and in no other.  Invalid packed bytes set
  * TQ_DEV_INVALID_BYTE; their contribution is then unspecified.
@@ -610,7 +610,7 @@ int64_t tq_lora_workspace(int64_t M, int64_t N, int64_t K, int G, int64_t R);
  * Gated feed-forward block on bf16 weights (training), forward:
  *   g = x Wg^T, u = x Wu^T (fp32), h = act(g) * u, each rounded once to bf16
  * with Wg, Wu the w_hat that tq_fake_quantize makes of the latent weights.
- *   x        [M,K] bf16, 16-byte aligned;  K % 64 == 0, K <= 2^22
+ *   x        [M,K] bf16, 16-byte aligned;  K % 64 == 0; N, K <= 2^21
  *   wg, wu   [N,K] bf16, 16-byte aligned
  *   h        [M,N] bf16, 16-byte aligned, overwritten
  *   g, u     [M,N] bf16, 16-byte aligned, overwritten: what the backward call

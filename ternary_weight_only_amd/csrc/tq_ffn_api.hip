@@ -11,8 +11,8 @@ namespace {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-constexpr int64_t kMaxK = int64_t(1) << 22;
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1024;  // rows and columns fit an int with tiles
+constexpr int64_t kMaxK = int64_t(1) << 21;  // a 256-row slab of x stays below 2^31 bytes
+constexpr int64_t kMaxRows = int64_t(1) << 30;  // tiles times threads fit a launch
 constexpr int64_t kMaxElems = int64_t(1) << 40;          // every byte count stays below 2^62
 
 bool product_ok(int64_t a, int64_t b) { return a == 0 || b <= kMaxElems / a; }
@@ -33,7 +33,7 @@ int check_packed_shape(int64_t M, int64_t N, int64_t K, int G) {
 int check_train_shape(int64_t M, int64_t N, int64_t K) {
   const int rc = check_mnk(M, N, K);
   if (rc) return rc;
-  return K % 64 == 0 ? TQ_OK : TQ_ERR_SHAPE;
+  return K % 64 == 0 && N <= kMaxK ? TQ_OK : TQ_ERR_SHAPE;  // N is a reduction length too
 }
 
 int check_rank(int64_t M, int64_t N, int64_t K, int64_t adapters, int64_t R) {
