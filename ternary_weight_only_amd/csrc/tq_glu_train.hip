@@ -90,7 +90,7 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void train_kernel(const TrainArgs A) 
   // The requests of one stage: L loads a thread, loads 0..1 of P then of Q.
   constexpr int L = PS::kLoads + QS::kLoads;
   struct Request {
-    __amdgpu_buffer_rsrc_t p, p_up, q;  // kFwd: p holds gate rows, p_up up rows
+    const uint16_t *p, *p_up, *q;  // kFwd: p holds gate rows, p_up up rows
     lds_bytes *pslot, *qslot;
     int prem, qrem;
   };
@@ -103,20 +103,20 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void train_kernel(const TrainArgs A) 
     const bool in = s < s1;
     if constexpr (MODE == kFwd) {
       const int64_t k = (int64_t)s * kKS;
-      r.p = mm_rsrc(A.p0 + (int64_t)n0 * A.K + k);
-      r.p_up = mm_rsrc(A.p1 + (int64_t)n0 * A.K + k);
-      r.q = mm_rsrc(qbase + k);
+      r.p = A.p0 + (int64_t)n0 * A.K + k;
+      r.p_up = A.p1 + (int64_t)n0 * A.K + k;
+      r.q = qbase + k;
       r.prem = r.qrem = in ? 1 : 0;
     } else if constexpr (MODE == kDx) {
       const int half = A.Np / kKS, sn = s < half ? s : s - half;
-      r.p = mm_rsrc((s < half ? A.p0 : A.p1) + (int64_t)sn * kKS * A.K + ip * BP);
-      r.q = mm_rsrc(qbase + (int64_t)s * kKS);
+      r.p = (s < half ? A.p0 : A.p1) + (int64_t)sn * kKS * A.K + ip * BP;
+      r.q = qbase + (int64_t)s * kKS;
       r.prem = in ? A.N - sn * kKS : 0;
       r.qrem = in ? 1 : 0;
     } else {
       const int64_t m = (int64_t)s * kKS;
-      r.p = mm_rsrc(A.p0 + m * A.K + ip * BP);
-      r.q = mm_rsrc(qbase + m * (2 * A.Np));
+      r.p = A.p0 + m * A.K + ip * BP;
+      r.q = qbase + m * (2 * A.Np);
       r.prem = r.qrem = !in ? 0 : A.M - m < kKS ? (int)(A.M - m) : kKS;
     }
     return r;
@@ -177,7 +177,7 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void train_kernel(const TrainArgs A) 
       pa[a] = pf.read(smem, pn, a);
       if (a < L) request(r, a);
     }
-    order_stage<PK, QK, TP, TQ, L>();
+    order_stage<PK, QK, TP, TQ>();
     __builtin_amdgcn_sched_barrier(0);
     // stage s + 2 has landed when only the 8 loads of s + 3 and s + 4 are out
     asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
