@@ -39,11 +39,6 @@ struct TrainArgs {
   int stages, splits;       // stages of 32 k in all (even), and the blocks they are shared by
 };
 
-__device__ __forceinline__ void store4(uint16_t *p, f32x4 v) {
-  *(u32x2 *)p = u32x2{(uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
-                      (uint32_t)f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
-}
-
 template <int MODE, int ACT, int BP, int BQ, int WP, int WQ>
 __global__ __launch_bounds__(64 * WP * WQ)
 __attribute__((amdgpu_waves_per_eu(2, 2))) void train_kernel(const TrainArgs A) {
@@ -144,7 +139,7 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void train_kernel(const TrainArgs A) 
 #pragma unroll
     for (int b = 0; b < TQ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  static_assert(L == 4 && TP >= TQ, "the waits below count four loads a thread and stage");
+  static_assert(TP >= TQ && TP >= L, "rows of MFMAs to put the reads and requests between");
   bf16x8 pa[TP], qa[TQ], qb[TQ];
 #pragma unroll
   for (int s = 0; s < kRing - 1; ++s) {
@@ -153,12 +148,12 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void train_kernel(const TrainArgs A) 
     for (int i = 0; i < L; ++i) request(r, i);
   }
   static_assert(kRing == 5, "the waits count the loads of four stages in flight");
-  asm volatile("s_waitcnt vmcnt(12)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(3 * L) : "memory");
 #pragma unroll
   for (int b = 0; b < TQ; ++b) qa[b] = qf.read(smem, kQOff, b);
 #pragma unroll
   for (int a = 0; a < TP; ++a) pa[a] = pf.read(smem, 0, a);
-  asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * L) : "memory");
 
   // Stage s: its fragments are pa and qc; those of s + 1 are read into pa (as
   // its blocks are used up) and qn.
@@ -179,8 +174,8 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void train_kernel(const TrainArgs A) 
     }
     order_stage<PK, QK, TP, TQ>();
     __builtin_amdgcn_sched_barrier(0);
-    // stage s + 2 has landed when only the 8 loads of s + 3 and s + 4 are out
-    asm volatile("s_waitcnt vmcnt(8)\n\ts_barrier" ::: "memory");
+    // stage s + 2 has landed when only the loads of s + 3 and s + 4 are out
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * L) : "memory");
   };
   for (int s = s0; s < s1; s += 2) {
     stage(s, qa, qb);

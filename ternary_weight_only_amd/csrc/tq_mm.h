@@ -69,9 +69,9 @@ __device__ __forceinline__ uint32_t rows_at(uint32_t r, uint32_t c) {
 // kernels' own (vmcnt before the barrier of a stage).  It has no register
 // results.
 __device__ __forceinline__ void dma16(const void *base, lds_bytes *dst, uint32_t off) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass knows no such registers
   const uint64_t b = (uint64_t)base;
   const u32x4 rs{(uint32_t)b, (uint32_t)(b >> 32) & 0xFFFFu, 0x7FFFFFFFu, 0x00020000u};
-#if defined(__HIP_DEVICE_COMPILE__)
   asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "{m0}"((uint32_t)dst), "v"(off), "s"(rs));
 #endif
@@ -105,6 +105,19 @@ struct Stream {
       krow[i] = k;
       off[i] = (int)(8u * c) < cols ? k * ld * 2u + 16u * c : kNoRow;
     }
+  }
+  // As load, for a kernel whose LDS reads the compiler can tell apart from
+  // these writes: its own wait counts include them.
+  __device__ __forceinline__ void load_tracked(int i, const void *base, lds_bytes *slot, uint32_t wave,
+                                               int krem) const {
+    static_assert(KIND == kRows, "");
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass knows no 16-byte load into LDS
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<void *>(base), (short)0, 0x7FFFFFFF, 0x00020000);
+    lds_bytes *dst = slot + 16u * ((uint32_t)(i * NT) + 64u * wave);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)dst, 16,
+                                             krem > 0 ? off[i] : kNoRow, 0, 0, 0);
+#endif
   }
   // Request i of the stage at `base` into `slot`; k rows >= krem read as
   // zeros.
@@ -173,6 +186,12 @@ __device__ __forceinline__ f32x4 mfma32(bf16x8 a, bf16x8 b, f32x4 c) {
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
   else
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// Four values as bf16, at an 8-byte aligned address.
+__device__ __forceinline__ void store4(uint16_t *p, f32x4 v) {
+  *(u32x2 *)p = u32x2{(uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
+                      (uint32_t)f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
 }
 
 // Tile of block b of a launch: consecutive tiles run on one XCD (blocks go to
