@@ -13,10 +13,13 @@
 // (five of each byte, and the few of the last byte or two shared out), and x
 // is put into the same order once, by whoever reads it (tq_ternary.h).
 //
-// Two kernels multiply:
-//   dec_kernel    few rows: every packed byte is decoded in registers by the
-//                 lane that feeds it to the matrix cores; the waves of a block
-//                 share the groups of the same 16 or 32 weight rows.
+// Three kernels multiply:
+//   few_kernel    up to 16 rows: bound by the weights' bytes.  Every byte is
+//                 decoded in registers by the lane that feeds it to the matrix
+//                 cores; the waves of a block share the groups of a tile of 16
+//                 weight rows, x stays in LDS.
+//   mid_kernel    some more rows: the same decode, a tile of weight rows a
+//                 wave, 64 rows of x streamed through LDS for all eight.
 //   wide_kernel   many rows: 256 x 256 tiles (tq_mm.h); each block decodes its
 //                 weight rows into LDS, where 256 rows of x use them.
 #include <hip/hip_fp16.h>
@@ -40,14 +43,17 @@ struct ProjArgs {
   const uint16_t *scales[2];
   const int32_t *shift;           // wide: x of row m is stored times 2^shift[m]
   const int32_t *ids;             // lora
-  const float *t;                 // lora: [M,R] fp32, scaled
+  const float *t;                 // lora: [tsplits][M,R] fp32, scaled
+  int tsplits;
   const uint16_t *b;              // lora: [adapters,N,R]
   int adapters, R;
   void *out;                      // bf16 [M,N] (glu) or fp32 [M,N] (lora)
   float *partial;                 // splits > 1: fp32 [split][NB][M][N]
   int64_t M;
   int N, K;
-  int splits, chunks;             // dec: blocks along K, and chunks of rows
+  int splits;                     // blocks along K
+  int wk;                         // few: waves along K (a power of two)
+  int chunks;                     // mid: chunks of rows
   int tp, tq;                     // wide: tiles
   int32_t *status;
 };
@@ -67,278 +73,425 @@ __device__ __forceinline__ uint64_t adapter_leaders(int id, int lane) {
   return __ballot(first);
 }
 
-// A row's t in three bf16 pieces (24 bits together): eight ranks of it.
+// Eight ranks of row m's t in three bf16 pieces (24 bits together); zeros
+// unless `in`.
 struct Pieces {
   bf16x8 p[3];
 };
-__device__ __forceinline__ Pieces split_t(const float *t, bool in) {
-  Pieces r;
+__device__ __forceinline__ Pieces split_t(const ProjArgs &A, int64_t m, int r, bool in) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.f;
+  if (in)
+    for (int k = 0; k < A.tsplits; ++k) {
+      const f32x4 *t = (const f32x4 *)(A.t + ((int64_t)k * A.M + m) * A.R + r);
+      const f32x4 lo = t[0], hi = t[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] += lo[i];
+        v[4 + i] += hi[i];
+      }
+    }
+  Pieces out;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float v = in ? t[i] : 0.f;
-    const __bf16 a = (__bf16)v;
-    const float ra = v - (float)a;
+    const __bf16 a = (__bf16)v[i];
+    const float ra = v[i] - (float)a;
     const __bf16 b = (__bf16)ra;
-    r.p[0][i] = a;
-    r.p[1][i] = b;
-    r.p[2][i] = (__bf16)(ra - (float)b);
+    out.p[0][i] = a;
+    out.p[1][i] = b;
+    out.p[2][i] = (__bf16)(ra - (float)b);
   }
-  return r;
+  return out;
+}
+
+// Add the adapters' part to one tile of 16 weight rows (columns n0 + lane %
+// 16) by 16 MT rows of x (row m0 + i named by lane i's id, -1 for none).  The
+// distinct adapters are taken in turn, those with turn % share == mine here.
+// A product of one adapter is made for all the rows and kept for its own, so
+// nothing in an adapter reaches another's rows.
+template <int MT>
+__device__ void add_adapters(const ProjArgs &A, int64_t m0, int n0, int id, int share, int mine,
+                             f32x4 (&acc)[MT]) {
+  const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
+  const int64_t n = min(n0 + l, A.N - 1);
+  uint64_t todo = adapter_leaders(id, lane);
+  for (int turn = 0; todo; ++turn) {
+    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+    todo &= todo - 1;
+    if (turn % share != mine) continue;
+    f32x4 add[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) add[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int r0 = 0; r0 < A.R; r0 += 32) {
+      const int r = r0 + 8 * q;
+      u32x4 v{0u, 0u, 0u, 0u};
+      if (r < A.R) v = *(const u32x4 *)(A.b + ((int64_t)a * A.N + n) * A.R + r);
+      const bf16x8 bv = __builtin_bit_cast(bf16x8, v);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const bool own = __shfl(id, 16 * mt + l) == a;
+        if (!__ballot(own)) continue;
+        const Pieces p = split_t(A, m0 + 16 * mt + l, r, own && r < A.R);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) add[mt] = mfma32<false>(p.p[i], bv, add[mt]);
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[mt][j] += __shfl(id, 16 * mt + 4 * q + j) == a ? add[mt][j] : 0.f;
+  }
+}
+
+// The id of row m as add_adapters takes it.
+__device__ __forceinline__ int adapter_of(const ProjArgs &A, int64_t m, bool in) {
+  const int id = in && m < A.M ? A.ids[m] : -1;
+  return id < A.adapters ? id : -1;
 }
 
 // ---------------------------------------------------------------------------
-// few rows
+// up to 16 rows
 // ---------------------------------------------------------------------------
-
-constexpr int kDecWaves = 8, kDecThreads = 64 * kDecWaves;
-constexpr int kStagedRows = 4;            // rows of x a block puts in order itself
-constexpr uint32_t kStagedBytes = 48 << 10;  // and the LDS for them
 
 // One lane's bytes of one group of one weight row.
 struct Raw {
   uint32_t w0, w1, tail, scale;
 };
 
+// `tile` is the group's bytes in the tile's first row and `stile` its scale
+// there (both the same for the wave); row, srow the lane's row within the tile
+// in bytes and in scales.
 template <int G>
-__device__ __forceinline__ Raw load_raw(const uint8_t *row, const uint16_t *srow, int g, int q) {
+__device__ __forceinline__ Raw load_raw(const uint8_t *tile, const uint16_t *stile, uint32_t row,
+                                        uint32_t srow, uint32_t q) {
   Raw r;
-  const uint8_t *p = row + (int64_t)g * bytes_per_group(G);
   if constexpr (G == 128) {
     uint64_t w;
     uint16_t tail;
-    __builtin_memcpy(&w, p + 6 * q, 8);  // six bytes of it; q = 3 ends at the group's end
-    __builtin_memcpy(&tail, p + 24, 2);
+    __builtin_memcpy(&w, tile + (row + 6u * q), 8);  // six of them; q = 3 ends at the group's end
+    __builtin_memcpy(&tail, tile + (row + 24u), 2);
     r.w0 = (uint32_t)w;
     r.w1 = (uint32_t)(w >> 32);
     r.tail = tail;
   } else {
-    __builtin_memcpy(&r.w0, p + 3 * q, 4);  // three bytes of it; q = 3 ends at the group's end
+    __builtin_memcpy(&r.w0, tile + (row + 3u * q), 4);  // three; q = 3 ends at the group's end
     r.w1 = 0;
-    r.tail = p[12];
+    r.tail = tile[row + 12u];
   }
-  r.scale = srow[g];
+  r.scale = stile[srow];
   return r;
 }
 
-// A block: RT tiles of 16 rows of W (of each matrix), one chunk of 16 MT rows
-// of x, the groups of one split; wave w takes groups w, w + 8, ...
-// STAGED: x is bf16 [M,K], M <= 4, and each block puts its slice in order in
-// LDS; else x comes in fragment order from frag_role, a fragment 1 KB.
+constexpr int kFewRows = 16;
+constexpr int kFewWaves = 16, kFewThreads = 64 * kFewWaves;
+constexpr uint32_t kFewX = 64 << 10;  // LDS for a block's slice of x
+// Groups a wave requests together: what 128 registers a lane leave room for.
+constexpr int few_u(int G, int NB) { return G == 128 && NB == 2 ? 2 : 4; }
+
+// A block: one split of K, and tiles of 16 weight rows (of each matrix) one
+// set after another, kFewWaves / wk tiles a set; wk waves share the groups of
+// a tile.  x [M,K] (M <= 16) of the split is put in order once, in LDS.
 // The matrix cores take x as the row operand and W as the column operand, so
 // a lane's partial sums belong to the weight row whose bytes it decoded.
-template <int G, int NB, int MT, int RT, bool STAGED, int ACT>
-__global__ __launch_bounds__(kDecThreads) void dec_kernel(const ProjArgs A) {
-  constexpr int S32 = G / 32;
-  constexpr uint32_t kRedBytes = kDecWaves * MT * 1024;
-  constexpr uint32_t kBuf = STAGED ? kStagedBytes : kRedBytes;
-  static_assert(kBuf >= kRedBytes, "the sums of the waves reuse x's LDS");
-  __shared__ __align__(16) unsigned char smem_raw[kLutBytes + kBuf];
+// A wave requests few_u groups of bytes while it works on as many others,
+// across the ends of tiles.  One block a CU: 64 KB table, 64 KB x, 16 KB a matrix for
+// the sums of the waves.
+template <int G, int NB, int ACT>
+__global__ __launch_bounds__(kFewThreads) void few_kernel(const ProjArgs A) {
+  constexpr int S32 = G / 32, B = bytes_per_group(G), kFewU = few_u(G, NB);
+  typedef Lut<kLutBf16, 32> L;
+  constexpr uint32_t kXOff = L::kBytes, kRedOff = kXOff + kFewX;
+  __shared__ __align__(16) unsigned char smem_raw[kRedOff + kFewWaves * NB * 1024];
   lds_bytes *smem = (lds_bytes *)smem_raw;
-  lds_bytes *buf = smem + kLutBytes;
+  const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int nG = A.K / G, M = (int)A.M;
+  const int split = (int)blockIdx.x % A.splits, b0 = (int)blockIdx.x / A.splits;
+  const int blocks = (int)gridDim.x / A.splits;
+  const int g0 = (int)((int64_t)nG * split / A.splits);
+  const int g1 = (int)((int64_t)nG * (split + 1) / A.splits);
+  const int wk = A.wk, wt = kFewWaves / wk;       // waves of a tile, tiles of a set
+  const int kw = wv % wk, tw = wv / wk;           // this wave's place
+  const int tiles = (A.N + 15) / 16, sets = (tiles + wt - 1) / wt;
+  const int steps = b0 < sets ? (sets - b0 + blocks - 1) / blocks : 0;
+  const int batches = (g1 - g0 + wk * kFewU - 1) / (wk * kFewU);  // of a tile
+
+  // the set of step j is b0 + j * blocks
+  auto tile_row = [&](int j) { return ((b0 + j * blocks) * wt + tw) * 16; };
+  struct Batch {
+    Raw r[kFewU][NB];
+  };
+  int fj = 0, fk = 0;  // step and batch of the next request
+  auto fetch = [&](Batch &f) {
+    const int n0 = tile_row(fj);
+    if (fj < steps && n0 < A.N) {
+      // rows past N read row N - 1; their sums are not stored
+      const uint32_t ln = (uint32_t)min(l, A.N - 1 - n0);
+      const uint32_t row = ln * (uint32_t)nG * B, srow = ln * (uint32_t)nG;
+#pragma unroll
+      for (int u = 0; u < kFewU; ++u) {
+        const int g = g0 + kw + wk * (fk * kFewU + u);
+        if (g >= g1) break;
+        const int64_t at = (int64_t)n0 * nG + g;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+          f.r[u][i] = load_raw<G>(A.packed[i] + at * B, A.scales[i] + at, row, srow, (uint32_t)q);
+      }
+    }
+    if (++fk == batches) {
+      fk = 0;
+      ++fj;
+    }
+  };
+
+  // the first bytes are requested before the table is built and x put in order
+  Batch ba, bb;
+  fetch(ba);
+  L::build(smem, tid, kFewThreads);
+  {
+    // unit: a quarter's codes of a group of one row
+    const int quarters = 4 * (g1 - g0), units = quarters * M;
+    for (int e = tid; e < units; e += kFewThreads) {
+      const int m = e / quarters, gq = e - m * quarters, g = gq >> 2, uq = gq & 3;
+      u32x4 f[S32];
+      order_quarter<G>(A.x + (int64_t)m * A.K + (int64_t)(g0 + g) * G, uq, f);
+#pragma unroll
+      for (int s = 0; s < S32; ++s)
+        *(lds_u32x4 *)(smem + kXOff + 16u * (uint32_t)(((g * S32 + s) * 4 + uq) * M + m)) = f[s];
+    }
+  }
+  __syncthreads();
+
+  const L lut(0, lane);
+  const uint32_t xlane = kXOff + 16u * (uint32_t)(q * M + min(l, M - 1));  // rows past M: row M - 1
+  int id = -1;
+  if constexpr (NB == 1) id = adapter_of(A, lane, lane < 16);
+  uint32_t flags = 0;
+  f32x4 acc[NB][1];
+#pragma unroll
+  for (int i = 0; i < NB; ++i) acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  int j = 0, k = 0;  // step and batch being worked on
+  auto work = [&](Batch &f, Batch &next) {
+    fetch(next);
+    const int n0 = tile_row(j);
+    if (n0 < A.N) {
+#pragma unroll
+      for (int u = 0; u < kFewU; ++u) {
+        const int g = g0 + kw + wk * (k * kFewU + u);
+        if (g >= g1) break;
+        bf16x8 xf[S32];
+#pragma unroll
+        for (int s = 0; s < S32; ++s)
+          xf[s] = *(lds_bf16x8_c *)(smem + xlane + 64u * (uint32_t)(((g - g0) * S32 + s) * M));
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const Raw r = f.r[u][i];
+          uint32_t d[G / 8];
+          decode_quarter<G>(smem, lut, r.w0, r.w1, r.tail, q, d, flags);
+          f32x4 part{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int s = 0; s < S32; ++s)
+            part = mfma32<false>(
+                xf[s], __builtin_bit_cast(bf16x8, u32x4{d[4 * s], d[4 * s + 1], d[4 * s + 2], d[4 * s + 3]}),
+                part);
+          // codes entered as 2c
+          const float sh = 0.5f * __half2float(__ushort_as_half((unsigned short)r.scale));
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[i][0][c] = fmaf(sh, part[c], acc[i][0][c]);
+        }
+      }
+    }
+    if (++k < batches) return;
+    k = 0;
+    // the tile's last batch: adapters (split 0), then the waves' sums in order
+    if constexpr (NB == 1)
+      if (split == 0 && A.adapters > 0 && n0 < A.N) add_adapters<1>(A, 0, n0, id, wk, kw, acc[0]);
+    __syncthreads();  // the sums of the set before have been read
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+      *(__attribute__((address_space(3))) f32x4 *)(smem + kRedOff + 16u * (uint32_t)((i * kFewWaves + wv) * 64 + lane)) =
+          acc[i][0];
+      acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    __syncthreads();
+    for (int o = tid; o < wt * 256; o += kFewThreads) {  // [tile][row][column]
+      const int m = (o >> 4) & 15, n = ((b0 + j * blocks) * wt + (o >> 8)) * 16 + (o & 15);
+      if (m >= M || n >= A.N) continue;
+      // row m of column c is element m % 4 of lane 16 (m / 4) + c
+      const uint32_t at = kRedOff + 16u * (uint32_t)((o >> 8) * wk * 64 + (m >> 2) * 16 + (o & 15)) + 4u * (m & 3);
+      float v[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        v[i] = 0.f;
+        for (int w = 0; w < wk; ++w)
+          v[i] += *(__attribute__((address_space(3))) float *)(smem + at + 1024u * (uint32_t)(i * kFewWaves + w));
+      }
+      const int64_t at_out = (int64_t)m * A.N + n;
+      if (A.splits > 1) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) A.partial[((int64_t)split * NB + i) * M * A.N + at_out] = v[i];
+      } else if constexpr (NB == 2) {
+        ((uint16_t *)A.out)[at_out] = f32_to_bf16(act_value<ACT>(v[0]) * v[1]);
+      } else {
+        ((float *)A.out)[at_out] = v[0];
+      }
+    }
+    ++j;
+  };
+  const int total = steps * batches;
+  for (int t = 0; t < total; t += 2) {
+    work(ba, bb);
+    if (t + 1 < total) work(bb, ba);
+  }
+  if ((flags & kBadFlag) && A.status) atomicOr(A.status, kDevInvalidByte);
+}
+
+// ---------------------------------------------------------------------------
+// some rows
+// ---------------------------------------------------------------------------
+
+constexpr int kMidWaves = 8, kMidThreads = 64 * kMidWaves;
+
+// A block: 128 weight rows (of each matrix), a tile of 16 a wave; one chunk of
+// 16 MT rows of x; one split of K.  x comes in fragment order (frag_role), a
+// group at a time, through a ring of LDS slots that all waves read.
+template <int G, int NB, int MT, int ACT>
+__global__ __launch_bounds__(kMidThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
+void mid_kernel(const ProjArgs A) {
+  constexpr int S32 = G / 32, B = bytes_per_group(G);
+  typedef Lut<kLutBf16, 16> L;
+  constexpr uint32_t kStage = S32 * MT * 1024, kLoad = 16 * kMidThreads;
+  constexpr uint32_t kSlot = kStage > kLoad ? kStage : kLoad;
+  constexpr int kD = kSlot / kLoad;                             // loads a thread and stage
+  constexpr int kSlots = 49152 / kSlot > 6 ? 6 : 49152 / kSlot;  // 80 KB in all: two blocks a CU
+  __shared__ __align__(16) unsigned char smem_raw[L::kBytes + kSlots * kSlot];
+  lds_bytes *smem = (lds_bytes *)smem_raw;
+  lds_bytes *ring = smem + L::kBytes;
   const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nG = A.K / G;
-
   int b = (int)blockIdx.x;
   const int chunk = b % A.chunks;
   b /= A.chunks;
-  const int split = b % A.splits, n0 = b / A.splits * (16 * RT);
+  const int split = b % A.splits, n0 = (b / A.splits) * 128 + 16 * wv;
   const int g0 = (int)((int64_t)nG * split / A.splits);
   const int g1 = (int)((int64_t)nG * (split + 1) / A.splits);
   const int64_t m0 = (int64_t)chunk * (16 * MT);
 
   // rows past N read row N - 1; their sums are not stored
-  const uint8_t *row[RT][NB];
-  const uint16_t *srow[RT][NB];
+  const int nt = min(n0, A.N - 1);
+  const uint32_t ln = (uint32_t)min(l, A.N - 1 - nt);
+  const uint32_t row = ln * (uint32_t)nG * B, srow = ln * (uint32_t)nG;
+  Raw ra[NB], rb[NB];
+  auto fetch = [&](Raw(&r)[NB], int g) {  // always: the waits below count its loads
+    const int64_t at = (int64_t)nt * nG + min(g, nG - 1);
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
+    for (int i = 0; i < NB; ++i)
+      r[i] = load_raw<G>(A.packed[i] + at * B, A.scales[i] + at, row, srow, (uint32_t)q);
+  };
+  uint32_t off[kD];
+#pragma unroll
+  for (int i = 0; i < kD; ++i) {
+    off[i] = (uint32_t)(i * kLoad + 16 * tid);
+    if (off[i] >= kStage) off[i] = kNoRow;
+  }
+  const uint16_t *xbase = A.x + (int64_t)chunk * nG * (kStage / 2);
+  int put = 0;  // slot of the next request
+  auto request = [&](int g) {
+#pragma unroll
+    for (int i = 0; i < kD; ++i)
+      dma16_tracked(xbase + (int64_t)g * (kStage / 2),
+                    ring + (uint32_t)put * kSlot + (uint32_t)(i * kLoad) + 1024u * (uint32_t)wv,
+                    g < g1 ? off[i] : kNoRow);
+    put = put == kSlots - 1 ? 0 : put + 1;
+  };
+
+  fetch(ra, g0);
+  fetch(rb, g0 + 1);
+#pragma unroll
+  for (int s = 0; s < kSlots - 1; ++s) request(g0 + s);
+  L::build(smem, tid, kMidThreads);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  f32x4 acc[NB][MT];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) acc[i][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const L lut(0, lane);
+  uint32_t flags = 0;
+  int get = 0;
+  auto stage = [&](int g, Raw(&r)[NB]) {
+    request(g + kSlots - 1);
+    lds_bytes *x = ring + (uint32_t)get * kSlot + 16u * (uint32_t)lane;
+    get = get == kSlots - 1 ? 0 : get + 1;
+    uint32_t d[NB][G / 8];
+    float sh[NB];
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      const int64_t n = min(n0 + 16 * rt + l, A.N - 1);
-      row[rt][i] = A.packed[i] + n * nG * bytes_per_group(G);
-      srow[rt][i] = A.scales[i] + n * nG;
+      decode_quarter<G>(smem, lut, r[i].w0, r[i].w1, r[i].tail, q, d[i], flags);
+      // codes entered as 2c
+      sh[i] = 0.5f * __half2float(__ushort_as_half((unsigned short)r[i].scale));
     }
-
-  // the first bytes are requested before the table is built and x put in
-  // order, which take as long as the bytes do
-  constexpr int U = RT * NB >= 4 ? 2 : 4;  // groups in flight
-  Raw raw[U][RT][NB];
-  auto fetch = [&](int u, int g) {
-    const int gc = min(g, nG - 1);
+    fetch(r, g + 2);
+    f32x4 part[NB][MT];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+    for (int s = 0; s < S32; ++s)
 #pragma unroll
-      for (int i = 0; i < NB; ++i) raw[u][rt][i] = load_raw<G>(row[rt][i], srow[rt][i], gc, q);
-  };
+      for (int mt = 0; mt < MT; ++mt) {
+        const bf16x8 xf = *(lds_bf16x8_c *)(x + 1024u * (uint32_t)(s * MT + mt));
 #pragma unroll
-  for (int u = 0; u < U; ++u) fetch(u, g0 + wv + kDecWaves * u);
-
-  build_lut<kLutBf16>(smem, tid, kDecThreads);
-  if constexpr (STAGED) {
-    // unit (g, quarter, m): a quarter's codes of a group of one row
-    const int M = (int)A.M, units = (g1 - g0) * 4 * M;
-    for (int e = tid; e < units; e += kDecThreads) {
-      const int m = e % M, gq = e / M, g = gq >> 2, uq = gq & 3;
-      u32x4 f[S32];
-      order_quarter<G>(A.x + (int64_t)m * A.K + (int64_t)(g0 + g) * G, uq, f);
-#pragma unroll
-      for (int s = 0; s < S32; ++s)
-        *(lds_u32x4 *)(buf + 16u * (uint32_t)(((g * S32 + s) * 4 + uq) * M + m)) = f[s];
-    }
-  }
-  __syncthreads();
-
-  f32x4 acc[RT][NB][MT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
+        for (int i = 0; i < NB; ++i)
+          part[i][mt] = mfma32<false>(
+              xf,
+              __builtin_bit_cast(bf16x8, u32x4{d[i][4 * s], d[i][4 * s + 1], d[i][4 * s + 2], d[i][4 * s + 3]}),
+              s == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : part[i][mt]);
+      }
 #pragma unroll
     for (int i = 0; i < NB; ++i)
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) acc[rt][i][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  const uint32_t lut = lut_lane(lane);
-  uint32_t flags = 0;
-  for (int g = g0 + wv; g < g1; g += kDecWaves * U) {
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int gu = g + kDecWaves * u;
-      if (gu >= g1) break;
-      bf16x8 xf[S32][MT];
-#pragma unroll
-      for (int s = 0; s < S32; ++s)
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          if constexpr (STAGED) {
-            // rows past M read row M - 1
-            const int M = (int)A.M;
-            xf[s][mt] = *(lds_bf16x8_c *)(buf + 16u * (uint32_t)((((gu - g0) * S32 + s) * 4 + q) * M +
-                                                                 min(l, M - 1)));
-          } else {
-            xf[s][mt] = *(const bf16x8 *)(A.x + ((((int64_t)chunk * nG + gu) * S32 + s) * MT + mt) * 512 +
-                                          lane * 8);
-          }
-        }
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          const Raw r = raw[u][rt][i];
-          uint32_t d[4 * S32];
-          decode_quarter<G>(smem, lut, r.w0, r.w1, r.tail, q, d, flags);
-          f32x4 part[MT];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) part[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int s = 0; s < S32; ++s) {
-            const bf16x8 w = __builtin_bit_cast(bf16x8, u32x4{d[4 * s], d[4 * s + 1], d[4 * s + 2], d[4 * s + 3]});
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) part[mt] = mfma32<false>(xf[s][mt], w, part[mt]);
-          }
-          // codes entered as 2c
-          const float sh = 0.5f * __half2float(__ushort_as_half((unsigned short)r.scale));
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[rt][i][mt][j] = fmaf(sh, part[mt][j], acc[rt][i][mt][j]);
-        }
-      fetch(u, gu + kDecWaves * U);
-    }
+        for (int c = 0; c < 4; ++c) acc[i][mt][c] = fmaf(sh[i], part[i][mt][c], acc[i][mt][c]);
+    // x of group g + 1 has landed when what was requested after it is all
+    // that is out: the rest of its stage at the least, and kSlots - 2 stages
+    // of kD loads of x and 3 NB of bytes and scales
+    constexpr int kOut = (kSlots - 2) * (kD + 3 * NB);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kOut > 63 ? 63 : kOut) : "memory");
+  };
+  for (int g = g0; g < g1; g += 2) {
+    stage(g, ra);
+    if (g + 1 < g1) stage(g + 1, rb);
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may still write this block's LDS
   if ((flags & kBadFlag) && A.status) atomicOr(A.status, kDevInvalidByte);
 
   if constexpr (NB == 1) {
-    // adapters, once per output (split 0); the waves take the distinct ones
-    // in turn and add to their partial sums.  A product of one adapter is
-    // made for all rows of the chunk and kept for its own, so nothing in an
-    // adapter reaches another's rows.
-    if (split == 0 && A.adapters > 0) {
-      int id = -1;
-      if (lane < 16 * MT && m0 + lane < A.M) id = A.ids[m0 + lane];
-      if (id >= A.adapters) id = -1;
-      uint64_t todo = adapter_leaders(id, lane);
-      for (int turn = 0; todo; ++turn) {
-        const int first = __builtin_ctzll(todo);
-        todo &= todo - 1;
-        if (turn % kDecWaves != wv) continue;
-        const int a = __builtin_amdgcn_readlane(id, first);
-        f32x4 add[RT][MT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) add[rt][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int r0 = 0; r0 < A.R; r0 += 32) {
-          const bool in = r0 + 8 * q < A.R;
-          bf16x8 bv[RT];
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            const int64_t n = min(n0 + 16 * rt + l, A.N - 1);
-            u32x4 v{0u, 0u, 0u, 0u};
-            if (in) v = *(const u32x4 *)(A.b + ((int64_t)a * A.N + n) * A.R + r0 + 8 * q);
-            bv[rt] = __builtin_bit_cast(bf16x8, v);
-          }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const int own = __shfl(id, 16 * mt + l);
-            const Pieces p = split_t(A.t + (m0 + 16 * mt + l) * A.R + r0 + 8 * q, in && own == a);
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-              for (int i = 0; i < 3; ++i) add[rt][mt] = mfma32<false>(p.p[i], bv[rt], add[rt][mt]);
-          }
-        }
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const bool mine = __shfl(id, 16 * mt + 4 * q + j) == a;
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) acc[rt][0][mt][j] += mine ? add[rt][mt][j] : 0.f;
-          }
-      }
-    }
+    // the splits share the adapters
+    const int64_t m = m0 + lane;
+    if (A.adapters > 0 && n0 < A.N)
+      add_adapters<MT>(A, m0, n0, adapter_of(A, m, lane < 16 * MT), A.splits, split, acc[0]);
   }
-
-  // sums of the waves, in wave order
-  constexpr int E = (MT * 256 + kDecThreads - 1) / kDecThreads;  // outputs a thread and matrix
+  const int n = n0 + l;
+  if (n >= A.N) return;
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    float v[NB][E];
+  for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      __syncthreads();
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-        *(__attribute__((address_space(3))) f32x4 *)(buf + 16u * (uint32_t)((wv * MT + mt) * 64 + lane)) =
-            acc[rt][i][mt];
-      __syncthreads();
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int o = e * kDecThreads + tid;
-        v[i][e] = 0.f;
-        if (o < MT * 256)
-#pragma unroll
-          for (int w = 0; w < kDecWaves; ++w)
-            v[i][e] += *(__attribute__((address_space(3))) float *)(buf + 4u * (uint32_t)(w * MT * 256 + o));
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const int o = e * kDecThreads + tid;  // [mt][lane][j]
-      const int j = o & 3, ol = (o >> 2) & 63;
-      const int64_t m = m0 + 16 * (o >> 8) + 4 * (ol >> 4) + j;
-      const int n = n0 + 16 * rt + (ol & 15);
-      if (o >= MT * 256 || m >= A.M || n >= A.N) continue;
+    for (int c = 0; c < 4; ++c) {
+      const int64_t m = m0 + 16 * mt + 4 * q + c;
+      if (m >= A.M) continue;
+      const int64_t o = m * A.N + n;
       if (A.splits > 1) {
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
-          A.partial[(((int64_t)split * NB + i) * A.M + m) * A.N + n] = v[i][e];
+        for (int i = 0; i < NB; ++i) A.partial[((int64_t)split * NB + i) * A.M * A.N + o] = acc[i][mt][c];
       } else if constexpr (NB == 2) {
-        ((uint16_t *)A.out)[m * A.N + n] = f32_to_bf16(act_value<ACT>(v[0][e]) * v[1][e]);
+        ((uint16_t *)A.out)[o] = f32_to_bf16(act_value<ACT>(acc[0][mt][c]) * acc[1][mt][c]);
       } else {
-        ((float *)A.out)[m * A.N + n] = v[0][e];
+        ((float *)A.out)[o] = acc[0][mt][c];
       }
     }
-  }
 }
 
 // The splits' partial sums, in order, and the operator's last step.
@@ -364,7 +517,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const float *__restrict__ 
 // ---------------------------------------------------------------------------
 
 constexpr int kWideP = 256, kWideQ = 256, kWideThreads = 512;
-constexpr int kWideRing = 4;  // slots of x, and of codes
+constexpr int kWideX = 5, kWideC = 4;  // slots of x, and of codes
 
 // 256 rows of W (NB = 1) or 128 of each of two (NB = 2) by 256 rows of x, in
 // stages of 32 k; codes times their scale and x as f16 (both exact, see
@@ -373,24 +526,30 @@ constexpr int kWideRing = 4;  // slots of x, and of codes
 //   - reads the fragments of s + 1,
 //   - decodes the codes of s + 3: two threads a weight row, three bytes and
 //     one of the group's left-over codes each,
-//   - requests x of s + 3 and the bytes of s + 5.
-// LDS: 64 KB x, 64 KB codes, 32 KB table.
+//   - requests x of s + 4 and the bytes of s + 7.
+// LDS: 80 KB x, 64 KB codes, 16 KB table.  K is split between blocks when the
+// tiles are few.
 template <int G, int NB, int ACT>
 __global__ __launch_bounds__(kWideThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void wide_kernel(const ProjArgs A) {
   constexpr int S32 = G / 32, WP = 2, WQ = 4, TP = 8, TQ = 4, B = bytes_per_group(G);
   typedef Stream<kRows, kWideQ, kWideThreads> QS;
+  typedef Lut<kLutF16, 8> L;
   constexpr uint32_t kPSlot = kWideP * kKS * 2;
-  constexpr uint32_t kQOff = kWideRing * kPSlot, kLutOff = kQOff + kWideRing * QS::kSlot;
-  __shared__ __align__(16) unsigned char smem_raw[kLutOff + kLutBytes];
+  constexpr uint32_t kQOff = kWideC * kPSlot, kLutOff = kQOff + kWideX * QS::kSlot;
+  __shared__ __align__(16) unsigned char smem_raw[kLutOff + L::kBytes];
   lds_bytes *smem = (lds_bytes *)smem_raw;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wp = wv / WQ, wq = wv % WQ;
-  const int nG = A.K / G, S = A.K / kKS;
+  const int nG = A.K / G, tiles = A.tp * A.tq, split = (int)blockIdx.x / tiles;
+  // this block's groups, and its stages counted from the first
+  const int g0 = (int)((int64_t)nG * split / A.splits);
+  const int g1 = (int)((int64_t)nG * (split + 1) / A.splits);
+  const int S = (g1 - g0) * S32;
 
   int ip, iq;
-  tile_of_block((int)blockIdx.x, A.tp * A.tq, A.tp, A.tq, ip, iq);
+  tile_of_block((int)blockIdx.x - split * tiles, tiles, A.tp, A.tq, ip, iq);
   constexpr int HP = kWideP / WP / NB;  // rows of one matrix in a wave
   const int n0 = ip * (kWideP / NB);
   const int64_t q0 = (int64_t)iq * kWideQ;
@@ -405,69 +564,69 @@ void wide_kernel(const ProjArgs A) {
     prow = A.packed[which] + n * nG * B;
     srow = A.scales[which] + n * nG;
   }
-  uint32_t raw[2], tail = 0, tail_next, flags = 0;
-  uint32_t scale = 0, scale_next;
+  // bytes and group values are requested four stages before they are decoded
+  constexpr int kGroups = 4 / S32;  // groups of four stages
+  uint32_t raw[4], tail_next[kGroups], scale_next[kGroups], scale = 0, flags = 0;
   u32x2 left{0u, 0u};  // high bytes of the group's left-over codes
-  // bytes of stage s, J = s % S32 (past the end: of the last group)
+  // bytes of stage s, J = s % 4 (past the end: of the last group)
   auto load_raw = [&](int s, auto jc) {
     constexpr int J = decltype(jc)::value;
-    const int g = min(s / S32, nG - 1);
-    __builtin_memcpy(&raw[J & 1], prow + (int64_t)g * B + 6 * J + 3 * hf, 4);
-  };
-  auto load_group = [&](int s) {
-    const int g = min(s / S32, nG - 1);
+    const int g = min(g0 + s / S32, nG - 1);
     const uint8_t *p = prow + (int64_t)g * B;
-    if constexpr (G == 128) {
-      uint16_t v;
-      __builtin_memcpy(&v, p + 24, 2);
-      tail_next = v;
-    } else {
-      tail_next = p[12];
+    __builtin_memcpy(&raw[J], p + 6 * (J % S32) + 3 * hf, 4);
+    if constexpr (J % S32 == 0) {
+      if constexpr (G == 128) {
+        uint16_t v;
+        __builtin_memcpy(&v, p + 24, 2);
+        tail_next[J / S32] = v;
+      } else {
+        tail_next[J / S32] = p[12];
+      }
+      scale_next[J / S32] = srow[g];
     }
-    scale_next = srow[g];
   };
-  const uint32_t lut = kLutOff + lut_lane(lane);
+  const L lut(kLutOff, lane);
   const uint32_t put0 = rows_at((uint32_t)sr, 2u * hf), put1 = rows_at((uint32_t)sr, 2u * hf + 1u);
-  // codes of the stage whose bytes are loaded (J = its index % S32) -> slot
+  // codes of the stage whose bytes are raw[J], J = its index % 4, -> slot
   auto decode = [&](auto jc, uint32_t slot) {
     constexpr int J = decltype(jc)::value;
-    if constexpr (J == 0) {
-      tail = tail_next;
-      scale = scale_next * 0x10001u;
-      left = leftover_pool<G>(smem, lut, tail, flags);
+    if constexpr (J % S32 == 0) {
+      scale = scale_next[J / S32] * 0x10001u;
+      left = leftover_pool<G>(smem, lut, tail_next[J / S32], flags);
     }
     u32x4 c0, c1;
-    decode_eighth(smem, lut, raw[J & 1], left, (uint32_t)(2 * J + hf), scale, c0, c1, flags);
+    decode_eighth(smem, lut, raw[J], left, (uint32_t)(2 * (J % S32) + hf), scale, c0, c1, flags);
     *(lds_u32x4 *)(smem + slot + put0) = c0;
     *(lds_u32x4 *)(smem + slot + put1) = c1;
   };
 
   QS qs;
   qs.init_rows(tid, (uint32_t)A.K, [&](int r) -> int64_t { return q0 + r < A.M ? r : -1; });
-  const uint16_t *qbase = A.x + q0 * A.K;
+  const uint16_t *qbase = A.x + q0 * A.K + (int64_t)g0 * G;
+  int xput = 0;  // slot of the next request
   auto request = [&](int s, int i) {
-    qs.load_tracked(i, qbase + (int64_t)s * kKS, smem + kQOff + (uint32_t)(s % kWideRing) * QS::kSlot,
-                    (uint32_t)wv, s < S ? 1 : 0);
+    qs.load_tracked(i, qbase + (int64_t)s * kKS, smem + kQOff + (uint32_t)xput * QS::kSlot, (uint32_t)wv,
+                    s < S ? 1 : 0);
+    if (i == QS::kLoads - 1) xput = xput == kWideX - 1 ? 0 : xput + 1;
   };
 
-  // ---- prologue: bytes of stages 0 .. 4, x of 0 .. 2, codes of 0 .. 2 ----
-  load_group(0);
+  // ---- prologue: bytes of stages 0 .. 6, x of 0 .. 3, codes of 0 .. 2 ----
   load_raw(0, Int<0>{});
   load_raw(1, Int<1>{});
+  load_raw(2, Int<2>{});
+  load_raw(3, Int<3>{});
 #pragma unroll
-  for (int s = 0; s < kWideRing - 1; ++s)
+  for (int s = 0; s < kWideX - 1; ++s)
 #pragma unroll
     for (int i = 0; i < QS::kLoads; ++i) request(s, i);
-  build_lut<kLutF16>(smem + kLutOff, tid, kWideThreads);
+  L::build(smem + kLutOff, tid, kWideThreads);
   __syncthreads();
   decode(Int<0>{}, 0);
-  load_raw(2, Int<2 % S32>{});
-  if constexpr (S32 == 2) load_group(2);
-  decode(Int<1>{}, kPSlot);
-  load_raw(3, Int<3 % S32>{});
-  decode(Int<2 % S32>{}, 2 * kPSlot);
   load_raw(4, Int<0>{});
-  load_group(4);
+  decode(Int<1>{}, kPSlot);
+  load_raw(5, Int<1>{});
+  decode(Int<2>{}, 2 * kPSlot);
+  load_raw(6, Int<2>{});
 
   Frags<kRows, kWideP, TP> pf;
   Frags<kRows, kWideQ, TQ> qf;
@@ -485,10 +644,12 @@ void wide_kernel(const ProjArgs A) {
 #pragma unroll
   for (int a = 0; a < TP; ++a) pa[a] = pf.read(smem, 0, a);
 
+  int xget = 1;  // slot of x of stage s + 1
   auto stage = [&](int s, auto jc, bf16x8(&qc)[TQ], bf16x8(&qn)[TQ]) {
-    constexpr int J = decltype(jc)::value;
-    const uint32_t pn = (uint32_t)((s + 1) % kWideRing) * kPSlot;
-    const uint32_t qn0 = kQOff + (uint32_t)((s + 1) % kWideRing) * QS::kSlot;
+    constexpr int J = decltype(jc)::value;  // s % 4
+    const uint32_t pn = (uint32_t)((J + 1) % kWideC) * kPSlot;
+    const uint32_t qn0 = kQOff + (uint32_t)xget * QS::kSlot;
+    xget = xget == kWideX - 1 ? 0 : xget + 1;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int a = 0; a < TP; ++a) {
@@ -496,11 +657,10 @@ void wide_kernel(const ProjArgs A) {
       for (int b = 0; b < TQ; ++b) acc[a][b] = mfma32<true>(pa[a], qc[b], acc[a][b]);
       if (a < TQ) qn[a] = qf.read(smem, qn0, a);
       pa[a] = pf.read(smem, pn, a);
-      if (a < QS::kLoads) request(s + kWideRing - 1, a);
+      if (a < QS::kLoads) request(s + kWideX - 1, a);
       if (a == 3) {
-        decode(Int<(J + 3) % S32>{}, (uint32_t)((s + 3) % kWideRing) * kPSlot);
-        load_raw(s + 5, Int<(J + 5) % S32>{});
-        if constexpr ((J + 5) % S32 == 0) load_group(s + 5);
+        decode(Int<(J + 3) % 4>{}, (uint32_t)((J + 3) % kWideC) * kPSlot);
+        load_raw(s + 7, Int<(J + 7) % 4>{});
         // the codes are written before the fragments of rows 4 .. 7 are read:
         // when the last of those is used, in stage s + 1, the writes are done,
         // a barrier before stage s + 2 reads them
@@ -508,16 +668,20 @@ void wide_kernel(const ProjArgs A) {
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    // every stage issues at least three loads after x of stage s + 2
-    asm volatile("s_waitcnt vmcnt(3)\n\ts_barrier" ::: "memory");
+    // x of stage s + 2 was requested in stage s - 2: at least the bytes of
+    // that stage and three loads of each of s - 1 and s follow it
+    asm volatile("s_waitcnt vmcnt(7)\n\ts_barrier" ::: "memory");
   };
-  for (int s = 0; s < S; s += S32) {
+  int s = 0;
+  for (; s + 4 <= S; s += 4) {
     stage(s, Int<0>{}, qa, qb);
     stage(s + 1, Int<1>{}, qb, qa);
-    if constexpr (S32 == 4) {
-      stage(s + 2, Int<2>{}, qa, qb);
-      stage(s + 3, Int<3>{}, qb, qa);
-    }
+    stage(s + 2, Int<2>{}, qa, qb);
+    stage(s + 3, Int<3>{}, qb, qa);
+  }
+  if (S32 == 2 && s < S) {
+    stage(s, Int<0>{}, qa, qb);
+    stage(s + 1, Int<1>{}, qb, qa);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   if ((flags & kBadFlag) && A.status) atomicOr(A.status, kDevInvalidByte);
@@ -535,20 +699,72 @@ void wide_kernel(const ProjArgs A) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) acc[a][b][r] = ldexpf(acc[a][b][r], sh);
   }
-  if constexpr (NB == 2) {
-    uint16_t *h = (uint16_t *)A.out;
+  const bool vec = (A.N & 3) == 0 && (reinterpret_cast<uintptr_t>(A.out) & 15) == 0;
+  const int nw = n0 + wp * HP;  // first row of this wave
+  auto store_f32 = [&](float *y, int64_t m, int n, f32x4 v, bool aligned) {
+    float *o = y + m * A.N + n;
+    if (aligned && n < A.N) {
+      *(f32x4 *)o = v;
+    } else {
 #pragma unroll
-    for (int b = 0; b < TQ; ++b) {
-      const int64_t m = mq + 16 * b;
-      if (m >= A.M) continue;
+      for (int r = 0; r < 4; ++r)
+        if (n + r < A.N) o[r] = v[r];
+    }
+  };
+  if constexpr (NB == 1) {
+    if (A.adapters > 0) {
+      // the wave's 64 columns, one a lane; the splits share the adapters
+      const int64_t mw = q0 + wq * (kWideQ / WQ);
+      const int id = adapter_of(A, mw + lane, true);
+      uint64_t todo = adapter_leaders(id, lane);
+      for (int turn = 0; todo; ++turn) {
+        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        todo &= todo - 1;
+        if (turn % A.splits != split) continue;
+        for (int r0 = 0; r0 < A.R; r0 += 32) {
+          const int r = r0 + 8 * q;
+#pragma unroll
+          for (int b = 0; b < TQ; ++b) {
+            const bool own = __shfl(id, 16 * b + l) == a;
+            if (!__ballot(own)) continue;
+            const Pieces t = split_t(A, mw + 16 * b + l, r, own && r < A.R);
+#pragma unroll
+            for (int p = 0; p < TP; ++p) {
+              const int64_t n = min(nw + 16 * p + l, A.N - 1);
+              u32x4 v{0u, 0u, 0u, 0u};
+              if (r < A.R) v = *(const u32x4 *)(A.b + ((int64_t)a * A.N + n) * A.R + r);
+              const bf16x8 bv = __builtin_bit_cast(bf16x8, v);
+              f32x4 add{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int i = 0; i < 3; ++i) add = mfma32<false>(bv, t.p[i], add);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) acc[p][b][c] += own ? add[c] : 0.f;
+            }
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int b = 0; b < TQ; ++b) {
+    const int64_t m = mq + 16 * b;
+    if (m >= A.M) continue;
+    if (A.splits > 1) {
+#pragma unroll
+      for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int a = 0; a < TP / NB; ++a)
+          store_f32(A.partial + ((int64_t)split * NB + i) * A.M * A.N, m, nw + 16 * a + 4 * q,
+                    acc[a + i * (TP / NB)][b], (A.N & 3) == 0);
+    } else if constexpr (NB == 2) {
 #pragma unroll
       for (int a = 0; a < TP / 2; ++a) {
-        const int n = n0 + wp * HP + 16 * a + 4 * q;
+        const int n = nw + 16 * a + 4 * q;
         f32x4 v;
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[r] = act_value<ACT>(acc[a][b][r]) * acc[a + TP / 2][b][r];
-        uint16_t *o = h + m * A.N + n;
-        if ((A.N & 3) == 0 && (reinterpret_cast<uintptr_t>(h) & 7) == 0 && n < A.N) {
+        uint16_t *o = (uint16_t *)A.out + m * A.N + n;
+        if (vec && n < A.N) {
           store4(o, v);
         } else {
 #pragma unroll
@@ -556,62 +772,9 @@ void wide_kernel(const ProjArgs A) {
             if (n + r < A.N) o[r] = f32_to_bf16(v[r]);
         }
       }
-    }
-  } else {
-    const int nw = n0 + wp * HP;  // first row of this wave
-    if (A.adapters > 0) {
-      // the wave's 64 columns, one a lane
-      const int64_t mw = q0 + wq * (kWideQ / WQ);
-      int id = mw + lane < A.M ? A.ids[mw + lane] : -1;
-      if (id >= A.adapters) id = -1;
-      uint64_t todo = adapter_leaders(id, lane);
-      while (todo) {
-        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-        todo &= todo - 1;
-        bool mine[TQ];
+    } else {
 #pragma unroll
-        for (int b = 0; b < TQ; ++b) mine[b] = __shfl(id, 16 * b + l) == a;
-        for (int r0 = 0; r0 < A.R; r0 += 32) {
-          const bool in = r0 + 8 * q < A.R;
-          Pieces tp[TQ];
-#pragma unroll
-          for (int b = 0; b < TQ; ++b)
-            tp[b] = split_t(A.t + (mw + 16 * b + l) * A.R + r0 + 8 * q, in && mine[b]);
-#pragma unroll
-          for (int t = 0; t < TP; ++t) {
-            const int64_t n = min(nw + 16 * t + l, A.N - 1);
-            u32x4 v{0u, 0u, 0u, 0u};
-            if (in) v = *(const u32x4 *)(A.b + ((int64_t)a * A.N + n) * A.R + r0 + 8 * q);
-            const bf16x8 bv = __builtin_bit_cast(bf16x8, v);
-#pragma unroll
-            for (int b = 0; b < TQ; ++b) {
-              f32x4 add{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int i = 0; i < 3; ++i) add = mfma32<false>(bv, tp[b].p[i], add);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) acc[t][b][r] += mine[b] ? add[r] : 0.f;
-            }
-          }
-        }
-      }
-    }
-    float *y = (float *)A.out;
-#pragma unroll
-    for (int b = 0; b < TQ; ++b) {
-      const int64_t m = mq + 16 * b;
-      if (m >= A.M) continue;
-#pragma unroll
-      for (int a = 0; a < TP; ++a) {
-        const int n = nw + 16 * a + 4 * q;
-        float *o = y + m * A.N + n;
-        if ((A.N & 3) == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0 && n < A.N) {
-          *(f32x4 *)o = acc[a][b];
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (n + r < A.N) o[r] = acc[a][b][r];
-        }
-      }
+      for (int a = 0; a < TP; ++a) store_f32((float *)A.out, m, nw + 16 * a + 4 * q, acc[a][b], vec);
     }
   }
 }
@@ -632,14 +795,15 @@ struct PreArgs {
   float *t;
   int64_t M;
   int K, adapters, R, mt;
-  int shrink_blocks, units, rtiles;  // shrink: blocks, units a tile of rows, tiles of 16 ranks
+  // shrink: blocks, units a tile of rows, tiles of 16 ranks, splits of K
+  int shrink_blocks, units, rtiles, tsplits;
   int32_t *status;
 };
 
 // t of one unit: up to 16 rows of one adapter, 16 ranks.  The rows of a tile
 // that name the same adapter are numbered in order and cut into units of 16,
-// so rows in any order share the adapter's A.  Waves split K; sums of the
-// waves in order.
+// so rows in any order share the adapter's A.  One split of K; its waves
+// share the split, and their sums are added in order.
 __device__ void shrink_role(const PreArgs &A, int64_t blk, unsigned char *smem_raw) {
   int *ids = (int *)smem_raw;                       // [256]
   int *rows = ids + kShrinkTile;                    // [16]
@@ -647,6 +811,8 @@ __device__ void shrink_role(const PreArgs &A, int64_t blk, unsigned char *smem_r
   int *counts = info + 4;                           // [8] leaders of each wave
   float *red = (float *)(counts + 12);              // [8][64][4]
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, l = lane & 15, q = lane >> 4;
+  const int split = (int)(blk % A.tsplits);
+  blk /= A.tsplits;
   const int rt = (int)(blk % A.rtiles), unit = (int)(blk / A.rtiles % A.units);
   const int64_t m0 = blk / A.rtiles / A.units * kShrinkTile;
   const int nrows = (int)min((int64_t)kShrinkTile, A.M - m0);
@@ -654,7 +820,7 @@ __device__ void shrink_role(const PreArgs &A, int64_t blk, unsigned char *smem_r
   if (tid < nrows) {
     id = A.ids[m0 + tid];
     if (id < -1 || id >= A.adapters) {
-      if (unit == 0 && rt == 0 && A.status) atomicOr(A.status, kDevBadAdapter);
+      if (unit == 0 && rt == 0 && split == 0 && A.status) atomicOr(A.status, kDevBadAdapter);
       id = -1;
     }
   }
@@ -689,20 +855,32 @@ __device__ void shrink_role(const PreArgs &A, int64_t blk, unsigned char *smem_r
   const uint16_t *ar = A.a + ((int64_t)a * A.R + r) * A.K + 8 * q;
   f32x4 acc{0.f, 0.f, 0.f, 0.f};
   const int steps = A.K / 32;
-#pragma unroll 4
-  for (int s = wv; s < steps; s += kPreWaves)
-    acc = mfma32<false>(*(const bf16x8 *)(ar + 32 * s), *(const bf16x8 *)(xr + 32 * s), acc);
+  const int s0 = (int)((int64_t)steps * split / A.tsplits), s1 = (int)((int64_t)steps * (split + 1) / A.tsplits);
+  for (int s = s0 + wv; s < s1; s += kPreWaves * 8) {
+    // eight steps requested together; those past the end read the last one
+    // and add nothing
+    bf16x8 av[8], xv[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int si = min(s + kPreWaves * i, steps - 1);
+      av[i] = *(const bf16x8 *)(ar + 32 * si);
+      xv[i] = *(const bf16x8 *)(xr + 32 * si);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (s + kPreWaves * i < s1) acc = mfma32<false>(av[i], xv[i], acc);
+  }
   *(f32x4 *)(red + 4 * tid) = acc;
   __syncthreads();
   if (tid < 256) {
     float sum = 0.f;
     for (int w = 0; w < kPreWaves; ++w) sum += red[w * 256 + tid];
     const int ol = tid >> 2, rr = 16 * rt + 4 * (ol >> 4) + (tid & 3), row = rows[ol & 15];
-    if (row >= 0 && rr < A.R) A.t[(m0 + row) * A.R + rr] = A.scaling[a] * sum;
+    if (row >= 0 && rr < A.R) A.t[((int64_t)split * A.M + m0 + row) * A.R + rr] = A.scaling[a] * sum;
   }
 }
 
-// x in the fragment order of dec_kernel: [chunk][group][step][16-row tile]
+// x in the fragment order of mid_kernel: [chunk][group][step][16-row tile]
 // [lane][8]; rows past M are zeros.
 template <int G>
 __device__ void frag_role(const PreArgs &A, int64_t first, int64_t stride) {
@@ -732,11 +910,12 @@ __device__ void frag_role(const PreArgs &A, int64_t first, int64_t stride) {
 // element down to 2^-32 of the row's largest is exact, and a smaller one is
 // off by at most 2^-40 of it.  In the order of wide_kernel's codes.
 template <int G>
-__device__ void f16_role(const PreArgs &A, int64_t m) {
-  const int lane = threadIdx.x & 63;
+__device__ void f16_role(const PreArgs &A, int64_t m, unsigned char *smem_raw) {
+  uint32_t *tops = (uint32_t *)smem_raw;  // [8]
+  const int tid = threadIdx.x, lane = tid & 63;
   const uint16_t *xr = A.x + m * A.K;
   uint32_t top = 0;
-  for (int k = 8 * lane; k < A.K; k += 512) {
+  for (int k = 8 * tid; k < A.K; k += 8 * kPreThreads) {
     uint16_t v[8];
     *(u32x4 *)v = *(const u32x4 *)(xr + k);
 #pragma unroll
@@ -747,12 +926,17 @@ __device__ void f16_role(const PreArgs &A, int64_t m) {
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+  __syncthreads();  // the row before has been read
+  if (lane == 0) tops[tid >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kPreWaves; ++w) top = max(top, tops[w]);
   int exponent;  // top is in [2^(exponent - 1), 2^exponent)
   (void)frexpf(bf16_to_f32(top), &exponent);
   const int shift = top ? 15 - exponent : 0;
-  if (lane == 0) A.shift[m] = shift;
+  if (tid == 0) A.shift[m] = shift;
   uint16_t *o = A.xo + m * A.K;
-  for (int e = lane; e < A.K / 16; e += 64) {
+  for (int e = tid; e < A.K / 16; e += kPreThreads) {
     const int g = e / (G / 16), part = e % (G / 16);
     const uint16_t *p = xr + g * G;
     _Float16 f[16];
@@ -771,7 +955,7 @@ template <int G, int MODE>
 __global__ __launch_bounds__(kPreThreads) void pre_kernel(const PreArgs A) {
   __shared__ __align__(16) unsigned char smem[4 * (kShrinkTile + 32) + 16 * kPreThreads];
   if ((int)blockIdx.x < A.shrink_blocks) {
-    const int64_t work = (A.M + kShrinkTile - 1) / kShrinkTile * A.units * A.rtiles;
+    const int64_t work = (A.M + kShrinkTile - 1) / kShrinkTile * A.units * A.rtiles * A.tsplits;
     for (int64_t w = blockIdx.x; w < work; w += A.shrink_blocks) {
       shrink_role(A, w, smem);
       __syncthreads();
@@ -783,8 +967,7 @@ __global__ __launch_bounds__(kPreThreads) void pre_kernel(const PreArgs A) {
   if constexpr (MODE == kPreFrag) {
     frag_role<G>(A, blk * kPreThreads + threadIdx.x, blocks * kPreThreads);
   } else if constexpr (MODE == kPreF16) {
-    for (int64_t m = blk * kPreWaves + (threadIdx.x >> 6); m < A.M; m += blocks * kPreWaves)
-      f16_role<G>(A, m);
+    for (int64_t m = blk; m < A.M; m += blocks) f16_role<G>(A, m, smem);
   }
 }
 
@@ -795,53 +978,68 @@ __global__ __launch_bounds__(kPreThreads) void pre_kernel(const PreArgs A) {
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
 
+constexpr int kFew = 0, kMid = 1, kWide = 2;
+
 struct Plan {
-  bool wide, staged;
-  int mt, rt, splits, chunks;
+  int kind, wk, mt, splits, tsplits;
+  int64_t blocks, chunks;
   int64_t x, shift, t, partial;  // workspace bytes, each a multiple of 16, in this order
   int64_t total() const { return x + shift + t + partial; }
 };
 
 Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
   Plan p{};
-  p.t = R ? round16(M * R * 4) : 0;
-  // wide: from about half the chip's CUs on, a tile each
-  p.wide = ceil_div(NB * N, kWideP) * ceil_div(M, kWideQ) >= 128 && M > 128;
-  if (p.wide) {
+  const int64_t nG = K / G;
+  p.splits = 1;
+  const int64_t wide_tiles = ceil_div(NB * N, kWideP) * ceil_div(M, kWideQ);
+  if (M <= kFewRows) {
+    p.kind = kFew;
+    // a block's slice of x fits its LDS
+    p.splits = (int)ceil_div(nG, kFewX / (M * G * 2));
+    // waves along K: few_u groups a wave, more waves while the sets of tiles
+    // are fewer than the CUs
+    const int64_t ng = ceil_div(nG, p.splits), tiles = ceil_div(N, 16);
+    p.wk = 1;
+    while (p.wk < kFewWaves && (ng > few_u(G, NB) * p.wk || tiles * p.wk / kFewWaves * p.splits < 192)) p.wk *= 2;
+    p.blocks = std::min(ceil_div(tiles, kFewWaves / p.wk), std::max<int64_t>(1, 256 / p.splits)) * p.splits;
+  } else if (M > 128 && wide_tiles >= 64) {
+    p.kind = kWide;
+    // a tile a CU; K is split while every block keeps 64 stages
+    while (wide_tiles * p.splits < 160 && nG / (2 * p.splits) * (G / 32) >= 64) p.splits *= 2;
+    p.blocks = wide_tiles * p.splits;
     p.x = round16(M * K * 2);
     p.shift = round16(M * 4);
-    return p;
+  } else {
+    p.kind = kMid;
+    p.mt = M <= 32 ? 2 : 4;
+    p.chunks = ceil_div(M, 16 * p.mt);
+    const int64_t blocks = ceil_div(N, 128) * p.chunks;
+    // two blocks a CU; K is split while every block keeps four groups
+    while (blocks * p.splits < 384 && nG / (2 * p.splits) >= 4) p.splits *= 2;
+    p.blocks = blocks * p.splits;
+    p.x = p.chunks * 16 * p.mt * K * 2;
   }
-  p.staged = M <= kStagedRows;
-  p.mt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-  p.chunks = (int)ceil_div(M, 16 * p.mt);
-  const int64_t tiles = ceil_div(N, 16), nG = K / G;
-  p.rt = !p.staged && tiles * p.chunks >= 1024 ? 2 : 1;
-  const int64_t blocks = ceil_div(tiles, p.rt) * p.chunks;
-  // staged: a block's slice of x fits its LDS.  Otherwise K is split only
-  // while blocks are few and every wave keeps two groups.
-  int64_t s = p.staged ? ceil_div(nG, std::max<int64_t>(1, kStagedBytes / (M * G * 2))) : 1;
-  while (blocks * s < 192 && nG / (2 * s) >= 2 * kDecWaves) s *= 2;
-  p.splits = (int)std::min(s, nG);
-  if (!p.staged) p.x = (int64_t)p.chunks * 16 * p.mt * K * 2;
   if (p.splits > 1) p.partial = round16((int64_t)p.splits * NB * M * N * 4);
+  if (R) {
+    // t: about eight steps a wave of a block
+    p.tsplits = (int)std::min<int64_t>(8, ceil_div(K / 32, 8 * kPreWaves));
+    if (M > 64) p.tsplits = std::min(p.tsplits, 2);
+    p.t = round16(p.tsplits * M * R * 4);
+  }
   return p;
 }
 
 template <int G, int NB, int ACT>
-void launch_dec(const Plan &p, const ProjArgs &a, hipStream_t stream) {
-  const dim3 grid((unsigned)(ceil_div(ceil_div(a.N, 16), p.rt) * p.splits * p.chunks));
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(kDecThreads), 0, stream, a);
-  };
-  if (p.staged)
-    go(dec_kernel<G, NB, 1, 1, true, ACT>);
-  else if (p.mt == 1)
-    p.rt == 1 ? go(dec_kernel<G, NB, 1, 1, false, ACT>) : go(dec_kernel<G, NB, 1, 2, false, ACT>);
+void launch_product(const Plan &p, const ProjArgs &a, hipStream_t stream) {
+  const dim3 grid((unsigned)p.blocks);
+  if (p.kind == kFew)
+    hipLaunchKernelGGL((few_kernel<G, NB, ACT>), grid, dim3(kFewThreads), 0, stream, a);
+  else if (p.kind == kWide)
+    hipLaunchKernelGGL((wide_kernel<G, NB, ACT>), grid, dim3(kWideThreads), 0, stream, a);
   else if (p.mt == 2)
-    p.rt == 1 ? go(dec_kernel<G, NB, 2, 1, false, ACT>) : go(dec_kernel<G, NB, 2, 2, false, ACT>);
+    hipLaunchKernelGGL((mid_kernel<G, NB, 2, ACT>), grid, dim3(kMidThreads), 0, stream, a);
   else
-    p.rt == 1 ? go(dec_kernel<G, NB, 4, 1, false, ACT>) : go(dec_kernel<G, NB, 4, 2, false, ACT>);
+    hipLaunchKernelGGL((mid_kernel<G, NB, 4, ACT>), grid, dim3(kMidThreads), 0, stream, a);
 }
 
 // All launches of a call; `a` and `pre` hold the caller's arguments.
@@ -855,40 +1053,38 @@ void launch_proj(const Plan &p, ProjArgs a, PreArgs pre, void *workspace, hipStr
   a.partial = (float *)(ws + p.x + p.shift + p.t);
   a.t = pre.t;
   a.shift = pre.shift;
+  a.tsplits = pre.tsplits = p.tsplits;
+  a.splits = p.splits;
+  a.wk = p.wk;
+  a.chunks = (int)p.chunks;
+  a.tp = (int)ceil_div(NB * (int64_t)a.N, kWideP);
+  a.tq = (int)ceil_div(a.M, kWideQ);
   pre.M = a.M, pre.K = a.K, pre.mt = p.mt, pre.status = a.status;
   pre.ids = a.ids, pre.adapters = a.adapters, pre.R = a.R;
   if (NB == 1) {
     const int64_t tiles = ceil_div(a.M, kShrinkTile);
     const int64_t rows = std::min<int64_t>(a.M, kShrinkTile);
     // units of a tile: one for each 16 rows and one more for each adapter
-    pre.units = (int)std::max<int64_t>(1, std::min(rows, ceil_div(rows, 16) + std::min<int64_t>(rows, a.adapters)));
+    pre.units = (int)std::min(rows, ceil_div(rows, 16) + std::min<int64_t>(rows, a.adapters));
     pre.rtiles = (int)ceil_div(a.R, 16);
-    if (a.adapters == 0) pre.units = pre.rtiles = 1;  // the ids are still checked
-    pre.shrink_blocks = (int)std::min(kMaxPreBlocks, tiles * pre.units * pre.rtiles);
+    if (a.adapters == 0) pre.units = pre.rtiles = pre.tsplits = 1;  // the ids are still checked
+    pre.shrink_blocks = (int)std::min(kMaxPreBlocks, tiles * pre.units * pre.rtiles * pre.tsplits);
   }
-  if (p.wide) {
-    const dim3 grid((unsigned)(pre.shrink_blocks + std::min(kMaxPreBlocks, ceil_div(a.M, kPreWaves))));
-    hipLaunchKernelGGL((pre_kernel<G, kPreF16>), grid, dim3(kPreThreads), 0, stream, pre);
-    a.x = pre.xo;
-  } else if (!p.staged) {
-    const int64_t units = (int64_t)p.chunks * 16 * p.mt * (a.K / G) * 4;
-    const dim3 grid((unsigned)(pre.shrink_blocks + std::min<int64_t>(4096, ceil_div(units, kPreThreads))));
-    hipLaunchKernelGGL((pre_kernel<G, kPreFrag>), grid, dim3(kPreThreads), 0, stream, pre);
-    a.x = pre.xo;
-  } else if (pre.shrink_blocks) {
-    hipLaunchKernelGGL((pre_kernel<G, kPreNone>), dim3((unsigned)pre.shrink_blocks),
+  const int64_t sb = pre.shrink_blocks;
+  if (p.kind == kWide) {
+    hipLaunchKernelGGL((pre_kernel<G, kPreF16>), dim3((unsigned)(sb + std::min(kMaxPreBlocks, a.M))),
                        dim3(kPreThreads), 0, stream, pre);
+    a.x = pre.xo;
+  } else if (p.kind == kMid) {
+    const int64_t units = p.chunks * 16 * p.mt * (a.K / G) * 4;
+    hipLaunchKernelGGL((pre_kernel<G, kPreFrag>),
+                       dim3((unsigned)(sb + std::min<int64_t>(4096, ceil_div(units, kPreThreads)))),
+                       dim3(kPreThreads), 0, stream, pre);
+    a.x = pre.xo;
+  } else if (sb) {
+    hipLaunchKernelGGL((pre_kernel<G, kPreNone>), dim3((unsigned)sb), dim3(kPreThreads), 0, stream, pre);
   }
-  if (p.wide) {
-    a.tp = (int)ceil_div(NB * (int64_t)a.N, kWideP);
-    a.tq = (int)ceil_div(a.M, kWideQ);
-    hipLaunchKernelGGL((wide_kernel<G, NB, ACT>), dim3((unsigned)(a.tp * a.tq)), dim3(kWideThreads), 0,
-                       stream, a);
-    return;
-  }
-  a.splits = p.splits;
-  a.chunks = p.chunks;
-  launch_dec<G, NB, ACT>(p, a, stream);
+  launch_product<G, NB, ACT>(p, a, stream);
   if (p.splits > 1) {
     const int64_t mn = a.M * a.N;
     hipLaunchKernelGGL((combine_kernel<NB, ACT>), dim3((unsigned)std::min<int64_t>(4096, ceil_div(mn, 256))),

@@ -46,6 +46,16 @@ constexpr uint32_t kNoRow = 0x80000000u;  // past every range: such a load write
 
 constexpr int kRows = 0, kCols = 1;  // operand storage
 
+// The same load for a kernel whose LDS reads the compiler can tell apart from
+// these writes; its own wait counts then include it.
+__device__ __forceinline__ void dma16_tracked(const void *base, lds_bytes *dst, uint32_t off) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass knows no 16-byte load into LDS
+  const __amdgpu_buffer_rsrc_t rs =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, 0x7FFFFFFF, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)dst, 16, off, 0, 0, 0);
+#endif
+}
+
 // Unit exchange of a kCols slot: the 32-byte unit u of k sits at u ^ this.
 __device__ __forceinline__ uint32_t cols_swz(uint32_t k) { return (k & 3u) | ((k >> 1) & 4u); }
 
@@ -106,18 +116,11 @@ struct Stream {
       off[i] = (int)(8u * c) < cols ? k * ld * 2u + 16u * c : kNoRow;
     }
   }
-  // As load, for a kernel whose LDS reads the compiler can tell apart from
-  // these writes: its own wait counts include them.
+  // As load, with dma16_tracked.
   __device__ __forceinline__ void load_tracked(int i, const void *base, lds_bytes *slot, uint32_t wave,
                                                int krem) const {
     static_assert(KIND == kRows, "");
-#if defined(__HIP_DEVICE_COMPILE__)  // the host pass knows no 16-byte load into LDS
-    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<void *>(base), (short)0, 0x7FFFFFFF, 0x00020000);
-    lds_bytes *dst = slot + 16u * ((uint32_t)(i * NT) + 64u * wave);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)dst, 16,
-                                             krem > 0 ? off[i] : kNoRow, 0, 0, 0);
-#endif
+    dma16_tracked(base, slot + 16u * ((uint32_t)(i * NT) + 64u * wave), krem > 0 ? off[i] : kNoRow);
   }
   // Request i of the stage at `base` into `slot`; k rows >= krem read as
   // zeros.

@@ -6,9 +6,9 @@
 // G % 5-ish left-over codes of the last byte (G = 64: byte 12, codes 60..63) or
 // two (G = 128: bytes 24 and 25, codes 120..127) are dealt out singly, so that
 // everyone holds 32 (or 16) codes without straddling a byte:
-//   quarter q (dec_kernel), G = 128: bytes 6q .. 6q+5 and left-over codes 2q, 2q+1
+//   quarter q (few, mid), G = 128: bytes 6q .. 6q+5 and left-over codes 2q, 2q+1
 //                           G = 64:  bytes 3q .. 3q+2 and left-over code q
-//   eighth e (wide_kernel): bytes 3e .. 3e+2 and left-over code e (G = 64: e < 4)
+//   eighth e (wide): bytes 3e .. 3e+2 and left-over code e (G = 64: e < 4)
 // Codes become 16-bit floats two at a time by one v_perm of bytes: a table in
 // LDS gives, for each byte value, the high bytes of its five codes' floats,
 // whose low bytes are zero (bf16: 2c, +-2 = 0xC000, 0x4000; f16: c, +-1 =
@@ -28,39 +28,51 @@ struct Int {
 };
 
 constexpr int kLutBf16 = 0, kLutF16 = 1;
-constexpr uint32_t kLutCopies = 16, kLutStride = 8 * kLutCopies;  // bytes an entry
-constexpr uint32_t kLutBytes = 256 * kLutStride;                  // 32 KB
 constexpr uint32_t kBadFlag = 0xFF00u;  // in the second dword of invalid bytes' entries
 
-// Lane i reads copy i % 16: 16 lanes' 8-byte reads touch all 32 pairs of
-// banks whatever the bytes are.
-__device__ __forceinline__ uint32_t lut_lane(int lane) { return 8u * ((uint32_t)lane & 15u); }
+// The table: 256 entries of 8 bytes, COPIES times, copy i read by lanes i,
+// i + COPIES, ...  32 copies (64 KB): the 32 lanes of each half of an 8-byte
+// read touch all 64 banks once whatever the bytes are, and an entry's 256
+// bytes make its address one v_perm of the byte and the lane's offset.  Fewer
+// copies leave LDS to other uses; lanes that share one then meet in a bank
+// now and then.
+template <int KIND, uint32_t COPIES>
+struct Lut {
+  static constexpr uint32_t kStride = 8 * COPIES, kBytes = 256 * kStride;
+  uint32_t at;  // LDS byte of this lane's copy of entry 0
 
-template <int KIND>
-__device__ __forceinline__ void build_lut(lds_bytes *at, int tid, int threads) {
-  constexpr uint32_t neg = KIND == kLutBf16 ? 0xC0u : 0xBCu, pos = KIND == kLutBf16 ? 0x40u : 0x3Cu;
-  // two threads an entry, eight copies each
-  const uint32_t half = (uint32_t)tid & 1u;
-  for (uint32_t e = (uint32_t)tid >> 1; e < 256u; e += (uint32_t)threads / 2u) {
-    uint32_t h[5], v = e;
+  __device__ __forceinline__ Lut(uint32_t base, int lane)
+      : at(base + 8u * ((uint32_t)lane & (COPIES - 1u))) {}
+
+  __device__ static __forceinline__ void build(lds_bytes *table, int tid, int threads) {
+    constexpr uint32_t neg = KIND == kLutBf16 ? 0xC0u : 0xBCu, pos = KIND == kLutBf16 ? 0x40u : 0x3Cu;
+    constexpr uint32_t kParts = 2, kPer = COPIES / 2 / kParts;  // 16-byte stores a thread
+    const uint32_t part = (uint32_t)tid % kParts;
+    for (uint32_t e = (uint32_t)tid / kParts; e < 256u; e += (uint32_t)threads / kParts) {
+      uint32_t h[5], v = e;
 #pragma unroll
-    for (int i = 0; i < 5; ++i) {
-      const uint32_t d = v % 3u;
-      v /= 3u;
-      h[i] = d == 0u ? neg : (d == 2u ? pos : 0u);
+      for (int i = 0; i < 5; ++i) {
+        const uint32_t d = v % 3u;
+        v /= 3u;
+        h[i] = d == 0u ? neg : (d == 2u ? pos : 0u);
+      }
+      const u32x2 entry = e >= 243u ? u32x2{0u, kBadFlag}
+                                    : u32x2{h[0] | (h[1] << 8) | (h[2] << 16) | (h[3] << 24), h[4]};
+      const u32x4 two{entry.x, entry.y, entry.x, entry.y};
+#pragma unroll
+      for (uint32_t k = 0; k < kPer; ++k)  // neighbouring entries start at different banks
+        *(lds_u32x4 *)(table + e * kStride + 16u * (part + kParts * ((k + (e >> 1)) % kPer))) = two;
     }
-    const u32x2 entry = e >= 243u ? u32x2{0u, kBadFlag}
-                                  : u32x2{h[0] | (h[1] << 8) | (h[2] << 16) | (h[3] << 24), h[4]};
-    const u32x4 two{entry.x, entry.y, entry.x, entry.y};
-#pragma unroll
-    for (uint32_t k = 0; k < 4; ++k)
-      *(lds_u32x4 *)(at + e * kLutStride + 16u * (half + 2u * ((k + (e >> 1)) & 3u))) = two;
   }
-}
 
-__device__ __forceinline__ u32x2 lut_read(lds_bytes *smem, uint32_t lut, uint32_t word, int byte) {
-  return *(lds_u32x2_c *)(smem + (((word >> (8 * byte)) & 0xFFu) * kLutStride + lut));
-}
+  // The entry of byte `i` of `word`.
+  __device__ __forceinline__ u32x2 read(lds_bytes *smem, uint32_t word, int i) const {
+    if constexpr (COPIES == 32)  // `at` is below 256: byte 0 the lane, byte 1 the byte
+      return *(lds_u32x2_c *)(smem + __builtin_amdgcn_perm(word, at, 0x0C0C0400u + 0x100u * (uint32_t)i));
+    else
+      return *(lds_u32x2_c *)(smem + (((word >> (8 * i)) & 0xFFu) * kStride + at));
+  }
+};
 
 // Codes 0, 1 and 2, 3 of an entry; code 4 of entries a and b.
 __device__ __forceinline__ uint32_t pair01(u32x2 e) { return __builtin_amdgcn_perm(e.x, e.x, 0x010C000Cu); }
@@ -70,29 +82,29 @@ __device__ __forceinline__ uint32_t pair44(u32x2 a, u32x2 b) {
 }
 
 // High bytes of a group's left-over codes, code i in byte i.
-template <int G>
-__device__ __forceinline__ u32x2 leftover_pool(lds_bytes *smem, uint32_t lut, uint32_t tail,
+template <int G, class L>
+__device__ __forceinline__ u32x2 leftover_pool(lds_bytes *smem, const L &lut, uint32_t tail,
                                                uint32_t &flags) {
-  const u32x2 a = lut_read(smem, lut, tail, 0);
+  const u32x2 a = lut.read(smem, tail, 0);
   flags |= a.y;
   if constexpr (G == 64) return u32x2{a.x, 0u};
-  const u32x2 b = lut_read(smem, lut, tail, 1);
+  const u32x2 b = lut.read(smem, tail, 1);
   flags |= b.y;
   return u32x2{a.x, __builtin_amdgcn_perm(b.x, a.y, 0x06050400u)};
 }
 
 // Quarter q of a group: 4 (G = 64: 2) fragments of eight codes, d[4 s ..].
 // order_quarter lists the codes in the same order.
-template <int G>
-__device__ __forceinline__ void decode_quarter(lds_bytes *smem, uint32_t lut, uint32_t w0, uint32_t w1,
+template <int G, class L>
+__device__ __forceinline__ void decode_quarter(lds_bytes *smem, const L &lut, uint32_t w0, uint32_t w1,
                                                uint32_t tail, int q, uint32_t (&d)[G / 8],
                                                uint32_t &flags) {
   if constexpr (G == 128) {
     u32x2 e[6];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = lut_read(smem, lut, w0, i);
+    for (int i = 0; i < 4; ++i) e[i] = lut.read(smem, w0, i);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) e[4 + i] = lut_read(smem, lut, w1, i);
+    for (int i = 0; i < 2; ++i) e[4 + i] = lut.read(smem, w1, i);
     const u32x2 pool = leftover_pool<G>(smem, lut, tail, flags);
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
@@ -106,8 +118,8 @@ __device__ __forceinline__ void decode_quarter(lds_bytes *smem, uint32_t lut, ui
     }
     d[15] = __builtin_amdgcn_perm(pool.y, pool.x, 0x010C000Cu + 0x02000200u * (uint32_t)q);
   } else {
-    const u32x2 a = lut_read(smem, lut, w0, 0), b = lut_read(smem, lut, w0, 1),
-                c = lut_read(smem, lut, w0, 2);
+    const u32x2 a = lut.read(smem, w0, 0), b = lut.read(smem, w0, 1),
+                c = lut.read(smem, w0, 2);
     const u32x2 pool = leftover_pool<G>(smem, lut, tail, flags);
     flags |= a.y | b.y | c.y;
     d[0] = pair01(a);
@@ -163,12 +175,13 @@ __device__ __forceinline__ void order_quarter(const uint16_t *xg, int q, u32x4 (
 
 // Eighth e of a group: the 16 codes of three bytes (in `word`) and left-over
 // code e, times the scale (twice, packed), as f16: exact, codes are -1, 0, 1.
-__device__ __forceinline__ void decode_eighth(lds_bytes *smem, uint32_t lut, uint32_t word, u32x2 left,
+template <class L>
+__device__ __forceinline__ void decode_eighth(lds_bytes *smem, const L &lut, uint32_t word, u32x2 left,
                                               uint32_t e, uint32_t scale2, u32x4 &c0, u32x4 &c1,
                                               uint32_t &flags) {
   typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-  const u32x2 a = lut_read(smem, lut, word, 0), b = lut_read(smem, lut, word, 1),
-              c = lut_read(smem, lut, word, 2);
+  const u32x2 a = lut.read(smem, word, 0), b = lut.read(smem, word, 1),
+              c = lut.read(smem, word, 2);
   flags |= a.y | b.y | c.y;
   const uint32_t one = __builtin_amdgcn_perm(left.y, left.x, 0x0C0C0C00u + e);
   const f16x2 s = __builtin_bit_cast(f16x2, scale2);
