@@ -36,7 +36,9 @@
 namespace tq {
 namespace {
 
-// What both kernels read and write.
+__host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// What the kernels read and write.
 struct ProjArgs {
   const uint16_t *x;              // bf16 [M,K] (staged), or x in fragment order, or f16 rows
   const uint8_t *packed[2];
@@ -155,90 +157,66 @@ __device__ __forceinline__ int adapter_of(const ProjArgs &A, int64_t m, bool in)
 // up to 16 rows
 // ---------------------------------------------------------------------------
 
-// One lane's bytes of one group of one weight row.
+constexpr int kFewRows = 16;
+constexpr int kFewWaves = 16;          // most waves of a block
+constexpr uint32_t kFewX = 64 << 10;   // LDS for a block's slice of x
+
+// The bytes and scale of one group.
+template <int G>
 struct Raw {
-  uint32_t w0, w1, tail, scale;
+  GroupBytes<G> w;
+  uint32_t scale;
 };
 
-// `tile` is the group's bytes in the tile's first row and `stile` its scale
-// there (both the same for the wave); row, srow the lane's row within the tile
-// in bytes and in scales.
-template <int G>
-__device__ __forceinline__ Raw load_raw(const uint8_t *tile, const uint16_t *stile, uint32_t row,
-                                        uint32_t srow, uint32_t q) {
-  Raw r;
-  if constexpr (G == 128) {
-    uint64_t w;
-    uint16_t tail;
-    __builtin_memcpy(&w, tile + (row + 6u * q), 8);  // six of them; q = 3 ends at the group's end
-    __builtin_memcpy(&tail, tile + (row + 24u), 2);
-    r.w0 = (uint32_t)w;
-    r.w1 = (uint32_t)(w >> 32);
-    r.tail = tail;
-  } else {
-    __builtin_memcpy(&r.w0, tile + (row + 3u * q), 4);  // three; q = 3 ends at the group's end
-    r.w1 = 0;
-    r.tail = tile[row + 12u];
-  }
-  r.scale = stile[srow];
-  return r;
-}
-
-constexpr int kFewRows = 16;
-constexpr int kFewWaves = 16, kFewThreads = 64 * kFewWaves;
-constexpr uint32_t kFewX = 64 << 10;  // LDS for a block's slice of x
-// Groups a wave requests together: what 128 registers a lane leave room for.
-constexpr int few_u(int G, int NB) { return G == 128 && NB == 2 ? 2 : 4; }
-
 // A block: one split of K, and tiles of 16 weight rows (of each matrix) one
-// set after another, kFewWaves / wk tiles a set; wk waves share the groups of
-// a tile.  x [M,K] (M <= 16) of the split is put in order once, in LDS.
-// The matrix cores take x as the row operand and W as the column operand, so
-// a lane's partial sums belong to the weight row whose bytes it decoded.
-// A wave requests few_u groups of bytes while it works on as many others,
-// across the ends of tiles.  One block a CU: 64 KB table, 64 KB x, 16 KB a matrix for
-// the sums of the waves.
+// set after another, wt tiles a set; wk waves share a tile's groups, four at
+// a time: lane (l, q) decodes group q of the four of row l, so that its bytes
+// are two wide loads and the four lanes of a row read 104 neighbouring ones.
+// (With each group dealt to four lanes instead, three small loads each, the
+// address units took four times as long as the bytes.)  Scales are multiplied
+// into the codes, since a lane's sums then run over all groups.
+// x [M,K] (M <= 16) of the split, as f16 times a power of two for each row, is
+// put in order once, in LDS; it is the row operand of the matrix cores and W
+// the column operand.
+// A wave requests four groups while it works on the four before, across the
+// ends of tiles.  LDS: 64 KB table, 64 KB x, up to 16 KB a matrix for the sums
+// of the waves.
 template <int G, int NB, int ACT>
-__global__ __launch_bounds__(kFewThreads) void few_kernel(const ProjArgs A) {
-  constexpr int S32 = G / 32, B = bytes_per_group(G), kFewU = few_u(G, NB);
-  typedef Lut<kLutBf16, 32> L;
+__global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A) {
+  constexpr int T = G / 8, B = bytes_per_group(G);  // T: matrix steps of a group
+  typedef Lut<32> L;
   constexpr uint32_t kXOff = L::kBytes, kRedOff = kXOff + kFewX;
-  __shared__ __align__(16) unsigned char smem_raw[kRedOff + kFewWaves * NB * 1024];
+  __shared__ __align__(16) unsigned char smem_raw[L::kBytes + kFewX + kFewWaves * NB * 1024];
   lds_bytes *smem = (lds_bytes *)smem_raw;
-  const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
-  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), waves = threads >> 6;
   const int nG = A.K / G, M = (int)A.M;
   const int split = (int)blockIdx.x % A.splits, b0 = (int)blockIdx.x / A.splits;
   const int blocks = (int)gridDim.x / A.splits;
-  const int g0 = (int)((int64_t)nG * split / A.splits);
-  const int g1 = (int)((int64_t)nG * (split + 1) / A.splits);
-  const int wk = A.wk, wt = kFewWaves / wk;       // waves of a tile, tiles of a set
-  const int kw = wv % wk, tw = wv / wk;           // this wave's place
+  const int nQ = (nG + 3) / 4;  // quads of groups
+  const int g0 = 4 * (int)((int64_t)nQ * split / A.splits);
+  const int g1 = min(nG, 4 * (int)((int64_t)nQ * (split + 1) / A.splits));
+  const int wk = A.wk, wt = waves / wk;  // waves of a tile, tiles of a set
+  const int kw = wv % wk, tw = wv / wk;  // this wave's place
   const int tiles = (A.N + 15) / 16, sets = (tiles + wt - 1) / wt;
   const int steps = b0 < sets ? (sets - b0 + blocks - 1) / blocks : 0;
-  const int batches = (g1 - g0 + wk * kFewU - 1) / (wk * kFewU);  // of a tile
+  const int quads = (g1 - g0 + 3) / 4, batches = (quads + wk - 1) / wk;  // of a tile
 
   // the set of step j is b0 + j * blocks
   auto tile_row = [&](int j) { return ((b0 + j * blocks) * wt + tw) * 16; };
-  struct Batch {
-    Raw r[kFewU][NB];
-  };
   int fj = 0, fk = 0;  // step and batch of the next request
-  auto fetch = [&](Batch &f) {
-    const int n0 = tile_row(fj);
-    if (fj < steps && n0 < A.N) {
-      // rows past N read row N - 1; their sums are not stored
-      const uint32_t ln = (uint32_t)min(l, A.N - 1 - n0);
-      const uint32_t row = ln * (uint32_t)nG * B, srow = ln * (uint32_t)nG;
+  auto fetch = [&](Raw<G>(&f)[NB]) {
+    const int n0 = tile_row(fj), quad = kw + wk * fk;
+    // rows past N read row N - 1 and groups past the last read it, with scale
+    // 0; neither is stored or counts
+    const int64_t n = min(n0 + l, A.N - 1);
+    const int g = g0 + 4 * quad + q;
+    const int64_t at = n * nG + min(g, g1 - 1);
 #pragma unroll
-      for (int u = 0; u < kFewU; ++u) {
-        const int g = g0 + kw + wk * (fk * kFewU + u);
-        if (g >= g1) break;
-        const int64_t at = (int64_t)n0 * nG + g;
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-          f.r[u][i] = load_raw<G>(A.packed[i] + at * B, A.scales[i] + at, row, srow, (uint32_t)q);
-      }
+    for (int i = 0; i < NB; ++i) {
+      f[i].w = load_bytes<G>(A.packed[i] + at * B);
+      const uint32_t sc = A.scales[i][at];
+      f[i].scale = g < g1 ? sc : 0u;
     }
     if (++fk == batches) {
       fk = 0;
@@ -247,21 +225,66 @@ __global__ __launch_bounds__(kFewThreads) void few_kernel(const ProjArgs A) {
   };
 
   // the first bytes are requested before the table is built and x put in order
-  Batch ba, bb;
-  fetch(ba);
-  L::build(smem, tid, kFewThreads);
+  Raw<G> ra[NB], rb[NB];
+  fetch(ra);
+  L::build(smem, tid, threads);
+  // largest magnitudes, [wave][row], where the sums will be
+  auto top_at = [&](int w, int m) {
+    return (__attribute__((address_space(3))) uint32_t *)(smem + kRedOff + 4u * (uint32_t)(w * kFewRows + m));
+  };
   {
-    // unit: a quarter's codes of a group of one row
-    const int quarters = 4 * (g1 - g0), units = quarters * M;
-    for (int e = tid; e < units; e += kFewThreads) {
-      const int m = e / quarters, gq = e - m * quarters, g = gq >> 2, uq = gq & 3;
-      u32x4 f[S32];
-      order_quarter<G>(A.x + (int64_t)m * A.K + (int64_t)(g0 + g) * G, uq, f);
-#pragma unroll
-      for (int s = 0; s < S32; ++s)
-        *(lds_u32x4 *)(smem + kXOff + 16u * (uint32_t)(((g * S32 + s) * 4 + uq) * M + m)) = f[s];
+    const uint16_t *xs = A.x + (int64_t)g0 * G;
+    const int len = (g1 - g0) * G;
+    for (int m = 0; m < M; ++m) {
+      uint32_t top = 0;
+      for (int k = 8 * tid; k < len; k += 8 * threads) top = top_of(top, xs + (int64_t)m * A.K + k);
+      top = wave_max(top);
+      if (lane == 0) *top_at(wv, m) = top;
     }
   }
+  __syncthreads();
+  auto shift_of = [&](int m) {
+    uint32_t top = 0;
+    for (int w = 0; w < waves; ++w) top = max(top, *top_at(w, m));
+    return f16_shift(top);
+  };
+  {
+    // unit: the steps of 40 codes, or those that are left, of a group of a row
+    constexpr int U = (G + 39) / 40;
+    const int units = quads * 4 * U;
+    for (int m = 0; m < M; ++m) {
+      const int shift = shift_of(m);
+      for (int e = tid; e < units; e += threads) {
+        const int g = e / U, u = e - g * U;
+        const bool in = g0 + g < g1, last = u == U - 1;
+        const int count = last ? G - 40 * (U - 1) : 40;
+        const uint16_t *p = A.x + (int64_t)m * A.K + (int64_t)min(g0 + g, g1 - 1) * G + 40 * u;
+        uint16_t v[40];
+#pragma unroll
+        for (int s = 0; s < 5; ++s)
+          *(u32x4 *)(v + 8 * s) = *(const u32x4 *)(p + (8 * s < count ? 8 * s : 0));
+#pragma unroll
+        for (int s = 0; s < 5; ++s) {
+          if (8 * s >= count) break;
+          _Float16 f[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            // the codes past a group's tens are in their own order
+            constexpr int kTens = (G - 40 * (U - 1)) / 10 * 10;
+            const int o = 8 * s + i;
+            const uint16_t tens = v[group_source<40>(o)];
+            f[i] = f16_of(!in ? 0 : last && o >= kTens ? v[o] : tens, shift);
+          }
+          // [quad][step][group of the quad][row]
+          *(lds_u32x4 *)(smem + kXOff + 16u * (uint32_t)((((g >> 2) * T + 5 * u + s) * 4 + (g & 3)) * M + m)) =
+              *(u32x4 *)f;
+        }
+      }
+    }
+  }
+  int unshift[4];  // of rows 4 q .. 4 q + 3
+#pragma unroll
+  for (int c = 0; c < 4; ++c) unshift[c] = -shift_of(min(4 * q + c, M - 1));
   __syncthreads();
 
   const L lut(0, lane);
@@ -273,50 +296,59 @@ __global__ __launch_bounds__(kFewThreads) void few_kernel(const ProjArgs A) {
 #pragma unroll
   for (int i = 0; i < NB; ++i) acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
   int j = 0, k = 0;  // step and batch being worked on
-  auto work = [&](Batch &f, Batch &next) {
+  auto work = [&](Raw<G>(&f)[NB], Raw<G>(&next)[NB]) {
     fetch(next);
-    const int n0 = tile_row(j);
-    if (n0 < A.N) {
+    const int n0 = tile_row(j), quad = kw + wk * k;
+    if (n0 < A.N && quad < quads) {
+      const uint32_t xq = xlane + 64u * (uint32_t)(quad * T * M);
+      // five steps at a time: eight bytes of each matrix
+      auto part = [&](auto p0, auto p1, auto tail) {
+        constexpr int P0 = decltype(p0)::value, P1 = decltype(p1)::value;
+        constexpr int S0 = 5 * P0 / 4, S1 = decltype(tail)::value ? T : 5 * P1 / 4;
+        bf16x8 xf[S1 - S0];
 #pragma unroll
-      for (int u = 0; u < kFewU; ++u) {
-        const int g = g0 + kw + wk * (k * kFewU + u);
-        if (g >= g1) break;
-        bf16x8 xf[S32];
-#pragma unroll
-        for (int s = 0; s < S32; ++s)
-          xf[s] = *(lds_bf16x8_c *)(smem + xlane + 64u * (uint32_t)(((g - g0) * S32 + s) * M));
+        for (int s = S0; s < S1; ++s) xf[s - S0] = *(lds_bf16x8_c *)(smem + xq + 64u * (uint32_t)(s * M));
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-          const Raw r = f.r[u][i];
-          uint32_t d[G / 8];
-          decode_quarter<G>(smem, lut, r.w0, r.w1, r.tail, q, d, flags);
-          f32x4 part{0.f, 0.f, 0.f, 0.f};
+          uint32_t d[G / 2];
+          const f16x2 sc = __builtin_bit_cast(f16x2, f[i].scale * 0x10001u);
+          decode_group<G, P0, P1, decltype(tail)::value>(smem, lut, f[i].w, sc, d, flags);
 #pragma unroll
-          for (int s = 0; s < S32; ++s)
-            part = mfma32<false>(
-                xf[s], __builtin_bit_cast(bf16x8, u32x4{d[4 * s], d[4 * s + 1], d[4 * s + 2], d[4 * s + 3]}),
-                part);
-          // codes entered as 2c
-          const float sh = 0.5f * __half2float(__ushort_as_half((unsigned short)r.scale));
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[i][0][c] = fmaf(sh, part[c], acc[i][0][c]);
+          for (int s = S0; s < S1; ++s)
+            acc[i][0] = mfma32<true>(
+                xf[s - S0],
+                __builtin_bit_cast(bf16x8, u32x4{d[4 * s], d[4 * s + 1], d[4 * s + 2], d[4 * s + 3]}),
+                acc[i][0]);
+          __builtin_amdgcn_sched_barrier(0);  // one part's registers at a time
         }
+      };
+      if constexpr (G == 128) {
+        part(Int<0>{}, Int<4>{}, Int<0>{});
+        part(Int<4>{}, Int<8>{}, Int<0>{});
+        part(Int<8>{}, Int<12>{}, Int<1>{});
+      } else {
+        part(Int<0>{}, Int<4>{}, Int<0>{});
+        part(Int<4>{}, Int<6>{}, Int<1>{});
       }
     }
     if (++k < batches) return;
     k = 0;
     // the tile's last batch: adapters (split 0), then the waves' sums in order
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[i][0][c] = ldexpf(acc[i][0][c], unshift[c]);
     if constexpr (NB == 1)
       if (split == 0 && A.adapters > 0 && n0 < A.N) add_adapters<1>(A, 0, n0, id, wk, kw, acc[0]);
     __syncthreads();  // the sums of the set before have been read
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      *(__attribute__((address_space(3))) f32x4 *)(smem + kRedOff + 16u * (uint32_t)((i * kFewWaves + wv) * 64 + lane)) =
+      *(__attribute__((address_space(3))) f32x4 *)(smem + kRedOff + 16u * (uint32_t)((i * waves + wv) * 64 + lane)) =
           acc[i][0];
       acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     __syncthreads();
-    for (int o = tid; o < wt * 256; o += kFewThreads) {  // [tile][row][column]
+    for (int o = tid; o < wt * 256; o += threads) {  // [tile][row][column]
       const int m = (o >> 4) & 15, n = ((b0 + j * blocks) * wt + (o >> 8)) * 16 + (o & 15);
       if (m >= M || n >= A.N) continue;
       // row m of column c is element m % 4 of lane 16 (m / 4) + c
@@ -326,7 +358,7 @@ __global__ __launch_bounds__(kFewThreads) void few_kernel(const ProjArgs A) {
       for (int i = 0; i < NB; ++i) {
         v[i] = 0.f;
         for (int w = 0; w < wk; ++w)
-          v[i] += *(__attribute__((address_space(3))) float *)(smem + at + 1024u * (uint32_t)(i * kFewWaves + w));
+          v[i] += *(__attribute__((address_space(3))) float *)(smem + at + 1024u * (uint32_t)(i * waves + w));
       }
       const int64_t at_out = (int64_t)m * A.N + n;
       if (A.splits > 1) {
@@ -342,8 +374,8 @@ __global__ __launch_bounds__(kFewThreads) void few_kernel(const ProjArgs A) {
   };
   const int total = steps * batches;
   for (int t = 0; t < total; t += 2) {
-    work(ba, bb);
-    if (t + 1 < total) work(bb, ba);
+    work(ra, rb);
+    if (t + 1 < total) work(rb, ra);
   }
   if ((flags & kBadFlag) && A.status) atomicOr(A.status, kDevInvalidByte);
 }
@@ -355,63 +387,59 @@ __global__ __launch_bounds__(kFewThreads) void few_kernel(const ProjArgs A) {
 constexpr int kMidWaves = 8, kMidThreads = 64 * kMidWaves;
 
 // A block: 128 weight rows (of each matrix), a tile of 16 a wave; one chunk of
-// 16 MT rows of x; one split of K.  x comes in fragment order (frag_role), a
-// group at a time, through a ring of LDS slots that all waves read.
+// 16 MT rows of x; one split of K, in whole quads of groups.  The weights as
+// few_kernel has them; x comes in the same order and as f16 (f16_role), four
+// matrix steps at a time, through a ring of LDS slots that all waves read.
 template <int G, int NB, int MT, int ACT>
 __global__ __launch_bounds__(kMidThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void mid_kernel(const ProjArgs A) {
-  constexpr int S32 = G / 32, B = bytes_per_group(G);
-  typedef Lut<kLutBf16, 16> L;
-  constexpr uint32_t kStage = S32 * MT * 1024, kLoad = 16 * kMidThreads;
-  constexpr uint32_t kSlot = kStage > kLoad ? kStage : kLoad;
-  constexpr int kD = kSlot / kLoad;                             // loads a thread and stage
-  constexpr int kSlots = 49152 / kSlot > 6 ? 6 : 49152 / kSlot;  // 80 KB in all: two blocks a CU
+  constexpr int T = G / 8, B = bytes_per_group(G), SQ = T / 4;  // SQ: stages of a quad
+  typedef Lut<8> L;
+  constexpr uint32_t kSlot = 4 * MT * 1024, kLoad = 16 * kMidThreads;
+  constexpr int kD = kSlot / kLoad;      // loads of x a thread and stage
+  constexpr int kSlots = 65536 / kSlot;  // 80 KB in all: two blocks a CU
   __shared__ __align__(16) unsigned char smem_raw[L::kBytes + kSlots * kSlot];
   lds_bytes *smem = (lds_bytes *)smem_raw;
   lds_bytes *ring = smem + L::kBytes;
   const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int nG = A.K / G;
+  const int nG = A.K / G, nQ = (nG + 3) / 4;
   int b = (int)blockIdx.x;
   const int chunk = b % A.chunks;
   b /= A.chunks;
   const int split = b % A.splits, n0 = (b / A.splits) * 128 + 16 * wv;
-  const int g0 = (int)((int64_t)nG * split / A.splits);
-  const int g1 = (int)((int64_t)nG * (split + 1) / A.splits);
+  const int q0 = (int)((int64_t)nQ * split / A.splits);
+  const int q1 = (int)((int64_t)nQ * (split + 1) / A.splits);
   const int64_t m0 = (int64_t)chunk * (16 * MT);
 
   // rows past N read row N - 1; their sums are not stored
-  const int nt = min(n0, A.N - 1);
-  const uint32_t ln = (uint32_t)min(l, A.N - 1 - nt);
-  const uint32_t row = ln * (uint32_t)nG * B, srow = ln * (uint32_t)nG;
-  Raw ra[NB], rb[NB];
-  auto fetch = [&](Raw(&r)[NB], int g) {  // always: the waits below count its loads
-    const int64_t at = (int64_t)nt * nG + min(g, nG - 1);
+  const int64_t n = min(n0 + l, A.N - 1);
+  Raw<G> ra[NB], rb[NB];
+  auto fetch = [&](Raw<G>(&r)[NB], int quad) {  // always: the waits below count on its loads
+    // groups past the last read it, with scale 0
+    const int g = 4 * quad + q;
+    const int64_t at = n * nG + min(g, nG - 1);
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
-      r[i] = load_raw<G>(A.packed[i] + at * B, A.scales[i] + at, row, srow, (uint32_t)q);
+    for (int i = 0; i < NB; ++i) {
+      r[i].w = load_bytes<G>(A.packed[i] + at * B);
+      const uint32_t sc = A.scales[i][at];
+      r[i].scale = g < nG ? sc : 0u;
+    }
   };
-  uint32_t off[kD];
-#pragma unroll
-  for (int i = 0; i < kD; ++i) {
-    off[i] = (uint32_t)(i * kLoad + 16 * tid);
-    if (off[i] >= kStage) off[i] = kNoRow;
-  }
-  const uint16_t *xbase = A.x + (int64_t)chunk * nG * (kStage / 2);
+  const uint16_t *xbase = A.x + (int64_t)chunk * nQ * SQ * (kSlot / 2);
   int put = 0;  // slot of the next request
-  auto request = [&](int g) {
+  auto request = [&](int s) {  // stage s of the whole of K
 #pragma unroll
     for (int i = 0; i < kD; ++i)
-      dma16_tracked(xbase + (int64_t)g * (kStage / 2),
+      dma16_tracked(xbase + (int64_t)s * (kSlot / 2),
                     ring + (uint32_t)put * kSlot + (uint32_t)(i * kLoad) + 1024u * (uint32_t)wv,
-                    g < g1 ? off[i] : kNoRow);
+                    s < q1 * SQ ? (uint32_t)(i * kLoad + 16 * tid) : kNoRow);
     put = put == kSlots - 1 ? 0 : put + 1;
   };
 
-  fetch(ra, g0);
-  fetch(rb, g0 + 1);
+  fetch(ra, q0);
 #pragma unroll
-  for (int s = 0; s < kSlots - 1; ++s) request(g0 + s);
+  for (int s = 0; s < kSlots - 1; ++s) request(q0 * SQ + s);
   L::build(smem, tid, kMidThreads);
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
@@ -423,59 +451,71 @@ void mid_kernel(const ProjArgs A) {
   const L lut(0, lane);
   uint32_t flags = 0;
   int get = 0;
-  auto stage = [&](int g, Raw(&r)[NB]) {
-    request(g + kSlots - 1);
-    lds_bytes *x = ring + (uint32_t)get * kSlot + 16u * (uint32_t)lane;
-    get = get == kSlots - 1 ? 0 : get + 1;
-    uint32_t d[NB][G / 8];
-    float sh[NB];
+  auto quad_of = [&](int quad, Raw<G>(&r)[NB], Raw<G>(&next)[NB]) {
+    uint32_t d[NB][G / 2];
+    auto stage = [&](auto sc) {
+      constexpr int S = decltype(sc)::value;
+      request(quad * SQ + S + kSlots - 1);
+      if constexpr (S == 0) fetch(next, quad + 1);
+      lds_bytes *x = ring + (uint32_t)get * kSlot + 16u * (uint32_t)lane;
+      get = get == kSlots - 1 ? 0 : get + 1;
+      // the byte pairs whose first dword is among this stage's sixteen
+      constexpr int P = G / 10, P0 = (16 * S + 4) / 5, P1 = (16 * S + 20) / 5 < P ? (16 * S + 20) / 5 : P;
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      decode_quarter<G>(smem, lut, r[i].w0, r[i].w1, r[i].tail, q, d[i], flags);
-      // codes entered as 2c
-      sh[i] = 0.5f * __half2float(__ushort_as_half((unsigned short)r[i].scale));
+      for (int i = 0; i < NB; ++i)
+        decode_group<G, P0, P1, S == SQ - 1>(smem, lut, r[i].w,
+                                             __builtin_bit_cast(f16x2, r[i].scale * 0x10001u), d[i], flags);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const bf16x8 xf = *(lds_bf16x8_c *)(x + 1024u * (uint32_t)(s * MT + mt));
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            const uint32_t *w = d[i] + 16 * S + 4 * s;
+            acc[i][mt] =
+                mfma32<true>(xf, __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]}), acc[i][mt]);
+          }
+        }
+      // x of the next stage was requested kSlots - 2 stages ago, before at
+      // least the x requests of the stages since and, if the quad's first
+      // stage is one of them, three loads a matrix
+      constexpr int kSince = kSlots - 2;
+      constexpr bool kFetched = S < kSince;
+      constexpr int kOut = kSince * kD + (kFetched ? 3 * NB : 0);
+      // every read of this stage's slot is done before the barrier: the next
+      // stage's request may fill it at once (one past the end needs no memory)
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kOut) : "memory");
+    };
+    stage(Int<0>{});
+    stage(Int<1>{});
+    if constexpr (SQ == 4) {
+      stage(Int<2>{});
+      stage(Int<3>{});
     }
-    fetch(r, g + 2);
-    f32x4 part[NB][MT];
-#pragma unroll
-    for (int s = 0; s < S32; ++s)
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const bf16x8 xf = *(lds_bf16x8_c *)(x + 1024u * (uint32_t)(s * MT + mt));
-#pragma unroll
-        for (int i = 0; i < NB; ++i)
-          part[i][mt] = mfma32<false>(
-              xf,
-              __builtin_bit_cast(bf16x8, u32x4{d[i][4 * s], d[i][4 * s + 1], d[i][4 * s + 2], d[i][4 * s + 3]}),
-              s == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : part[i][mt]);
-      }
-#pragma unroll
-    for (int i = 0; i < NB; ++i)
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[i][mt][c] = fmaf(sh[i], part[i][mt][c], acc[i][mt][c]);
-    // x of group g + 1 has landed when what was requested after it is all
-    // that is out: the rest of its stage at the least, and kSlots - 2 stages
-    // of kD loads of x and 3 NB of bytes and scales
-    constexpr int kOut = (kSlots - 2) * (kD + 3 * NB);
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(kOut > 63 ? 63 : kOut) : "memory");
   };
-  for (int g = g0; g < g1; g += 2) {
-    stage(g, ra);
-    if (g + 1 < g1) stage(g + 1, rb);
+  for (int quad = q0; quad < q1; quad += 2) {
+    quad_of(quad, ra, rb);
+    if (quad + 1 < q1) quad_of(quad + 1, rb, ra);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may still write this block's LDS
   if ((flags & kBadFlag) && A.status) atomicOr(A.status, kDevInvalidByte);
 
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int64_t m = m0 + 16 * mt + 4 * q + c;
+      const int sh = m < A.M ? -A.shift[m] : 0;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) acc[i][mt][c] = ldexpf(acc[i][mt][c], sh);
+    }
   if constexpr (NB == 1) {
     // the splits share the adapters
-    const int64_t m = m0 + lane;
     if (A.adapters > 0 && n0 < A.N)
-      add_adapters<MT>(A, m0, n0, adapter_of(A, m, lane < 16 * MT), A.splits, split, acc[0]);
+      add_adapters<MT>(A, m0, n0, adapter_of(A, m0 + lane, lane < 16 * MT), A.splits, split, acc[0]);
   }
-  const int n = n0 + l;
-  if (n >= A.N) return;
+  if (n0 + l >= A.N) return;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -534,7 +574,7 @@ __global__ __launch_bounds__(kWideThreads) __attribute__((amdgpu_waves_per_eu(2,
 void wide_kernel(const ProjArgs A) {
   constexpr int S32 = G / 32, WP = 2, WQ = 4, TP = 8, TQ = 4, B = bytes_per_group(G);
   typedef Stream<kRows, kWideQ, kWideThreads> QS;
-  typedef Lut<kLutF16, 8> L;
+  typedef Lut<8> L;
   constexpr uint32_t kPSlot = kWideP * kKS * 2;
   constexpr uint32_t kQOff = kWideC * kPSlot, kLutOff = kQOff + kWideX * QS::kSlot;
   __shared__ __align__(16) unsigned char smem_raw[kLutOff + L::kBytes];
@@ -880,76 +920,58 @@ __device__ void shrink_role(const PreArgs &A, int64_t blk, unsigned char *smem_r
   }
 }
 
-// x in the fragment order of mid_kernel: [chunk][group][step][16-row tile]
-// [lane][8]; rows past M are zeros.
-template <int G>
-__device__ void frag_role(const PreArgs &A, int64_t first, int64_t stride) {
-  constexpr int S32 = G / 32;
-  const int nG = A.K / G, rows = 16 * A.mt;
-  const int64_t chunks = (A.M + rows - 1) / rows, units = chunks * nG * 4 * rows;
-  for (int64_t e = first; e < units; e += stride) {
-    // a wave's lanes take neighbouring quarters of one row
-    const int uq = (int)(e & 3);
-    const int64_t rest = e >> 2;
-    const int g = (int)(rest % nG);
-    const int64_t row = rest / nG, chunk = row / rows;
-    const int rr = (int)(row - chunk * rows);
-    u32x4 f[S32];
-#pragma unroll
-    for (int s = 0; s < S32; ++s) f[s] = u32x4{0u, 0u, 0u, 0u};
-    if (row < A.M) order_quarter<G>(A.x + row * A.K + (int64_t)g * G, uq, f);
-#pragma unroll
-    for (int s = 0; s < S32; ++s)
-      *(u32x4 *)(A.xo + (((chunk * nG + g) * S32 + s) * A.mt + (rr >> 4)) * 512 + (uq * 16 + (rr & 15)) * 8) =
-          f[s];
-  }
-}
-
-// Row m of x as f16 times a power of two that brings its largest finite value
-// to [2^14, 2^15): a bf16 value's eight bits fit f16's eleven, so every
-// element down to 2^-32 of the row's largest is exact, and a smaller one is
-// off by at most 2^-40 of it.  In the order of wide_kernel's codes.
-template <int G>
+// Row m of x as f16 times 2^shift[m], for mid_kernel in its fragments
+// [chunk][quad][step][16-row tile][lane][8] (rows past M and groups past the
+// last are zeros), for wide_kernel in rows, in the order of its codes.
+template <int G, bool FRAG>
 __device__ void f16_role(const PreArgs &A, int64_t m, unsigned char *smem_raw) {
   uint32_t *tops = (uint32_t *)smem_raw;  // [8]
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x;
   const uint16_t *xr = A.x + m * A.K;
-  uint32_t top = 0;
-  for (int k = 8 * tid; k < A.K; k += 8 * kPreThreads) {
-    uint16_t v[8];
-    *(u32x4 *)v = *(const u32x4 *)(xr + k);
+  int shift = 0;
+  if (!FRAG || m < A.M) {
+    uint32_t top = 0;
+    for (int k = 8 * tid; k < A.K; k += 8 * kPreThreads) top = top_of(top, xr + k);
+    top = wave_max(top);
+    __syncthreads();  // the row before has been read
+    if ((tid & 63) == 0) tops[tid >> 6] = top;
+    __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t b = v[j] & 0x7FFFu;
-      top = b < 0x7F80u && b > top ? b : top;
-    }
+    for (int w = 0; w < kPreWaves; ++w) top = max(top, tops[w]);
+    shift = f16_shift(top);
+    if (tid == 0) A.shift[m] = shift;
   }
+  if constexpr (FRAG) {
+    constexpr int T = G / 8;
+    const int nG = A.K / G, nQ = (nG + 3) / 4, rows = 16 * A.mt;
+    const int64_t chunk = m / rows;
+    const int r = (int)(m - chunk * rows);
+    for (int e = tid; e < nQ * 4 * T; e += kPreThreads) {
+      const int g = e / T, t = e % T;
+      const bool in = g < nG && m < A.M;
+      _Float16 f[8];
 #pragma unroll
-  for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
-  __syncthreads();  // the row before has been read
-  if (lane == 0) tops[tid >> 6] = top;
-  __syncthreads();
+      for (int i = 0; i < 8; ++i)
+        f[i] = in ? f16_of(xr[g * G + group_source<G>(8 * t + i)], shift) : (_Float16)0.f;
+      *(u32x4 *)(A.xo + (((chunk * nQ + (g >> 2)) * T + t) * A.mt + (r >> 4)) * 512 +
+                 ((g & 3) * 16 + (r & 15)) * 8) = *(u32x4 *)f;
+    }
+  } else {
+    uint16_t *o = A.xo + m * A.K;
+    for (int e = tid; e < A.K / 16; e += kPreThreads) {
+      const int g = e / (G / 16), part = e % (G / 16);
+      const uint16_t *p = xr + g * G;
+      _Float16 f[16];
 #pragma unroll
-  for (int w = 0; w < kPreWaves; ++w) top = max(top, tops[w]);
-  int exponent;  // top is in [2^(exponent - 1), 2^exponent)
-  (void)frexpf(bf16_to_f32(top), &exponent);
-  const int shift = top ? 15 - exponent : 0;
-  if (tid == 0) A.shift[m] = shift;
-  uint16_t *o = A.xo + m * A.K;
-  for (int e = tid; e < A.K / 16; e += kPreThreads) {
-    const int g = e / (G / 16), part = e % (G / 16);
-    const uint16_t *p = xr + g * G;
-    _Float16 f[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-      f[j] = (_Float16)ldexpf(bf16_to_f32(p[eighth_source<G>(part, j)]), shift);
-    *(u32x4 *)(o + 16 * e) = *(u32x4 *)f;
-    *(u32x4 *)(o + 16 * e + 8) = *(u32x4 *)(f + 8);
+      for (int j = 0; j < 16; ++j) f[j] = f16_of(p[eighth_source<G>(part, j)], shift);
+      *(u32x4 *)(o + 16 * e) = *(u32x4 *)f;
+      *(u32x4 *)(o + 16 * e + 8) = *(u32x4 *)(f + 8);
+    }
   }
 }
 
 constexpr int64_t kMaxPreBlocks = 1 << 16;  // of a role; each strides over its work
-constexpr int kPreNone = 0, kPreFrag = 1, kPreF16 = 2;
+constexpr int kPreNone = 0, kPreFrag = 1, kPreRows = 2;
 
 template <int G, int MODE>
 __global__ __launch_bounds__(kPreThreads) void pre_kernel(const PreArgs A) {
@@ -964,10 +986,9 @@ __global__ __launch_bounds__(kPreThreads) void pre_kernel(const PreArgs A) {
   }
   const int64_t blk = (int64_t)blockIdx.x - A.shrink_blocks;
   const int64_t blocks = (int64_t)gridDim.x - A.shrink_blocks;
-  if constexpr (MODE == kPreFrag) {
-    frag_role<G>(A, blk * kPreThreads + threadIdx.x, blocks * kPreThreads);
-  } else if constexpr (MODE == kPreF16) {
-    for (int64_t m = blk; m < A.M; m += blocks) f16_role<G>(A, m, smem);
+  if constexpr (MODE != kPreNone) {
+    const int64_t rows = MODE == kPreFrag ? ceil_div(A.M, 16 * A.mt) * (16 * A.mt) : A.M;
+    for (int64_t m = blk; m < rows; m += blocks) f16_role<G, MODE == kPreFrag>(A, m, smem);
   }
 }
 
@@ -975,13 +996,12 @@ __global__ __launch_bounds__(kPreThreads) void pre_kernel(const PreArgs A) {
 // which kernel, and the workspace
 // ---------------------------------------------------------------------------
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
 
 constexpr int kFew = 0, kMid = 1, kWide = 2;
 
 struct Plan {
-  int kind, wk, mt, splits, tsplits;
+  int kind, wk, wt, mt, splits, tsplits;
   int64_t blocks, chunks;
   int64_t x, shift, t, partial;  // workspace bytes, each a multiple of 16, in this order
   int64_t total() const { return x + shift + t + partial; }
@@ -994,14 +1014,20 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
   const int64_t wide_tiles = ceil_div(NB * N, kWideP) * ceil_div(M, kWideQ);
   if (M <= kFewRows) {
     p.kind = kFew;
-    // a block's slice of x fits its LDS
-    p.splits = (int)ceil_div(nG, kFewX / (M * G * 2));
-    // waves along K: few_u groups a wave, more waves while the sets of tiles
-    // are fewer than the CUs
-    const int64_t ng = ceil_div(nG, p.splits), tiles = ceil_div(N, 16);
-    p.wk = 1;
-    while (p.wk < kFewWaves && (ng > few_u(G, NB) * p.wk || tiles * p.wk / kFewWaves * p.splits < 192)) p.wk *= 2;
-    p.blocks = std::min(ceil_div(tiles, kFewWaves / p.wk), std::max<int64_t>(1, 256 / p.splits)) * p.splits;
+    // a block's slice of x, in whole quads of groups, fits its LDS
+    p.splits = (int)ceil_div(ceil_div(nG, 4), kFewX / (M * 4 * G * 2));
+    const int64_t quads = ceil_div(ceil_div(nG, 4), p.splits), tiles = ceil_div(N, 16);
+    // waves along K: a quad of groups each where that many waves are to be
+    // had; as many tiles a block as leave every CU one
+    p.wk = (int)std::min<int64_t>(quads, kFewWaves);
+    const int64_t spread = std::max<int64_t>(1, tiles * p.splits / 224);
+    p.wt = (int)std::min<int64_t>(kFewWaves / p.wk, spread);
+    if (p.wt == 1 && spread >= 4 && p.wk > 4) {
+      // many tiles: fewer sums to gather, more bytes a wave in flight
+      p.wk = 4;
+      p.wt = kFewWaves / p.wk;
+    }
+    p.blocks = std::min(ceil_div(tiles, p.wt), std::max<int64_t>(1, 256 / p.splits)) * p.splits;
   } else if (M > 128 && wide_tiles >= 64) {
     p.kind = kWide;
     // a tile a CU; K is split while every block keeps 64 stages
@@ -1014,10 +1040,12 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
     p.mt = M <= 32 ? 2 : 4;
     p.chunks = ceil_div(M, 16 * p.mt);
     const int64_t blocks = ceil_div(N, 128) * p.chunks;
-    // two blocks a CU; K is split while every block keeps four groups
-    while (blocks * p.splits < 384 && nG / (2 * p.splits) >= 4) p.splits *= 2;
+    // two blocks a CU; K is split while every block keeps two quads of groups
+    const int64_t quads = ceil_div(nG, 4);
+    while (blocks * p.splits < 384 && quads / (2 * p.splits) >= 2) p.splits *= 2;
     p.blocks = blocks * p.splits;
-    p.x = p.chunks * 16 * p.mt * K * 2;
+    p.x = p.chunks * 16 * p.mt * quads * 4 * G * 2;
+    p.shift = round16(M * 4);
   }
   if (p.splits > 1) p.partial = round16((int64_t)p.splits * NB * M * N * 4);
   if (R) {
@@ -1033,7 +1061,7 @@ template <int G, int NB, int ACT>
 void launch_product(const Plan &p, const ProjArgs &a, hipStream_t stream) {
   const dim3 grid((unsigned)p.blocks);
   if (p.kind == kFew)
-    hipLaunchKernelGGL((few_kernel<G, NB, ACT>), grid, dim3(kFewThreads), 0, stream, a);
+    hipLaunchKernelGGL((few_kernel<G, NB, ACT>), grid, dim3(64 * p.wk * p.wt), 0, stream, a);
   else if (p.kind == kWide)
     hipLaunchKernelGGL((wide_kernel<G, NB, ACT>), grid, dim3(kWideThreads), 0, stream, a);
   else if (p.mt == 2)
@@ -1072,13 +1100,12 @@ void launch_proj(const Plan &p, ProjArgs a, PreArgs pre, void *workspace, hipStr
   }
   const int64_t sb = pre.shrink_blocks;
   if (p.kind == kWide) {
-    hipLaunchKernelGGL((pre_kernel<G, kPreF16>), dim3((unsigned)(sb + std::min(kMaxPreBlocks, a.M))),
+    hipLaunchKernelGGL((pre_kernel<G, kPreRows>), dim3((unsigned)(sb + std::min(kMaxPreBlocks, a.M))),
                        dim3(kPreThreads), 0, stream, pre);
     a.x = pre.xo;
   } else if (p.kind == kMid) {
-    const int64_t units = p.chunks * 16 * p.mt * (a.K / G) * 4;
     hipLaunchKernelGGL((pre_kernel<G, kPreFrag>),
-                       dim3((unsigned)(sb + std::min<int64_t>(4096, ceil_div(units, kPreThreads)))),
+                       dim3((unsigned)(sb + std::min(kMaxPreBlocks, p.chunks * 16 * p.mt))),
                        dim3(kPreThreads), 0, stream, pre);
     a.x = pre.xo;
   } else if (sb) {

@@ -1,23 +1,23 @@
 // tq_ternary.h -- decoding base-3 bytes into matrix operands, and the order
 // of the terms of a group that goes with it.
 //
-// A group of G codes is ceil(G/5) bytes of five (format: include/tq.h).  Its
-// whole bytes are dealt to the lanes or threads that build an operand, and the
-// G % 5-ish left-over codes of the last byte (G = 64: byte 12, codes 60..63) or
-// two (G = 128: bytes 24 and 25, codes 120..127) are dealt out singly, so that
-// everyone holds 32 (or 16) codes without straddling a byte:
-//   quarter q (few, mid), G = 128: bytes 6q .. 6q+5 and left-over codes 2q, 2q+1
-//                           G = 64:  bytes 3q .. 3q+2 and left-over code q
-//   eighth e (wide): bytes 3e .. 3e+2 and left-over code e (G = 64: e < 4)
-// Codes become 16-bit floats two at a time by one v_perm of bytes: a table in
-// LDS gives, for each byte value, the high bytes of its five codes' floats,
-// whose low bytes are zero (bf16: 2c, +-2 = 0xC000, 0x4000; f16: c, +-1 =
-// 0xBC00, 0x3C00).
+// A group of G codes is ceil(G/5) bytes of five (format: include/tq.h).  Codes
+// become f16 two at a time by one v_perm of bytes -- a table in LDS gives, for
+// each byte value, the high bytes of its five codes' floats, whose low bytes
+// are zero (+-1 = 0xBC00, 0x3C00) -- and are multiplied by their group's
+// fp16 scale, which is exact.  Two orders of the codes:
+//   group order (few_kernel, mid_kernel: a lane holds whole groups): bytes in
+//     pairs, codes 0 1 | 2 3 | 5 6 | 7 8 | 4 9 of each pair's ten, then the
+//     last G % 10 codes as they are;
+//   eighth order (wide_kernel: eight, or for G = 64 four, threads share a
+//     group): thread e has bytes 3e .. 3e+2 and one of the codes that are left
+//     over, 120 + e (G = 64: 60 + e).
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "tq_internal.h"
 #include "tq_mm.h"
 
 namespace tq {
@@ -27,7 +27,6 @@ struct Int {
   static constexpr int value = V;
 };
 
-constexpr int kLutBf16 = 0, kLutF16 = 1;
 constexpr uint32_t kBadFlag = 0xFF00u;  // in the second dword of invalid bytes' entries
 
 // The table: 256 entries of 8 bytes, COPIES times, copy i read by lanes i,
@@ -36,7 +35,7 @@ constexpr uint32_t kBadFlag = 0xFF00u;  // in the second dword of invalid bytes'
 // bytes make its address one v_perm of the byte and the lane's offset.  Fewer
 // copies leave LDS to other uses; lanes that share one then meet in a bank
 // now and then.
-template <int KIND, uint32_t COPIES>
+template <uint32_t COPIES>
 struct Lut {
   static constexpr uint32_t kStride = 8 * COPIES, kBytes = 256 * kStride;
   uint32_t at;  // LDS byte of this lane's copy of entry 0
@@ -45,7 +44,7 @@ struct Lut {
       : at(base + 8u * ((uint32_t)lane & (COPIES - 1u))) {}
 
   __device__ static __forceinline__ void build(lds_bytes *table, int tid, int threads) {
-    constexpr uint32_t neg = KIND == kLutBf16 ? 0xC0u : 0xBCu, pos = KIND == kLutBf16 ? 0x40u : 0x3Cu;
+    constexpr uint32_t neg = 0xBCu, pos = 0x3Cu;
     constexpr uint32_t kParts = 2, kPer = COPIES / 2 / kParts;  // 16-byte stores a thread
     const uint32_t part = (uint32_t)tid % kParts;
     for (uint32_t e = (uint32_t)tid / kParts; e < 256u; e += (uint32_t)threads / kParts) {
@@ -93,84 +92,118 @@ __device__ __forceinline__ u32x2 leftover_pool(lds_bytes *smem, const L &lut, ui
   return u32x2{a.x, __builtin_amdgcn_perm(b.x, a.y, 0x06050400u)};
 }
 
-// Quarter q of a group: 4 (G = 64: 2) fragments of eight codes, d[4 s ..].
-// order_quarter lists the codes in the same order.
+// A group's bytes as two loads bring them, within the group whatever its
+// place: G = 128: bytes 0 .. 15 and 10 .. 25; G = 64: 0 .. 7 and 5 .. 12.
+template <int G>
+struct GroupBytes;
+template <>
+struct GroupBytes<128> {
+  u32x4 a, b;
+};
+template <>
+struct GroupBytes<64> {
+  u32x2 a, b;
+};
+
+template <int G>
+__device__ __forceinline__ GroupBytes<G> load_bytes(const uint8_t *p) {
+  GroupBytes<G> w;
+  __builtin_memcpy(&w.a, p, G / 8);
+  __builtin_memcpy(&w.b, p + (bytes_per_group(G) - G / 8), G / 8);
+  return w;
+}
+
+// The entry of byte i (a constant once unrolled).
 template <int G, class L>
-__device__ __forceinline__ void decode_quarter(lds_bytes *smem, const L &lut, uint32_t w0, uint32_t w1,
-                                               uint32_t tail, int q, uint32_t (&d)[G / 8],
-                                               uint32_t &flags) {
-  if constexpr (G == 128) {
-    u32x2 e[6];
+__device__ __forceinline__ u32x2 entry_of(lds_bytes *smem, const L &lut, const GroupBytes<G> &w, int i) {
+  const bool first = i < G / 8;
+  const int at = first ? i : i - bytes_per_group(G) + G / 8;
+  return lut.read(smem, first ? w.a[at >> 2] : w.b[at >> 2], at & 3);
+}
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t scaled(uint32_t pair, f16x2 s) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, pair) * s);
+}
+
+// Keeps the OR of entries' second dwords where it is written: left to itself
+// the compiler gathers them at the end and keeps every entry until then.
+__device__ __forceinline__ void settle(uint32_t &flags) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(flags));
+#endif
+}
+
+// Scaled codes of byte pairs [P0, P1) of a group in group order: dwords 5 P0 ..
+// of d; with TAIL the last G % 10 codes follow.
+template <int G, int P0, int P1, bool TAIL, class L>
+__device__ __forceinline__ void decode_group(lds_bytes *smem, const L &lut, const GroupBytes<G> &w,
+                                             f16x2 s, uint32_t (&d)[G / 2], uint32_t &flags) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = lut.read(smem, w0, i);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) e[4 + i] = lut.read(smem, w1, i);
-    const u32x2 pool = leftover_pool<G>(smem, lut, tail, flags);
-#pragma unroll
-    for (int p = 0; p < 3; ++p) {
-      const u32x2 a = e[2 * p], b = e[2 * p + 1];
-      flags |= a.y | b.y;
-      d[5 * p] = pair01(a);
-      d[5 * p + 1] = pair23(a);
-      d[5 * p + 2] = pair01(b);
-      d[5 * p + 3] = pair23(b);
-      d[5 * p + 4] = pair44(a, b);
+  for (int p = P0; p < P1; ++p) {
+    const u32x2 a = entry_of(smem, lut, w, 2 * p), b = entry_of(smem, lut, w, 2 * p + 1);
+    flags |= a.y | b.y;
+    d[5 * p] = scaled(pair01(a), s);
+    d[5 * p + 1] = scaled(pair23(a), s);
+    d[5 * p + 2] = scaled(pair01(b), s);
+    d[5 * p + 3] = scaled(pair23(b), s);
+    d[5 * p + 4] = scaled(pair44(a, b), s);
+    settle(flags);
+  }
+  if constexpr (TAIL) {
+    const u32x2 a = entry_of(smem, lut, w, G / 10 * 2);
+    flags |= a.y;
+    constexpr int D = G / 10 * 5;
+    d[D] = scaled(pair01(a), s);
+    d[D + 1] = scaled(pair23(a), s);
+    if constexpr (G == 128) {
+      const u32x2 b = entry_of(smem, lut, w, 25);
+      flags |= b.y;
+      d[D + 2] = scaled(__builtin_amdgcn_perm(b.x, a.y, 0x040C000Cu), s);  // code 4 of a, 0 of b
+      d[D + 3] = scaled(__builtin_amdgcn_perm(b.x, b.x, 0x020C010Cu), s);  // codes 1, 2 of b
     }
-    d[15] = __builtin_amdgcn_perm(pool.y, pool.x, 0x010C000Cu + 0x02000200u * (uint32_t)q);
-  } else {
-    const u32x2 a = lut.read(smem, w0, 0), b = lut.read(smem, w0, 1),
-                c = lut.read(smem, w0, 2);
-    const u32x2 pool = leftover_pool<G>(smem, lut, tail, flags);
-    flags |= a.y | b.y | c.y;
-    d[0] = pair01(a);
-    d[1] = pair23(a);
-    d[2] = pair01(b);
-    d[3] = pair23(b);
-    d[4] = pair44(a, b);
-    d[5] = pair01(c);
-    d[6] = pair23(c);
-    d[7] = __builtin_amdgcn_perm(pool.x, c.y, 0x040C000Cu + 0x01000000u * (uint32_t)q);
   }
 }
 
-// The 16-bit x values of quarter q of the group at xg (4-byte aligned), in the
-// order of decode_quarter.
+// Where in its group code i of the group order comes from.
 template <int G>
-__device__ __forceinline__ void order_quarter(const uint16_t *xg, int q, u32x4 (&f)[G / 32]) {
-  uint32_t d[G / 8];
-  auto lo_hi = [](uint32_t a, uint32_t b) {  // low half of a, high half of b
-    return __builtin_amdgcn_perm(b, a, 0x07060100u);
-  };
-  auto hi_lo = [](uint32_t a, uint32_t b) {  // high half of a, low half of b
-    return __builtin_amdgcn_perm(b, a, 0x05040302u);
-  };
-  if constexpr (G == 128) {
-    const uint32_t *p = (const uint32_t *)(xg + 30 * q);
+__device__ __forceinline__ int group_source(int i) {
+  constexpr int at[10] = {0, 1, 2, 3, 5, 6, 7, 8, 4, 9};
+  return i < G / 10 * 10 ? i / 10 * 10 + at[i % 10] : i;
+}
+
+// x as f16 times 2^shift.
+__device__ __forceinline__ _Float16 f16_of(uint32_t bf16, int shift) {
+  return (_Float16)ldexpf(bf16_to_f32(bf16), shift);
+}
+
+// The power of two that brings the largest finite magnitude `top` (bf16 bits
+// without sign) to [2^14, 2^15): a bf16 value's eight bits fit f16's eleven,
+// so every element down to 2^-32 of the largest is exact in f16, and a smaller
+// one is off by at most 2^-40 of it.
+__device__ __forceinline__ int f16_shift(uint32_t top) {
+  int exponent;  // top is in [2^(exponent - 1), 2^exponent)
+  (void)frexpf(bf16_to_f32(top), &exponent);
+  return top ? 15 - exponent : 0;
+}
+
+// The larger of `top` and the largest finite magnitude of eight bf16 values.
+__device__ __forceinline__ uint32_t top_of(uint32_t top, const uint16_t *p) {
+  uint16_t v[8];
+  *(u32x4 *)v = *(const u32x4 *)p;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const uint32_t w0 = p[5 * i], w1 = p[5 * i + 1], w2 = p[5 * i + 2], w3 = p[5 * i + 3],
-                     w4 = p[5 * i + 4];
-      d[5 * i] = w0;
-      d[5 * i + 1] = w1;
-      d[5 * i + 2] = hi_lo(w2, w3);
-      d[5 * i + 3] = hi_lo(w3, w4);
-      d[5 * i + 4] = lo_hi(w2, w4);
-    }
-    d[15] = *(const uint32_t *)(xg + 120 + 2 * q);
-  } else {
-    const uint16_t *p = xg + 15 * q;  // odd offsets: 16-bit loads
-    auto two = [&](int i, int j) { return (uint32_t)p[i] | (uint32_t)p[j] << 16; };
-    d[0] = two(0, 1);
-    d[1] = two(2, 3);
-    d[2] = two(5, 6);
-    d[3] = two(7, 8);
-    d[4] = two(4, 9);
-    d[5] = two(10, 11);
-    d[6] = two(12, 13);
-    d[7] = (uint32_t)p[14] | (uint32_t)xg[60 + q] << 16;
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t b = v[j] & 0x7FFFu;
+    top = b < 0x7F80u && b > top ? b : top;
   }
+  return top;
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 #pragma unroll
-  for (int s = 0; s < G / 32; ++s) f[s] = u32x4{d[4 * s], d[4 * s + 1], d[4 * s + 2], d[4 * s + 3]};
+  for (int o = 32; o; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
+  return v;
 }
 
 // Eighth e of a group: the 16 codes of three bytes (in `word`) and left-over
@@ -179,16 +212,14 @@ template <class L>
 __device__ __forceinline__ void decode_eighth(lds_bytes *smem, const L &lut, uint32_t word, u32x2 left,
                                               uint32_t e, uint32_t scale2, u32x4 &c0, u32x4 &c1,
                                               uint32_t &flags) {
-  typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
   const u32x2 a = lut.read(smem, word, 0), b = lut.read(smem, word, 1),
               c = lut.read(smem, word, 2);
   flags |= a.y | b.y | c.y;
   const uint32_t one = __builtin_amdgcn_perm(left.y, left.x, 0x0C0C0C00u + e);
   const f16x2 s = __builtin_bit_cast(f16x2, scale2);
-  auto times = [&](uint32_t v) { return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, v) * s); };
-  c0 = u32x4{times(pair01(a)), times(pair23(a)), times(__builtin_amdgcn_perm(one, a.y, 0x040C000Cu)),
-             times(pair01(b))};
-  c1 = u32x4{times(pair23(b)), times(pair44(b, c)), times(pair01(c)), times(pair23(c))};
+  c0 = u32x4{scaled(pair01(a), s), scaled(pair23(a), s),
+             scaled(__builtin_amdgcn_perm(one, a.y, 0x040C000Cu), s), scaled(pair01(b), s)};
+  c1 = u32x4{scaled(pair23(b), s), scaled(pair44(b, c), s), scaled(pair01(c), s), scaled(pair23(c), s)};
 }
 
 // Where in its group element j of eighth e comes from.
