@@ -54,7 +54,7 @@ struct ProjArgs {
   int64_t M;
   int N, K;
   int splits;                     // blocks along K
-  int wk;                         // few: waves along K (a power of two)
+  int wk, wt;                     // few: waves of a tile (along K), tiles of a set
   int chunks;                     // mid: chunks of rows
   int tp, tq;                     // wide: tiles
   int32_t *status;
@@ -81,24 +81,23 @@ struct Pieces {
   bf16x8 p[3];
 };
 __device__ __forceinline__ Pieces split_t(const ProjArgs &A, int64_t m, int r, bool in) {
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.f;
-  if (in)
-    for (int k = 0; k < A.tsplits; ++k) {
-      const f32x4 *t = (const f32x4 *)(A.t + ((int64_t)k * A.M + m) * A.R + r);
-      const f32x4 lo = t[0], hi = t[1];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] += lo[i];
-        v[4 + i] += hi[i];
-      }
+  f32x4 lo{0.f, 0.f, 0.f, 0.f}, hi = lo;
+  if (in) {
+    const f32x4 *t = (const f32x4 *)(A.t + m * A.R + r);
+    lo = t[0];
+    hi = t[1];
+    if (A.tsplits > 1) {
+      const f32x4 *u = (const f32x4 *)(A.t + (A.M + m) * A.R + r);
+      lo += u[0];
+      hi += u[1];
     }
+  }
   Pieces out;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const __bf16 a = (__bf16)v[i];
-    const float ra = v[i] - (float)a;
+    const float v = i < 4 ? lo[i] : hi[i - 4];
+    const __bf16 a = (__bf16)v;
+    const float ra = v - (float)a;
     const __bf16 b = (__bf16)ra;
     out.p[0][i] = a;
     out.p[1][i] = b;
@@ -107,43 +106,75 @@ __device__ __forceinline__ Pieces split_t(const ProjArgs &A, int64_t m, int r, b
   return out;
 }
 
-// Add the adapters' part to one tile of 16 weight rows (columns n0 + lane %
-// 16) by 16 MT rows of x (row m0 + i named by lane i's id, -1 for none).  The
-// distinct adapters are taken in turn, those with turn % share == mine here.
-// A product of one adapter is made for all the rows and kept for its own, so
-// nothing in an adapter reaches another's rows.
-template <int MT>
-__device__ void add_adapters(const ProjArgs &A, int64_t m0, int n0, int id, int share, int mine,
-                             f32x4 (&acc)[MT]) {
+// Add the adapters' part to T tiles of 16 weight rows (n0 + 16 t + ..) by C
+// of 16 rows of x (m0 + i, named by lane i's id, -1 for none): acc[t][c] has
+// the weight rows as the matrix cores' rows if WROWS, else as their columns.
+// The distinct adapters are taken in turn, those with turn % share == mine
+// here, the next one's B requested while one is multiplied.  A row's t is its
+// own adapter's; a product with an adapter is made for all the rows and kept
+// for those that name it, so nothing in an adapter reaches another's rows.
+template <bool WROWS, int T, int C>
+__device__ __forceinline__ void add_adapters(const ProjArgs &A, int64_t m0, int n0, int id, int share,
+                                             int mine, f32x4 (&acc)[T][C]) {
   const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
-  const int64_t n = min(n0 + l, A.N - 1);
-  uint64_t todo = adapter_leaders(id, lane);
-  for (int turn = 0; todo; ++turn) {
-    const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-    todo &= todo - 1;
-    if (turn % share != mine) continue;
-    f32x4 add[MT];
+  const uint64_t leaders = adapter_leaders(id, lane);
+  int64_t n[T];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) add[mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int r0 = 0; r0 < A.R; r0 += 32) {
-      const int r = r0 + 8 * q;
-      u32x4 v{0u, 0u, 0u, 0u};
-      if (r < A.R) v = *(const u32x4 *)(A.b + ((int64_t)a * A.N + n) * A.R + r);
-      const bf16x8 bv = __builtin_bit_cast(bf16x8, v);
+  for (int t = 0; t < T; ++t) n[t] = min(n0 + 16 * t + l, A.N - 1);
+  for (int r0 = 0; r0 < A.R; r0 += 32) {
+    const int r = r0 + 8 * q;
+    Pieces x[C];
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        const bool own = __shfl(id, 16 * mt + l) == a;
-        if (!__ballot(own)) continue;
-        const Pieces p = split_t(A, m0 + 16 * mt + l, r, own && r < A.R);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) add[mt] = mfma32<false>(p.p[i], bv, add[mt]);
+    for (int c = 0; c < C; ++c)
+      x[c] = split_t(A, m0 + 16 * c + l, r, __shfl(id, 16 * c + l) >= 0 && r < A.R);
+    uint64_t todo = leaders;
+    int turn = 0;
+    auto next = [&]() {  // the next adapter of ours, or -1
+      while (todo) {
+        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
+        todo &= todo - 1;
+        if (turn++ % share == mine) return a;
       }
+      return -1;
+    };
+    u32x4 b[T];
+    auto fetch = [&](int a) {
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        b[t] = u32x4{0u, 0u, 0u, 0u};
+        if (r < A.R) b[t] = *(const u32x4 *)(A.b + ((int64_t)a * A.N + n[t]) * A.R + r);
+      }
+    };
+    int a = next();
+    if (a >= 0) fetch(a);
+    while (a >= 0) {
+      bf16x8 w[T];
+#pragma unroll
+      for (int t = 0; t < T; ++t) w[t] = __builtin_bit_cast(bf16x8, b[t]);
+      const int an = next();
+      if (an >= 0) fetch(an);
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        if (!__ballot(__shfl(id, 16 * c + l) == a)) continue;
+        bool own[4];  // WROWS: of this lane's column; else of its four rows
+        if constexpr (WROWS) {
+          own[0] = __shfl(id, 16 * c + l) == a;
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) own[j] = __shfl(id, 16 * c + 4 * q + j) == a;
+        }
+#pragma unroll
+        for (int t = 0; t < T; ++t) {
+          f32x4 add{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            add = WROWS ? mfma32<false>(w[t], x[c].p[i], add) : mfma32<false>(x[c].p[i], w[t], add);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[t][c][j] += own[WROWS ? 0 : j] ? add[j] : 0.f;
+        }
+      }
+      a = an;
     }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        acc[mt][j] += __shfl(id, 16 * mt + 4 * q + j) == a ? add[mt][j] : 0.f;
   }
 }
 
@@ -159,6 +190,7 @@ __device__ __forceinline__ int adapter_of(const ProjArgs &A, int64_t m, bool in)
 
 constexpr int kFewRows = 16;
 constexpr int kFewWaves = 16;          // most waves of a block
+constexpr int kFewSetUp = 8;           // least: they share the table and x
 constexpr uint32_t kFewX = 64 << 10;   // LDS for a block's slice of x
 
 // The bytes and scale of one group.
@@ -196,14 +228,15 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A) {
   const int nQ = (nG + 3) / 4;  // quads of groups
   const int g0 = 4 * (int)((int64_t)nQ * split / A.splits);
   const int g1 = min(nG, 4 * (int)((int64_t)nQ * (split + 1) / A.splits));
-  const int wk = A.wk, wt = waves / wk;  // waves of a tile, tiles of a set
-  const int kw = wv % wk, tw = wv / wk;  // this wave's place
+  const int wk = A.wk, wt = A.wt;        // waves of a tile, tiles of a set
+  const int kw = wv % wk, tw = wv / wk;  // this wave's place (tw >= wt: it helps set up)
   const int tiles = (A.N + 15) / 16, sets = (tiles + wt - 1) / wt;
   const int steps = b0 < sets ? (sets - b0 + blocks - 1) / blocks : 0;
   const int quads = (g1 - g0 + 3) / 4, batches = (quads + wk - 1) / wk;  // of a tile
 
   // the set of step j is b0 + j * blocks
   auto tile_row = [&](int j) { return ((b0 + j * blocks) * wt + tw) * 16; };
+  const bool active = tw < wt;
   int fj = 0, fk = 0;  // step and batch of the next request
   auto fetch = [&](Raw<G>(&f)[NB]) {
     const int n0 = tile_row(fj), quad = kw + wk * fk;
@@ -232,53 +265,54 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A) {
   auto top_at = [&](int w, int m) {
     return (__attribute__((address_space(3))) uint32_t *)(smem + kRedOff + 4u * (uint32_t)(w * kFewRows + m));
   };
+  // rows are shared by the waves, `parts` waves a row
+  const int parts = max(1, waves / M);
   {
     const uint16_t *xs = A.x + (int64_t)g0 * G;
-    const int len = (g1 - g0) * G;
-    for (int m = 0; m < M; ++m) {
+    const int len = (g1 - g0) * G, part = wv % parts;
+    for (int m = wv / parts; m < M; m += waves / parts) {
       uint32_t top = 0;
-      for (int k = 8 * tid; k < len; k += 8 * threads) top = top_of(top, xs + (int64_t)m * A.K + k);
+#pragma unroll 4
+      for (int k = 8 * (64 * part + lane); k < len; k += 512 * parts)
+        top = top_of(top, xs + (int64_t)m * A.K + k);
       top = wave_max(top);
-      if (lane == 0) *top_at(wv, m) = top;
+      if (lane == 0) *top_at(part, m) = top;
     }
   }
   __syncthreads();
   auto shift_of = [&](int m) {
     uint32_t top = 0;
-    for (int w = 0; w < waves; ++w) top = max(top, *top_at(w, m));
+    for (int w = 0; w < parts; ++w) top = max(top, *top_at(w, m));
     return f16_shift(top);
   };
   {
     // unit: the steps of 40 codes, or those that are left, of a group of a row
     constexpr int U = (G + 39) / 40;
     const int units = quads * 4 * U;
-    for (int m = 0; m < M; ++m) {
-      const int shift = shift_of(m);
-      for (int e = tid; e < units; e += threads) {
-        const int g = e / U, u = e - g * U;
-        const bool in = g0 + g < g1, last = u == U - 1;
-        const int count = last ? G - 40 * (U - 1) : 40;
-        const uint16_t *p = A.x + (int64_t)m * A.K + (int64_t)min(g0 + g, g1 - 1) * G + 40 * u;
-        uint16_t v[40];
+    for (int o = tid; o < units * M; o += threads) {
+      const int m = o / units, e = o - m * units, shift = shift_of(m);
+      const int g = e / U, u = e - g * U;
+      const bool in = g0 + g < g1, last = u == U - 1;
+      const int count = last ? G - 40 * (U - 1) : 40;
+      const uint16_t *p = A.x + (int64_t)m * A.K + (int64_t)min(g0 + g, g1 - 1) * G + 40 * u;
+      uint16_t v[40];
 #pragma unroll
-        for (int s = 0; s < 5; ++s)
-          *(u32x4 *)(v + 8 * s) = *(const u32x4 *)(p + (8 * s < count ? 8 * s : 0));
+      for (int s = 0; s < 5; ++s) *(u32x4 *)(v + 8 * s) = *(const u32x4 *)(p + (8 * s < count ? 8 * s : 0));
 #pragma unroll
-        for (int s = 0; s < 5; ++s) {
-          if (8 * s >= count) break;
-          _Float16 f[8];
+      for (int s = 0; s < 5; ++s) {
+        if (8 * s >= count) break;
+        _Float16 f[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            // the codes past a group's tens are in their own order
-            constexpr int kTens = (G - 40 * (U - 1)) / 10 * 10;
-            const int o = 8 * s + i;
-            const uint16_t tens = v[group_source<40>(o)];
-            f[i] = f16_of(!in ? 0 : last && o >= kTens ? v[o] : tens, shift);
-          }
-          // [quad][step][group of the quad][row]
-          *(lds_u32x4 *)(smem + kXOff + 16u * (uint32_t)((((g >> 2) * T + 5 * u + s) * 4 + (g & 3)) * M + m)) =
-              *(u32x4 *)f;
+        for (int i = 0; i < 8; ++i) {
+          // the codes past a group's tens are in their own order
+          constexpr int kTens = (G - 40 * (U - 1)) / 10 * 10;
+          const int c = 8 * s + i;
+          const uint16_t tens = v[group_source<40>(c)];
+          f[i] = f16_of(!in ? 0 : last && c >= kTens ? v[c] : tens, shift);
         }
+        // [quad][step][group of the quad][row]
+        *(lds_u32x4 *)(smem + kXOff + 16u * (uint32_t)((((g >> 2) * T + 5 * u + s) * 4 + (g & 3)) * M + m)) =
+            *(u32x4 *)f;
       }
     }
   }
@@ -299,7 +333,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A) {
   auto work = [&](Raw<G>(&f)[NB], Raw<G>(&next)[NB]) {
     fetch(next);
     const int n0 = tile_row(j), quad = kw + wk * k;
-    if (n0 < A.N && quad < quads) {
+    if (active && n0 < A.N && quad < quads) {
       const uint32_t xq = xlane + 64u * (uint32_t)(quad * T * M);
       // five steps at a time: eight bytes of each matrix
       auto part = [&](auto p0, auto p1, auto tail) {
@@ -339,7 +373,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) acc[i][0][c] = ldexpf(acc[i][0][c], unshift[c]);
     if constexpr (NB == 1)
-      if (split == 0 && A.adapters > 0 && n0 < A.N) add_adapters<1>(A, 0, n0, id, wk, kw, acc[0]);
+      if (split == 0 && A.adapters > 0 && n0 < A.N && tw < wt) add_adapters<false>(A, 0, n0, id, wk, kw, acc);
     __syncthreads();  // the sums of the set before have been read
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
@@ -513,7 +547,7 @@ void mid_kernel(const ProjArgs A) {
   if constexpr (NB == 1) {
     // the splits share the adapters
     if (A.adapters > 0 && n0 < A.N)
-      add_adapters<MT>(A, m0, n0, adapter_of(A, m0 + lane, lane < 16 * MT), A.splits, split, acc[0]);
+      add_adapters<false>(A, m0, n0, adapter_of(A, m0 + lane, lane < 16 * MT), A.splits, split, acc);
   }
   if (n0 + l >= A.N) return;
 #pragma unroll
@@ -755,34 +789,7 @@ void wide_kernel(const ProjArgs A) {
     if (A.adapters > 0) {
       // the wave's 64 columns, one a lane; the splits share the adapters
       const int64_t mw = q0 + wq * (kWideQ / WQ);
-      const int id = adapter_of(A, mw + lane, true);
-      uint64_t todo = adapter_leaders(id, lane);
-      for (int turn = 0; todo; ++turn) {
-        const int a = __builtin_amdgcn_readlane(id, __builtin_ctzll(todo));
-        todo &= todo - 1;
-        if (turn % A.splits != split) continue;
-        for (int r0 = 0; r0 < A.R; r0 += 32) {
-          const int r = r0 + 8 * q;
-#pragma unroll
-          for (int b = 0; b < TQ; ++b) {
-            const bool own = __shfl(id, 16 * b + l) == a;
-            if (!__ballot(own)) continue;
-            const Pieces t = split_t(A, mw + 16 * b + l, r, own && r < A.R);
-#pragma unroll
-            for (int p = 0; p < TP; ++p) {
-              const int64_t n = min(nw + 16 * p + l, A.N - 1);
-              u32x4 v{0u, 0u, 0u, 0u};
-              if (r < A.R) v = *(const u32x4 *)(A.b + ((int64_t)a * A.N + n) * A.R + r);
-              const bf16x8 bv = __builtin_bit_cast(bf16x8, v);
-              f32x4 add{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-              for (int i = 0; i < 3; ++i) add = mfma32<false>(bv, t.p[i], add);
-#pragma unroll
-              for (int c = 0; c < 4; ++c) acc[p][b][c] += own ? add[c] : 0.f;
-            }
-          }
-        }
-      }
+      add_adapters<true>(A, mw, nw, adapter_of(A, mw + lane, true), A.splits, split, acc);
     }
   }
 #pragma unroll
@@ -823,8 +830,10 @@ void wide_kernel(const ProjArgs A) {
 // before the product: x in order, and t
 // ---------------------------------------------------------------------------
 
-constexpr int kPreThreads = 512, kPreWaves = 8;
+constexpr int kPreThreads = 1024, kPreWaves = 16;
+constexpr int kRowLds = 16384;    // elements of a row of x in LDS
 constexpr int kShrinkTile = 256;  // rows among which equal adapters are gathered
+constexpr int kShrinkRanks = 4;   // tiles of 16 ranks that share a read of x
 
 struct PreArgs {
   const uint16_t *x, *a;
@@ -835,21 +844,22 @@ struct PreArgs {
   float *t;
   int64_t M;
   int K, adapters, R, mt;
-  // shrink: blocks, units a tile of rows, tiles of 16 ranks, splits of K
+  // shrink: blocks, units a tile of rows, tiles of 16 RT ranks, splits of K
   int shrink_blocks, units, rtiles, tsplits;
   int32_t *status;
 };
 
-// t of one unit: up to 16 rows of one adapter, 16 ranks.  The rows of a tile
+// t of one unit: up to 16 rows of one adapter, 16 RT ranks.  The rows of a tile
 // that name the same adapter are numbered in order and cut into units of 16,
 // so rows in any order share the adapter's A.  One split of K; its waves
 // share the split, and their sums are added in order.
-__device__ void shrink_role(const PreArgs &A, int64_t blk, unsigned char *smem_raw) {
+template <int RT>
+__device__ __forceinline__ void shrink_role(const PreArgs &A, int64_t blk, unsigned char *smem_raw) {
   int *ids = (int *)smem_raw;                       // [256]
   int *rows = ids + kShrinkTile;                    // [16]
   int *info = rows + 16;                            // adapter, leader's rank
-  int *counts = info + 4;                           // [8] leaders of each wave
-  float *red = (float *)(counts + 12);              // [8][64][4]
+  int *counts = info + 4;                           // [16] leaders of each wave
+  float *red = (float *)(counts + 28);              // [16][64][4]
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, l = lane & 15, q = lane >> 4;
   const int split = (int)(blk % A.tsplits);
   blk /= A.tsplits;
@@ -891,49 +901,67 @@ __device__ void shrink_role(const PreArgs &A, int64_t blk, unsigned char *smem_r
   // ranks 16 rt + l
   const int own = rows[l], mr = own < 0 ? rows[0] : own;
   const uint16_t *xr = A.x + (m0 + mr) * A.K + 8 * q;
-  const int r = min(16 * rt + l, A.R - 1);
-  const uint16_t *ar = A.a + ((int64_t)a * A.R + r) * A.K + 8 * q;
-  f32x4 acc{0.f, 0.f, 0.f, 0.f};
+  const uint16_t *ar[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+    ar[i] = A.a + ((int64_t)a * A.R + min(16 * (RT * rt + i) + l, A.R - 1)) * A.K + 8 * q;
+  f32x4 acc[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int steps = A.K / 32;
   const int s0 = (int)((int64_t)steps * split / A.tsplits), s1 = (int)((int64_t)steps * (split + 1) / A.tsplits);
-  for (int s = s0 + wv; s < s1; s += kPreWaves * 8) {
-    // eight steps requested together; those past the end read the last one
-    // and add nothing
-    bf16x8 av[8], xv[8];
+  constexpr int kAhead = RT == 1 ? 8 : 4;  // steps requested together
+  for (int s = s0 + wv; s < s1; s += kPreWaves * kAhead) {
+    // steps past the end read the last one and add nothing
+    bf16x8 av[kAhead][RT], xv[kAhead];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int si = min(s + kPreWaves * i, steps - 1);
-      av[i] = *(const bf16x8 *)(ar + 32 * si);
-      xv[i] = *(const bf16x8 *)(xr + 32 * si);
+    for (int j = 0; j < kAhead; ++j) {
+      const int sj = min(s + kPreWaves * j, steps - 1);
+      xv[j] = *(const bf16x8 *)(xr + 32 * sj);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) av[j][i] = *(const bf16x8 *)(ar[i] + 32 * sj);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (s + kPreWaves * i < s1) acc = mfma32<false>(av[i], xv[i], acc);
+    for (int j = 0; j < kAhead; ++j)
+      if (s + kPreWaves * j < s1)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[i] = mfma32<false>(av[j][i], xv[j], acc[i]);
   }
-  *(f32x4 *)(red + 4 * tid) = acc;
-  __syncthreads();
-  if (tid < 256) {
-    float sum = 0.f;
-    for (int w = 0; w < kPreWaves; ++w) sum += red[w * 256 + tid];
-    const int ol = tid >> 2, rr = 16 * rt + 4 * (ol >> 4) + (tid & 3), row = rows[ol & 15];
-    if (row >= 0 && rr < A.R) A.t[((int64_t)split * A.M + m0 + row) * A.R + rr] = A.scaling[a] * sum;
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    *(f32x4 *)(red + 4 * tid) = acc[i];
+    __syncthreads();
+    if (tid < 256) {
+      float sum = 0.f;
+      for (int w = 0; w < kPreWaves; ++w) sum += red[w * 256 + tid];
+      const int ol = tid >> 2, rr = 16 * (RT * rt + i) + 4 * (ol >> 4) + (tid & 3), row = rows[ol & 15];
+      if (row >= 0 && rr < A.R) A.t[((int64_t)split * A.M + m0 + row) * A.R + rr] = A.scaling[a] * sum;
+    }
+    __syncthreads();
   }
 }
 
 // Row m of x as f16 times 2^shift[m], for mid_kernel in its fragments
 // [chunk][quad][step][16-row tile][lane][8] (rows past M and groups past the
 // last are zeros), for wide_kernel in rows, in the order of its codes.
+// A row passes through LDS, from which its elements are picked.
 template <int G, bool FRAG>
-__device__ void f16_role(const PreArgs &A, int64_t m, unsigned char *smem_raw) {
-  uint32_t *tops = (uint32_t *)smem_raw;  // [8]
+__device__ __forceinline__ void f16_role(const PreArgs &A, int64_t m, unsigned char *smem_raw) {
+  uint32_t *tops = (uint32_t *)smem_raw;             // [16]
+  uint16_t *row = (uint16_t *)(smem_raw + 64);       // [kRowLds]
   const int tid = threadIdx.x;
   const uint16_t *xr = A.x + m * A.K;
+  const bool in = !FRAG || m < A.M;
   int shift = 0;
-  if (!FRAG || m < A.M) {
+  __syncthreads();  // the row before has been read
+  if (in) {
     uint32_t top = 0;
-    for (int k = 8 * tid; k < A.K; k += 8 * kPreThreads) top = top_of(top, xr + k);
+#pragma unroll 2
+    for (int k = 8 * tid; k < A.K; k += 8 * kPreThreads) {
+      top = top_of(top, xr + k);
+      if (k < kRowLds) *(u32x4 *)(row + k) = *(const u32x4 *)(xr + k);
+    }
     top = wave_max(top);
-    __syncthreads();  // the row before has been read
     if ((tid & 63) == 0) tops[tid >> 6] = top;
     __syncthreads();
 #pragma unroll
@@ -941,31 +969,39 @@ __device__ void f16_role(const PreArgs &A, int64_t m, unsigned char *smem_raw) {
     shift = f16_shift(top);
     if (tid == 0) A.shift[m] = shift;
   }
-  if constexpr (FRAG) {
-    constexpr int T = G / 8;
-    const int nG = A.K / G, nQ = (nG + 3) / 4, rows = 16 * A.mt;
-    const int64_t chunk = m / rows;
-    const int r = (int)(m - chunk * rows);
-    for (int e = tid; e < nQ * 4 * T; e += kPreThreads) {
-      const int g = e / T, t = e % T;
-      const bool in = g < nG && m < A.M;
-      _Float16 f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        f[i] = in ? f16_of(xr[g * G + group_source<G>(8 * t + i)], shift) : (_Float16)0.f;
-      *(u32x4 *)(A.xo + (((chunk * nQ + (g >> 2)) * T + t) * A.mt + (r >> 4)) * 512 +
-                 ((g & 3) * 16 + (r & 15)) * 8) = *(u32x4 *)f;
+  constexpr int T = G / 8;
+  const int nG = A.K / G, nQ = (nG + 3) / 4, rows = 16 * A.mt;
+  const int64_t chunk = FRAG ? m / rows : 0;
+  const int r = FRAG ? (int)(m - chunk * rows) : 0;
+  for (int k0 = 0; k0 < A.K; k0 += kRowLds) {  // pieces of whole quads of groups
+    const int len = min(A.K - k0, kRowLds);
+    if (k0 > 0 && in) {
+      __syncthreads();
+      for (int k = 8 * tid; k < len; k += 8 * kPreThreads) *(u32x4 *)(row + k) = *(const u32x4 *)(xr + k0 + k);
+      __syncthreads();
     }
-  } else {
-    uint16_t *o = A.xo + m * A.K;
-    for (int e = tid; e < A.K / 16; e += kPreThreads) {
-      const int g = e / (G / 16), part = e % (G / 16);
-      const uint16_t *p = xr + g * G;
-      _Float16 f[16];
+    if constexpr (FRAG) {
+      const int g0 = k0 / G, quads = (len / G + 3) / 4;
+      for (int e = tid; e < quads * 4 * T; e += kPreThreads) {
+        const int g = e / T, t = e % T;
+        const bool has = in && g0 + g < nG;
+        _Float16 f[8];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) f[j] = f16_of(p[eighth_source<G>(part, j)], shift);
-      *(u32x4 *)(o + 16 * e) = *(u32x4 *)f;
-      *(u32x4 *)(o + 16 * e + 8) = *(u32x4 *)(f + 8);
+        for (int i = 0; i < 8; ++i)
+          f[i] = f16_of(has ? row[g * G + group_source<G>(8 * t + i)] : 0, shift);
+        *(u32x4 *)(A.xo + (((chunk * nQ + ((g0 + g) >> 2)) * T + t) * A.mt + (r >> 4)) * 512 +
+                   ((g & 3) * 16 + (r & 15)) * 8) = *(u32x4 *)f;
+      }
+    } else {
+      uint16_t *o = A.xo + m * A.K + k0;
+      for (int e = tid; e < len / 16; e += kPreThreads) {
+        const int g = e / (G / 16), part = e % (G / 16);
+        _Float16 f[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) f[j] = f16_of(row[g * G + eighth_source<G>(part, j)], shift);
+        *(u32x4 *)(o + 16 * e) = *(u32x4 *)f;
+        *(u32x4 *)(o + 16 * e + 8) = *(u32x4 *)(f + 8);
+      }
     }
   }
 }
@@ -973,13 +1009,15 @@ __device__ void f16_role(const PreArgs &A, int64_t m, unsigned char *smem_raw) {
 constexpr int64_t kMaxPreBlocks = 1 << 16;  // of a role; each strides over its work
 constexpr int kPreNone = 0, kPreFrag = 1, kPreRows = 2;
 
-template <int G, int MODE>
+template <int G, int MODE, int RT>
 __global__ __launch_bounds__(kPreThreads) void pre_kernel(const PreArgs A) {
-  __shared__ __align__(16) unsigned char smem[4 * (kShrinkTile + 32) + 16 * kPreThreads];
+  constexpr int kShrinkLds = 4 * (kShrinkTile + 48) + 16 * kPreThreads;
+  constexpr int kRowBytes = MODE == kPreNone ? 0 : 64 + 2 * kRowLds;
+  __shared__ __align__(16) unsigned char smem[kShrinkLds > kRowBytes ? kShrinkLds : kRowBytes];
   if ((int)blockIdx.x < A.shrink_blocks) {
-    const int64_t work = (A.M + kShrinkTile - 1) / kShrinkTile * A.units * A.rtiles * A.tsplits;
+    const int64_t work = ceil_div(A.M, kShrinkTile) * A.units * A.rtiles * A.tsplits;
     for (int64_t w = blockIdx.x; w < work; w += A.shrink_blocks) {
-      shrink_role(A, w, smem);
+      shrink_role<RT>(A, w, smem);
       __syncthreads();
     }
     return;
@@ -1049,9 +1087,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
   }
   if (p.splits > 1) p.partial = round16((int64_t)p.splits * NB * M * N * 4);
   if (R) {
-    // t: about eight steps a wave of a block
-    p.tsplits = (int)std::min<int64_t>(8, ceil_div(K / 32, 8 * kPreWaves));
-    if (M > 64) p.tsplits = std::min(p.tsplits, 2);
+    p.tsplits = M <= 256 && K > 4096 ? 2 : 1;  // where the blocks are few
     p.t = round16(p.tsplits * M * R * 4);
   }
   return p;
@@ -1061,7 +1097,7 @@ template <int G, int NB, int ACT>
 void launch_product(const Plan &p, const ProjArgs &a, hipStream_t stream) {
   const dim3 grid((unsigned)p.blocks);
   if (p.kind == kFew)
-    hipLaunchKernelGGL((few_kernel<G, NB, ACT>), grid, dim3(64 * p.wk * p.wt), 0, stream, a);
+    hipLaunchKernelGGL((few_kernel<G, NB, ACT>), grid, dim3(64 * std::max(kFewSetUp, p.wk * p.wt)), 0, stream, a);
   else if (p.kind == kWide)
     hipLaunchKernelGGL((wide_kernel<G, NB, ACT>), grid, dim3(kWideThreads), 0, stream, a);
   else if (p.mt == 2)
@@ -1084,6 +1120,7 @@ void launch_proj(const Plan &p, ProjArgs a, PreArgs pre, void *workspace, hipStr
   a.tsplits = pre.tsplits = p.tsplits;
   a.splits = p.splits;
   a.wk = p.wk;
+  a.wt = p.wt;
   a.chunks = (int)p.chunks;
   a.tp = (int)ceil_div(NB * (int64_t)a.N, kWideP);
   a.tq = (int)ceil_div(a.M, kWideQ);
@@ -1094,22 +1131,25 @@ void launch_proj(const Plan &p, ProjArgs a, PreArgs pre, void *workspace, hipStr
     const int64_t rows = std::min<int64_t>(a.M, kShrinkTile);
     // units of a tile: one for each 16 rows and one more for each adapter
     pre.units = (int)std::min(rows, ceil_div(rows, 16) + std::min<int64_t>(rows, a.adapters));
-    pre.rtiles = (int)ceil_div(a.R, 16);
+    pre.rtiles = (int)ceil_div(a.R, a.R > 16 ? 16 * kShrinkRanks : 16);
     if (a.adapters == 0) pre.units = pre.rtiles = pre.tsplits = 1;  // the ids are still checked
     pre.shrink_blocks = (int)std::min(kMaxPreBlocks, tiles * pre.units * pre.rtiles * pre.tsplits);
   }
   const int64_t sb = pre.shrink_blocks;
+  auto prepare = [&](auto kernel, int64_t rows) {
+    const dim3 grid((unsigned)(sb + std::min(kMaxPreBlocks, rows)));
+    hipLaunchKernelGGL(kernel, grid, dim3(kPreThreads), 0, stream, pre);
+  };
+  const bool ranks = NB == 1 && a.R > 16;
   if (p.kind == kWide) {
-    hipLaunchKernelGGL((pre_kernel<G, kPreRows>), dim3((unsigned)(sb + std::min(kMaxPreBlocks, a.M))),
-                       dim3(kPreThreads), 0, stream, pre);
+    ranks ? prepare(pre_kernel<G, kPreRows, kShrinkRanks>, a.M) : prepare(pre_kernel<G, kPreRows, 1>, a.M);
     a.x = pre.xo;
   } else if (p.kind == kMid) {
-    hipLaunchKernelGGL((pre_kernel<G, kPreFrag>),
-                       dim3((unsigned)(sb + std::min(kMaxPreBlocks, p.chunks * 16 * p.mt))),
-                       dim3(kPreThreads), 0, stream, pre);
+    const int64_t rows = p.chunks * 16 * p.mt;
+    ranks ? prepare(pre_kernel<G, kPreFrag, kShrinkRanks>, rows) : prepare(pre_kernel<G, kPreFrag, 1>, rows);
     a.x = pre.xo;
   } else if (sb) {
-    hipLaunchKernelGGL((pre_kernel<G, kPreNone>), dim3((unsigned)sb), dim3(kPreThreads), 0, stream, pre);
+    ranks ? prepare(pre_kernel<G, kPreNone, kShrinkRanks>, 0) : prepare(pre_kernel<G, kPreNone, 1>, 0);
   }
   launch_product<G, NB, ACT>(p, a, stream);
   if (p.splits > 1) {
