@@ -14,7 +14,7 @@
 // is put into the same order once, by whoever reads it (tq_ternary.h).
 //
 // Three kernels multiply:
-//   few_kernel    up to 16 rows: bound by the weights' bytes.  Every byte is
+//   few_kernel    up to 32 rows: bound by the weights' bytes.  Every byte is
 //                 decoded in registers by the lane that feeds it to the matrix
 //                 cores; the waves of a block share the groups of a tile of 16
 //                 weight rows, x stays in LDS.
@@ -185,10 +185,135 @@ __device__ __forceinline__ int adapter_of(const ProjArgs &A, int64_t m, bool in)
 }
 
 // ---------------------------------------------------------------------------
-// up to 16 rows
+// t
 // ---------------------------------------------------------------------------
 
-constexpr int kFewRows = 16;
+constexpr int kPreThreads = 1024, kPreWaves = 16;
+constexpr int kRowLds = 16384;    // elements of a row of x in LDS
+constexpr int kShrinkTile = 256;  // rows among which equal adapters are gathered
+constexpr int kShrinkRanks = 4;   // tiles of 16 ranks that share a read of x
+
+struct PreArgs {
+  const uint16_t *x, *a;
+  const int32_t *ids;
+  const float *scaling;
+  uint16_t *xo;     // fragments or f16 rows
+  int32_t *shift;   // f16 rows
+  float *t;
+  int64_t M;
+  int K, adapters, R, rpb;
+  // shrink: blocks, units a tile of rows, tiles of 16 RT ranks, splits of K
+  int shrink_blocks, units, rtiles, tsplits;
+  int32_t *status;
+};
+
+// t of one unit: up to 16 rows of one adapter, 16 RT ranks.  The rows of a tile
+// that name the same adapter are numbered in order and cut into units of 16,
+// so rows in any order share the adapter's A.  One split of K; its waves
+// share the split, and their sums are added in order.
+template <int RT>
+__device__ __forceinline__ void shrink_role(const PreArgs &A, int64_t blk, unsigned char *smem_raw) {
+  int *ids = (int *)smem_raw;                       // [256]
+  int *rows = ids + kShrinkTile;                    // [16]
+  int *info = rows + 16;                            // adapter, leader's rank
+  int *counts = info + 4;                           // [16] leaders of each wave
+  float *red = (float *)(counts + 28);              // [16][64][4]
+  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, l = lane & 15, q = lane >> 4;
+  const int split = (int)(blk % A.tsplits);
+  blk /= A.tsplits;
+  const int rt = (int)(blk % A.rtiles), unit = (int)(blk / A.rtiles % A.units);
+  const int64_t m0 = blk / A.rtiles / A.units * kShrinkTile;
+  const int nrows = (int)min((int64_t)kShrinkTile, A.M - m0);
+  int id = -1;
+  if (tid < nrows) {
+    id = A.ids[m0 + tid];
+    if (id < -1 || id >= A.adapters) {
+      if (unit == 0 && rt == 0 && split == 0 && A.status) atomicOr(A.status, kDevBadAdapter);
+      id = -1;
+    }
+  }
+  if (tid < kShrinkTile) ids[tid] = id;
+  if (tid < 16) rows[tid] = -1;
+  if (tid == 0) info[0] = -1;
+  __syncthreads();
+  int rank = 0;  // among the rows of this adapter
+  if (id >= 0)
+    for (int j = 0; j < tid; ++j) rank += ids[j] == id;
+  const bool leads = id >= 0 && rank % 16 == 0;
+  const uint64_t mask = __ballot(leads);
+  if (lane == 0) counts[wv] = __popcll(mask);
+  __syncthreads();
+  int before = __popcll(mask & ((1ull << lane) - 1));
+  for (int w = 0; w < wv; ++w) before += counts[w];
+  if (leads && before == unit) {
+    info[0] = id;
+    info[1] = rank;
+  }
+  __syncthreads();
+  const int a = info[0];
+  if (a < 0) return;  // fewer units than this
+  if (id == a && rank / 16 == info[1] / 16) rows[rank % 16] = tid;
+  __syncthreads();
+
+  // columns: the unit's rows (the first one in place of absent ones); rows:
+  // ranks 16 rt + l
+  const int own = rows[l], mr = own < 0 ? rows[0] : own;
+  const uint16_t *xr = A.x + (m0 + mr) * A.K + 8 * q;
+  const uint16_t *ar[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+    ar[i] = A.a + ((int64_t)a * A.R + min(16 * (RT * rt + i) + l, A.R - 1)) * A.K + 8 * q;
+  f32x4 acc[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const int steps = A.K / 32;
+  const int s0 = (int)((int64_t)steps * split / A.tsplits), s1 = (int)((int64_t)steps * (split + 1) / A.tsplits);
+  constexpr int kAhead = RT == 1 ? 8 : 4;  // steps requested together
+  for (int s = s0 + wv; s < s1; s += kPreWaves * kAhead) {
+    // steps past the end read the last one and add nothing
+    bf16x8 av[kAhead][RT], xv[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int sj = min(s + kPreWaves * j, steps - 1);
+      xv[j] = *(const bf16x8 *)(xr + 32 * sj);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) av[j][i] = *(const bf16x8 *)(ar[i] + 32 * sj);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+      if (s + kPreWaves * j < s1)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) acc[i] = mfma32<false>(av[j][i], xv[j], acc[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < RT; ++i) {
+    *(f32x4 *)(red + 4 * tid) = acc[i];
+    __syncthreads();
+    if (tid < 256) {
+      float sum = 0.f;
+      for (int w = 0; w < kPreWaves; ++w) sum += red[w * 256 + tid];
+      const int ol = tid >> 2, rr = 16 * (RT * rt + i) + 4 * (ol >> 4) + (tid & 3), row = rows[ol & 15];
+      if (row >= 0 && rr < A.R) A.t[((int64_t)split * A.M + m0 + row) * A.R + rr] = A.scaling[a] * sum;
+    }
+    __syncthreads();
+  }
+}
+
+// The share of one of A.shrink_blocks blocks of kPreThreads.
+template <int RT>
+__device__ __forceinline__ void shrink_all(const PreArgs &A, int block, unsigned char *smem) {
+  const int64_t work = ceil_div(A.M, kShrinkTile) * A.units * A.rtiles * A.tsplits;
+  for (int64_t w = block; w < work; w += A.shrink_blocks) {
+    shrink_role<RT>(A, w, smem);
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// up to 32 rows
+// ---------------------------------------------------------------------------
+
+constexpr int kFewRows = 32;
 constexpr int kFewWaves = 16;          // most waves of a block
 constexpr int kFewSetUp = 8;           // least: they share the table and x
 constexpr uint32_t kFewX = 64 << 10;   // LDS for a block's slice of x
@@ -207,24 +332,32 @@ struct Raw {
 // (With each group dealt to four lanes instead, three small loads each, the
 // address units took four times as long as the bytes.)  Scales are multiplied
 // into the codes, since a lane's sums then run over all groups.
-// x [M,K] (M <= 16) of the split, as f16 times a power of two for each row, is
-// put in order once, in LDS; it is the row operand of the matrix cores and W
+// x [M,K] (M <= 16 MT) of the split, as f16 times a power of two for each row,
+// is put in order once, in LDS; it is the row operand of the matrix cores and W
 // the column operand.
 // A wave requests four groups while it works on the four before, across the
-// ends of tiles.  LDS: 64 KB table, 64 KB x, up to 16 KB a matrix for the sums
-// of the waves.
-template <int G, int NB, int ACT>
-__global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A) {
+// ends of tiles.  LDS: 64 KB table, 64 KB x, up to 32 KB for the sums of the
+// waves.
+// lora: the projection alone; the blocks past the product's make t meanwhile
+// (RT as in shrink_role, 0 for none), and expand_kernel adds the adapters.
+template <int G, int NB, int MT, int ACT, int RT>
+__global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, const PreArgs P) {
   constexpr int T = G / 8, B = bytes_per_group(G);  // T: matrix steps of a group
   typedef Lut<32> L;
   constexpr uint32_t kXOff = L::kBytes, kRedOff = kXOff + kFewX;
-  __shared__ __align__(16) unsigned char smem_raw[L::kBytes + kFewX + kFewWaves * NB * 1024];
+  __shared__ __align__(16) unsigned char smem_raw[L::kBytes + kFewX + kFewWaves * 2048];
+  const int work_blocks = (int)gridDim.x - P.shrink_blocks;
+  if constexpr (RT > 0)
+    if ((int)blockIdx.x >= work_blocks) {
+      shrink_all<RT>(P, (int)blockIdx.x - work_blocks, smem_raw);
+      return;
+    }
   lds_bytes *smem = (lds_bytes *)smem_raw;
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), waves = threads >> 6;
   const int nG = A.K / G, M = (int)A.M;
   const int split = (int)blockIdx.x % A.splits, b0 = (int)blockIdx.x / A.splits;
-  const int blocks = (int)gridDim.x / A.splits;
+  const int blocks = work_blocks / A.splits;
   const int nQ = (nG + 3) / 4;  // quads of groups
   const int g0 = 4 * (int)((int64_t)nQ * split / A.splits);
   const int g1 = min(nG, 4 * (int)((int64_t)nQ * (split + 1) / A.splits));
@@ -239,6 +372,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A) {
   const bool active = tw < wt;
   int fj = 0, fk = 0;  // step and batch of the next request
   auto fetch = [&](Raw<G>(&f)[NB]) {
+    if (!active) return;
     const int n0 = tile_row(fj), quad = kw + wk * fk;
     // rows past N read row N - 1 and groups past the last read it, with scale
     // 0; neither is stored or counts
@@ -316,32 +450,39 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A) {
       }
     }
   }
-  int unshift[4];  // of rows 4 q .. 4 q + 3
+  int unshift[MT][4];  // of rows 16 mt + 4 q + c
 #pragma unroll
-  for (int c = 0; c < 4; ++c) unshift[c] = -shift_of(min(4 * q + c, M - 1));
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) unshift[mt][c] = -shift_of(min(16 * mt + 4 * q + c, M - 1));
   __syncthreads();
 
   const L lut(0, lane);
-  const uint32_t xlane = kXOff + 16u * (uint32_t)(q * M + min(l, M - 1));  // rows past M: row M - 1
-  int id = -1;
-  if constexpr (NB == 1) id = adapter_of(A, lane, lane < 16);
-  uint32_t flags = 0;
-  f32x4 acc[NB][1];
+  uint32_t xlane[MT];  // rows past M: row M - 1
 #pragma unroll
-  for (int i = 0; i < NB; ++i) acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int mt = 0; mt < MT; ++mt) xlane[mt] = kXOff + 16u * (uint32_t)(q * M + min(16 * mt + l, M - 1));
+  uint32_t flags = 0;
+  f32x4 acc[NB][MT];
+#pragma unroll
+  for (int i = 0; i < NB; ++i)
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) acc[i][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
   int j = 0, k = 0;  // step and batch being worked on
   auto work = [&](Raw<G>(&f)[NB], Raw<G>(&next)[NB]) {
     fetch(next);
     const int n0 = tile_row(j), quad = kw + wk * k;
     if (active && n0 < A.N && quad < quads) {
-      const uint32_t xq = xlane + 64u * (uint32_t)(quad * T * M);
+      const uint32_t xq = 64u * (uint32_t)(quad * T * M);
       // five steps at a time: eight bytes of each matrix
       auto part = [&](auto p0, auto p1, auto tail) {
         constexpr int P0 = decltype(p0)::value, P1 = decltype(p1)::value;
         constexpr int S0 = 5 * P0 / 4, S1 = decltype(tail)::value ? T : 5 * P1 / 4;
-        bf16x8 xf[S1 - S0];
+        bf16x8 xf[S1 - S0][MT];
 #pragma unroll
-        for (int s = S0; s < S1; ++s) xf[s - S0] = *(lds_bf16x8_c *)(smem + xq + 64u * (uint32_t)(s * M));
+        for (int s = S0; s < S1; ++s)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+            xf[s - S0][mt] = *(lds_bf16x8_c *)(smem + xlane[mt] + xq + 64u * (uint32_t)(s * M));
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
           uint32_t d[G / 2];
@@ -349,10 +490,12 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A) {
           decode_group<G, P0, P1, decltype(tail)::value>(smem, lut, f[i].w, sc, d, flags);
 #pragma unroll
           for (int s = S0; s < S1; ++s)
-            acc[i][0] = mfma32<true>(
-                xf[s - S0],
-                __builtin_bit_cast(bf16x8, u32x4{d[4 * s], d[4 * s + 1], d[4 * s + 2], d[4 * s + 3]}),
-                acc[i][0]);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+              acc[i][mt] = mfma32<true>(
+                  xf[s - S0][mt],
+                  __builtin_bit_cast(bf16x8, u32x4{d[4 * s], d[4 * s + 1], d[4 * s + 2], d[4 * s + 3]}),
+                  acc[i][mt]);
           __builtin_amdgcn_sched_barrier(0);  // one part's registers at a time
         }
       };
@@ -367,41 +510,48 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A) {
     }
     if (++k < batches) return;
     k = 0;
-    // the tile's last batch: adapters (split 0), then the waves' sums in order
+    // the tile's last batch: the waves' sums, in wave order; a matrix and 16
+    // rows of x at a time where LDS holds no more
+    constexpr int kOnce = NB * MT > 2 ? 1 : MT;  // 16-row tiles a pass (with all matrices)
+    static_assert(kFewWaves * NB * kOnce * 1024 <= kFewWaves * 2048, "the sums' LDS");
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
+    for (int c0 = 0; c0 < MT; c0 += kOnce) {
+      __syncthreads();  // the sums before have been read
 #pragma unroll
-      for (int c = 0; c < 4; ++c) acc[i][0][c] = ldexpf(acc[i][0][c], unshift[c]);
-    if constexpr (NB == 1)
-      if (split == 0 && A.adapters > 0 && n0 < A.N && tw < wt) add_adapters<false>(A, 0, n0, id, wk, kw, acc);
-    __syncthreads();  // the sums of the set before have been read
+      for (int i = 0; i < NB; ++i)
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      *(__attribute__((address_space(3))) f32x4 *)(smem + kRedOff + 16u * (uint32_t)((i * waves + wv) * 64 + lane)) =
-          acc[i][0];
-      acc[i][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    __syncthreads();
-    for (int o = tid; o < wt * 256; o += threads) {  // [tile][row][column]
-      const int m = (o >> 4) & 15, n = ((b0 + j * blocks) * wt + (o >> 8)) * 16 + (o & 15);
-      if (m >= M || n >= A.N) continue;
-      // row m of column c is element m % 4 of lane 16 (m / 4) + c
-      const uint32_t at = kRedOff + 16u * (uint32_t)((o >> 8) * wk * 64 + (m >> 2) * 16 + (o & 15)) + 4u * (m & 3);
-      float v[NB];
+        for (int ct = 0; ct < kOnce; ++ct) {
+          const int mt = c0 + ct;
+          f32x4 v;
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {
-        v[i] = 0.f;
-        for (int w = 0; w < wk; ++w)
-          v[i] += *(__attribute__((address_space(3))) float *)(smem + at + 1024u * (uint32_t)(i * waves + w));
-      }
-      const int64_t at_out = (int64_t)m * A.N + n;
-      if (A.splits > 1) {
+          for (int c = 0; c < 4; ++c) v[c] = ldexpf(acc[i][mt][c], unshift[mt][c]);
+          *(__attribute__((address_space(3))) f32x4 *)(smem + kRedOff + 16u * (uint32_t)(((i * kOnce + ct) * waves + wv) * 64 + lane)) = v;
+          acc[i][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+      __syncthreads();
+      for (int o = tid; o < wt * kOnce * 256; o += threads) {  // [tile][16-row tile][row][column]
+        const int ct = (o >> 8) % kOnce, ts = (o >> 8) / kOnce;
+        const int mr = (o >> 4) & 15, m = 16 * (c0 + ct) + mr;
+        const int n = ((b0 + j * blocks) * wt + ts) * 16 + (o & 15);
+        if (m >= M || n >= A.N) continue;
+        // row mr of column c is element mr % 4 of lane 16 (mr / 4) + c
+        const uint32_t at = kRedOff + 16u * (uint32_t)(ts * wk * 64 + (mr >> 2) * 16 + (o & 15)) + 4u * (mr & 3);
+        float v[NB];
 #pragma unroll
-        for (int i = 0; i < NB; ++i) A.partial[((int64_t)split * NB + i) * M * A.N + at_out] = v[i];
-      } else if constexpr (NB == 2) {
-        ((uint16_t *)A.out)[at_out] = f32_to_bf16(act_value<ACT>(v[0]) * v[1]);
-      } else {
-        ((float *)A.out)[at_out] = v[0];
+        for (int i = 0; i < NB; ++i) {
+          v[i] = 0.f;
+          for (int w = 0; w < wk; ++w)
+            v[i] += *(__attribute__((address_space(3))) float *)(smem + at + 1024u * (uint32_t)((i * kOnce + ct) * waves + w));
+        }
+        const int64_t at_out = (int64_t)m * A.N + n;
+        if (A.splits > 1) {
+#pragma unroll
+          for (int i = 0; i < NB; ++i) A.partial[((int64_t)split * NB + i) * M * A.N + at_out] = v[i];
+        } else if constexpr (NB == 2) {
+          ((uint16_t *)A.out)[at_out] = f32_to_bf16(act_value<ACT>(v[0]) * v[1]);
+        } else {
+          ((float *)A.out)[at_out] = v[0];
+        }
       }
     }
     ++j;
@@ -419,15 +569,16 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A) {
 // ---------------------------------------------------------------------------
 
 constexpr int kMidWaves = 8, kMidThreads = 64 * kMidWaves;
+constexpr int kMidRows = 64;  // of x a block
 
 // A block: 128 weight rows (of each matrix), a tile of 16 a wave; one chunk of
-// 16 MT rows of x; one split of K, in whole quads of groups.  The weights as
+// 64 rows of x; one split of K, in whole quads of groups.  The weights as
 // few_kernel has them; x comes in the same order and as f16 (f16_role), four
 // matrix steps at a time, through a ring of LDS slots that all waves read.
-template <int G, int NB, int MT, int ACT>
+template <int G, int NB, int ACT>
 __global__ __launch_bounds__(kMidThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void mid_kernel(const ProjArgs A) {
-  constexpr int T = G / 8, B = bytes_per_group(G), SQ = T / 4;  // SQ: stages of a quad
+  constexpr int MT = kMidRows / 16, T = G / 8, B = bytes_per_group(G), SQ = T / 4;  // SQ: stages of a quad
   typedef Lut<8> L;
   constexpr uint32_t kSlot = 4 * MT * 1024, kLoad = 16 * kMidThreads;
   constexpr int kD = kSlot / kLoad;      // loads of x a thread and stage
@@ -475,13 +626,31 @@ void mid_kernel(const ProjArgs A) {
 #pragma unroll
   for (int s = 0; s < kSlots - 1; ++s) request(q0 * SQ + s);
   L::build(smem, tid, kMidThreads);
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-
   f32x4 acc[NB][MT];
 #pragma unroll
   for (int i = 0; i < NB; ++i)
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[i][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto shift_rows = [&](int sign) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int64_t m = m0 + 16 * mt + 4 * q + c;
+        const int sh = m < A.M ? sign * A.shift[m] : 0;
+#pragma unroll
+        for (int i = 0; i < NB; ++i) acc[i][mt][c] = ldexpf(acc[i][mt][c], sh);
+      }
+  };
+  if constexpr (NB == 1) {
+    // the adapters' part while the first bytes are on their way, times
+    // 2^shift as the sums that follow; the splits share the adapters
+    if (A.adapters > 0 && n0 < A.N) {
+      add_adapters<false>(A, m0, n0, adapter_of(A, m0 + lane, lane < 16 * MT), A.splits, split, acc);
+      shift_rows(1);
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   const L lut(0, lane);
   uint32_t flags = 0;
   int get = 0;
@@ -535,20 +704,7 @@ void mid_kernel(const ProjArgs A) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may still write this block's LDS
   if ((flags & kBadFlag) && A.status) atomicOr(A.status, kDevInvalidByte);
 
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int64_t m = m0 + 16 * mt + 4 * q + c;
-      const int sh = m < A.M ? -A.shift[m] : 0;
-#pragma unroll
-      for (int i = 0; i < NB; ++i) acc[i][mt][c] = ldexpf(acc[i][mt][c], sh);
-    }
-  if constexpr (NB == 1) {
-    // the splits share the adapters
-    if (A.adapters > 0 && n0 < A.N)
-      add_adapters<false>(A, m0, n0, adapter_of(A, m0 + lane, lane < 16 * MT), A.splits, split, acc);
-  }
+  shift_rows(-1);
   if (n0 + l >= A.N) return;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt)
@@ -584,6 +740,39 @@ __global__ __launch_bounds__(256) void combine_kernel(const float *__restrict__ 
     else
       ((float *)out)[i] = v[0];
   }
+}
+
+// After few_kernel: y = the splits' partial sums in order (y itself where
+// there is one split) + the adapters' part.  A block: 16 columns, all rows;
+// its waves share the adapters, their sums added in wave order.
+constexpr int kExpandWaves = 8;
+template <int MT>
+__global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(const ProjArgs A) {
+  __shared__ __align__(16) float red[kExpandWaves * MT * 256];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n0 = (int)blockIdx.x * 16;
+  // an output a thread: [16-row tile][row][column]
+  const int o = tid, mr = (o >> 4) & 15, m = 16 * (o >> 8) + mr, n = n0 + (o & 15);
+  const bool mine = o < MT * 256 && m < A.M && n < A.N;
+  float v = 0.f;
+  if (mine) {
+    const float *p = A.splits > 1 ? A.partial : (const float *)A.out;
+    const int64_t mn = A.M * A.N;
+#pragma unroll 4
+    for (int s = 0; s < A.splits; ++s) v += p[s * mn + (int64_t)m * A.N + n];
+  }
+  f32x4 acc[1][MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) acc[0][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
+  add_adapters<false>(A, 0, n0, adapter_of(A, lane, lane < 16 * MT), kExpandWaves, wv, acc);
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) *(f32x4 *)(red + 4 * ((wv * MT + mt) * 64 + lane)) = acc[0][mt];
+  __syncthreads();
+  if (!mine) return;
+  const int at = ((o >> 8) * 64 + (mr >> 2) * 16 + (o & 15)) * 4 + (mr & 3);
+  for (int w = 0; w < kExpandWaves; ++w) v += red[w * MT * 256 + at];
+  ((float *)A.out)[(int64_t)m * A.N + n] = v;
 }
 
 // ---------------------------------------------------------------------------
@@ -827,178 +1016,69 @@ void wide_kernel(const ProjArgs A) {
 }
 
 // ---------------------------------------------------------------------------
-// before the product: x in order, and t
+// before the product, in a launch of its own
 // ---------------------------------------------------------------------------
-
-constexpr int kPreThreads = 1024, kPreWaves = 16;
-constexpr int kRowLds = 16384;    // elements of a row of x in LDS
-constexpr int kShrinkTile = 256;  // rows among which equal adapters are gathered
-constexpr int kShrinkRanks = 4;   // tiles of 16 ranks that share a read of x
-
-struct PreArgs {
-  const uint16_t *x, *a;
-  const int32_t *ids;
-  const float *scaling;
-  uint16_t *xo;     // fragments or f16 rows
-  int32_t *shift;   // f16 rows
-  float *t;
-  int64_t M;
-  int K, adapters, R, mt;
-  // shrink: blocks, units a tile of rows, tiles of 16 RT ranks, splits of K
-  int shrink_blocks, units, rtiles, tsplits;
-  int32_t *status;
-};
-
-// t of one unit: up to 16 rows of one adapter, 16 RT ranks.  The rows of a tile
-// that name the same adapter are numbered in order and cut into units of 16,
-// so rows in any order share the adapter's A.  One split of K; its waves
-// share the split, and their sums are added in order.
-template <int RT>
-__device__ __forceinline__ void shrink_role(const PreArgs &A, int64_t blk, unsigned char *smem_raw) {
-  int *ids = (int *)smem_raw;                       // [256]
-  int *rows = ids + kShrinkTile;                    // [16]
-  int *info = rows + 16;                            // adapter, leader's rank
-  int *counts = info + 4;                           // [16] leaders of each wave
-  float *red = (float *)(counts + 28);              // [16][64][4]
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, l = lane & 15, q = lane >> 4;
-  const int split = (int)(blk % A.tsplits);
-  blk /= A.tsplits;
-  const int rt = (int)(blk % A.rtiles), unit = (int)(blk / A.rtiles % A.units);
-  const int64_t m0 = blk / A.rtiles / A.units * kShrinkTile;
-  const int nrows = (int)min((int64_t)kShrinkTile, A.M - m0);
-  int id = -1;
-  if (tid < nrows) {
-    id = A.ids[m0 + tid];
-    if (id < -1 || id >= A.adapters) {
-      if (unit == 0 && rt == 0 && split == 0 && A.status) atomicOr(A.status, kDevBadAdapter);
-      id = -1;
-    }
-  }
-  if (tid < kShrinkTile) ids[tid] = id;
-  if (tid < 16) rows[tid] = -1;
-  if (tid == 0) info[0] = -1;
-  __syncthreads();
-  int rank = 0;  // among the rows of this adapter
-  if (id >= 0)
-    for (int j = 0; j < tid; ++j) rank += ids[j] == id;
-  const bool leads = id >= 0 && rank % 16 == 0;
-  const uint64_t mask = __ballot(leads);
-  if (lane == 0) counts[wv] = __popcll(mask);
-  __syncthreads();
-  int before = __popcll(mask & ((1ull << lane) - 1));
-  for (int w = 0; w < wv; ++w) before += counts[w];
-  if (leads && before == unit) {
-    info[0] = id;
-    info[1] = rank;
-  }
-  __syncthreads();
-  const int a = info[0];
-  if (a < 0) return;  // fewer units than this
-  if (id == a && rank / 16 == info[1] / 16) rows[rank % 16] = tid;
-  __syncthreads();
-
-  // columns: the unit's rows (the first one in place of absent ones); rows:
-  // ranks 16 rt + l
-  const int own = rows[l], mr = own < 0 ? rows[0] : own;
-  const uint16_t *xr = A.x + (m0 + mr) * A.K + 8 * q;
-  const uint16_t *ar[RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-    ar[i] = A.a + ((int64_t)a * A.R + min(16 * (RT * rt + i) + l, A.R - 1)) * A.K + 8 * q;
-  f32x4 acc[RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int steps = A.K / 32;
-  const int s0 = (int)((int64_t)steps * split / A.tsplits), s1 = (int)((int64_t)steps * (split + 1) / A.tsplits);
-  constexpr int kAhead = RT == 1 ? 8 : 4;  // steps requested together
-  for (int s = s0 + wv; s < s1; s += kPreWaves * kAhead) {
-    // steps past the end read the last one and add nothing
-    bf16x8 av[kAhead][RT], xv[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int sj = min(s + kPreWaves * j, steps - 1);
-      xv[j] = *(const bf16x8 *)(xr + 32 * sj);
-#pragma unroll
-      for (int i = 0; i < RT; ++i) av[j][i] = *(const bf16x8 *)(ar[i] + 32 * sj);
-    }
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (s + kPreWaves * j < s1)
-#pragma unroll
-        for (int i = 0; i < RT; ++i) acc[i] = mfma32<false>(av[j][i], xv[j], acc[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    *(f32x4 *)(red + 4 * tid) = acc[i];
-    __syncthreads();
-    if (tid < 256) {
-      float sum = 0.f;
-      for (int w = 0; w < kPreWaves; ++w) sum += red[w * 256 + tid];
-      const int ol = tid >> 2, rr = 16 * (RT * rt + i) + 4 * (ol >> 4) + (tid & 3), row = rows[ol & 15];
-      if (row >= 0 && rr < A.R) A.t[((int64_t)split * A.M + m0 + row) * A.R + rr] = A.scaling[a] * sum;
-    }
-    __syncthreads();
-  }
-}
 
 // Row m of x as f16 times 2^shift[m], for mid_kernel in its fragments
 // [chunk][quad][step][16-row tile][lane][8] (rows past M and groups past the
 // last are zeros), for wide_kernel in rows, in the order of its codes.
-// A row passes through LDS, from which its elements are picked.
+// Rows pass through LDS, from which their elements are picked; a block takes
+// `rpb` rows at a time (1, 2 or 4, so that they fit), threads / rpb each.
 template <int G, bool FRAG>
-__device__ __forceinline__ void f16_role(const PreArgs &A, int64_t m, unsigned char *smem_raw) {
+__device__ __forceinline__ void f16_role(const PreArgs &A, int64_t first, int64_t rows_in_all,
+                                         unsigned char *smem_raw) {
   uint32_t *tops = (uint32_t *)smem_raw;             // [16]
-  uint16_t *row = (uint16_t *)(smem_raw + 64);       // [kRowLds]
-  const int tid = threadIdx.x;
+  const int threads = kPreThreads / A.rpb, room = kRowLds / A.rpb;
+  const int tid = threadIdx.x % threads, part = threadIdx.x / threads;
+  uint16_t *row = (uint16_t *)(smem_raw + 64) + part * room;
+  const int64_t m = first + part;
   const uint16_t *xr = A.x + m * A.K;
-  const bool in = !FRAG || m < A.M;
-  int shift = 0;
-  __syncthreads();  // the row before has been read
-  if (in) {
-    uint32_t top = 0;
+  const bool in = m < A.M;
+  __syncthreads();  // the rows before have been read
+  uint32_t top = 0;
+  if (in)
 #pragma unroll 2
-    for (int k = 8 * tid; k < A.K; k += 8 * kPreThreads) {
+    for (int k = 8 * tid; k < A.K; k += 8 * threads) {
       top = top_of(top, xr + k);
-      if (k < kRowLds) *(u32x4 *)(row + k) = *(const u32x4 *)(xr + k);
+      if (k < room) *(u32x4 *)(row + k) = *(const u32x4 *)(xr + k);
     }
-    top = wave_max(top);
-    if ((tid & 63) == 0) tops[tid >> 6] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kPreWaves; ++w) top = max(top, tops[w]);
-    shift = f16_shift(top);
-    if (tid == 0) A.shift[m] = shift;
-  }
+  top = wave_max(top);
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  __syncthreads();
+  for (int w = 0; w < threads / 64; ++w) top = max(top, tops[part * (threads / 64) + w]);
+  const int shift = f16_shift(top);
+  if (in && tid == 0) A.shift[m] = shift;
   constexpr int T = G / 8;
-  const int nG = A.K / G, nQ = (nG + 3) / 4, rows = 16 * A.mt;
+  const int nG = A.K / G, nQ = (nG + 3) / 4, rows = kMidRows;
   const int64_t chunk = FRAG ? m / rows : 0;
   const int r = FRAG ? (int)(m - chunk * rows) : 0;
-  for (int k0 = 0; k0 < A.K; k0 += kRowLds) {  // pieces of whole quads of groups
-    const int len = min(A.K - k0, kRowLds);
-    if (k0 > 0 && in) {
+  for (int k0 = 0; k0 < A.K; k0 += room) {  // pieces of whole quads of groups; one if rpb > 1
+    const int len = min(A.K - k0, room);
+    if (k0 > 0) {
       __syncthreads();
-      for (int k = 8 * tid; k < len; k += 8 * kPreThreads) *(u32x4 *)(row + k) = *(const u32x4 *)(xr + k0 + k);
+      if (in)
+        for (int k = 8 * tid; k < len; k += 8 * threads) *(u32x4 *)(row + k) = *(const u32x4 *)(xr + k0 + k);
       __syncthreads();
     }
     if constexpr (FRAG) {
       const int g0 = k0 / G, quads = (len / G + 3) / 4;
-      for (int e = tid; e < quads * 4 * T; e += kPreThreads) {
+      for (int e = tid; m < rows_in_all && e < quads * 4 * T; e += threads) {
         const int g = e / T, t = e % T;
         const bool has = in && g0 + g < nG;
         _Float16 f[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           f[i] = f16_of(has ? row[g * G + group_source<G>(8 * t + i)] : 0, shift);
-        *(u32x4 *)(A.xo + (((chunk * nQ + ((g0 + g) >> 2)) * T + t) * A.mt + (r >> 4)) * 512 +
+        *(u32x4 *)(A.xo + (((chunk * nQ + ((g0 + g) >> 2)) * T + t) * (kMidRows / 16) + (r >> 4)) * 512 +
                    ((g & 3) * 16 + (r & 15)) * 8) = *(u32x4 *)f;
       }
     } else {
       uint16_t *o = A.xo + m * A.K + k0;
-      for (int e = tid; e < len / 16; e += kPreThreads) {
-        const int g = e / (G / 16), part = e % (G / 16);
+      for (int e = tid; in && e < len / 16; e += threads) {
+        const int g = e / (G / 16), part16 = e % (G / 16);
         _Float16 f[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) f[j] = f16_of(row[g * G + eighth_source<G>(part, j)], shift);
+        for (int j = 0; j < 16; ++j) f[j] = f16_of(row[g * G + eighth_source<G>(part16, j)], shift);
         *(u32x4 *)(o + 16 * e) = *(u32x4 *)f;
         *(u32x4 *)(o + 16 * e + 8) = *(u32x4 *)(f + 8);
       }
@@ -1007,27 +1087,22 @@ __device__ __forceinline__ void f16_role(const PreArgs &A, int64_t m, unsigned c
 }
 
 constexpr int64_t kMaxPreBlocks = 1 << 16;  // of a role; each strides over its work
-constexpr int kPreNone = 0, kPreFrag = 1, kPreRows = 2;
+constexpr int kPreFrag = 1, kPreRows = 2;
 
 template <int G, int MODE, int RT>
 __global__ __launch_bounds__(kPreThreads) void pre_kernel(const PreArgs A) {
   constexpr int kShrinkLds = 4 * (kShrinkTile + 48) + 16 * kPreThreads;
-  constexpr int kRowBytes = MODE == kPreNone ? 0 : 64 + 2 * kRowLds;
+  constexpr int kRowBytes = 64 + 2 * kRowLds;
   __shared__ __align__(16) unsigned char smem[kShrinkLds > kRowBytes ? kShrinkLds : kRowBytes];
   if ((int)blockIdx.x < A.shrink_blocks) {
-    const int64_t work = ceil_div(A.M, kShrinkTile) * A.units * A.rtiles * A.tsplits;
-    for (int64_t w = blockIdx.x; w < work; w += A.shrink_blocks) {
-      shrink_role<RT>(A, w, smem);
-      __syncthreads();
-    }
+    shrink_all<RT>(A, (int)blockIdx.x, smem);
     return;
   }
   const int64_t blk = (int64_t)blockIdx.x - A.shrink_blocks;
   const int64_t blocks = (int64_t)gridDim.x - A.shrink_blocks;
-  if constexpr (MODE != kPreNone) {
-    const int64_t rows = MODE == kPreFrag ? ceil_div(A.M, 16 * A.mt) * (16 * A.mt) : A.M;
-    for (int64_t m = blk; m < rows; m += blocks) f16_role<G, MODE == kPreFrag>(A, m, smem);
-  }
+  const int64_t rows = MODE == kPreFrag ? ceil_div(A.M, kMidRows) * kMidRows : A.M;
+  for (int64_t m = blk * A.rpb; m < rows; m += blocks * A.rpb)
+    f16_role<G, MODE == kPreFrag>(A, m, rows, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -1038,8 +1113,10 @@ int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
 
 constexpr int kFew = 0, kMid = 1, kWide = 2;
 
+int shrink_tiles(int R) { return R > 16 ? kShrinkRanks : 1; }
+
 struct Plan {
-  int kind, wk, wt, mt, splits, tsplits;
+  int kind, wk, wt, splits, tsplits;
   int64_t blocks, chunks;
   int64_t x, shift, t, partial;  // workspace bytes, each a multiple of 16, in this order
   int64_t total() const { return x + shift + t + partial; }
@@ -1075,14 +1152,13 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
     p.shift = round16(M * 4);
   } else {
     p.kind = kMid;
-    p.mt = M <= 32 ? 2 : 4;
-    p.chunks = ceil_div(M, 16 * p.mt);
+    p.chunks = ceil_div(M, kMidRows);
     const int64_t blocks = ceil_div(N, 128) * p.chunks;
     // two blocks a CU; K is split while every block keeps two quads of groups
     const int64_t quads = ceil_div(nG, 4);
     while (blocks * p.splits < 384 && quads / (2 * p.splits) >= 2) p.splits *= 2;
     p.blocks = blocks * p.splits;
-    p.x = p.chunks * 16 * p.mt * quads * 4 * G * 2;
+    p.x = p.chunks * kMidRows * quads * 4 * G * 2;
     p.shift = round16(M * 4);
   }
   if (p.splits > 1) p.partial = round16((int64_t)p.splits * NB * M * N * 4);
@@ -1093,17 +1169,29 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
   return p;
 }
 
+template <int G, int NB, int MT, int ACT>
+void launch_few(const Plan &p, const ProjArgs &a, const PreArgs &pre, hipStream_t stream) {
+  if constexpr (NB == 2) {
+    hipLaunchKernelGGL((few_kernel<G, NB, MT, ACT, 0>), dim3((unsigned)p.blocks),
+                       dim3(64 * std::max(kFewSetUp, p.wk * p.wt)), 0, stream, a, pre);
+  } else {
+    const dim3 grid((unsigned)(p.blocks + pre.shrink_blocks));
+    auto kernel = shrink_tiles(a.R) == 1 ? few_kernel<G, NB, MT, ACT, 1> : few_kernel<G, NB, MT, ACT, kShrinkRanks>;
+    hipLaunchKernelGGL(kernel, grid, dim3(kPreThreads), 0, stream, a, pre);
+    hipLaunchKernelGGL(expand_kernel<MT>, dim3((unsigned)ceil_div(a.N, 16)), dim3(64 * kExpandWaves), 0,
+                       stream, a);
+  }
+}
+
 template <int G, int NB, int ACT>
-void launch_product(const Plan &p, const ProjArgs &a, hipStream_t stream) {
+void launch_product(const Plan &p, const ProjArgs &a, const PreArgs &pre, hipStream_t stream) {
   const dim3 grid((unsigned)p.blocks);
   if (p.kind == kFew)
-    hipLaunchKernelGGL((few_kernel<G, NB, ACT>), grid, dim3(64 * std::max(kFewSetUp, p.wk * p.wt)), 0, stream, a);
+    a.M <= 16 ? launch_few<G, NB, 1, ACT>(p, a, pre, stream) : launch_few<G, NB, 2, ACT>(p, a, pre, stream);
   else if (p.kind == kWide)
     hipLaunchKernelGGL((wide_kernel<G, NB, ACT>), grid, dim3(kWideThreads), 0, stream, a);
-  else if (p.mt == 2)
-    hipLaunchKernelGGL((mid_kernel<G, NB, 2, ACT>), grid, dim3(kMidThreads), 0, stream, a);
   else
-    hipLaunchKernelGGL((mid_kernel<G, NB, 4, ACT>), grid, dim3(kMidThreads), 0, stream, a);
+    hipLaunchKernelGGL((mid_kernel<G, NB, ACT>), grid, dim3(kMidThreads), 0, stream, a);
 }
 
 // All launches of a call; `a` and `pre` hold the caller's arguments.
@@ -1124,35 +1212,34 @@ void launch_proj(const Plan &p, ProjArgs a, PreArgs pre, void *workspace, hipStr
   a.chunks = (int)p.chunks;
   a.tp = (int)ceil_div(NB * (int64_t)a.N, kWideP);
   a.tq = (int)ceil_div(a.M, kWideQ);
-  pre.M = a.M, pre.K = a.K, pre.mt = p.mt, pre.status = a.status;
+  pre.M = a.M, pre.K = a.K, pre.status = a.status;
   pre.ids = a.ids, pre.adapters = a.adapters, pre.R = a.R;
   if (NB == 1) {
     const int64_t tiles = ceil_div(a.M, kShrinkTile);
     const int64_t rows = std::min<int64_t>(a.M, kShrinkTile);
     // units of a tile: one for each 16 rows and one more for each adapter
     pre.units = (int)std::min(rows, ceil_div(rows, 16) + std::min<int64_t>(rows, a.adapters));
-    pre.rtiles = (int)ceil_div(a.R, a.R > 16 ? 16 * kShrinkRanks : 16);
+    pre.rtiles = (int)ceil_div(a.R, 16 * shrink_tiles(a.R));
     if (a.adapters == 0) pre.units = pre.rtiles = pre.tsplits = 1;  // the ids are still checked
     pre.shrink_blocks = (int)std::min(kMaxPreBlocks, tiles * pre.units * pre.rtiles * pre.tsplits);
   }
   const int64_t sb = pre.shrink_blocks;
+  pre.rpb = a.K <= kRowLds / 4 ? 4 : a.K <= kRowLds / 2 ? 2 : 1;
   auto prepare = [&](auto kernel, int64_t rows) {
-    const dim3 grid((unsigned)(sb + std::min(kMaxPreBlocks, rows)));
+    const dim3 grid((unsigned)(sb + std::min(kMaxPreBlocks, ceil_div(rows, pre.rpb))));
     hipLaunchKernelGGL(kernel, grid, dim3(kPreThreads), 0, stream, pre);
   };
-  const bool ranks = NB == 1 && a.R > 16;
+  const bool ranks = NB == 1 && shrink_tiles(a.R) > 1;
   if (p.kind == kWide) {
     ranks ? prepare(pre_kernel<G, kPreRows, kShrinkRanks>, a.M) : prepare(pre_kernel<G, kPreRows, 1>, a.M);
     a.x = pre.xo;
   } else if (p.kind == kMid) {
-    const int64_t rows = p.chunks * 16 * p.mt;
+    const int64_t rows = p.chunks * kMidRows;
     ranks ? prepare(pre_kernel<G, kPreFrag, kShrinkRanks>, rows) : prepare(pre_kernel<G, kPreFrag, 1>, rows);
     a.x = pre.xo;
-  } else if (sb) {
-    ranks ? prepare(pre_kernel<G, kPreNone, kShrinkRanks>, 0) : prepare(pre_kernel<G, kPreNone, 1>, 0);
   }
-  launch_product<G, NB, ACT>(p, a, stream);
-  if (p.splits > 1) {
+  launch_product<G, NB, ACT>(p, a, pre, stream);
+  if (p.splits > 1 && !(p.kind == kFew && NB == 1)) {
     const int64_t mn = a.M * a.N;
     hipLaunchKernelGGL((combine_kernel<NB, ACT>), dim3((unsigned)std::min<int64_t>(4096, ceil_div(mn, 256))),
                        dim3(256), 0, stream, a.partial, p.splits, mn, a.out);
