@@ -802,26 +802,77 @@ def w4a16_gemv_grouped(xs, packeds, scales_list, biases_list, Ns, Ks, G: int, ou
 # ---------------------------------------------------------------------------
 
 I32 = (torch.int32,)
+F16U = F16 + (torch.uint16,)
 
 
 def _act(act) -> int:
-    if act not in ACTS:
+    a = ACTS.get(act) if isinstance(act, str) else None
+    if a is None:
         raise TQError("act must be one of %s, not %r" % (sorted(ACTS), act))
-    return ACTS[act]
+    return a
 
 
 def _shaped(t, name: str, shape, dtypes, device):
-    """An input of exactly `shape`, as _dev."""
+    """The address of an input of exactly `shape`, checked as _dev does.  One
+    expression on the way of a good call: small ones take no longer on the GPU
+    than their checks on the host."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
+            and t.is_cuda and t.device == device):
+        return t.data_ptr()
     _dev(t, name, dtypes, None, device)
-    if tuple(t.shape) != tuple(shape):
-        raise TQError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    return t
+    raise TQError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+
+
+def _pair(packed, scales, nbytes: int, nscales: int, device, what: str):
+    """The addresses of packed bytes and their scales, of these sizes."""
+    if (isinstance(packed, torch.Tensor) and isinstance(scales, torch.Tensor)
+            and packed.dtype is torch.uint8 and scales.dtype in F16U and packed.numel() == nbytes
+            and scales.numel() == nscales and packed.is_contiguous() and scales.is_contiguous()
+            and packed.is_cuda and scales.is_cuda and packed.device == device
+            and scales.device == device):
+        return packed.data_ptr(), scales.data_ptr()
+    _dev(packed, "packed", U8, None, device)
+    _dev(scales, "scales", F16U, None, device)
+    raise TQError("%s: packed/scales sizes (%d, %d), expected (%d, %d)"
+                  % (what, packed.numel(), scales.numel(), nbytes, nscales))
+
+
+def _activations(x, K: int):
+    """(address, rows, device) of x [M,K] bf16."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] != K:
+        _dev(x, "x", BF16, 2)
+        raise TQError("x has K=%d, expected %d" % (x.shape[1], K))
+    M, dev = x.shape[0], x.device
+    return _shaped(x, "x", (M, K), BF16, dev), M, dev
+
+
+def _stream_of(device) -> int:
+    """The raw current stream of `device`."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _packed_sizes(N: int, K: int, G: int):
+    """Packed bytes and scales of an [N,K] matrix; the library refuses a K
+    that G does not divide."""
+    if G not in (64, 128) or N < 1 or K < 1 or K % G:
+        raise TQError("bad sizes N=%d K=%d G=%d" % (N, K, G))
+    n = N * (K // G)
+    return n * ((G + 4) // 5), n
+
+
+def _result(t, name: str, shape, dtype, dtypes, device):
+    """A call's output, as _out; (tensor, address)."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+    else:
+        _out(t, name, shape, dtype, dtypes, device)
+    return t, t.data_ptr()
 
 
 def _workspace(ws, need: int, device):
-    """(address, bytes) of a call's workspace: the caller's uint8 tensor, or
-    one allocated here.  The tensor is returned too, to keep it alive until
-    the call is enqueued (torch's allocator reuses it in stream order)."""
+    """(tensor, address, bytes) of a call's workspace: the caller's uint8
+    tensor, or one allocated here.  The tensor is returned to keep it alive
+    until the call is enqueued (torch's allocator reuses it in stream order)."""
     if ws is None:
         if need == 0:
             return None, 0, 0
@@ -844,18 +895,18 @@ def glu(x, gate, up, N: int, K: int, G: int, act="silu", status=None, out=None, 
     h bf16 [M,N] = act(x Wg^T) * (x Wu^T).  act is "silu" or "gelu" (tanh
     form).  `workspace`, if given, is a uint8 tensor of at least
     glu_workspace(M, N, K, G) bytes that no other call in flight uses."""
-    _dev(x, "x", BF16, 2)
-    dev, M = x.device, x.shape[0]
-    if x.shape[1] != K:
-        raise TQError("x has K=%d, expected %d" % (x.shape[1], K))
+    xp, M, dev = _activations(x, K)
     a = _act(act)
-    (gp, gs), (up_, us) = gate, up
-    _check_packed(gp, gs, N, K, G, dev, "tq_glu gate")
-    _check_packed(up_, us, N, K, G, dev, "tq_glu up")
-    h = _out(out, "h", (M, N), torch.bfloat16, BF16, dev)
-    ws, wp, wn = _workspace(workspace, glu_workspace(M, N, K, G), dev)
-    _rc(lib().tq_glu(x.data_ptr(), gp.data_ptr(), gs.data_ptr(), up_.data_ptr(), us.data_ptr(), M,
-                     N, K, G, a, h.data_ptr(), wp, wn, _st(status, dev), _stream()), "tq_glu")
+    nb, ns = _packed_sizes(N, K, G)
+    gp, gs = _pair(*gate, nb, ns, dev, "tq_glu gate")
+    up_, us = _pair(*up, nb, ns, dev, "tq_glu up")
+    h, hp = _result(out, "h", (M, N), torch.bfloat16, BF16, dev)
+    l = lib()
+    ws, wp, wn = _workspace(workspace, l.tq_glu_workspace(M, N, K, G), dev)
+    rc = l.tq_glu(xp, gp, gs, up_, us, M, N, K, G, a, hp, wp, wn,
+                  _st(status, dev) if status is not None else 0, _stream_of(dev))
+    if rc:
+        _rc(rc, "tq_glu")
     return h
 
 
@@ -873,33 +924,36 @@ def lora_matmul(x, packed, scales, ids, a, b, scaling, N: int, K: int, G: int, s
     y fp32 [M,N] = x W_hat^T + scaling[id] * (x a[id]^T) b[id]^T.
     R is a multiple of 8 up to 256.  `workspace` as for glu, of
     lora_workspace(M, N, K, G, R) bytes."""
-    _dev(x, "x", BF16, 2)
-    dev, M = x.device, x.shape[0]
-    if x.shape[1] != K:
-        raise TQError("x has K=%d, expected %d" % (x.shape[1], K))
-    _check_packed(packed, scales, N, K, G, dev, "tq_lora_matmul")
-    _shaped(ids, "ids", (M,), I32, dev)
-    _dev(a, "a", BF16, 3, dev)
+    xp, M, dev = _activations(x, K)
+    nb, ns = _packed_sizes(N, K, G)
+    wp_, sp = _pair(packed, scales, nb, ns, dev, "tq_lora_matmul")
+    ip = _shaped(ids, "ids", (M,), I32, dev)
+    if not isinstance(a, torch.Tensor) or a.dim() != 3:
+        raise TQError("a must be a 3-D tensor")
     n, R = a.shape[0], a.shape[1]
-    _shaped(a, "a", (n, R, K), BF16, dev)
-    _shaped(b, "b", (n, N, R), BF16, dev)
-    _shaped(scaling, "scaling", (n,), F32, dev)
-    y = _out(out, "y", (M, N), torch.float32, F32, dev)
-    ws, wp, wn = _workspace(workspace, lora_workspace(M, N, K, G, R), dev)
-    _rc(lib().tq_lora_matmul(x.data_ptr(), packed.data_ptr(), scales.data_ptr(), ids.data_ptr(),
-                             a.data_ptr(), b.data_ptr(), scaling.data_ptr(), M, N, K, G, n, R,
-                             y.data_ptr(), wp, wn, _st(status, dev), _stream()), "tq_lora_matmul")
+    ap = _shaped(a, "a", (n, R, K), BF16, dev)
+    bp = _shaped(b, "b", (n, N, R), BF16, dev)
+    cp = _shaped(scaling, "scaling", (n,), F32, dev)
+    y, yp = _result(out, "y", (M, N), torch.float32, F32, dev)
+    l = lib()
+    ws, wp, wn = _workspace(workspace, l.tq_lora_workspace(M, N, K, G, R), dev)
+    rc = l.tq_lora_matmul(xp, wp_, sp, ip, ap, bp, cp, M, N, K, G, n, R, yp, wp, wn,
+                          _st(status, dev) if status is not None else 0, _stream_of(dev))
+    if rc:
+        _rc(rc, "tq_lora_matmul")
     return y
 
 
 def _train_inputs(x, wg, wu):
-    _dev(x, "x", BF16, 2)
-    _dev(wg, "wg", BF16, 2, x.device)
+    """(addresses of x, wg and wu; M, N, K; device)."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(wg, torch.Tensor) or wg.dim() != 2:
+        _dev(x, "x", BF16, 2)
+        _dev(wg, "wg", BF16, 2, x.device)
+        raise TQError("x and wg must be 2-D tensors")
     M, K = x.shape
-    N = wg.shape[0]
-    _shaped(wg, "wg", (N, K), BF16, x.device)
-    _shaped(wu, "wu", (N, K), BF16, x.device)
-    return x.device, M, N, K
+    N, dev = wg.shape[0], x.device
+    return (_shaped(x, "x", (M, K), BF16, dev), _shaped(wg, "wg", (N, K), BF16, dev),
+            _shaped(wu, "wu", (N, K), BF16, dev), M, N, K, dev)
 
 
 def glu_forward(x, wg, wu, act="silu", save: bool = True, out=None):
@@ -907,16 +961,17 @@ def glu_forward(x, wg, wu, act="silu", save: bool = True, out=None):
     [N,K] bf16 -> (h, g, u) bf16 [M,N] with h = act(g) u, g = x wg^T,
     u = x wu^T; with save=False h alone (g and u are never written).
     `out`, if given, is (h, g, u) or, with save=False, h.  K % 64 == 0."""
-    dev, M, N, K = _train_inputs(x, wg, wu)
+    xp, gp, up, M, N, K, dev = _train_inputs(x, wg, wu)
     a = _act(act)
     h, g, u = (None, None, None) if out is None else out if save else (out, None, None)
-    h = _out(h, "h", (M, N), torch.bfloat16, BF16, dev)
+    h, hp = _result(h, "h", (M, N), torch.bfloat16, BF16, dev)
+    g_, u_ = 0, 0
     if save:
-        g = _out(g, "g", (M, N), torch.bfloat16, BF16, dev)
-        u = _out(u, "u", (M, N), torch.bfloat16, BF16, dev)
-    _rc(lib().tq_glu_forward(x.data_ptr(), wg.data_ptr(), wu.data_ptr(), M, N, K, a, h.data_ptr(),
-                             g.data_ptr() if save else 0, u.data_ptr() if save else 0, _stream()),
-        "tq_glu_forward")
+        g, g_ = _result(g, "g", (M, N), torch.bfloat16, BF16, dev)
+        u, u_ = _result(u, "u", (M, N), torch.bfloat16, BF16, dev)
+    rc = lib().tq_glu_forward(xp, gp, up, M, N, K, a, hp, g_, u_, _stream_of(dev))
+    if rc:
+        _rc(rc, "tq_glu_forward")
     return (h, g, u) if save else h
 
 
@@ -929,19 +984,19 @@ def glu_backward(dh, x, wg, wu, g, u, act="silu", out=None, workspace=None):
     """Gradients of glu_forward: dh, g, u [M,N] bf16 -> (dx [M,K], dwg [N,K],
     dwu [N,K]) bf16.  `out`, if given, is that triple; `workspace` as for glu,
     of glu_backward_workspace(M, N, K) bytes."""
-    dev, M, N, K = _train_inputs(x, wg, wu)
+    xp, wgp, wup, M, N, K, dev = _train_inputs(x, wg, wu)
     a = _act(act)
-    for t, name in ((dh, "dh"), (g, "g"), (u, "u")):
-        _shaped(t, name, (M, N), BF16, dev)
+    dhp = _shaped(dh, "dh", (M, N), BF16, dev)
+    gp, up = _shaped(g, "g", (M, N), BF16, dev), _shaped(u, "u", (M, N), BF16, dev)
     dx, dwg, dwu = (None, None, None) if out is None else out
-    dx = _out(dx, "dx", (M, K), torch.bfloat16, BF16, dev)
-    dwg = _out(dwg, "dwg", (N, K), torch.bfloat16, BF16, dev)
-    dwu = _out(dwu, "dwu", (N, K), torch.bfloat16, BF16, dev)
-    ws, wp, wn = _workspace(workspace, glu_backward_workspace(M, N, K), dev)
-    _rc(lib().tq_glu_backward(dh.data_ptr(), x.data_ptr(), wg.data_ptr(), wu.data_ptr(),
-                              g.data_ptr(), u.data_ptr(), M, N, K, a, dx.data_ptr(),
-                              dwg.data_ptr(), dwu.data_ptr(), wp, wn, _stream()),
-        "tq_glu_backward")
+    dx, dxp = _result(dx, "dx", (M, K), torch.bfloat16, BF16, dev)
+    dwg, dgp = _result(dwg, "dwg", (N, K), torch.bfloat16, BF16, dev)
+    dwu, dup = _result(dwu, "dwu", (N, K), torch.bfloat16, BF16, dev)
+    l = lib()
+    ws, wp, wn = _workspace(workspace, l.tq_glu_backward_workspace(M, N, K), dev)
+    rc = l.tq_glu_backward(dhp, xp, wgp, wup, gp, up, M, N, K, a, dxp, dgp, dup, wp, wn, _stream_of(dev))
+    if rc:
+        _rc(rc, "tq_glu_backward")
     return dx, dwg, dwu
 
 

@@ -318,72 +318,89 @@ constexpr int kFewWaves = 16;          // most waves of a block
 constexpr int kFewSetUp = 8;           // least: they share the table and x
 constexpr uint32_t kFewX = 64 << 10;   // LDS for a block's slice of x
 
-// The bytes and scale of one group.
-template <int G>
+// Fours of units a wave keeps requested: what 128 registers a lane leave
+// room for.
+constexpr int few_ahead(int NB, int MT) { return NB == 1 ? 4 : MT == 1 ? 3 : 2; }
+
+// Consecutive bytes of a row and their group's scale, or two groups' scales.
+template <int BYTES>
 struct Raw {
-  GroupBytes<G> w;
+  Bytes<BYTES> w;
   uint32_t scale;
 };
 
 // A block: one split of K, and tiles of 16 weight rows (of each matrix) one
-// set after another, wt tiles a set; wk waves share a tile's groups, four at
-// a time: lane (l, q) decodes group q of the four of row l, so that its bytes
-// are two wide loads and the four lanes of a row read 104 neighbouring ones.
-// (With each group dealt to four lanes instead, three small loads each, the
-// address units took four times as long as the bytes.)  Scales are multiplied
-// into the codes, since a lane's sums then run over all groups.
+// set after another, wt tiles a set; wk waves share a tile.  A unit is 128
+// codes, a group or (G = 64) two; a wave works on four units of the 16 rows at
+// a time, lane (l, q) on unit q of row l, so that its bytes are two wide loads
+// and the four lanes of a row read 104 neighbouring ones.  (With each group
+// dealt to four lanes instead, three small loads each, the address units took
+// four times as long as the bytes; with 13-byte groups singly, twice.)  Where
+// a row has an odd number of 64-groups, its last unit is the last two groups,
+// the first of them with scale 0.  Scales are multiplied into the codes, since
+// a lane's sums run over all groups.
 // x [M,K] (M <= 16 MT) of the split, as f16 times a power of two for each row,
 // is put in order once, in LDS; it is the row operand of the matrix cores and W
 // the column operand.
-// A wave requests four groups while it works on the four before, across the
-// ends of tiles.  LDS: 64 KB table, 64 KB x, up to 32 KB for the sums of the
+// A wave keeps few_ahead fours of units requested, across the ends of tiles,
+// from before the table is built: the bytes are on their way while x is put in
+// order.  LDS: 64 KB table, 64 KB x, up to 32 KB for the sums of the
 // waves.
-// lora: the projection alone; the blocks past the product's make t meanwhile
-// (RT as in shrink_role, 0 for none), and expand_kernel adds the adapters.
+// lora: the projection alone; the first blocks make t meanwhile (RT as in
+// shrink_role, 0 for none), and expand_kernel adds the adapters.
 template <int G, int NB, int MT, int ACT, int RT>
 __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, const PreArgs P) {
-  constexpr int T = G / 8, B = bytes_per_group(G);  // T: matrix steps of a group
+  constexpr int T = 16, B = bytes_per_group(G), GU = 128 / G;  // matrix steps and groups of a unit
   typedef Lut<32> L;
   constexpr uint32_t kXOff = L::kBytes, kRedOff = kXOff + kFewX;
   __shared__ __align__(16) unsigned char smem_raw[L::kBytes + kFewX + kFewWaves * 2048];
   const int work_blocks = (int)gridDim.x - P.shrink_blocks;
-  if constexpr (RT > 0)
-    if ((int)blockIdx.x >= work_blocks) {
-      shrink_all<RT>(P, (int)blockIdx.x - work_blocks, smem_raw);
+  int block = (int)blockIdx.x;
+  if constexpr (RT > 0) {
+    if (block < P.shrink_blocks) {
+      shrink_all<RT>(P, block, smem_raw);
       return;
     }
+    block -= P.shrink_blocks;
+  }
   lds_bytes *smem = (lds_bytes *)smem_raw;
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), waves = threads >> 6;
   const int nG = A.K / G, M = (int)A.M;
-  const int split = (int)blockIdx.x % A.splits, b0 = (int)blockIdx.x / A.splits;
+  const int split = block % A.splits, b0 = block / A.splits;
   const int blocks = work_blocks / A.splits;
-  const int nQ = (nG + 3) / 4;  // quads of groups
-  const int g0 = 4 * (int)((int64_t)nQ * split / A.splits);
-  const int g1 = min(nG, 4 * (int)((int64_t)nQ * (split + 1) / A.splits));
+  const int nU = (nG + GU - 1) / GU, nQ = (nU + 3) / 4;  // units, and fours of them
+  const int u0 = 4 * (int)((int64_t)nQ * split / A.splits);
+  const int u1 = min(nU, 4 * (int)((int64_t)nQ * (split + 1) / A.splits));
   const int wk = A.wk, wt = A.wt;        // waves of a tile, tiles of a set
   const int kw = wv % wk, tw = wv / wk;  // this wave's place (tw >= wt: it helps set up)
   const int tiles = (A.N + 15) / 16, sets = (tiles + wt - 1) / wt;
   const int steps = b0 < sets ? (sets - b0 + blocks - 1) / blocks : 0;
-  const int quads = (g1 - g0 + 3) / 4, batches = (quads + wk - 1) / wk;  // of a tile
+  const int quads = (u1 - u0 + 3) / 4, batches = (quads + wk - 1) / wk;  // of a tile
 
   // the set of step j is b0 + j * blocks
   auto tile_row = [&](int j) { return ((b0 + j * blocks) * wt + tw) * 16; };
   const bool active = tw < wt;
   int fj = 0, fk = 0;  // step and batch of the next request
-  auto fetch = [&](Raw<G>(&f)[NB]) {
+  auto fetch = [&](Raw<26>(&f)[NB]) {
     if (!active) return;
     const int n0 = tile_row(fj), quad = kw + wk * fk;
-    // rows past N read row N - 1 and groups past the last read it, with scale
+    // rows past N read row N - 1 and units past the last read it, with scales
     // 0; neither is stored or counts
     const int64_t n = min(n0 + l, A.N - 1);
-    const int g = g0 + 4 * quad + q;
-    const int64_t at = n * nG + min(g, g1 - 1);
+    const int u = u0 + 4 * quad + q, g = GU * min(u, u1 - 1);
+    const int64_t at = n * nG + min(g, nG - GU);
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      f[i].w = load_bytes<G>(A.packed[i] + at * B);
-      const uint32_t sc = A.scales[i][at];
-      f[i].scale = g < g1 ? sc : 0u;
+      f[i].w = load_bytes<26>(A.packed[i] + at * B);
+      uint32_t sc;
+      if constexpr (G == 128) {
+        sc = A.scales[i][at];
+      } else {
+        __builtin_memcpy(&sc, A.scales[i] + at, 4);
+        if (g + 1 == nG) sc &= 0xFFFF0000u;  // the first of the two belongs to the unit before
+      }
+      f[i].scale = u < u1 ? sc : 0u;
     }
     if (++fk == batches) {
       fk = 0;
@@ -392,8 +409,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
   };
 
   // the first bytes are requested before the table is built and x put in order
-  Raw<G> ra[NB], rb[NB];
-  fetch(ra);
+  constexpr int kAhead = few_ahead(NB, MT);
+  Raw<26> raw[kAhead][NB];
+#pragma unroll
+  for (int d = 0; d < kAhead; ++d) fetch(raw[d]);
   L::build(smem, tid, threads);
   // largest magnitudes, [wave][row], where the sums will be
   auto top_at = [&](int w, int m) {
@@ -402,8 +421,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
   // rows are shared by the waves, `parts` waves a row
   const int parts = max(1, waves / M);
   {
-    const uint16_t *xs = A.x + (int64_t)g0 * G;
-    const int len = (g1 - g0) * G, part = wv % parts;
+    const uint16_t *xs = A.x + (int64_t)u0 * 128;
+    const int len = min(A.K - u0 * 128, (u1 - u0) * 128), part = wv % parts;
     for (int m = wv / parts; m < M; m += waves / parts) {
       uint32_t top = 0;
 #pragma unroll 4
@@ -420,15 +439,19 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
     return f16_shift(top);
   };
   {
-    // unit: the steps of 40 codes, or those that are left, of a group of a row
-    constexpr int U = (G + 39) / 40;
-    const int units = quads * 4 * U;
-    for (int o = tid; o < units * M; o += threads) {
-      const int m = o / units, e = o - m * units, shift = shift_of(m);
-      const int g = e / U, u = e - g * U;
-      const bool in = g0 + g < g1, last = u == U - 1;
-      const int count = last ? G - 40 * (U - 1) : 40;
-      const uint16_t *p = A.x + (int64_t)m * A.K + (int64_t)min(g0 + g, g1 - 1) * G + 40 * u;
+    // a piece: the five steps of 40 codes, or those that are left, of a group
+    // of a row
+    constexpr int U = (G + 39) / 40, kLast = G - 40 * (U - 1);
+    const int pieces = quads * 4 * GU * U;
+    for (int o = tid; o < pieces * M; o += threads) {
+      const int m = o / pieces, e = o - m * pieces, shift = shift_of(m);
+      const int slot = e / U, piece = e - slot * U;  // slot: a group's place
+      // in a row's odd last unit the last group comes second
+      int g = GU * u0 + slot;
+      if (GU == 2 && (nG & 1)) g = g == nG ? nG - 1 : g == nG - 1 ? nG : g;
+      const bool in = g < min(nG, GU * u1), last = piece == U - 1;
+      const int count = last ? kLast : 40;
+      const uint16_t *p = A.x + (int64_t)m * A.K + (int64_t)(in ? g : 0) * G + 40 * piece;
       uint16_t v[40];
 #pragma unroll
       for (int s = 0; s < 5; ++s) *(u32x4 *)(v + 8 * s) = *(const u32x4 *)(p + (8 * s < count ? 8 * s : 0));
@@ -439,13 +462,13 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           // the codes past a group's tens are in their own order
-          constexpr int kTens = (G - 40 * (U - 1)) / 10 * 10;
           const int c = 8 * s + i;
           const uint16_t tens = v[group_source<40>(c)];
-          f[i] = f16_of(!in ? 0 : last && c >= kTens ? v[c] : tens, shift);
+          f[i] = f16_of(!in ? 0 : last && c >= kLast / 10 * 10 ? v[c] : tens, shift);
         }
-        // [quad][step][group of the quad][row]
-        *(lds_u32x4 *)(smem + kXOff + 16u * (uint32_t)((((g >> 2) * T + 5 * u + s) * 4 + (g & 3)) * M + m)) =
+        // [quad][step][unit of the quad][row]
+        const int unit = slot / GU, step = (slot % GU) * (T / GU) + 5 * piece + s;
+        *(lds_u32x4 *)(smem + kXOff + 16u * (uint32_t)((((unit >> 2) * T + step) * 4 + (unit & 3)) * M + m)) =
             *(u32x4 *)f;
       }
     }
@@ -468,26 +491,28 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[i][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
   int j = 0, k = 0;  // step and batch being worked on
-  auto work = [&](Raw<G>(&f)[NB], Raw<G>(&next)[NB]) {
-    fetch(next);
+  auto work = [&](Raw<26>(&f)[NB]) {
     const int n0 = tile_row(j), quad = kw + wk * k;
     if (active && n0 < A.N && quad < quads) {
       const uint32_t xq = 64u * (uint32_t)(quad * T * M);
-      // five steps at a time: eight bytes of each matrix
-      auto part = [&](auto p0, auto p1, auto tail) {
-        constexpr int P0 = decltype(p0)::value, P1 = decltype(p1)::value;
-        constexpr int S0 = 5 * P0 / 4, S1 = decltype(tail)::value ? T : 5 * P1 / 4;
+      // five steps at a time: eight bytes of each matrix, of the group at byte
+      // OFF whose steps start at S
+      auto part = [&](auto p0, auto p1, auto tail, auto which) {
+        constexpr int P0 = decltype(p0)::value, P1 = decltype(p1)::value, H = decltype(which)::value;
+        constexpr int S = H * (T / GU), OFF = H * B;
+        constexpr int S0 = 5 * P0 / 4, S1 = decltype(tail)::value ? G / 8 : 5 * P1 / 4;
         bf16x8 xf[S1 - S0][MT];
 #pragma unroll
         for (int s = S0; s < S1; ++s)
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
-            xf[s - S0][mt] = *(lds_bf16x8_c *)(smem + xlane[mt] + xq + 64u * (uint32_t)(s * M));
+            xf[s - S0][mt] = *(lds_bf16x8_c *)(smem + xlane[mt] + xq + 64u * (uint32_t)((S + s) * M));
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
           uint32_t d[G / 2];
-          const f16x2 sc = __builtin_bit_cast(f16x2, f[i].scale * 0x10001u);
-          decode_group<G, P0, P1, decltype(tail)::value>(smem, lut, f[i].w, sc, d, flags);
+          const uint32_t sc = f[i].scale;
+          const f16x2 two = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(sc, sc, H ? 0x03020302u : 0x01000100u));
+          decode_group<G, P0, P1, decltype(tail)::value, OFF>(smem, lut, f[i].w, two, d, flags);
 #pragma unroll
           for (int s = S0; s < S1; ++s)
 #pragma unroll
@@ -500,14 +525,17 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
         }
       };
       if constexpr (G == 128) {
-        part(Int<0>{}, Int<4>{}, Int<0>{});
-        part(Int<4>{}, Int<8>{}, Int<0>{});
-        part(Int<8>{}, Int<12>{}, Int<1>{});
+        part(Int<0>{}, Int<4>{}, Int<0>{}, Int<0>{});
+        part(Int<4>{}, Int<8>{}, Int<0>{}, Int<0>{});
+        part(Int<8>{}, Int<12>{}, Int<1>{}, Int<0>{});
       } else {
-        part(Int<0>{}, Int<4>{}, Int<0>{});
-        part(Int<4>{}, Int<6>{}, Int<1>{});
+        part(Int<0>{}, Int<4>{}, Int<0>{}, Int<0>{});
+        part(Int<4>{}, Int<6>{}, Int<1>{}, Int<0>{});
+        part(Int<0>{}, Int<4>{}, Int<0>{}, Int<1>{});
+        part(Int<4>{}, Int<6>{}, Int<1>{}, Int<1>{});
       }
     }
+    fetch(f);
     if (++k < batches) return;
     k = 0;
     // the tile's last batch: the waves' sums, in wave order; a matrix and 16
@@ -557,10 +585,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
     ++j;
   };
   const int total = steps * batches;
-  for (int t = 0; t < total; t += 2) {
-    work(ra, rb);
-    if (t + 1 < total) work(rb, ra);
-  }
+  for (int t = 0; t < total; t += kAhead)
+#pragma unroll
+    for (int d = 0; d < kAhead; ++d)
+      if (t + d < total) work(raw[d]);
   if ((flags & kBadFlag) && A.status) atomicOr(A.status, kDevInvalidByte);
 }
 
@@ -572,8 +600,8 @@ constexpr int kMidWaves = 8, kMidThreads = 64 * kMidWaves;
 constexpr int kMidRows = 64;  // of x a block
 
 // A block: 128 weight rows (of each matrix), a tile of 16 a wave; one chunk of
-// 64 rows of x; one split of K, in whole quads of groups.  The weights as
-// few_kernel has them; x comes in the same order and as f16 (f16_role), four
+// 64 rows of x; one split of K, in whole quads of groups.  Lane (l, q) decodes
+// group q of a quad of row l; x comes in the same order and as f16 (f16_role), four
 // matrix steps at a time, through a ring of LDS slots that all waves read.
 template <int G, int NB, int ACT>
 __global__ __launch_bounds__(kMidThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
@@ -599,14 +627,14 @@ void mid_kernel(const ProjArgs A) {
 
   // rows past N read row N - 1; their sums are not stored
   const int64_t n = min(n0 + l, A.N - 1);
-  Raw<G> ra[NB], rb[NB];
-  auto fetch = [&](Raw<G>(&r)[NB], int quad) {  // always: the waits below count on its loads
+  Raw<B> ra[NB], rb[NB];
+  auto fetch = [&](Raw<B>(&r)[NB], int quad) {  // always: the waits below count on its loads
     // groups past the last read it, with scale 0
     const int g = 4 * quad + q;
     const int64_t at = n * nG + min(g, nG - 1);
 #pragma unroll
     for (int i = 0; i < NB; ++i) {
-      r[i].w = load_bytes<G>(A.packed[i] + at * B);
+      r[i].w = load_bytes<B>(A.packed[i] + at * B);
       const uint32_t sc = A.scales[i][at];
       r[i].scale = g < nG ? sc : 0u;
     }
@@ -654,7 +682,7 @@ void mid_kernel(const ProjArgs A) {
   const L lut(0, lane);
   uint32_t flags = 0;
   int get = 0;
-  auto quad_of = [&](int quad, Raw<G>(&r)[NB], Raw<G>(&next)[NB]) {
+  auto quad_of = [&](int quad, Raw<B>(&r)[NB], Raw<B>(&next)[NB]) {
     uint32_t d[NB][G / 2];
     auto stage = [&](auto sc) {
       constexpr int S = decltype(sc)::value;
@@ -666,8 +694,8 @@ void mid_kernel(const ProjArgs A) {
       constexpr int P = G / 10, P0 = (16 * S + 4) / 5, P1 = (16 * S + 20) / 5 < P ? (16 * S + 20) / 5 : P;
 #pragma unroll
       for (int i = 0; i < NB; ++i)
-        decode_group<G, P0, P1, S == SQ - 1>(smem, lut, r[i].w,
-                                             __builtin_bit_cast(f16x2, r[i].scale * 0x10001u), d[i], flags);
+        decode_group<G, P0, P1, S == SQ - 1, 0>(
+            smem, lut, r[i].w, __builtin_bit_cast(f16x2, r[i].scale * 0x10001u), d[i], flags);
 #pragma unroll
       for (int s = 0; s < 4; ++s)
 #pragma unroll
@@ -745,7 +773,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const float *__restrict__ 
 // After few_kernel: y = the splits' partial sums in order (y itself where
 // there is one split) + the adapters' part.  A block: 16 columns, all rows;
 // its waves share the adapters, their sums added in wave order.
-constexpr int kExpandWaves = 8;
+constexpr int kExpandWaves = 16;
 template <int MT>
 __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(const ProjArgs A) {
   __shared__ __align__(16) float red[kExpandWaves * MT * 256];
@@ -759,7 +787,7 @@ __global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(const ProjArg
   if (mine) {
     const float *p = A.splits > 1 ? A.partial : (const float *)A.out;
     const int64_t mn = A.M * A.N;
-#pragma unroll 4
+#pragma unroll 8
     for (int s = 0; s < A.splits; ++s) v += p[s * mn + (int64_t)m * A.N + n];
   }
   f32x4 acc[1][MT];
@@ -1126,13 +1154,18 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
   Plan p{};
   const int64_t nG = K / G;
   p.splits = 1;
+  if (R) {
+    p.tsplits = M <= 256 && K > 4096 ? 2 : 1;  // where the blocks are few
+    p.t = round16(p.tsplits * M * R * 4);
+  }
   const int64_t wide_tiles = ceil_div(NB * N, kWideP) * ceil_div(M, kWideQ);
-  if (M <= kFewRows) {
+  if (M <= kFewRows && K >= 128) {
     p.kind = kFew;
-    // a block's slice of x, in whole quads of groups, fits its LDS
-    p.splits = (int)ceil_div(ceil_div(nG, 4), kFewX / (M * 4 * G * 2));
-    const int64_t quads = ceil_div(ceil_div(nG, 4), p.splits), tiles = ceil_div(N, 16);
-    // waves along K: a quad of groups each where that many waves are to be
+    // a block's slice of x, in whole fours of units, fits its LDS
+    const int64_t fours = ceil_div(K, 512);
+    p.splits = (int)ceil_div(fours, kFewX / (M * 512 * 2));
+    const int64_t quads = ceil_div(fours, p.splits), tiles = ceil_div(N, 16);
+    // waves along K: four units each where that many waves are to be
     // had; as many tiles a block as leave every CU one
     p.wk = (int)std::min<int64_t>(quads, kFewWaves);
     const int64_t spread = std::max<int64_t>(1, tiles * p.splits / 224);
@@ -1142,7 +1175,9 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
       p.wk = 4;
       p.wt = kFewWaves / p.wk;
     }
-    p.blocks = std::min(ceil_div(tiles, p.wt), std::max<int64_t>(1, 256 / p.splits)) * p.splits;
+    // a block a CU, beside those that make t
+    const int64_t cus = 256 - (R ? std::min<int64_t>(64, M * p.tsplits) : 0);
+    p.blocks = std::min(ceil_div(tiles, p.wt), std::max<int64_t>(1, cus / p.splits)) * p.splits;
   } else if (M > 128 && wide_tiles >= 64) {
     p.kind = kWide;
     // a tile a CU; K is split while every block keeps 64 stages
@@ -1162,10 +1197,6 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
     p.shift = round16(M * 4);
   }
   if (p.splits > 1) p.partial = round16((int64_t)p.splits * NB * M * N * 4);
-  if (R) {
-    p.tsplits = M <= 256 && K > 4096 ? 2 : 1;  // where the blocks are few
-    p.t = round16(p.tsplits * M * R * 4);
-  }
   return p;
 }
 

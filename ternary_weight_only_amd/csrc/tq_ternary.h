@@ -92,32 +92,33 @@ __device__ __forceinline__ u32x2 leftover_pool(lds_bytes *smem, const L &lut, ui
   return u32x2{a.x, __builtin_amdgcn_perm(b.x, a.y, 0x06050400u)};
 }
 
-// A group's bytes as two loads bring them, within the group whatever its
-// place: G = 128: bytes 0 .. 15 and 10 .. 25; G = 64: 0 .. 7 and 5 .. 12.
-template <int G>
-struct GroupBytes;
+// BYTES consecutive bytes as two loads bring them, whatever their place: of
+// 26, bytes 0 .. 15 and 10 .. 25; of 13, bytes 0 .. 7 and 5 .. 12.
+template <int BYTES>
+struct Bytes;
 template <>
-struct GroupBytes<128> {
+struct Bytes<26> {
   u32x4 a, b;
 };
 template <>
-struct GroupBytes<64> {
+struct Bytes<13> {
   u32x2 a, b;
 };
 
-template <int G>
-__device__ __forceinline__ GroupBytes<G> load_bytes(const uint8_t *p) {
-  GroupBytes<G> w;
-  __builtin_memcpy(&w.a, p, G / 8);
-  __builtin_memcpy(&w.b, p + (bytes_per_group(G) - G / 8), G / 8);
+template <int BYTES>
+__device__ __forceinline__ Bytes<BYTES> load_bytes(const uint8_t *p) {
+  Bytes<BYTES> w;
+  __builtin_memcpy(&w.a, p, sizeof(w.a));
+  __builtin_memcpy(&w.b, p + (BYTES - (int)sizeof(w.b)), sizeof(w.b));
   return w;
 }
 
 // The entry of byte i (a constant once unrolled).
-template <int G, class L>
-__device__ __forceinline__ u32x2 entry_of(lds_bytes *smem, const L &lut, const GroupBytes<G> &w, int i) {
-  const bool first = i < G / 8;
-  const int at = first ? i : i - bytes_per_group(G) + G / 8;
+template <int BYTES, class L>
+__device__ __forceinline__ u32x2 entry_of(lds_bytes *smem, const L &lut, const Bytes<BYTES> &w, int i) {
+  constexpr int kLoad = sizeof(w.a);
+  const bool first = i < kLoad;
+  const int at = first ? i : i - BYTES + kLoad;
   return lut.read(smem, first ? w.a[at >> 2] : w.b[at >> 2], at & 3);
 }
 
@@ -135,14 +136,14 @@ __device__ __forceinline__ void settle(uint32_t &flags) {
 #endif
 }
 
-// Scaled codes of byte pairs [P0, P1) of a group in group order: dwords 5 P0 ..
-// of d; with TAIL the last G % 10 codes follow.
-template <int G, int P0, int P1, bool TAIL, class L>
-__device__ __forceinline__ void decode_group(lds_bytes *smem, const L &lut, const GroupBytes<G> &w,
-                                             f16x2 s, uint32_t (&d)[G / 2], uint32_t &flags) {
+// Scaled codes of byte pairs [P0, P1) of the group that starts at byte OFF of
+// w, in group order: dwords 5 P0 .. of d; with TAIL the last G % 10 codes follow.
+template <int G, int P0, int P1, bool TAIL, int OFF, int BYTES, class L>
+__device__ __forceinline__ void decode_group(lds_bytes *smem, const L &lut, const Bytes<BYTES> &w, f16x2 s,
+                                             uint32_t (&d)[G / 2], uint32_t &flags) {
 #pragma unroll
   for (int p = P0; p < P1; ++p) {
-    const u32x2 a = entry_of(smem, lut, w, 2 * p), b = entry_of(smem, lut, w, 2 * p + 1);
+    const u32x2 a = entry_of(smem, lut, w, OFF + 2 * p), b = entry_of(smem, lut, w, OFF + 2 * p + 1);
     flags |= a.y | b.y;
     d[5 * p] = scaled(pair01(a), s);
     d[5 * p + 1] = scaled(pair23(a), s);
@@ -152,13 +153,13 @@ __device__ __forceinline__ void decode_group(lds_bytes *smem, const L &lut, cons
     settle(flags);
   }
   if constexpr (TAIL) {
-    const u32x2 a = entry_of(smem, lut, w, G / 10 * 2);
+    const u32x2 a = entry_of(smem, lut, w, OFF + G / 10 * 2);
     flags |= a.y;
     constexpr int D = G / 10 * 5;
     d[D] = scaled(pair01(a), s);
     d[D + 1] = scaled(pair23(a), s);
     if constexpr (G == 128) {
-      const u32x2 b = entry_of(smem, lut, w, 25);
+      const u32x2 b = entry_of(smem, lut, w, OFF + 25);
       flags |= b.y;
       d[D + 2] = scaled(__builtin_amdgcn_perm(b.x, a.y, 0x040C000Cu), s);  // code 4 of a, 0 of b
       d[D + 3] = scaled(__builtin_amdgcn_perm(b.x, b.x, 0x020C010Cu), s);  // codes 1, 2 of b
