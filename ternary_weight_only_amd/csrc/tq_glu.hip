@@ -318,10 +318,6 @@ constexpr int kFewWaves = 16;          // most waves of a block
 constexpr int kFewSetUp = 8;           // least: they share the table and x
 constexpr uint32_t kFewX = 64 << 10;   // LDS for a block's slice of x
 
-// Fours of units a wave keeps requested: what 128 registers a lane leave
-// room for.
-constexpr int few_ahead(int NB, int MT) { return NB == 1 ? 4 : MT == 1 ? 3 : 2; }
-
 // Consecutive bytes of a row and their group's scale, or two groups' scales.
 template <int BYTES>
 struct Raw {
@@ -342,9 +338,10 @@ struct Raw {
 // x [M,K] (M <= 16 MT) of the split, as f16 times a power of two for each row,
 // is put in order once, in LDS; it is the row operand of the matrix cores and W
 // the column operand.
-// A wave keeps few_ahead fours of units requested, across the ends of tiles,
-// from before the table is built: the bytes are on their way while x is put in
-// order.  LDS: 64 KB table, 64 KB x, up to 32 KB for the sums of the
+// A wave requests its next four units when it has decoded the last, across the
+// ends of tiles, and the first before the table is built.  (Two or three ahead
+// cost 2 to 4 us more at M = 7, 2 x [14336,4096]: x's loads wait behind them.)
+// LDS: 64 KB table, 64 KB x, up to 32 KB for the sums of the
 // waves.
 // lora: the projection alone; the first blocks make t meanwhile (RT as in
 // shrink_role, 0 for none), and expand_kernel adds the adapters.
@@ -382,7 +379,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
   auto tile_row = [&](int j) { return ((b0 + j * blocks) * wt + tw) * 16; };
   const bool active = tw < wt;
   int fj = 0, fk = 0;  // step and batch of the next request
-  auto fetch = [&](Raw<26>(&f)[NB]) {
+  Raw<26> f[NB];
+  auto fetch = [&]() {
     if (!active) return;
     const int n0 = tile_row(fj), quad = kw + wk * fk;
     // rows past N read row N - 1 and units past the last read it, with scales
@@ -409,10 +407,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
   };
 
   // the first bytes are requested before the table is built and x put in order
-  constexpr int kAhead = few_ahead(NB, MT);
-  Raw<26> raw[kAhead][NB];
-#pragma unroll
-  for (int d = 0; d < kAhead; ++d) fetch(raw[d]);
+  fetch();
   L::build(smem, tid, threads);
   // largest magnitudes, [wave][row], where the sums will be
   auto top_at = [&](int w, int m) {
@@ -491,7 +486,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[i][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
   int j = 0, k = 0;  // step and batch being worked on
-  auto work = [&](Raw<26>(&f)[NB]) {
+  const int total = steps * batches;
+  for (int t = 0; t < total; ++t) {
     const int n0 = tile_row(j), quad = kw + wk * k;
     if (active && n0 < A.N && quad < quads) {
       const uint32_t xq = 64u * (uint32_t)(quad * T * M);
@@ -535,8 +531,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
         part(Int<4>{}, Int<6>{}, Int<1>{}, Int<1>{});
       }
     }
-    fetch(f);
-    if (++k < batches) return;
+    fetch();
+    if (++k < batches) continue;
     k = 0;
     // the tile's last batch: the waves' sums, in wave order; a matrix and 16
     // rows of x at a time where LDS holds no more
@@ -583,12 +579,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
       }
     }
     ++j;
-  };
-  const int total = steps * batches;
-  for (int t = 0; t < total; t += kAhead)
-#pragma unroll
-    for (int d = 0; d < kAhead; ++d)
-      if (t + d < total) work(raw[d]);
+  }
   if ((flags & kBadFlag) && A.status) atomicOr(A.status, kDevInvalidByte);
 }
 
