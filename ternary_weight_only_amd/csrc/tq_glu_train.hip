@@ -39,6 +39,30 @@ struct TrainArgs {
   int stages, splits;       // stages of 32 k in all (even), and the blocks they are shared by
 };
 
+// One tile of one split of K.
+struct Item {
+  int ip, iq, split, s0, s1;  // stages [s0, s1), an even number
+};
+
+__device__ __forceinline__ Item item_of(const TrainArgs &A, int w) {
+  Item r;
+  const int tiles = A.tp * A.tq, pairs = A.stages / 2;
+  const int split = w / tiles;
+  int ip, iq;
+  tile_of_block(w - split * tiles, tiles, A.tp, A.tq, ip, iq);
+  // the same for the wave: kept in scalar registers, as load addresses need
+  r.split = __builtin_amdgcn_readfirstlane(split);
+  r.ip = __builtin_amdgcn_readfirstlane(ip);
+  r.iq = __builtin_amdgcn_readfirstlane(iq);
+  r.s0 = __builtin_amdgcn_readfirstlane(2 * (pairs * split / A.splits));
+  r.s1 = __builtin_amdgcn_readfirstlane(2 * (pairs * (split + 1) / A.splits));
+  return r;
+}
+
+// Persistent blocks: block b computes items b, b + grid, ...  The requests run
+// on across items, so an item's first stages load while the one before is
+// multiplied and stored, and the stores of one drain under the next.  (A block
+// an item cost 12 to 16 us an item beside its stages, most of it stores.)
 template <int MODE, int ACT, int BP, int BQ, int WP, int WQ>
 __global__ __launch_bounds__(64 * WP * WQ)
 __attribute__((amdgpu_waves_per_eu(2, 2))) void train_kernel(const TrainArgs A) {
@@ -47,73 +71,81 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void train_kernel(const TrainArgs A) 
   typedef Stream<PK, BP, NT> PS;
   typedef Stream<QK, BQ, NT> QS;
   constexpr uint32_t kQOff = kRing * PS::kSlot;
+  constexpr int L = PS::kLoads + QS::kLoads;  // loads a thread and stage: P's, then Q's
+  static_assert(2 * TQ % TP == 0 && TP >= L, "rows of MFMAs to put the reads and requests between");
   __shared__ __align__(16) unsigned char smem_raw[kRing * (PS::kSlot + QS::kSlot)];
   lds_bytes *smem = (lds_bytes *)smem_raw;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wp = wv / WQ, wq = wv % WQ;
+  constexpr int HP = BP / WP / 2;  // kFwd: gate (and up) columns of a wave
+  const int total = A.tp * A.tq * A.splits, grid = (int)gridDim.x;
 
-  int ip, iq;
-  const int tiles = A.tp * A.tq, split = (int)blockIdx.x / tiles;
-  tile_of_block((int)blockIdx.x - split * tiles, tiles, A.tp, A.tq, ip, iq);
-  // this block's stages [s0, s1), an even number of them
-  const int pairs = A.stages / 2;
-  const int s0 = 2 * (int)((int64_t)pairs * split / A.splits);
-  const int s1 = 2 * (int)((int64_t)pairs * (split + 1) / A.splits);
-
+  // ---- requests ----
   PS ps;
   QS qs;
-  constexpr int HP = BP / WP / 2;  // kFwd: gate (and up) columns of a wave
-  const int n0 = ip * (BP / 2);    // kFwd: first column of the tile
-  const int64_t q0 = (int64_t)iq * BQ;
-  if constexpr (MODE == kFwd) {
-    // slot row r: wave column r / 2HP, gate if (r % 2HP) < HP, else up
-    ps.init_rows(tid, (uint32_t)A.K, [&](int r) -> int64_t {
-      const int n = (r / (2 * HP)) * HP + r % HP;
-      return n0 + n < A.N ? n : -1;
-    });
-  } else {
-    ps.init_cols(tid, (uint32_t)A.K, A.K - ip * BP);
-  }
-  if constexpr (MODE == kDw)
-    qs.init_cols(tid, (uint32_t)(2 * A.Np), 2 * A.Np - (int)q0);
-  else
-    qs.init_rows(tid, (uint32_t)(MODE == kFwd ? A.K : 2 * A.Np),
-                 [&](int r) -> int64_t { return q0 + r < A.M ? r : -1; });
-
-  const uint16_t *qbase = A.q + (MODE == kDw ? q0 : q0 * (MODE == kFwd ? A.K : 2 * A.Np));
-  // The requests of one stage: L loads a thread, loads 0..1 of P then of Q.
-  constexpr int L = PS::kLoads + QS::kLoads;
+  Item rq;                              // item of the next request
+  int rw = (int)blockIdx.x, rs = 0;     // its index; stage
+  const uint16_t *rp0, *rp1, *rqb;      // its operands at k = 0: P (kDx: of the first and the
+                                        // second half of k; kFwd: gate and up), Q
+  auto open = [&]() {
+    rq = item_of(A, rw);
+    rs = rq.s0;
+    const int64_t q0 = (int64_t)rq.iq * BQ;
+    if constexpr (MODE == kFwd) {
+      const int n0 = rq.ip * (BP / 2);
+      // slot row r: wave column r / 2HP, gate if (r % 2HP) < HP, else up
+      ps.init_rows(tid, (uint32_t)A.K, [&](int r) -> int64_t {
+        const int n = (r / (2 * HP)) * HP + r % HP;
+        return n0 + n < A.N ? n : -1;
+      });
+      rp0 = A.p0 + (int64_t)n0 * A.K;
+      rp1 = A.p1 + (int64_t)n0 * A.K;
+    } else {
+      ps.init_cols(tid, (uint32_t)A.K, A.K - rq.ip * BP);
+      rp0 = A.p0 + rq.ip * BP;
+      rp1 = A.p1 + rq.ip * BP;
+    }
+    if constexpr (MODE == kDw) {
+      qs.init_cols(tid, (uint32_t)(2 * A.Np), 2 * A.Np - (int)q0);
+      rqb = A.q + q0;
+    } else {
+      const int64_t ld = MODE == kFwd ? A.K : 2 * A.Np;
+      qs.init_rows(tid, (uint32_t)ld, [&](int r) -> int64_t { return q0 + r < A.M ? r : -1; });
+      rqb = A.q + q0 * ld;
+    }
+  };
   struct Request {
     const uint16_t *p, *p_up, *q;  // kFwd: p holds gate rows, p_up up rows
     lds_bytes *pslot, *qslot;
     int prem, qrem;
   };
-  int rslot = 0;  // slot of the next request; stage s0 is in slot 0
-  auto request_of = [&](int s) {
+  int rslot = 0;  // slot of the next request; the first item's first stage is in slot 0
+  auto request_of = [&]() {
     Request r;
     r.pslot = smem + (uint32_t)rslot * PS::kSlot;
     r.qslot = smem + kQOff + (uint32_t)rslot * QS::kSlot;
     rslot = next_slot(rslot);
-    const bool in = s < s1;
+    const bool in = rw < total;  // past the last item: zeros that nothing uses
     if constexpr (MODE == kFwd) {
-      const int64_t k = (int64_t)s * kKS;
-      r.p = A.p0 + (int64_t)n0 * A.K + k;
-      r.p_up = A.p1 + (int64_t)n0 * A.K + k;
-      r.q = qbase + k;
+      const int64_t k = (int64_t)rs * kKS;
+      r.p = rp0 + k;
+      r.p_up = rp1 + k;
+      r.q = rqb + k;
       r.prem = r.qrem = in ? 1 : 0;
     } else if constexpr (MODE == kDx) {
-      const int half = A.Np / kKS, sn = s < half ? s : s - half;
-      r.p = (s < half ? A.p0 : A.p1) + (int64_t)sn * kKS * A.K + ip * BP;
-      r.q = qbase + (int64_t)s * kKS;
+      const int half = A.Np / kKS, sn = rs < half ? rs : rs - half;
+      r.p = (rs < half ? rp0 : rp1) + (int64_t)sn * kKS * A.K;
+      r.q = rqb + (int64_t)rs * kKS;
       r.prem = in ? A.N - sn * kKS : 0;
       r.qrem = in ? 1 : 0;
     } else {
-      const int64_t m = (int64_t)s * kKS;
-      r.p = A.p0 + m * A.K + ip * BP;
-      r.q = qbase + m * (2 * A.Np);
+      const int64_t m = (int64_t)rs * kKS;
+      r.p = rp0 + m * A.K;
+      r.q = rqb + m * (2 * A.Np);
       r.prem = r.qrem = !in ? 0 : A.M - m < kKS ? (int)(A.M - m) : kKS;
     }
+    ++rs;
     return r;
   };
   auto request = [&](const Request &r, int i) {
@@ -127,25 +159,30 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void train_kernel(const TrainArgs A) 
       ps.load(i, r.p, r.pslot, (uint32_t)wv, r.prem);
     }
   };
+  auto advance = [&]() {  // to the next item after an item's last request
+    if (rs == rq.s1 && rw < total) {
+      rw += grid;
+      if (rw < total) open();
+    }
+  };
 
   Frags<PK, BP, TP> pf;
   Frags<QK, BQ, TQ> qf;
   pf.init(lane, wp * (BP / WP));
   qf.init(lane, wq * (BQ / WQ));
-
   f32x4 acc[TP][TQ];
 #pragma unroll
   for (int a = 0; a < TP; ++a)
 #pragma unroll
     for (int b = 0; b < TQ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  static_assert(TP >= TQ && TP >= L, "rows of MFMAs to put the reads and requests between");
   bf16x8 pa[TP], qa[TQ], qb[TQ];
+  open();
 #pragma unroll
   for (int s = 0; s < kRing - 1; ++s) {
-    const Request r = request_of(s0 + s);
+    const Request r = request_of();
 #pragma unroll
     for (int i = 0; i < L; ++i) request(r, i);
+    advance();
   }
   static_assert(kRing == 5, "the waits count the loads of four stages in flight");
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(3 * L) : "memory");
@@ -155,102 +192,145 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void train_kernel(const TrainArgs A) 
   for (int a = 0; a < TP; ++a) pa[a] = pf.read(smem, 0, a);
   asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * L) : "memory");
 
-  // Stage s: its fragments are pa and qc; those of s + 1 are read into pa (as
-  // its blocks are used up) and qn.
-  int fslot = 1;  // slot of stage s + 1
-  auto stage = [&](int s, bf16x8(&qc)[TQ], bf16x8(&qn)[TQ]) {
+  // A stage: its fragments are pa and qc; those of the next are read into pa
+  // (as its blocks are used up) and qn.  `stores`: how many stores at least
+  // were issued between the requests of the two stages before the last two and
+  // those of the last two.
+  int fslot = 1;  // slot of the next stage
+  auto stage = [&](bf16x8(&qc)[TQ], bf16x8(&qn)[TQ], int stores) {
     const uint32_t pn = (uint32_t)fslot * PS::kSlot;
     const uint32_t qn0 = kQOff + (uint32_t)fslot * QS::kSlot;
     fslot = next_slot(fslot);
     __builtin_amdgcn_sched_barrier(0);
-    const Request r = request_of(s + kRing - 1);
+    const Request r = request_of();
 #pragma unroll
     for (int a = 0; a < TP; ++a) {
 #pragma unroll
       for (int b = 0; b < TQ; ++b) acc[a][b] = mfma32<false>(pa[a], qc[b], acc[a][b]);
-      if (a < TQ) qn[a] = qf.read(smem, qn0, a);
+      constexpr int R = 2 * TQ / TP;  // Q's fragments in the first half of the rows
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (R * a + i < TQ) qn[R * a + i] = qf.read(smem, qn0, R * a + i);
       pa[a] = pf.read(smem, pn, a);
       if (a < L) request(r, a);
     }
     order_stage<PK, QK, TP, TQ>();
     __builtin_amdgcn_sched_barrier(0);
-    // stage s + 2 has landed when only the loads of s + 3 and s + 4 are out
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * L) : "memory");
+    // Stage s + 2 has landed when only the loads of s + 3 and s + 4 are out,
+    // and the stores issued after its own.
+    if (stores >= 16)
+      asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * L + 16) : "memory");
+    else if (stores >= 8)
+      asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * L + 8) : "memory");
+    else
+      asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(2 * L) : "memory");
+    advance();
   };
-  for (int s = s0; s < s1; s += 2) {
-    stage(s, qa, qb);
-    stage(s + 1, qb, qa);
+
+  // Two neighbouring 16-row tiles of P: lane (l, h) has rows 4 h .. 4 h + 3 of
+  // each; after the exchange rows 8 (h / 2) .. + 7 of the first (h even) or the
+  // second, so that a row of the output gets 64 bytes at once.
+  const int h = lane >> 4, l = lane & 15;
+  auto pack8 = [&](f32x4 v, f32x4 w) {
+    uint32_t d[4] = {pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(w[0], w[1]), pack2(w[2], w[3])};
+    swap_rows(d[0], d[2]);
+    swap_rows(d[1], d[3]);
+    return u32x4{d[0], d[1], d[2], d[3]};
+  };
+  const int p8 = 16 * (h & 1) + 8 * (h >> 1);  // where a lane's eight rows start
+  // All of a wave's columns and rows are inside and aligned: returns the
+  // number of stores issued, which every such wave issues alike; else 0.
+  auto store = [&](const Item &t) -> int {
+    const int64_t q0 = (int64_t)t.iq * BQ + wq * (BQ / WQ);
+    const bool rows_in = q0 + BQ / WQ <= (MODE == kDw ? 2 * (int64_t)A.Np : A.M);
+    if constexpr (MODE == kFwd) {
+      static_assert(TP / 2 % 2 == 0, "pairs of tiles");
+      const int n0 = t.ip * (BP / 2) + wp * HP;
+      const bool full = rows_in && n0 + HP <= A.N && (A.N & 7) == 0;
+#pragma unroll
+      for (int b = 0; b < TQ; ++b) {
+        const int64_t m = q0 + 16 * b + l;
+        f32x4 hv[TP / 2];
+#pragma unroll
+        for (int a = 0; a < TP / 2; ++a)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) hv[a][r] = act_value<ACT>(acc[a][b][r]) * acc[a + TP / 2][b][r];
+        if (full) {
+#pragma unroll
+          for (int a = 0; a < TP / 2; a += 2) {
+            const int64_t o = m * A.N + n0 + 16 * a + p8;
+            *(u32x4 *)(A.o0 + o) = pack8(hv[a], hv[a + 1]);
+            if (A.o1) {
+              *(u32x4 *)(A.o1 + o) = pack8(acc[a][b], acc[a + 1][b]);
+              *(u32x4 *)(A.o2 + o) = pack8(acc[a + TP / 2][b], acc[a + 1 + TP / 2][b]);
+            }
+          }
+        } else if (m < A.M) {
+#pragma unroll
+          for (int a = 0; a < TP / 2; ++a)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int n = n0 + 16 * a + 4 * h + r;
+              if (n >= A.N) continue;
+              const int64_t o = m * A.N + n;
+              A.o0[o] = f32_to_bf16(hv[a][r]);
+              if (A.o1) {
+                A.o1[o] = f32_to_bf16(acc[a][b][r]);
+                A.o2[o] = f32_to_bf16(acc[a + TP / 2][b][r]);
+              }
+            }
+        }
+      }
+      return full ? TQ * (TP / 4) : 0;  // h alone; more with g and u
+    } else {
+      const int64_t rows = MODE == kDw ? 2 * (int64_t)A.Np : A.M;
+      const int p0 = t.ip * BP + wp * (BP / WP);
+      const bool full = rows_in && p0 + BP / WP <= A.K && (MODE == kDx || A.N == A.Np);
+#pragma unroll
+      for (int b = 0; b < TQ; ++b) {
+        const int64_t q = q0 + 16 * b + l;
+        if (!full && q >= rows) continue;
+        if (A.splits > 1) {
+          float *o = A.partial + ((int64_t)t.split * rows + q) * A.K + p0;
+#pragma unroll
+          for (int a = 0; a < TP; ++a)
+            if (full || p0 + 16 * a < A.K) *(f32x4 *)(o + 16 * a + 4 * h) = acc[a][b];
+          continue;
+        }
+        uint16_t *o;
+        if constexpr (MODE == kDx) {
+          o = A.o0 + q * A.K + p0;
+        } else {
+          const bool up = q >= A.Np;
+          const int64_t n = up ? q - A.Np : q;
+          if (!full && n >= A.N) continue;
+          o = (up ? A.o1 : A.o0) + n * A.K + p0;
+        }
+#pragma unroll
+        for (int a = 0; a < TP; a += 2)
+          if (full || p0 + 16 * a < A.K)  // K % 64 == 0: both tiles or neither
+            *(u32x4 *)(o + 16 * a + p8) = pack8(acc[a][b], acc[a + 1][b]);
+      }
+      return full ? TQ * (TP / 2) : 0;
+    }
+  };
+
+  int stores = 0;
+  for (int w = (int)blockIdx.x; w < total; w += grid) {
+    const Item t = item_of(A, w);
+    for (int s = t.s0; s < t.s1; s += 2) {
+      stage(qa, qb, stores);
+      stage(qb, qa, stores);
+      stores = 0;
+    }
+    stores = store(t);
+#pragma unroll
+    for (int a = 0; a < TP; ++a)
+#pragma unroll
+      for (int b = 0; b < TQ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
   // no load may still be writing this block's LDS when it exits
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-
-  // ---- epilogue: lane holds rows p = 16 a + 4 (lane / 16) + r, column
-  // q = 16 b + lane % 16 ----
-  const int lp = 4 * (lane >> 4);
-  const int64_t lq = q0 + wq * (BQ / WQ) + (lane & 15);
-  if constexpr (MODE == kFwd) {
-#pragma unroll
-    for (int b = 0; b < TQ; ++b) {
-      const int64_t m = lq + 16 * b;
-      if (m >= A.M) continue;
-#pragma unroll
-      for (int a = 0; a < TP / 2; ++a) {
-        const int n = n0 + wp * HP + 16 * a + lp;
-        const f32x4 g = acc[a][b], u = acc[a + TP / 2][b];
-        f32x4 h;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) h[r] = act_value<ACT>(g[r]) * u[r];
-        const int64_t o = m * A.N + n;
-        if ((A.N & 3) == 0 && n < A.N) {  // four columns, 8-byte aligned
-          store4(A.o0 + o, h);
-          if (A.o1) {
-            store4(A.o1 + o, g);
-            store4(A.o2 + o, u);
-          }
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            if (n + r >= A.N) continue;
-            A.o0[o + r] = f32_to_bf16(h[r]);
-            if (A.o1) {
-              A.o1[o + r] = f32_to_bf16(g[r]);
-              A.o2[o + r] = f32_to_bf16(u[r]);
-            }
-          }
-        }
-      }
-    }
-  } else {
-    const int64_t rows = MODE == kDx ? A.M : 2 * (int64_t)A.Np;
-#pragma unroll
-    for (int b = 0; b < TQ; ++b) {
-      const int64_t q = lq + 16 * b;
-      if (q >= rows) continue;
-      if (A.splits > 1) {
-        float *o = A.partial + ((int64_t)split * rows + q) * A.K;
-#pragma unroll
-        for (int a = 0; a < TP; ++a) {
-          const int p = ip * BP + wp * (BP / WP) + 16 * a + lp;
-          if (p < A.K) *(f32x4 *)(o + p) = acc[a][b];
-        }
-        continue;
-      }
-      uint16_t *o;
-      if constexpr (MODE == kDx) {
-        o = A.o0 + q * A.K;
-      } else {
-        const bool up = q >= A.Np;
-        const int64_t n = up ? q - A.Np : q;
-        if (n >= A.N) continue;
-        o = (up ? A.o1 : A.o0) + n * A.K;
-      }
-#pragma unroll
-      for (int a = 0; a < TP; ++a) {
-        const int p = ip * BP + wp * (BP / WP) + 16 * a + lp;
-        if (p < A.K) store4(o + p, acc[a][b]);
-      }
-    }
-  }
 }
 
 // Sum the splits' partial sums in order and round: rows of [rows, K], four
@@ -314,7 +394,11 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const uint16_t *__restri
   }
 }
 
-// Tile size and k split of one product of p x q outputs.
+// Tile size and k split of one product of p x q outputs: the least of
+// microseconds by a rule of four measured rates.  A stage of a 256 x 256 tile
+// takes a CU 0.78 us, one of two 128 x 128 tiles side by side 0.60 us (half the
+// work); an item costs 4 us more than its stages; split sums cross memory
+// twice at about 4 TB/s, in a launch of 4 us.
 struct Plan {
   bool big;
   int tp, tq, splits;
@@ -322,26 +406,36 @@ struct Plan {
 
 Plan plan_of(int64_t p, int64_t q, int stages, bool may_split) {
   auto up = [](int64_t a, int64_t b) { return (int)((a + b - 1) / b); };
-  Plan r;
-  r.tp = up(p, 256), r.tq = up(q, 256), r.splits = 1;
-  r.big = (int64_t)r.tp * r.tq >= 192;
-  if (r.big) return r;
-  r.tp = up(p, 128), r.tq = up(q, 128);
-  const int tiles = r.tp * r.tq, most = stages / 16;
-  if (may_split && tiles > 0 && tiles <= 256 && most > 1) r.splits = std::min(512 / tiles, most);
-  return r;
+  Plan best{};
+  double least = 1e30;
+  for (int big = 1; big >= 0; --big) {
+    const int size = big ? 256 : 128, tp = up(p, size), tq = up(q, size);
+    for (int splits = 1; splits <= (may_split ? 16 : 1) && (splits == 1 || stages / splits >= 8); ++splits) {
+      const int64_t rounds = up((int64_t)tp * tq * splits, big ? 256 : 512);
+      double us = (double)rounds * ((double)stages / splits * (big ? 0.78 : 0.60) + 4.0);
+      if (splits > 1) us += 4.0 + 2.0 * 4.0 * (double)p * (double)q * splits / 4e6;
+      if (us < least) {
+        least = us;
+        best = Plan{big != 0, tp, tq, splits};
+      }
+    }
+  }
+  return best;
 }
 
 int pad64(int64_t n) { return (int)((n + 63) / 64 * 64); }
-int even_stages(int64_t k) { return 2 * (int)((k + 2 * kKS - 1) / (2 * kKS)); }
+// At least one pair: of no rows it adds zeros.
+int even_stages(int64_t k) { return k ? 2 * (int)((k + 2 * kKS - 1) / (2 * kKS)) : 2; }
 
 template <int MODE, int ACT>
 void launch_product(const TrainArgs &a, bool big, hipStream_t stream) {
-  const dim3 grid((unsigned)(a.tp * a.tq * a.splits));
+  const int items = a.tp * a.tq * a.splits;
   if (big)
-    hipLaunchKernelGGL((train_kernel<MODE, ACT, 256, 256, 2, 4>), grid, dim3(512), 0, stream, a);
+    hipLaunchKernelGGL((train_kernel<MODE, ACT, 256, 256, 4, 2>), dim3((unsigned)std::min(items, 256)),
+                       dim3(512), 0, stream, a);
   else
-    hipLaunchKernelGGL((train_kernel<MODE, ACT, 128, 128, 2, 2>), grid, dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((train_kernel<MODE, ACT, 128, 128, 2, 2>), dim3((unsigned)std::min(items, 512)),
+                       dim3(256), 0, stream, a);
 }
 
 struct BackwardPlan {

@@ -168,14 +168,15 @@ struct Frags {
 };
 
 // Order for the scheduler: the MFMAs of one stage in rows of TQ, each row
-// followed by the fragment reads that replace its operands (and, first, the
-// other operand's).
+// followed by the fragment reads that replace its operands (and, in the first
+// half, the other operand's).
 template <int PK, int QK, int TP, int TQ>
 __device__ __forceinline__ void order_stage() {
 #pragma unroll
   for (int a = 0; a < TP; ++a) {
     __builtin_amdgcn_sched_group_barrier(0x008, TQ, 0);                 // MFMA
-    if (a < TQ) __builtin_amdgcn_sched_group_barrier(0x100, QK == kRows ? 1 : 2, 0);  // LDS reads
+    if (2 * a < TP)  // LDS reads
+      __builtin_amdgcn_sched_group_barrier(0x100, (2 * TQ / TP) * (QK == kRows ? 1 : 2), 0);
     __builtin_amdgcn_sched_group_barrier(0x100, PK == kRows ? 1 : 2, 0);
   }
 }
@@ -191,10 +192,22 @@ __device__ __forceinline__ f32x4 mfma32(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return (uint32_t)f32_to_bf16(a) | (uint32_t)f32_to_bf16(b) << 16;
+}
+
 // Four values as bf16, at an 8-byte aligned address.
 __device__ __forceinline__ void store4(uint16_t *p, f32x4 v) {
-  *(u32x2 *)p = u32x2{(uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
-                      (uint32_t)f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
+  *(u32x2 *)p = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+}
+
+// Exchanges the odd 16-lane rows of a with the even ones of b.
+__device__ __forceinline__ void swap_rows(uint32_t &a, uint32_t &b) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+#endif
 }
 
 // Tile of block b of a launch: consecutive tiles run on one XCD (blocks go to
