@@ -37,6 +37,7 @@ struct TrainArgs {
   int N, K, Np;             // Np: columns of half of [dg | du]
   int tp, tq;               // tiles along p and q
   int stages, splits;       // stages of 32 k in all (even), and the blocks they are shared by
+  int blocks;               // blocks of the launch that work on this product
 };
 
 // One tile of one split of K.
@@ -59,13 +60,12 @@ __device__ __forceinline__ Item item_of(const TrainArgs &A, int w) {
   return r;
 }
 
-// Persistent blocks: block b computes items b, b + grid, ...  The requests run
-// on across items, so an item's first stages load while the one before is
+// Persistent blocks: block b of `grid` computes items b, b + grid, ...  The
+// requests run on across items, so an item's first stages load while the one before is
 // multiplied and stored, and the stores of one drain under the next.  (A block
 // an item cost 12 to 16 us an item beside its stages, most of it stores.)
 template <int MODE, int ACT, int BP, int BQ, int WP, int WQ>
-__global__ __launch_bounds__(64 * WP * WQ)
-__attribute__((amdgpu_waves_per_eu(2, 2))) void train_kernel(const TrainArgs A) {
+__device__ __forceinline__ void product(const TrainArgs &A, int block, int grid, lds_bytes *smem) {
   constexpr int NT = 64 * WP * WQ, TP = BP / WP / 16, TQ = BQ / WQ / 16;
   constexpr int PK = MODE == kFwd ? kRows : kCols, QK = MODE == kDw ? kCols : kRows;
   typedef Stream<PK, BP, NT> PS;
@@ -73,19 +73,17 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void train_kernel(const TrainArgs A) 
   constexpr uint32_t kQOff = kRing * PS::kSlot;
   constexpr int L = PS::kLoads + QS::kLoads;  // loads a thread and stage: P's, then Q's
   static_assert(2 * TQ % TP == 0 && TP >= L, "rows of MFMAs to put the reads and requests between");
-  __shared__ __align__(16) unsigned char smem_raw[kRing * (PS::kSlot + QS::kSlot)];
-  lds_bytes *smem = (lds_bytes *)smem_raw;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wp = wv / WQ, wq = wv % WQ;
   constexpr int HP = BP / WP / 2;  // kFwd: gate (and up) columns of a wave
-  const int total = A.tp * A.tq * A.splits, grid = (int)gridDim.x;
+  const int total = A.tp * A.tq * A.splits;
 
   // ---- requests ----
   PS ps;
   QS qs;
   Item rq;                              // item of the next request
-  int rw = (int)blockIdx.x, rs = 0;     // its index; stage
+  int rw = block, rs = 0;               // its index; stage
   const uint16_t *rp0, *rp1, *rqb;      // its operands at k = 0: P (kDx: of the first and the
                                         // second half of k; kFwd: gate and up), Q
   auto open = [&]() {
@@ -316,7 +314,7 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void train_kernel(const TrainArgs A) 
   };
 
   int stores = 0;
-  for (int w = (int)blockIdx.x; w < total; w += grid) {
+  for (int w = block; w < total; w += grid) {
     const Item t = item_of(A, w);
     for (int s = t.s0; s < t.s1; s += 2) {
       stage(qa, qb, stores);
@@ -333,25 +331,55 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) void train_kernel(const TrainArgs A) 
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-// Sum the splits' partial sums in order and round: rows of [rows, K], four
-// columns a thread.  The rows of dW go to dwg and dwu.
-__global__ __launch_bounds__(256) void reduce_kernel(const float *__restrict__ partial, int64_t rows,
-                                                     int K, int splits, int Np, int N,
-                                                     uint16_t *__restrict__ o0,
-                                                     uint16_t *__restrict__ o1) {
-  const int64_t n4 = rows * (K / 4);
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
-    f32x4 v = *(const f32x4 *)(partial + 4 * i);
-    for (int s = 1; s < splits; ++s) v += *(const f32x4 *)(partial + ((int64_t)s * n4 + i) * 4);
-    if (!o1) {
-      store4(o0 + 4 * i, v);
+constexpr int lds_of(int BP, int BQ) { return kRing * kKS * 2 * (BP + BQ); }
+
+template <int ACT, int BP, int BQ, int WP, int WQ>
+__global__ __launch_bounds__(64 * WP * WQ)
+__attribute__((amdgpu_waves_per_eu(2, 2))) void forward_kernel(const TrainArgs A) {
+  __shared__ __align__(16) unsigned char smem[lds_of(BP, BQ)];
+  product<kFwd, ACT, BP, BQ, WP, WQ>(A, (int)blockIdx.x, A.blocks, (lds_bytes *)smem);
+}
+
+// dW, dx, or both side by side, each on its share of the chip: alone, either
+// may leave CUs idle in its last round or have to split K, whose sums cross
+// memory twice.
+template <int BP, int BQ, int WP, int WQ>
+__global__ __launch_bounds__(64 * WP * WQ)
+__attribute__((amdgpu_waves_per_eu(2, 2))) void backward_kernel(const TrainArgs W, const TrainArgs X) {
+  __shared__ __align__(16) unsigned char smem[lds_of(BP, BQ)];
+  if ((int)blockIdx.x < W.blocks)
+    product<kDw, kActSilu, BP, BQ, WP, WQ>(W, (int)blockIdx.x, W.blocks, (lds_bytes *)smem);
+  else
+    product<kDx, kActSilu, BP, BQ, WP, WQ>(X, (int)blockIdx.x - W.blocks, X.blocks, (lds_bytes *)smem);
+}
+
+// Sum a product's splits in order and round, four columns a thread; dW's rows
+// go to dwg and dwu.
+template <int MODE>
+__device__ __forceinline__ void reduce_product(const TrainArgs &A, int64_t first, int64_t stride) {
+  const int64_t rows = MODE == kDx ? A.M : 2 * (int64_t)A.Np, n4 = rows * (A.K / 4);
+  for (int64_t i = first; i < n4; i += stride) {
+    f32x4 v = *(const f32x4 *)(A.partial + 4 * i);
+    for (int s = 1; s < A.splits; ++s) v += *(const f32x4 *)(A.partial + ((int64_t)s * n4 + i) * 4);
+    if constexpr (MODE == kDx) {
+      store4(A.o0 + 4 * i, v);
     } else {
-      const int64_t q = i / (K / 4), p = 4 * (i - q * (K / 4));
-      const bool up = q >= Np;
-      const int64_t n = up ? q - Np : q;
-      if (n < N) store4((up ? o1 : o0) + n * K + p, v);
+      const int64_t q = i / (A.K / 4), p = 4 * (i - q * (A.K / 4));
+      const bool up = q >= A.Np;
+      const int64_t n = up ? q - A.Np : q;
+      if (n < A.N) store4((up ? A.o1 : A.o0) + n * A.K + p, v);
     }
   }
+}
+
+// The products whose K is split, W's on the first `w_blocks` blocks.
+__global__ __launch_bounds__(256) void reduce_kernel(const TrainArgs W, const TrainArgs X, int w_blocks) {
+  const int b = (int)blockIdx.x;
+  if (b < w_blocks)
+    reduce_product<kDw>(W, (int64_t)b * 256 + threadIdx.x, (int64_t)w_blocks * 256);
+  else
+    reduce_product<kDx>(X, (int64_t)(b - w_blocks) * 256 + threadIdx.x,
+                        (int64_t)((int)gridDim.x - w_blocks) * 256);
 }
 
 // [dg | du], each rounded once to bf16 (the type the matrix cores take); the
@@ -394,67 +422,89 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(const uint16_t *__restri
   }
 }
 
-// Tile size and k split of one product of p x q outputs: the least of
-// microseconds by a rule of four measured rates.  A stage of a 256 x 256 tile
-// takes a CU 0.78 us, one of two 128 x 128 tiles side by side 0.60 us (half the
-// work); an item costs 4 us more than its stages; split sums cross memory
-// twice at about 4 TB/s, in a launch of 4 us.
-struct Plan {
-  bool big;
-  int tp, tq, splits;
+// Microseconds by measured rates.  A stage of a 256 x 256 tile takes a CU 0.78
+// us, one of two 128 x 128 tiles side by side 0.60 us (half the work), one of
+// such a tile alone 0.40 us; an item costs 4 us more than its stages; split
+// sums cross memory twice at about 4 TB/s, in a launch of 4 us; two products
+// side by side find less of their operands in the L2s and take 8% longer.
+struct Rates {
+  int size, slots;  // tile, and how many the chip works on at once
+  double stage, alone;
 };
+constexpr Rates kRates[2] = {{256, 256, 0.78, 0.78}, {128, 512, 0.60, 0.40}};
+constexpr double kItem = 4.0, kLaunch = 4.0, kPartialBytesPerUs = 4e6, kJoint = 1.08;
 
-Plan plan_of(int64_t p, int64_t q, int stages, bool may_split) {
-  auto up = [](int64_t a, int64_t b) { return (int)((a + b - 1) / b); };
-  Plan best{};
-  double least = 1e30;
-  for (int big = 1; big >= 0; --big) {
-    const int size = big ? 256 : 128, tp = up(p, size), tq = up(q, size);
-    for (int splits = 1; splits <= (may_split ? 16 : 1) && (splits == 1 || stages / splits >= 8); ++splits) {
-      const int64_t rounds = up((int64_t)tp * tq * splits, big ? 256 : 512);
-      double us = (double)rounds * ((double)stages / splits * (big ? 0.78 : 0.60) + 4.0);
-      if (splits > 1) us += 4.0 + 2.0 * 4.0 * (double)p * (double)q * splits / 4e6;
-      if (us < least) {
-        least = us;
-        best = Plan{big != 0, tp, tq, splits};
-      }
-    }
-  }
-  return best;
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// One product of p x q outputs: its tiles, split `splits` ways on `slots`.
+struct Tiling {
+  int tp, tq, splits, blocks;
+};
+Tiling tiling_of(const Rates &r, int64_t p, int64_t q, int splits, int64_t slots) {
+  const int64_t tp = ceil_div(p, r.size), tq = ceil_div(q, r.size);
+  return Tiling{(int)tp, (int)tq, splits, (int)std::min(slots, tp * tq * splits)};
+}
+double product_us(const Rates &r, int64_t p, int64_t q, int stages, int splits, int64_t slots) {
+  const int64_t items = ceil_div(p, r.size) * ceil_div(q, r.size) * splits;
+  const double stage = 2 * items <= slots ? r.alone : r.stage;
+  return (double)ceil_div(items, slots) * ((double)stages / splits * stage + kItem);
+}
+double partial_us(int64_t p, int64_t q, int splits) {
+  return splits > 1 ? 8.0 * (double)p * (double)q * splits / kPartialBytesPerUs : 0.0;
 }
 
 int pad64(int64_t n) { return (int)((n + 63) / 64 * 64); }
 // At least one pair: of no rows it adds zeros.
 int even_stages(int64_t k) { return k ? 2 * (int)((k + 2 * kKS - 1) / (2 * kKS)) : 2; }
 
-template <int MODE, int ACT>
-void launch_product(const TrainArgs &a, bool big, hipStream_t stream) {
-  const int items = a.tp * a.tq * a.splits;
-  if (big)
-    hipLaunchKernelGGL((train_kernel<MODE, ACT, 256, 256, 4, 2>), dim3((unsigned)std::min(items, 256)),
-                       dim3(512), 0, stream, a);
-  else
-    hipLaunchKernelGGL((train_kernel<MODE, ACT, 128, 128, 2, 2>), dim3((unsigned)std::min(items, 512)),
-                       dim3(256), 0, stream, a);
+void set_tiling(TrainArgs &a, const Tiling &t, int stages) {
+  a.tp = t.tp, a.tq = t.tq, a.splits = t.splits, a.blocks = t.blocks, a.stages = stages;
 }
 
 struct BackwardPlan {
-  Plan dx, dw;
-  int Np, sx, sw;          // stages
-  int64_t gates, partial;  // workspace bytes: [dg | du], then the larger partial array
+  bool big, joint;
+  Tiling w, x;
+  int Np, sw, sx;                      // stages
+  int64_t gates, partial_w, partial_x;  // workspace bytes: [dg | du], then the partial sums
 };
 
+// dW and dx one after the other on the whole chip, or side by side on shares
+// of it (in eights, one an XCD): tile size, shares and splits that take least.
 BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K) {
-  BackwardPlan b;
+  BackwardPlan b{};
   b.Np = pad64(N);
   b.sx = 2 * b.Np / kKS;
   b.sw = even_stages(M);
-  b.dx = plan_of(K, M, b.sx, true);
-  b.dw = plan_of(K, 2 * (int64_t)b.Np, b.sw, true);
   b.gates = M * 4 * b.Np;
-  const int64_t px = b.dx.splits > 1 ? b.dx.splits * M * K * 4 : 0;
-  const int64_t pw = b.dw.splits > 1 ? b.dw.splits * 2 * (int64_t)b.Np * K * 4 : 0;
-  b.partial = px > pw ? px : pw;
+  const int64_t qw = 2 * (int64_t)b.Np;
+  double least = 1e30;
+  auto look = [&](int i, bool joint, int64_t cw, int64_t cx) {
+    const Rates &r = kRates[i];
+    for (int sw = 1; sw <= 16 && (sw == 1 || b.sw / sw >= 8); sw *= 2) {
+      const double w = product_us(r, K, qw, b.sw, sw, cw), pw = partial_us(K, qw, sw);
+      for (int sx = 1; sx <= 16 && (sx == 1 || b.sx / sx >= 8); sx *= 2) {
+        const double x = M ? product_us(r, K, M, b.sx, sx, cx) : 0.0;
+        const double us = (joint ? kJoint * std::max(w, x) : w + x + kLaunch) + pw + partial_us(K, M, sx) +
+                          (sw > 1 || sx > 1 ? kLaunch : 0.0);
+        if (us < least) {
+          least = us;
+          b.big = i == 0, b.joint = joint;
+          b.w = tiling_of(r, K, qw, sw, cw);
+          b.x = tiling_of(r, K, M, sx, cx);
+        }
+      }
+    }
+  };
+  for (int i = 0; i < 2; ++i) {
+    const Rates &r = kRates[i];
+    look(i, false, r.slots, r.slots);
+    const double work_w = (double)ceil_div(qw, r.size) * b.sw, work_x = (double)ceil_div(M, r.size) * b.sx;
+    const int eights = r.slots / 8, share = (int)(eights * work_w / (work_w + work_x) + 0.5);
+    for (int e = std::max(share - 1, 1); M && e <= std::min(share + 1, eights - 1); ++e)
+      look(i, true, 8 * e, r.slots - 8 * e);
+  }
+  b.partial_w = b.w.splits > 1 ? b.w.splits * qw * K * 4 : 0;
+  b.partial_x = b.x.splits > 1 ? b.x.splits * M * K * 4 : 0;
   return b;
 }
 
@@ -463,20 +513,27 @@ BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K) {
 void launch_glu_forward(const uint16_t *x, const uint16_t *wg, const uint16_t *wu, int64_t M,
                         int64_t N, int64_t K, int act, uint16_t *h, uint16_t *g, uint16_t *u,
                         hipStream_t stream) {
-  const Plan p = plan_of(2 * N, M, (int)(K / kKS), false);
+  const int stages = (int)(K / kKS);
+  // 256 x 256 tiles unless the smaller ones fill the chip better
+  const bool big = product_us(kRates[0], 2 * N, M, stages, 1, kRates[0].slots) <=
+                   product_us(kRates[1], 2 * N, M, stages, 1, kRates[1].slots);
+  const Rates &r = kRates[big ? 0 : 1];
   TrainArgs a{};
   a.p0 = wg, a.p1 = wu, a.q = x, a.o0 = h, a.o1 = g, a.o2 = u;
   a.M = M, a.N = (int)N, a.K = (int)K;
-  a.tp = p.tp, a.tq = p.tq, a.stages = (int)(K / kKS), a.splits = 1;
+  set_tiling(a, tiling_of(r, 2 * N, M, 1, r.slots), stages);
+  auto go = [&](auto kernel, int threads) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)a.blocks), dim3(threads), 0, stream, a);
+  };
   if (act == kActSilu)
-    launch_product<kFwd, kActSilu>(a, p.big, stream);
+    big ? go(forward_kernel<kActSilu, 256, 256, 4, 2>, 512) : go(forward_kernel<kActSilu, 128, 128, 2, 2>, 256);
   else
-    launch_product<kFwd, kActGelu>(a, p.big, stream);
+    big ? go(forward_kernel<kActGelu, 256, 256, 4, 2>, 512) : go(forward_kernel<kActGelu, 128, 128, 2, 2>, 256);
 }
 
 int64_t glu_backward_workspace(int64_t M, int64_t N, int64_t K) {
   const BackwardPlan b = plan_backward(M, N, K);
-  return b.gates + b.partial;
+  return b.gates + b.partial_w + b.partial_x;
 }
 
 void launch_glu_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *wg,
@@ -485,36 +542,44 @@ void launch_glu_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *
                          void *workspace, hipStream_t stream) {
   const BackwardPlan b = plan_backward(M, N, K);
   uint16_t *gates = (uint16_t *)workspace;
-  TrainArgs a{};
-  a.q = gates;
-  a.partial = (float *)((char *)workspace + b.gates);
-  a.M = M, a.N = (int)N, a.K = (int)K, a.Np = b.Np;
-  auto blocks = [](int64_t threads) {
-    const int64_t n = (threads + 255) / 256;
-    return dim3((unsigned)(n < 8192 ? n : 8192));
-  };
+  TrainArgs w{}, v{};  // dW, dx
+  w.p0 = x, w.q = gates, w.o0 = dwg, w.o1 = dwu;
+  v.p0 = wg, v.p1 = wu, v.q = gates, v.o0 = dx;
+  w.M = v.M = M, w.N = v.N = (int)N, w.K = v.K = (int)K, w.Np = v.Np = b.Np;
+  w.partial = (float *)((char *)workspace + b.gates);
+  v.partial = (float *)((char *)workspace + b.gates + b.partial_w);
+  set_tiling(w, b.w, b.sw);
+  set_tiling(v, b.x, b.sx);
+  auto blocks = [](int64_t threads) { return (unsigned)std::min<int64_t>(8192, ceil_div(threads, 256)); };
   if (M > 0) {
     auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, blocks(M * (b.Np / 8)), dim3(256), 0, stream, dh, g, u, M, (int)N,
+      hipLaunchKernelGGL(kernel, dim3(blocks(M * (b.Np / 8))), dim3(256), 0, stream, dh, g, u, M, (int)N,
                          b.Np, gates);
     };
     if (N % 8 == 0)
       act == kActSilu ? go(gate_grad_kernel<kActSilu, true>) : go(gate_grad_kernel<kActGelu, true>);
     else
       act == kActSilu ? go(gate_grad_kernel<kActSilu, false>) : go(gate_grad_kernel<kActGelu, false>);
-    a.p0 = wg, a.p1 = wu, a.o0 = dx;
-    a.tp = b.dx.tp, a.tq = b.dx.tq, a.stages = b.sx, a.splits = b.dx.splits;
-    launch_product<kDx, kActSilu>(a, b.dx.big, stream);
-    if (a.splits > 1)
-      hipLaunchKernelGGL(reduce_kernel, blocks(M * (K / 4)), dim3(256), 0, stream, a.partial, M,
-                         (int)K, a.splits, 0, 0, dx, nullptr);
   }
-  a.p0 = x, a.p1 = nullptr, a.o0 = dwg, a.o1 = dwu;
-  a.tp = b.dw.tp, a.tq = b.dw.tq, a.stages = b.sw, a.splits = b.dw.splits;
-  launch_product<kDw, kActSilu>(a, b.dw.big, stream);
-  if (a.splits > 1)
-    hipLaunchKernelGGL(reduce_kernel, blocks(2 * (int64_t)b.Np * (K / 4)), dim3(256), 0, stream,
-                       a.partial, 2 * (int64_t)b.Np, (int)K, a.splits, b.Np, (int)N, dwg, dwu);
+  auto products = [&](TrainArgs pw, TrainArgs px) {
+    const dim3 grid((unsigned)(pw.blocks + px.blocks));
+    if (grid.x == 0) return;
+    if (b.big)
+      hipLaunchKernelGGL((backward_kernel<256, 256, 4, 2>), grid, dim3(512), 0, stream, pw, px);
+    else
+      hipLaunchKernelGGL((backward_kernel<128, 128, 2, 2>), grid, dim3(256), 0, stream, pw, px);
+  };
+  if (b.joint) {
+    products(w, v);
+  } else {
+    TrainArgs none{};
+    products(w, none);
+    products(none, v);
+  }
+  const unsigned rw = w.splits > 1 ? blocks(2 * (int64_t)b.Np * (K / 4)) : 0;
+  const unsigned rx = v.splits > 1 ? blocks(M * (K / 4)) : 0;
+  if (rw + rx > 0)
+    hipLaunchKernelGGL(reduce_kernel, dim3(rw + rx), dim3(256), 0, stream, w, v, (int)rw);
 }
 
 }  // namespace tq
