@@ -815,10 +815,10 @@ template <int G, int NB, int ACT>
 __global__ __launch_bounds__(kWideThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void wide_kernel(const ProjArgs A) {
   constexpr int S32 = G / 32, WP = 2, WQ = 4, TP = 8, TQ = 4, B = bytes_per_group(G);
-  typedef Stream<kRows, kWideQ, kWideThreads> QS;
   typedef Lut<8> L;
-  constexpr uint32_t kPSlot = kWideP * kKS * 2;
-  constexpr uint32_t kQOff = kWideC * kPSlot, kLutOff = kQOff + kWideX * QS::kSlot;
+  constexpr uint32_t kPSlot = kWideP * kKS * 2, kQSlot = kWideQ * kKS * 2;
+  constexpr int kXLoads = kQSlot / 16 / kWideThreads;  // a thread's requests of x in a stage
+  constexpr uint32_t kQOff = kWideC * kPSlot, kLutOff = kQOff + kWideX * kQSlot;
   __shared__ __align__(16) unsigned char smem_raw[kLutOff + L::kBytes];
   lds_bytes *smem = (lds_bytes *)smem_raw;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -836,16 +836,15 @@ void wide_kernel(const ProjArgs A) {
   const int n0 = ip * (kWideP / NB);
   const int64_t q0 = (int64_t)iq * kWideQ;
 
-  // this thread's weight row: slot row tid / 2; rows past N read row N - 1
+  // this thread's weight row: slot row tid / 2; rows past N read row N - 1.  A
+  // wave's 32 slot rows are of one matrix: the tile starts at a scalar address.
+  static_assert(HP % 32 == 0, "");
   const int sr = tid >> 1, hf = tid & 1;
-  const uint8_t *prow;
-  const uint16_t *srow;
-  {
-    const int which = NB == 1 ? 0 : sr % (NB * HP) / HP;
-    const int64_t n = min(n0 + sr / (NB * HP) * HP + sr % HP, A.N - 1);
-    prow = A.packed[which] + n * nG * B;
-    srow = A.scales[which] + n * nG;
-  }
+  const int which = NB == 1 ? 0 : wv * 32 % (NB * HP) / HP;
+  const uint32_t first = (uint32_t)min(sr / (NB * HP) * HP + sr % HP, A.N - 1 - n0) * (uint32_t)nG;
+  const uint32_t poff = first * B + 3u * hf, toff = first * B, soff = first * 2u;
+  const Scalar bytes(A.packed[which] + ((int64_t)n0 * nG + g0) * B);
+  const Scalar values(A.scales[which] + (int64_t)n0 * nG + g0);
   // bytes and group values are requested four stages before they are decoded
   constexpr int kGroups = 4 / S32;  // groups of four stages
   uint32_t raw[4], tail_next[kGroups], scale_next[kGroups], scale = 0, flags = 0;
@@ -853,43 +852,41 @@ void wide_kernel(const ProjArgs A) {
   // bytes of stage s, J = s % 4 (past the end: of the last group)
   auto load_raw = [&](int s, auto jc) {
     constexpr int J = decltype(jc)::value;
-    const int g = min(g0 + s / S32, nG - 1);
-    const uint8_t *p = prow + (int64_t)g * B;
-    __builtin_memcpy(&raw[J], p + 6 * (J % S32) + 3 * hf, 4);
+    const int g = min(s / S32, nG - 1 - g0);
+    raw[J] = bytes.load4(poff, g * B + 6 * (J % S32));
     if constexpr (J % S32 == 0) {
-      if constexpr (G == 128) {
-        uint16_t v;
-        __builtin_memcpy(&v, p + 24, 2);
-        tail_next[J / S32] = v;
-      } else {
-        tail_next[J / S32] = p[12];
-      }
-      scale_next[J / S32] = srow[g];
+      tail_next[J / S32] = G == 128 ? bytes.load2(toff, g * B + 24) : bytes.load1(toff, g * B + 12);
+      scale_next[J / S32] = values.load2(soff, g * 2);
     }
   };
   const L lut(kLutOff, lane);
   const uint32_t put0 = rows_at((uint32_t)sr, 2u * hf), put1 = rows_at((uint32_t)sr, 2u * hf + 1u);
-  // codes of the stage whose bytes are raw[J], J = its index % 4, -> slot
-  auto decode = [&](auto jc, uint32_t slot) {
+  // codes of the stage whose bytes are raw[J], J = its index % 4, -> slot: the
+  // table's entries first, some work of others' between, then the rest
+  auto look_up = [&](auto jc) {
     constexpr int J = decltype(jc)::value;
     if constexpr (J % S32 == 0) {
       scale = scale_next[J / S32] * 0x10001u;
       left = leftover_pool<G>(smem, lut, tail_next[J / S32], flags);
     }
+    return look_up_eighth(smem, lut, raw[J]);
+  };
+  auto decode = [&](auto jc, const Eighth &t, uint32_t slot) {
+    constexpr int J = decltype(jc)::value;
     u32x4 c0, c1;
-    decode_eighth(smem, lut, raw[J], left, (uint32_t)(2 * (J % S32) + hf), scale, c0, c1, flags);
+    decode_eighth(t, left, (uint32_t)(2 * (J % S32) + hf), scale, c0, c1, flags);
     *(lds_u32x4 *)(smem + slot + put0) = c0;
     *(lds_u32x4 *)(smem + slot + put1) = c1;
   };
 
-  QS qs;
-  qs.init_rows(tid, (uint32_t)A.K, [&](int r) -> int64_t { return q0 + r < A.M ? r : -1; });
-  const uint16_t *qbase = A.x + q0 * A.K + (int64_t)g0 * G;
+  // a stage of x is the image of its slot; past the end the last one again
+  const uint16_t *qbase = A.x + q0 * A.K + (int64_t)g0 * S32 * (kWideQ * kKS);
+  const uint32_t xoff = 16u * (uint32_t)tid;
   int xput = 0;  // slot of the next request
   auto request = [&](int s, int i) {
-    qs.load_tracked(i, qbase + (int64_t)s * kKS, smem + kQOff + (uint32_t)xput * QS::kSlot, (uint32_t)wv,
-                    s < S ? 1 : 0);
-    if (i == QS::kLoads - 1) xput = xput == kWideX - 1 ? 0 : xput + 1;
+    dma16_tracked(qbase + (int64_t)min(s, S - 1) * (kWideQ * kKS) + i * (8 * kWideThreads),
+                  smem + kQOff + (uint32_t)xput * kQSlot + 16u * (uint32_t)(i * kWideThreads + 64 * wv), xoff);
+    if (i == kXLoads - 1) xput = xput == kWideX - 1 ? 0 : xput + 1;
   };
 
   // ---- prologue: bytes of stages 0 .. 6, x of 0 .. 3, codes of 0 .. 2 ----
@@ -900,14 +897,14 @@ void wide_kernel(const ProjArgs A) {
 #pragma unroll
   for (int s = 0; s < kWideX - 1; ++s)
 #pragma unroll
-    for (int i = 0; i < QS::kLoads; ++i) request(s, i);
+    for (int i = 0; i < kXLoads; ++i) request(s, i);
   L::build(smem + kLutOff, tid, kWideThreads);
   __syncthreads();
-  decode(Int<0>{}, 0);
+  decode(Int<0>{}, look_up(Int<0>{}), 0);
   load_raw(4, Int<0>{});
-  decode(Int<1>{}, kPSlot);
+  decode(Int<1>{}, look_up(Int<1>{}), kPSlot);
   load_raw(5, Int<1>{});
-  decode(Int<2>{}, 2 * kPSlot);
+  decode(Int<2>{}, look_up(Int<2>{}), 2 * kPSlot);
   load_raw(6, Int<2>{});
 
   Frags<kRows, kWideP, TP> pf;
@@ -920,7 +917,11 @@ void wide_kernel(const ProjArgs A) {
 #pragma unroll
     for (int b = 0; b < TQ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
   bf16x8 pa[TP], qa[TQ], qb[TQ];
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  // a wait that the compiler sees: inside the loop it then counts only the
+  // loop's own loads, instead of waiting, on every pass, for the newest ones in
+  // case they were these
+  __builtin_amdgcn_s_waitcnt(0);
+  asm volatile("s_barrier" ::: "memory");
 #pragma unroll
   for (int b = 0; b < TQ; ++b) qa[b] = qf.read(smem, kQOff, b);
 #pragma unroll
@@ -930,24 +931,25 @@ void wide_kernel(const ProjArgs A) {
   auto stage = [&](int s, auto jc, bf16x8(&qc)[TQ], bf16x8(&qn)[TQ]) {
     constexpr int J = decltype(jc)::value;  // s % 4
     const uint32_t pn = (uint32_t)((J + 1) % kWideC) * kPSlot;
-    const uint32_t qn0 = kQOff + (uint32_t)xget * QS::kSlot;
+    const uint32_t qn0 = kQOff + (uint32_t)xget * kQSlot;
     xget = xget == kWideX - 1 ? 0 : xget + 1;
-    __builtin_amdgcn_sched_barrier(0);
+    Eighth next;
 #pragma unroll
     for (int a = 0; a < TP; ++a) {
+      // rows stay apart: reads spread between the MFMAs, the table's entries
+      // three rows before their use
+      __builtin_amdgcn_sched_barrier(0);
+      if (a == 0) next = look_up(Int<(J + 3) % 4>{});
 #pragma unroll
       for (int b = 0; b < TQ; ++b) acc[a][b] = mfma32<true>(pa[a], qc[b], acc[a][b]);
-      if (a < TQ) qn[a] = qf.read(smem, qn0, a);
+      // the codes are written before the fragments of rows 4 .. 7 are read:
+      // when the last of those is used, in stage s + 1, the writes are done, a
+      // barrier before stage s + 2 reads them
+      if (a == 3) decode(Int<(J + 3) % 4>{}, next, (uint32_t)((J + 3) % kWideC) * kPSlot);
+      if (a >= 3 && a < 3 + TQ) qn[a - 3] = qf.read(smem, qn0, a - 3);
       pa[a] = pf.read(smem, pn, a);
-      if (a < QS::kLoads) request(s + kWideX - 1, a);
-      if (a == 3) {
-        decode(Int<(J + 3) % 4>{}, (uint32_t)((J + 3) % kWideC) * kPSlot);
-        load_raw(s + 7, Int<(J + 7) % 4>{});
-        // the codes are written before the fragments of rows 4 .. 7 are read:
-        // when the last of those is used, in stage s + 1, the writes are done,
-        // a barrier before stage s + 2 reads them
-        asm volatile("" ::: "memory");
-      }
+      if (a >= 1 && a <= kXLoads) request(s + kWideX - 1, a - 1);
+      if (a == 5) load_raw(s + 7, Int<(J + 7) % 4>{});
     }
     __builtin_amdgcn_sched_barrier(0);
     // x of stage s + 2 was requested in stage s - 2: at least the bytes of
@@ -1092,14 +1094,17 @@ __device__ __forceinline__ void f16_role(const PreArgs &A, int64_t first, int64_
                    ((g & 3) * 16 + (r & 15)) * 8) = *(u32x4 *)f;
       }
     } else {
-      uint16_t *o = A.xo + m * A.K + k0;
+      const uint32_t r = (uint32_t)(m & (kWideQ - 1));
+      const int64_t s0 = m / kWideQ * (A.K / kKS) + k0 / kKS;
       for (int e = tid; in && e < len / 16; e += threads) {
         const int g = e / (G / 16), part16 = e % (G / 16);
         _Float16 f[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) f[j] = f16_of(row[g * G + eighth_source<G>(part16, j)], shift);
-        *(u32x4 *)(o + 16 * e) = *(u32x4 *)f;
-        *(u32x4 *)(o + 16 * e + 8) = *(u32x4 *)(f + 8);
+        unsigned char *o = (unsigned char *)A.xo + (s0 + (e >> 1)) * (kWideQ * kKS * 2);
+        const uint32_t c = 2u * (e & 1);
+        *(u32x4 *)(o + rows_at(r, c)) = *(u32x4 *)f;
+        *(u32x4 *)(o + rows_at(r, c + 1)) = *(u32x4 *)(f + 8);
       }
     }
   }
@@ -1174,7 +1179,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
     // a tile a CU; K is split while every block keeps 64 stages
     while (wide_tiles * p.splits < 160 && nG / (2 * p.splits) * (G / 32) >= 64) p.splits *= 2;
     p.blocks = wide_tiles * p.splits;
-    p.x = round16(M * K * 2);
+    p.x = ceil_div(M, kWideQ) * kWideQ * K * 2;  // rows past M are never read back
     p.shift = round16(M * 4);
   } else {
     p.kind = kMid;

@@ -225,17 +225,8 @@ __device__ __forceinline__ void product(const TrainArgs &A, int block, int grid,
     advance();
   };
 
-  // Two neighbouring 16-row tiles of P: lane (l, h) has rows 4 h .. 4 h + 3 of
-  // each; after the exchange rows 8 (h / 2) .. + 7 of the first (h even) or the
-  // second, so that a row of the output gets 64 bytes at once.
   const int h = lane >> 4, l = lane & 15;
-  auto pack8 = [&](f32x4 v, f32x4 w) {
-    uint32_t d[4] = {pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(w[0], w[1]), pack2(w[2], w[3])};
-    swap_rows(d[0], d[2]);
-    swap_rows(d[1], d[3]);
-    return u32x4{d[0], d[1], d[2], d[3]};
-  };
-  const int p8 = 16 * (h & 1) + 8 * (h >> 1);  // where a lane's eight rows start
+  const int p8 = pack8_row(lane);
   // All of a wave's columns and rows are inside and aligned: returns the
   // number of stores issued, which every such wave issues alike; else 0.
   auto store = [&](const Item &t) -> int {

@@ -56,6 +56,30 @@ __device__ __forceinline__ void dma16_tracked(const void *base, lds_bytes *dst, 
 #endif
 }
 
+// Loads at a scalar address, plus a lane's offset, plus a scalar one: no lane
+// holds or adds 64-bit addresses.  Any alignment.
+struct Scalar {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __amdgpu_buffer_rsrc_t rs;
+  __device__ __forceinline__ explicit Scalar(const void *base)
+      : rs(__builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, 0x7FFFFFFF, 0x00020000)) {}
+  __device__ __forceinline__ uint32_t load4(uint32_t off, int at) const {
+    return __builtin_amdgcn_raw_buffer_load_b32(rs, (int)off, at, 0);
+  }
+  __device__ __forceinline__ uint32_t load2(uint32_t off, int at) const {
+    return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)off, at, 0);
+  }
+  __device__ __forceinline__ uint32_t load1(uint32_t off, int at) const {
+    return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, (int)off, at, 0);
+  }
+#else
+  __device__ explicit Scalar(const void *) {}
+  __device__ uint32_t load4(uint32_t, int) const { return 0; }
+  __device__ uint32_t load2(uint32_t, int) const { return 0; }
+  __device__ uint32_t load1(uint32_t, int) const { return 0; }
+#endif
+};
+
 // Unit exchange of a kCols slot: the 32-byte unit u of k sits at u ^ this.
 __device__ __forceinline__ uint32_t cols_swz(uint32_t k) { return (k & 3u) | ((k >> 1) & 4u); }
 
@@ -115,12 +139,6 @@ struct Stream {
       krow[i] = k;
       off[i] = (int)(8u * c) < cols ? k * ld * 2u + 16u * c : kNoRow;
     }
-  }
-  // As load, with dma16_tracked.
-  __device__ __forceinline__ void load_tracked(int i, const void *base, lds_bytes *slot, uint32_t wave,
-                                               int krem) const {
-    static_assert(KIND == kRows, "");
-    dma16_tracked(base, slot + 16u * ((uint32_t)(i * NT) + 64u * wave), krem > 0 ? off[i] : kNoRow);
   }
   // Request i of the stage at `base` into `slot`; k rows >= krem read as
   // zeros.
@@ -208,6 +226,21 @@ __device__ __forceinline__ void swap_rows(uint32_t &a, uint32_t &b) {
   a = r[0];
   b = r[1];
 #endif
+}
+
+// Two neighbouring 16-row tiles of P as bf16: lane (l, h) holds rows 4 h ..
+// 4 h + 3 of each; after the exchange eight rows in order, from row
+// pack8_row(lane) of the two tiles' 32 on, so that a row of the output gets 64
+// bytes at once.
+__device__ __forceinline__ u32x4 pack8(f32x4 v, f32x4 w) {
+  uint32_t d[4] = {pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(w[0], w[1]), pack2(w[2], w[3])};
+  swap_rows(d[0], d[2]);
+  swap_rows(d[1], d[3]);
+  return u32x4{d[0], d[1], d[2], d[3]};
+}
+__device__ __forceinline__ int pack8_row(int lane) {
+  const int h = lane >> 4;
+  return 16 * (h & 1) + 8 * (h >> 1);
 }
 
 // Tile of block b of a launch: consecutive tiles run on one XCD (blocks go to

@@ -207,20 +207,25 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
   return v;
 }
 
-// Eighth e of a group: the 16 codes of three bytes (in `word`) and left-over
-// code e, times the scale (twice, packed), as f16: exact, codes are -1, 0, 1.
+// Eighth e of a group is the 16 codes of three bytes (in `word`) and left-over
+// code e.  Its entries:
+struct Eighth {
+  u32x2 a, b, c;
+};
 template <class L>
-__device__ __forceinline__ void decode_eighth(lds_bytes *smem, const L &lut, uint32_t word, u32x2 left,
-                                              uint32_t e, uint32_t scale2, u32x4 &c0, u32x4 &c1,
-                                              uint32_t &flags) {
-  const u32x2 a = lut.read(smem, word, 0), b = lut.read(smem, word, 1),
-              c = lut.read(smem, word, 2);
-  flags |= a.y | b.y | c.y;
+__device__ __forceinline__ Eighth look_up_eighth(lds_bytes *smem, const L &lut, uint32_t word) {
+  return Eighth{lut.read(smem, word, 0), lut.read(smem, word, 1), lut.read(smem, word, 2)};
+}
+// Its codes times the scale (twice, packed), as f16: exact, codes are -1, 0, 1.
+__device__ __forceinline__ void decode_eighth(const Eighth &t, u32x2 left, uint32_t e, uint32_t scale2,
+                                              u32x4 &c0, u32x4 &c1, uint32_t &flags) {
+  flags |= t.a.y | t.b.y | t.c.y;
   const uint32_t one = __builtin_amdgcn_perm(left.y, left.x, 0x0C0C0C00u + e);
   const f16x2 s = __builtin_bit_cast(f16x2, scale2);
-  c0 = u32x4{scaled(pair01(a), s), scaled(pair23(a), s),
-             scaled(__builtin_amdgcn_perm(one, a.y, 0x040C000Cu), s), scaled(pair01(b), s)};
-  c1 = u32x4{scaled(pair23(b), s), scaled(pair44(b, c), s), scaled(pair01(c), s), scaled(pair23(c), s)};
+  c0 = u32x4{scaled(pair01(t.a), s), scaled(pair23(t.a), s),
+             scaled(__builtin_amdgcn_perm(one, t.a.y, 0x040C000Cu), s), scaled(pair01(t.b), s)};
+  c1 = u32x4{scaled(pair23(t.b), s), scaled(pair44(t.b, t.c), s), scaled(pair01(t.c), s),
+             scaled(pair23(t.c), s)};
 }
 
 // Where in its group element j of eighth e comes from.
