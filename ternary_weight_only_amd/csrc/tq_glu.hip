@@ -985,6 +985,7 @@ void wide_kernel(const ProjArgs A) {
   }
   const bool vec = (A.N & 3) == 0 && (reinterpret_cast<uintptr_t>(A.out) & 15) == 0;
   const int nw = n0 + wp * HP;  // first row of this wave
+  const bool rows8 = nw + HP <= A.N && (A.N & 7) == 0 && (reinterpret_cast<uintptr_t>(A.out) & 15) == 0;
   auto store_f32 = [&](float *y, int64_t m, int n, f32x4 v, bool aligned) {
     float *o = y + m * A.N + n;
     if (aligned && n < A.N) {
@@ -1005,8 +1006,8 @@ void wide_kernel(const ProjArgs A) {
 #pragma unroll
   for (int b = 0; b < TQ; ++b) {
     const int64_t m = mq + 16 * b;
-    if (m >= A.M) continue;
     if (A.splits > 1) {
+      if (m >= A.M) continue;
 #pragma unroll
       for (int i = 0; i < NB; ++i)
 #pragma unroll
@@ -1015,21 +1016,25 @@ void wide_kernel(const ProjArgs A) {
                     acc[a + i * (TP / NB)][b], (A.N & 3) == 0);
     } else if constexpr (NB == 2) {
 #pragma unroll
-      for (int a = 0; a < TP / 2; ++a) {
-        const int n = nw + 16 * a + 4 * q;
-        f32x4 v;
+      for (int a = 0; a < TP / 2; a += 2) {
+        f32x4 v[2];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = act_value<ACT>(acc[a][b][r]) * acc[a + TP / 2][b][r];
-        uint16_t *o = (uint16_t *)A.out + m * A.N + n;
-        if (vec && n < A.N) {
-          store4(o, v);
-        } else {
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (n + r < A.N) o[r] = f32_to_bf16(v[r]);
+          for (int r = 0; r < 4; ++r) v[i][r] = act_value<ACT>(acc[a + i][b][r]) * acc[a + i + TP / 2][b][r];
+        uint16_t *o = (uint16_t *)A.out + m * A.N + nw + 16 * a;
+        if (rows8) {  // the same for the wave: lanes exchange values
+          const u32x4 d = pack8(v[0], v[1]);
+          if (m < A.M) *(u32x4 *)(o + pack8_row(lane)) = d;
+        } else if (m < A.M) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              if (nw + 16 * (a + i) + 4 * q + r < A.N) o[16 * i + 4 * q + r] = f32_to_bf16(v[i][r]);
         }
       }
-    } else {
+    } else if (m < A.M) {
 #pragma unroll
       for (int a = 0; a < TP; ++a) store_f32((float *)A.out, m, nw + 16 * a + 4 * q, acc[a][b], vec);
     }
