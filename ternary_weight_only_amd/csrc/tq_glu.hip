@@ -86,8 +86,8 @@ __device__ __forceinline__ Pieces split_t(const ProjArgs &A, int64_t m, int r, b
     const f32x4 *t = (const f32x4 *)(A.t + m * A.R + r);
     lo = t[0];
     hi = t[1];
-    if (A.tsplits > 1) {
-      const f32x4 *u = (const f32x4 *)(A.t + (A.M + m) * A.R + r);
+    for (int s = 1; s < A.tsplits; ++s) {
+      const f32x4 *u = (const f32x4 *)(A.t + (s * A.M + m) * A.R + r);
       lo += u[0];
       hi += u[1];
     }
@@ -192,6 +192,7 @@ constexpr int kPreThreads = 1024, kPreWaves = 16;
 constexpr int kRowLds = 16384;    // elements of a row of x in LDS
 constexpr int kShrinkTile = 256;  // rows among which equal adapters are gathered
 constexpr int kShrinkRanks = 4;   // tiles of 16 ranks that share a read of x
+constexpr int kPreTiles = 2;      // tiles of 16 rows of a unit of pre_kernel, one in few_kernel
 
 struct PreArgs {
   const uint16_t *x, *a;
@@ -207,22 +208,43 @@ struct PreArgs {
   int32_t *status;
 };
 
-// t of one unit: up to 16 rows of one adapter, 16 RT ranks.  The rows of a tile
-// that name the same adapter are numbered in order and cut into units of 16,
-// so rows in any order share the adapter's A.  One split of K; its waves
-// share the split, and their sums are added in order.
-template <int RT>
+// t of one unit: up to 16 CT rows of one adapter, 16 RT ranks.  The rows of a
+// tile that name the same adapter are numbered in order and cut into units, so
+// rows in any order share the adapter's A.  One split of K, which the waves
+// share; their sums are added in order.  A wave's steps of 32 k go through a
+// ring of its own in LDS, where 4 lanes bring a row's 64 bytes: loads straight
+// into the matrix cores' operands have 16 lanes on 16 rows, 16 bytes each (64
+// ranks of 1900 rows of 14336: 63 us that way, 52 this way, by itself).
+constexpr int kShrinkRing = 3;
+template <int RT, int CT>
+constexpr int shrink_waves() {  // as many as have room, two blocks a CU if CT is 2
+  constexpr int n = ((CT == 2 ? 72 : 144) << 10) / (kShrinkRing * (RT + CT) * 1024);
+  return n < kPreWaves ? n : kPreWaves;
+}
+template <int RT, int CT>
+constexpr int shrink_lds() {
+  return 4 * (kShrinkTile + 16 * CT + 32) + shrink_waves<RT, CT>() * kShrinkRing * (RT + CT) * 1024;
+}
+template <int RT, int CT>
 __device__ __forceinline__ void shrink_role(const PreArgs &A, int64_t blk, unsigned char *smem_raw) {
+  constexpr int kUnit = 16 * CT, L = RT + CT, W = shrink_waves<RT, CT>();
+  constexpr uint32_t kSlot = L * 1024, kRingOff = 4 * (kShrinkTile + kUnit + 32);
+  static_assert(kRingOff % 16 == 0, "");
   int *ids = (int *)smem_raw;                       // [256]
-  int *rows = ids + kShrinkTile;                    // [16]
-  int *info = rows + 16;                            // adapter, leader's rank
+  int *rows = ids + kShrinkTile;                    // [kUnit]
+  int *info = rows + kUnit;                         // adapter, leader's rank
   int *counts = info + 4;                           // [16] leaders of each wave
-  float *red = (float *)(counts + 28);              // [16][64][4]
-  const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6, l = lane & 15, q = lane >> 4;
-  const int split = (int)(blk % A.tsplits);
+  float *red = (float *)(smem_raw + kRingOff);      // [W][RT][CT][64][4], after the rings
+  const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // the same for the block: kept in scalar registers
+  const int split = __builtin_amdgcn_readfirstlane((int)(blk % A.tsplits));
   blk /= A.tsplits;
-  const int rt = (int)(blk % A.rtiles), unit = (int)(blk / A.rtiles % A.units);
-  const int64_t m0 = blk / A.rtiles / A.units * kShrinkTile;
+  const int rt = __builtin_amdgcn_readfirstlane((int)(blk % A.rtiles));
+  blk /= A.rtiles;
+  const int64_t tiles = ceil_div(A.M, kShrinkTile);
+  const int unit = (int)(blk / tiles);  // slowest: the last ones may be absent
+  const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane((int)(blk % tiles)) * kShrinkTile;
   const int nrows = (int)min((int64_t)kShrinkTile, A.M - m0);
   int id = -1;
   if (tid < nrows) {
@@ -233,13 +255,19 @@ __device__ __forceinline__ void shrink_role(const PreArgs &A, int64_t blk, unsig
     }
   }
   if (tid < kShrinkTile) ids[tid] = id;
-  if (tid < 16) rows[tid] = -1;
+  if (tid < kUnit) rows[tid] = -1;
   if (tid == 0) info[0] = -1;
   __syncthreads();
   int rank = 0;  // among the rows of this adapter
-  if (id >= 0)
-    for (int j = 0; j < tid; ++j) rank += ids[j] == id;
-  const bool leads = id >= 0 && rank % 16 == 0;
+  if (id >= 0) {
+#pragma unroll 4
+    for (int j = 0; j <= tid / 4; ++j) {
+      const u32x4 other = ((const u32x4 *)ids)[j];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) rank += (int)other[i] == id && 4 * j + i < tid;
+    }
+  }
+  const bool leads = id >= 0 && rank % kUnit == 0;
   const uint64_t mask = __ballot(leads);
   if (lane == 0) counts[wv] = __popcll(mask);
   __syncthreads();
@@ -250,61 +278,92 @@ __device__ __forceinline__ void shrink_role(const PreArgs &A, int64_t blk, unsig
     info[1] = rank;
   }
   __syncthreads();
-  const int a = info[0];
+  const int a = __builtin_amdgcn_readfirstlane(info[0]);
   if (a < 0) return;  // fewer units than this
-  if (id == a && rank / 16 == info[1] / 16) rows[rank % 16] = tid;
+  if (id == a && rank / kUnit == info[1] / kUnit) rows[rank % kUnit] = tid;
   __syncthreads();
 
-  // columns: the unit's rows (the first one in place of absent ones); rows:
-  // ranks 16 rt + l
-  const int own = rows[l], mr = own < 0 ? rows[0] : own;
-  const uint16_t *xr = A.x + (m0 + mr) * A.K + 8 * q;
-  const uint16_t *ar[RT];
+  if (wv < W) {
+    // slot rows: the unit's rows (the first one in place of absent ones), then
+    // ranks 16 RT rt on, zeros past R
+    lds_bytes *ring = (lds_bytes *)smem_raw + kRingOff + (uint32_t)wv * (kShrinkRing * kSlot);
+    const uint32_t ld = 2u * (uint32_t)A.K, sl = lane >> 2;
+    const uint32_t at = 16u * ((lane & 3u) ^ rows_swz(sl));  // rows 16 apart alike
+    const uint16_t *xb = A.x + m0 * A.K, *ab = A.a + (int64_t)a * A.R * A.K;
+    uint32_t off[L];
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
-    ar[i] = A.a + ((int64_t)a * A.R + min(16 * (RT * rt + i) + l, A.R - 1)) * A.K + 8 * q;
-  f32x4 acc[RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int steps = A.K / 32;
-  const int s0 = (int)((int64_t)steps * split / A.tsplits), s1 = (int)((int64_t)steps * (split + 1) / A.tsplits);
-  constexpr int kAhead = RT == 1 ? 8 : 4;  // steps requested together
-  for (int s = s0 + wv; s < s1; s += kPreWaves * kAhead) {
-    // steps past the end read the last one and add nothing
-    bf16x8 av[kAhead][RT], xv[kAhead];
-#pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      const int sj = min(s + kPreWaves * j, steps - 1);
-      xv[j] = *(const bf16x8 *)(xr + 32 * sj);
-#pragma unroll
-      for (int i = 0; i < RT; ++i) av[j][i] = *(const bf16x8 *)(ar[i] + 32 * sj);
+    for (int c = 0; c < CT; ++c) {
+      const int own = rows[16 * c + sl];
+      off[c] = (uint32_t)(own < 0 ? rows[0] : own) * ld + at;
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j)
-      if (s + kPreWaves * j < s1)
+    for (int i = 0; i < RT; ++i) {
+      const int r = 16 * (RT * rt + i) + (int)sl;
+      off[CT + i] = r < A.R ? (uint32_t)r * ld + at : kNoRow;
+    }
+    const int steps = A.K / 32;
+    const int s0 = steps * split / A.tsplits, s1 = steps * (split + 1) / A.tsplits;
+    // in pairs: 128 consecutive bytes of a row
+    const int share = (s1 - s0 + 2 * W - 1) / (2 * W) * 2;
+    const int first = min(s0 + wv * share, s1), n = min(first + share, s1) - first;
+    auto request = [&](int s, int slot) {  // steps past the end: the last one again, unused
+      const int k = __builtin_amdgcn_readfirstlane(32 * max(0, first + min(s, n - 1)));
 #pragma unroll
-        for (int i = 0; i < RT; ++i) acc[i] = mfma32<false>(av[j][i], xv[j], acc[i]);
+      for (int i = 0; i < L; ++i)
+        dma16((i < CT ? xb : ab) + k, ring + (uint32_t)slot * kSlot + 1024u * (uint32_t)i, off[i]);
+    };
+    f32x4 acc[RT][CT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) acc[i][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < kShrinkRing - 1; ++s) request(s, s);
+    const uint32_t get = rows_at((uint32_t)l, (uint32_t)q);
+    int slot = 0, put = kShrinkRing - 1;
+    for (int s = 0; s < n; ++s) {
+      // the slot before has been read; then step s is here when only the
+      // newest kShrinkRing - 1 are not
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      request(s + kShrinkRing - 1, put);
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"((kShrinkRing - 1) * L) : "memory");
+      bf16x8 v[L];
+#pragma unroll
+      for (int i = 0; i < L; ++i)
+        v[i] = *(lds_bf16x8_c *)(ring + (uint32_t)slot * kSlot + 1024u * (uint32_t)i + get);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[i][c] = mfma32<false>(v[CT + i], v[c], acc[i][c]);
+      put = slot;
+      slot = slot == kShrinkRing - 1 ? 0 : slot + 1;
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __syncthreads();  // no ring is in use
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) *(f32x4 *)(red + (((wv * RT + i) * CT + c) * 64 + lane) * 4) = acc[i][c];
+  } else {
+    __syncthreads();
   }
+  __syncthreads();
+  for (int o = tid; o < RT * CT * 256; o += kPreThreads) {
+    float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    *(f32x4 *)(red + 4 * tid) = acc[i];
-    __syncthreads();
-    if (tid < 256) {
-      float sum = 0.f;
-      for (int w = 0; w < kPreWaves; ++w) sum += red[w * 256 + tid];
-      const int ol = tid >> 2, rr = 16 * (RT * rt + i) + 4 * (ol >> 4) + (tid & 3), row = rows[ol & 15];
-      if (row >= 0 && rr < A.R) A.t[((int64_t)split * A.M + m0 + row) * A.R + rr] = A.scaling[a] * sum;
-    }
-    __syncthreads();
+    for (int w = 0; w < W; ++w) sum += red[w * (RT * CT * 256) + o];
+    const int i = o / (CT * 256), c = o / 256 % CT, ol = o >> 2 & 63;
+    const int rr = 16 * (RT * rt + i) + 4 * (ol >> 4) + (o & 3), row = rows[16 * c + (ol & 15)];
+    if (row >= 0 && rr < A.R) A.t[((int64_t)split * A.M + m0 + row) * A.R + rr] = A.scaling[a] * sum;
   }
 }
 
 // The share of one of A.shrink_blocks blocks of kPreThreads.
-template <int RT>
+template <int RT, int CT>
 __device__ __forceinline__ void shrink_all(const PreArgs &A, int block, unsigned char *smem) {
   const int64_t work = ceil_div(A.M, kShrinkTile) * A.units * A.rtiles * A.tsplits;
   for (int64_t w = block; w < work; w += A.shrink_blocks) {
-    shrink_role<RT>(A, w, smem);
+    shrink_role<RT, CT>(A, w, smem);
     __syncthreads();
   }
 }
@@ -355,7 +414,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
   int block = (int)blockIdx.x;
   if constexpr (RT > 0) {
     if (block < P.shrink_blocks) {
-      shrink_all<RT>(P, block, smem_raw);
+      shrink_all<RT, 1>(P, block, smem_raw);
       return;
     }
     block -= P.shrink_blocks;
@@ -422,7 +481,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
       uint32_t top = 0;
 #pragma unroll 4
       for (int k = 8 * (64 * part + lane); k < len; k += 512 * parts)
-        top = top_of(top, xs + (int64_t)m * A.K + k);
+        top = top_of(top, *(const u32x4 *)(xs + (int64_t)m * A.K + k));
       top = wave_max(top);
       if (lane == 0) *top_at(part, m) = top;
     }
@@ -1045,14 +1104,28 @@ void wide_kernel(const ProjArgs A) {
 // before the product, in a launch of its own
 // ---------------------------------------------------------------------------
 
+// The first kRowLds / rpb elements of a row, 16 a thread; zeros past its end.
+__device__ __forceinline__ void load_row(const PreArgs &A, int64_t first, u32x4 (&v)[2]) {
+  const int threads = kPreThreads / A.rpb, tid = threadIdx.x % threads;
+  const int64_t m = first + threadIdx.x / threads;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int k = 8 * (tid + i * threads);
+    v[i] = u32x4{0u, 0u, 0u, 0u};
+    if (m < A.M && k < A.K) v[i] = *(const u32x4 *)(A.x + m * A.K + k);
+  }
+}
+
 // Row m of x as f16 times 2^shift[m], for mid_kernel in its fragments
 // [chunk][quad][step][16-row tile][lane][8] (rows past M and groups past the
 // last are zeros), for wide_kernel in rows, in the order of its codes.
 // Rows pass through LDS, from which their elements are picked; a block takes
-// `rpb` rows at a time (1, 2 or 4, so that they fit), threads / rpb each.
+// `rpb` rows at a time (1, 2 or 4, so that they fit), threads / rpb each.  `v`
+// is load_row of these rows and, on return, of those `step` on, which are on
+// their way while these are converted.
 template <int G, bool FRAG>
-__device__ __forceinline__ void f16_role(const PreArgs &A, int64_t first, int64_t rows_in_all,
-                                         unsigned char *smem_raw) {
+__device__ __forceinline__ void f16_role(const PreArgs &A, int64_t first, int64_t step, int64_t rows_in_all,
+                                         u32x4 (&v)[2], unsigned char *smem_raw) {
   uint32_t *tops = (uint32_t *)smem_raw;             // [16]
   const int threads = kPreThreads / A.rpb, room = kRowLds / A.rpb;
   const int tid = threadIdx.x % threads, part = threadIdx.x / threads;
@@ -1062,12 +1135,14 @@ __device__ __forceinline__ void f16_role(const PreArgs &A, int64_t first, int64_
   const bool in = m < A.M;
   __syncthreads();  // the rows before have been read
   uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    top = top_of(top, v[i]);
+    *(u32x4 *)(row + 8 * (tid + i * threads)) = v[i];
+  }
   if (in)
-#pragma unroll 2
-    for (int k = 8 * tid; k < A.K; k += 8 * threads) {
-      top = top_of(top, xr + k);
-      if (k < room) *(u32x4 *)(row + k) = *(const u32x4 *)(xr + k);
-    }
+    for (int k = room + 8 * tid; k < A.K; k += 8 * threads) top = top_of(top, *(const u32x4 *)(xr + k));
+  if (first + step < rows_in_all) load_row(A, first + step, v);
   top = wave_max(top);
   if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
   __syncthreads();
@@ -1118,20 +1193,28 @@ __device__ __forceinline__ void f16_role(const PreArgs &A, int64_t first, int64_
 constexpr int64_t kMaxPreBlocks = 1 << 16;  // of a role; each strides over its work
 constexpr int kPreFrag = 1, kPreRows = 2;
 
+// The last A.shrink_blocks blocks make t (16 RT ranks at a time, none if 0),
+// the others convert rows; two blocks are on a CU.  Converting streams x once
+// in and once out and takes its bytes' time (1900 rows of 14336: 22 us, 109
+// MB); making t waits for loads, and runs in the gaps (together 55 us with 64
+// ranks, 39 with 16; in launches of their own 67 and 47).
 template <int G, int MODE, int RT>
-__global__ __launch_bounds__(kPreThreads) void pre_kernel(const PreArgs A) {
-  constexpr int kShrinkLds = 4 * (kShrinkTile + 48) + 16 * kPreThreads;
-  constexpr int kRowBytes = 64 + 2 * kRowLds;
+__global__ __launch_bounds__(kPreThreads) __attribute__((amdgpu_waves_per_eu(8, 8)))
+void pre_kernel(const PreArgs A) {
+  constexpr int kShrinkLds = RT ? shrink_lds<RT, kPreTiles>() : 0, kRowBytes = 64 + 2 * kRowLds;
   __shared__ __align__(16) unsigned char smem[kShrinkLds > kRowBytes ? kShrinkLds : kRowBytes];
-  if ((int)blockIdx.x < A.shrink_blocks) {
-    shrink_all<RT>(A, (int)blockIdx.x, smem);
-    return;
+  const int row_blocks = (int)gridDim.x - A.shrink_blocks;
+  if constexpr (RT > 0) {
+    if ((int)blockIdx.x >= row_blocks) {
+      shrink_all<RT, kPreTiles>(A, (int)blockIdx.x - row_blocks, smem);
+      return;
+    }
   }
-  const int64_t blk = (int64_t)blockIdx.x - A.shrink_blocks;
-  const int64_t blocks = (int64_t)gridDim.x - A.shrink_blocks;
+  const int64_t blk = blockIdx.x, step = (int64_t)row_blocks * A.rpb;
   const int64_t rows = MODE == kPreFrag ? ceil_div(A.M, kMidRows) * kMidRows : A.M;
-  for (int64_t m = blk * A.rpb; m < rows; m += blocks * A.rpb)
-    f16_role<G, MODE == kPreFrag>(A, m, rows, smem);
+  u32x4 v[2];
+  load_row(A, blk * A.rpb, v);
+  for (int64_t m = blk * A.rpb; m < rows; m += step) f16_role<G, MODE == kPreFrag>(A, m, step, rows, v, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -1156,7 +1239,11 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
   const int64_t nG = K / G;
   p.splits = 1;
   if (R) {
-    p.tsplits = M <= 256 && K > 4096 ? 2 : 1;  // where the blocks are few
+    // where the units are few K is split, while a wave keeps several steps
+    const bool few = M <= kFewRows && K >= 128;
+    const int64_t units = ceil_div(M, few ? 16 : 16 * kPreTiles) * ceil_div(R, 16 * shrink_tiles(R));
+    p.tsplits = 1;
+    while (p.tsplits < (few ? 2 : 4) && units * p.tsplits < 128 && K / p.tsplits > 4096) p.tsplits *= 2;
     p.t = round16(p.tsplits * M * R * 4);
   }
   const int64_t wide_tiles = ceil_div(NB * N, kWideP) * ceil_div(M, kWideQ);
@@ -1249,25 +1336,29 @@ void launch_proj(const Plan &p, ProjArgs a, PreArgs pre, void *workspace, hipStr
   if (NB == 1) {
     const int64_t tiles = ceil_div(a.M, kShrinkTile);
     const int64_t rows = std::min<int64_t>(a.M, kShrinkTile);
-    // units of a tile: one for each 16 rows and one more for each adapter
-    pre.units = (int)std::min(rows, ceil_div(rows, 16) + std::min<int64_t>(rows, a.adapters));
+    // units of a tile: one for each 16 (32) rows and one more for each adapter
+    const int64_t unit = p.kind == kFew ? 16 : 16 * kPreTiles;
+    pre.units = (int)std::min(rows, ceil_div(rows, unit) + std::min<int64_t>(rows, a.adapters));
     pre.rtiles = (int)ceil_div(a.R, 16 * shrink_tiles(a.R));
     if (a.adapters == 0) pre.units = pre.rtiles = pre.tsplits = 1;  // the ids are still checked
     pre.shrink_blocks = (int)std::min(kMaxPreBlocks, tiles * pre.units * pre.rtiles * pre.tsplits);
   }
-  const int64_t sb = pre.shrink_blocks;
   pre.rpb = a.K <= kRowLds / 4 ? 4 : a.K <= kRowLds / 2 ? 2 : 1;
-  auto prepare = [&](auto kernel, int64_t rows) {
-    const dim3 grid((unsigned)(sb + std::min(kMaxPreBlocks, ceil_div(rows, pre.rpb))));
-    hipLaunchKernelGGL(kernel, grid, dim3(kPreThreads), 0, stream, pre);
-  };
-  const bool ranks = NB == 1 && shrink_tiles(a.R) > 1;
-  if (p.kind == kWide) {
-    ranks ? prepare(pre_kernel<G, kPreRows, kShrinkRanks>, a.M) : prepare(pre_kernel<G, kPreRows, 1>, a.M);
-    a.x = pre.xo;
-  } else if (p.kind == kMid) {
-    const int64_t rows = p.chunks * kMidRows;
-    ranks ? prepare(pre_kernel<G, kPreFrag, kShrinkRanks>, rows) : prepare(pre_kernel<G, kPreFrag, 1>, rows);
+  if (p.kind != kFew) {
+    // two blocks a CU, each with a row on its way while it converts another; one
+    // beside those that make t
+    auto prepare = [&](auto kernel, int64_t rows) {
+      const int64_t convert = std::min<int64_t>(pre.shrink_blocks > 8 ? 256 : 512, ceil_div(rows, pre.rpb));
+      hipLaunchKernelGGL(kernel, dim3((unsigned)(convert + pre.shrink_blocks)), dim3(kPreThreads), 0, stream, pre);
+    };
+    const int64_t rows = p.kind == kWide ? a.M : p.chunks * kMidRows;
+    if constexpr (NB == 2)
+      p.kind == kWide ? prepare(pre_kernel<G, kPreRows, 0>, rows) : prepare(pre_kernel<G, kPreFrag, 0>, rows);
+    else if (shrink_tiles(a.R) > 1)
+      p.kind == kWide ? prepare(pre_kernel<G, kPreRows, kShrinkRanks>, rows)
+                      : prepare(pre_kernel<G, kPreFrag, kShrinkRanks>, rows);
+    else
+      p.kind == kWide ? prepare(pre_kernel<G, kPreRows, 1>, rows) : prepare(pre_kernel<G, kPreFrag, 1>, rows);
     a.x = pre.xo;
   }
   launch_product<G, NB, ACT>(p, a, pre, stream);

@@ -57,12 +57,15 @@ __device__ __forceinline__ void dma16_tracked(const void *base, lds_bytes *dst, 
 }
 
 // Loads at a scalar address, plus a lane's offset, plus a scalar one: no lane
-// holds or adds 64-bit addresses.  Any alignment.
+// holds or adds 64-bit addresses.  Any alignment; zeros past `bytes`.
 struct Scalar {
 #if defined(__HIP_DEVICE_COMPILE__)
   __amdgpu_buffer_rsrc_t rs;
-  __device__ __forceinline__ explicit Scalar(const void *base)
-      : rs(__builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, 0x7FFFFFFF, 0x00020000)) {}
+  __device__ __forceinline__ explicit Scalar(const void *base, uint32_t bytes = 0x7FFFFFFFu)
+      : rs(__builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000)) {}
+  __device__ __forceinline__ bf16x8 load16(uint32_t off, int at) const {
+    return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)off, at, 0));
+  }
   __device__ __forceinline__ uint32_t load4(uint32_t off, int at) const {
     return __builtin_amdgcn_raw_buffer_load_b32(rs, (int)off, at, 0);
   }
@@ -73,7 +76,8 @@ struct Scalar {
     return (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, (int)off, at, 0);
   }
 #else
-  __device__ explicit Scalar(const void *) {}
+  __device__ explicit Scalar(const void *, uint32_t = 0) {}
+  __device__ bf16x8 load16(uint32_t, int) const { return bf16x8{}; }
   __device__ uint32_t load4(uint32_t, int) const { return 0; }
   __device__ uint32_t load2(uint32_t, int) const { return 0; }
   __device__ uint32_t load1(uint32_t, int) const { return 0; }

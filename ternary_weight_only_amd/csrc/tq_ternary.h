@@ -190,12 +190,10 @@ __device__ __forceinline__ int f16_shift(uint32_t top) {
 }
 
 // The larger of `top` and the largest finite magnitude of eight bf16 values.
-__device__ __forceinline__ uint32_t top_of(uint32_t top, const uint16_t *p) {
-  uint16_t v[8];
-  *(u32x4 *)v = *(const u32x4 *)p;
+__device__ __forceinline__ uint32_t top_of(uint32_t top, u32x4 v) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const uint32_t b = v[j] & 0x7FFFu;
+    const uint32_t b = (j & 1 ? v[j / 2] >> 16 : v[j / 2]) & 0x7FFFu;
     top = b < 0x7F80u && b > top ? b : top;
   }
   return top;
