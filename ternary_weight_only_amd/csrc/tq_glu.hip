@@ -284,8 +284,7 @@ __device__ __forceinline__ void shrink_role(const PreArgs &A, int64_t blk, unsig
   __syncthreads();
 
   if (wv < W) {
-    // slot rows: the unit's rows (the first one in place of absent ones), then
-    // ranks 16 RT rt on, zeros past R
+    // slot rows: the unit's rows, then ranks 16 RT rt on; zeros for absent ones
     lds_bytes *ring = (lds_bytes *)smem_raw + kRingOff + (uint32_t)wv * (kShrinkRing * kSlot);
     const uint32_t ld = 2u * (uint32_t)A.K, sl = lane >> 2;
     const uint32_t at = 16u * ((lane & 3u) ^ rows_swz(sl));  // rows 16 apart alike
@@ -294,7 +293,7 @@ __device__ __forceinline__ void shrink_role(const PreArgs &A, int64_t blk, unsig
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
       const int own = rows[16 * c + sl];
-      off[c] = (uint32_t)(own < 0 ? rows[0] : own) * ld + at;
+      off[c] = own < 0 ? kNoRow : (uint32_t)own * ld + at;
     }
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -1234,6 +1233,32 @@ struct Plan {
   int64_t total() const { return x + shift + t + partial; }
 };
 
+// The number of splits of K that costs least, in us: blocks of `steps` steps,
+// `places` at a time, after `start`; a step takes `full` with every place taken,
+// down to `alone` with few.  Splits keep `least` steps, and their sums are
+// written, read and joined in a launch more.  The rates are measured ones:
+// wide_kernel takes 0.85 us for 32 k after 16 (28 where adapters follow); mid_kernel, for 256 k after 4, 2
+// alone and, with two blocks on every CU, 3.9 with one matrix and 5 with two.
+// (300 rows by 4096 x 14336, one matrix: mid, 3 splits, 96 us; 4 splits, in two
+// waves of blocks, 114; wide 120.  4000 rows by 1024 x 3584: mid 88, wide 153.
+// 700 rows by 4096 x 14336: wide 146, mid 180.)
+struct Split {
+  int splits;
+  double cost;
+};
+Split split_of(int64_t blocks, int64_t steps, int64_t least, int64_t places, double start, double alone,
+               double full, double sums) {
+  Split best{1, 1e30};
+  for (int s = 1; s == 1 || (s <= 16 && steps / s >= least); ++s) {
+    const int64_t waves = blocks * s / places, rest = blocks * s - waves * places;
+    const double last = rest ? alone + (full - alone) * rest / places : 0;
+    const double join = s > 1 ? 5 + s * sums * 8 / 5.2e6 : 0;
+    const double cost = start + (double)ceil_div(steps, s) * (waves * full + last) + join;
+    if (cost < best.cost) best = Split{s, cost};
+  }
+  return best;
+}
+
 Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
   Plan p{};
   const int64_t nG = K / G;
@@ -1266,23 +1291,26 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
     // a block a CU, beside those that make t
     const int64_t cus = 256 - (R ? std::min<int64_t>(64, M * p.tsplits) : 0);
     p.blocks = std::min(ceil_div(tiles, p.wt), std::max<int64_t>(1, cus / p.splits)) * p.splits;
-  } else if (M > 128 && wide_tiles >= 64) {
-    p.kind = kWide;
-    // a tile a CU; K is split while every block keeps 64 stages
-    while (wide_tiles * p.splits < 160 && nG / (2 * p.splits) * (G / 32) >= 64) p.splits *= 2;
-    p.blocks = wide_tiles * p.splits;
-    p.x = ceil_div(M, kWideQ) * kWideQ * K * 2;  // rows past M are never read back
-    p.shift = round16(M * 4);
   } else {
-    p.kind = kMid;
-    p.chunks = ceil_div(M, kMidRows);
-    const int64_t blocks = ceil_div(N, 128) * p.chunks;
-    // two blocks a CU; K is split while every block keeps two quads of groups
-    const int64_t quads = ceil_div(nG, 4);
-    while (blocks * p.splits < 384 && quads / (2 * p.splits) >= 2) p.splits *= 2;
-    p.blocks = blocks * p.splits;
-    p.x = p.chunks * kMidRows * quads * 4 * G * 2;
+    // the cheaper of the two by the model of split_of
+    const int64_t quads = ceil_div(nG, 4), chunks = ceil_div(M, kMidRows);
+    const double sums = (double)NB * M * N;
+    const Split wide = split_of(wide_tiles, K / 32, 16, 256, NB == 1 ? 28 : 16, 0.85, 0.85, sums);
+    const Split mid =
+        split_of(ceil_div(N, 128) * chunks, quads, 2, 512, 4, G / 32, (NB == 1 ? 3.9 : 5.0) * G / 64, sums);
+    // mid_kernel's results go out in runs of 32 bytes
+    p.kind = wide.cost < mid.cost + 1.4e-6 * M * N ? kWide : kMid;
     p.shift = round16(M * 4);
+    if (p.kind == kWide) {
+      p.splits = wide.splits;
+      p.blocks = wide_tiles * p.splits;
+      p.x = ceil_div(M, kWideQ) * kWideQ * K * 2;  // rows past M are never read back
+    } else {
+      p.splits = mid.splits;
+      p.chunks = chunks;
+      p.blocks = ceil_div(N, 128) * chunks * p.splits;
+      p.x = p.chunks * kMidRows * quads * 4 * G * 2;
+    }
   }
   if (p.splits > 1) p.partial = round16((int64_t)p.splits * NB * M * N * 4);
   return p;
