@@ -64,15 +64,16 @@ struct ProjArgs {
 // adapters
 // ---------------------------------------------------------------------------
 
-// The distinct adapters among the ids that a wave's lanes hold, as a mask of
-// the first lane of each.
-__device__ __forceinline__ uint64_t adapter_leaders(int id, int lane) {
-  bool first = id >= 0;
-  for (int j = 0; j < 63; ++j) {
-    const int other = __builtin_amdgcn_readlane(id, j);
-    if (j < lane && other == id) first = false;
+// The distinct adapters among the ids that a wave's lanes hold, as a mask of the first lane of each: the lanes of the first
+// one left are struck out in turn.
+__device__ __forceinline__ uint64_t adapter_leaders(int id) {
+  uint64_t left = __ballot(id >= 0), leaders = 0;
+  while (left) {
+    const int j = __builtin_ctzll(left);
+    leaders |= 1ull << j;
+    left &= ~__ballot(id == __builtin_amdgcn_readlane(id, j));
   }
-  return __ballot(first);
+  return leaders;
 }
 
 // Eight ranks of row m's t in three bf16 pieces (24 bits together); zeros
@@ -117,7 +118,7 @@ template <bool WROWS, int T, int C>
 __device__ __forceinline__ void add_adapters(const ProjArgs &A, int64_t m0, int n0, int id, int share,
                                              int mine, f32x4 (&acc)[T][C]) {
   const int lane = threadIdx.x & 63, l = lane & 15, q = lane >> 4;
-  const uint64_t leaders = adapter_leaders(id, lane);
+  const uint64_t leaders = adapter_leaders(id);
   int64_t n[T];
 #pragma unroll
   for (int t = 0; t < T; ++t) n[t] = min(n0 + 16 * t + l, A.N - 1);
