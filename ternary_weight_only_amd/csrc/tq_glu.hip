@@ -372,7 +372,7 @@ __device__ __forceinline__ void shrink_all(const PreArgs &A, int block, unsigned
 // up to 32 rows
 // ---------------------------------------------------------------------------
 
-constexpr int kFewRows = 32;
+constexpr int kFewRows = 32;           // two 16-row tiles of x
 constexpr int kFewWaves = 16;          // most waves of a block
 constexpr int kFewSetUp = 8;           // least: they share the table and x
 constexpr uint32_t kFewX = 64 << 10;   // LDS for a block's slice of x
@@ -400,8 +400,10 @@ struct Raw {
 // A wave requests its next four units when it has decoded the last, across the
 // ends of tiles, and the first before the table is built.  (Two or three ahead
 // cost 2 to 4 us more at M = 7, 2 x [14336,4096]: x's loads wait behind them.)
-// LDS: 64 KB table, 64 KB x, up to 32 KB for the sums of the
-// waves.
+// LDS: 64 KB table, 64 KB x, up to 32 KB for the sums of the waves.
+// Bound by the decode: 2 x [14336,4096], G = 64, takes 20 us at 7 rows (28 MB:
+// 1.4 TB/s; 5.4 us at copy rate), VALU issue 0.36 busy between waits for
+// weights.  2 x [3584,1024] at one row: 7.8 us, 4 to 5 of them any launch's.
 // lora: the projection alone; the first blocks make t meanwhile (RT as in
 // shrink_role, 0 for none), and expand_kernel adds the adapters.
 template <int G, int NB, int MT, int ACT, int RT>
@@ -653,6 +655,9 @@ constexpr int kMidRows = 64;  // of x a block
 // 64 rows of x; one split of K, in whole quads of groups.  Lane (l, q) decodes
 // group q of a quad of row l; x comes in the same order and as f16 (f16_role), four
 // matrix steps at a time, through a ring of LDS slots that all waves read.
+// A quad's decode, its x from LDS and its MFMAs take, by count, 2000, 4000 and
+// 2000 cycles of a CU with two blocks and overlap in part: 3.8 us for 256 k of one
+// matrix, 5 of two.  333 rows by 2 x [3584,1024]: 17 us, 0.3 PFLOP/s.
 template <int G, int NB, int ACT>
 __global__ __launch_bounds__(kMidThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void mid_kernel(const ProjArgs A) {
@@ -870,6 +875,9 @@ constexpr int kWideX = 5, kWideC = 4;  // slots of x, and of codes
 //   - requests x of s + 4 and the bytes of s + 7.
 // LDS: 80 KB x, 64 KB codes, 16 KB table.  K is split between blocks when the
 // tiles are few.
+// A stage takes 0.85 us (1.26 PFLOP/s on all CUs; a library's bf16 product
+// reaches 1.45): LDS is busy 0.4 of it, the MFMAs 0.55 to 0.6.  2 x
+// [14336,4096] by 2048 rows: 440 us, 1.09 PFLOP/s, 3.5 tiles a CU.
 template <int G, int NB, int ACT>
 __global__ __launch_bounds__(kWideThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void wide_kernel(const ProjArgs A) {
@@ -1273,6 +1281,8 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
     p.t = round16(p.tsplits * M * R * 4);
   }
   const int64_t wide_tiles = ceil_div(NB * N, kWideP) * ceil_div(M, kWideQ);
+  // few against mid_kernel at 32 rows: 33 us and 42 ([4096,14336]), 13 and 21
+  // ([1024,3584] of two); at 16 rows 24 and 39
   if (M <= kFewRows && K >= 128) {
     p.kind = kFew;
     // a block's slice of x, in whole fours of units, fits its LDS
