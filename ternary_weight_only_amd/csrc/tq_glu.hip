@@ -374,6 +374,12 @@ __device__ __forceinline__ void shrink_all(const PreArgs &A, int block, unsigned
 
 constexpr int kFewRows = 32;           // two 16-row tiles of x
 constexpr int kFewWaves = 16;          // most waves of a block
+constexpr int kOwnT = -1;
+// Most bytes of A that a block reads to make its own t.  One row, 8 ranks: K =
+// 1024 8.1 us this way, 11.1 the other, 3584 9.9 and 11.9; 64 KB, one row, 32
+// ranks of 1024, 11.1 and 11.0; 112 KB, 16 ranks of 3584, 11.7 and 11.9; two
+// rows of 16 ranks 15.9 and 12.0.
+constexpr int64_t kOwnTBytes = 64 << 10;
 constexpr int kFewSetUp = 8;           // least: they share the table and x
 constexpr uint32_t kFewX = 64 << 10;   // LDS for a block's slice of x
 
@@ -405,7 +411,9 @@ struct Raw {
 // 1.4 TB/s; 5.4 us at copy rate), VALU issue 0.36 busy between waits for
 // weights.  2 x [3584,1024] at one row: 7.8 us, 4 to 5 of them any launch's.
 // lora: the projection alone; the first blocks make t meanwhile (RT as in
-// shrink_role, 0 for none), and expand_kernel adds the adapters.
+// shrink_role, 0 for none), and expand_kernel adds the adapters.  Of few rows
+// and ranks (RT = kOwnT) every block makes the t of its split, in fp32 beside
+// setting up, and adds the adapters to its results: one launch less.
 template <int G, int NB, int MT, int ACT, int RT>
 __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, const PreArgs P) {
   constexpr int T = 16, B = bytes_per_group(G), GU = 128 / G;  // matrix steps and groups of a unit
@@ -414,6 +422,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
   __shared__ __align__(16) unsigned char smem_raw[L::kBytes + kFewX + kFewWaves * 2048];
   const int work_blocks = (int)gridDim.x - P.shrink_blocks;
   int block = (int)blockIdx.x;
+  constexpr uint32_t kTOff = kRedOff + kFewWaves * 1024;  // kOwnT: t [M][R], behind the sums
+  static_assert(RT != kOwnT || (NB == 1 && MT == 1), "the sums leave room");
   if constexpr (RT > 0) {
     if (block < P.shrink_blocks) {
       shrink_all<RT, 1>(P, block, smem_raw);
@@ -486,6 +496,33 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
         top = top_of(top, *(const u32x4 *)(xs + (int64_t)m * A.K + k));
       top = wave_max(top);
       if (lane == 0) *top_at(part, m) = top;
+    }
+    if constexpr (RT == kOwnT) {
+      if (block == 0 && tid < M && A.status) {
+        const int id = A.ids[tid];
+        if (id < -1 || id >= A.adapters) atomicOr(A.status, kDevBadAdapter);
+      }
+      for (int o = wv; o < M * A.R; o += waves) {  // a wave a rank
+        const int m = o / A.R, r = o - m * A.R, id = A.ids[m];
+        float sum = 0.f;
+        if (id >= 0 && id < A.adapters) {
+          const uint16_t *ar = P.a + ((int64_t)id * A.R + r) * A.K + (int64_t)u0 * 128;
+          const uint16_t *xr = xs + (int64_t)m * A.K;
+#pragma unroll 8
+          for (int k = 8 * lane; k < len; k += 512) {
+            const u32x4 av = *(const u32x4 *)(ar + k), xv = *(const u32x4 *)(xr + k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              sum = fmaf(bf16_to_f32((uint16_t)av[i]), bf16_to_f32((uint16_t)xv[i]), sum);
+              sum = fmaf(bf16_to_f32((uint16_t)(av[i] >> 16)), bf16_to_f32((uint16_t)(xv[i] >> 16)), sum);
+            }
+          }
+#pragma unroll
+          for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+          sum *= P.scaling[id];
+        }
+        if (lane == 0) *(__attribute__((address_space(3))) float *)(smem + kTOff + 4u * (uint32_t)o) = sum;
+      }
     }
   }
   __syncthreads();
@@ -627,6 +664,22 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
           v[i] = 0.f;
           for (int w = 0; w < wk; ++w)
             v[i] += *(__attribute__((address_space(3))) float *)(smem + at + 1024u * (uint32_t)((i * kOnce + ct) * waves + w));
+        }
+        if constexpr (RT == kOwnT) {
+          const int id = A.ids[m];
+          if (id >= 0 && id < A.adapters) {
+            const uint16_t *br = A.b + ((int64_t)id * A.N + n) * A.R;
+            float add = 0.f;
+            for (int r = 0; r < A.R; r += 8) {
+              const u32x4 bv = *(const u32x4 *)(br + r);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float t = *(__attribute__((address_space(3))) float *)(smem + kTOff + 4u * (uint32_t)(m * A.R + r + i));
+                add = fmaf(t, bf16_to_f32((uint16_t)(bv[i / 2] >> (i & 1 ? 16 : 0))), add);
+              }
+            }
+            v[0] += add;
+          }
         }
         const int64_t at_out = (int64_t)m * A.N + n;
         if (A.splits > 1) {
@@ -1237,6 +1290,7 @@ int shrink_tiles(int R) { return R > 16 ? kShrinkRanks : 1; }
 
 struct Plan {
   int kind, wk, wt, splits, tsplits;
+  bool own_t;
   int64_t blocks, chunks;
   int64_t x, shift, t, partial;  // workspace bytes, each a multiple of 16, in this order
   int64_t total() const { return x + shift + t + partial; }
@@ -1288,6 +1342,8 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
     // a block's slice of x, in whole fours of units, fits its LDS
     const int64_t fours = ceil_div(K, 512);
     p.splits = (int)ceil_div(fours, kFewX / (M * 512 * 2));
+    p.own_t = R && M <= 16 && M * R * ceil_div(fours, p.splits) * 512 * 2 <= kOwnTBytes;
+    // (the workspace has room for t either way: callers need not know which)
     const int64_t quads = ceil_div(fours, p.splits), tiles = ceil_div(N, 16);
     // waves along K: four units each where that many waves are to be
     // had; as many tiles a block as leave every CU one
@@ -1300,7 +1356,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
       p.wt = kFewWaves / p.wk;
     }
     // a block a CU, beside those that make t
-    const int64_t cus = 256 - (R ? std::min<int64_t>(64, M * p.tsplits) : 0);
+    const int64_t cus = 256 - (R && !p.own_t ? std::min<int64_t>(64, M * p.tsplits) : 0);
     p.blocks = std::min(ceil_div(tiles, p.wt), std::max<int64_t>(1, cus / p.splits)) * p.splits;
   } else {
     // the cheaper of the two by the model of split_of
@@ -1333,6 +1389,13 @@ void launch_few(const Plan &p, const ProjArgs &a, const PreArgs &pre, hipStream_
     hipLaunchKernelGGL((few_kernel<G, NB, MT, ACT, 0>), dim3((unsigned)p.blocks),
                        dim3(64 * std::max(kFewSetUp, p.wk * p.wt)), 0, stream, a, pre);
   } else {
+    if constexpr (MT == 1) {
+      if (p.own_t) {
+        hipLaunchKernelGGL((few_kernel<G, NB, MT, ACT, kOwnT>), dim3((unsigned)p.blocks),
+                           dim3(64 * std::max(kFewSetUp, p.wk * p.wt)), 0, stream, a, pre);
+        return;
+      }
+    }
     const dim3 grid((unsigned)(p.blocks + pre.shrink_blocks));
     auto kernel = shrink_tiles(a.R) == 1 ? few_kernel<G, NB, MT, ACT, 1> : few_kernel<G, NB, MT, ACT, kShrinkRanks>;
     hipLaunchKernelGGL(kernel, grid, dim3(kPreThreads), 0, stream, a, pre);
@@ -1372,7 +1435,7 @@ void launch_proj(const Plan &p, ProjArgs a, PreArgs pre, void *workspace, hipStr
   a.tq = (int)ceil_div(a.M, kWideQ);
   pre.M = a.M, pre.K = a.K, pre.status = a.status;
   pre.ids = a.ids, pre.adapters = a.adapters, pre.R = a.R;
-  if (NB == 1) {
+  if (NB == 1 && !p.own_t) {
     const int64_t tiles = ceil_div(a.M, kShrinkTile);
     const int64_t rows = std::min<int64_t>(a.M, kShrinkTile);
     // units of a tile: one for each 16 (32) rows and one more for each adapter
@@ -1401,7 +1464,7 @@ void launch_proj(const Plan &p, ProjArgs a, PreArgs pre, void *workspace, hipStr
     a.x = pre.xo;
   }
   launch_product<G, NB, ACT>(p, a, pre, stream);
-  if (p.splits > 1 && !(p.kind == kFew && NB == 1)) {
+  if (p.splits > 1 && !(p.kind == kFew && NB == 1 && !p.own_t)) {
     const int64_t mn = a.M * a.N;
     hipLaunchKernelGGL((combine_kernel<NB, ACT>), dim3((unsigned)std::min<int64_t>(4096, ceil_div(mn, 256))),
                        dim3(256), 0, stream, a.partial, p.splits, mn, a.out);
