@@ -376,10 +376,9 @@ constexpr int kFewRows = 32;           // two 16-row tiles of x
 constexpr int kFewWaves = 16;          // most waves of a block
 constexpr int kOwnT = -1;
 // Most bytes of A that a block reads to make its own t.  One row, 8 ranks: K =
-// 1024 8.1 us this way, 11.1 the other, 3584 9.9 and 11.9; 64 KB, one row, 32
-// ranks of 1024, 11.1 and 11.0; 112 KB, 16 ranks of 3584, 11.7 and 11.9; two
-// rows of 16 ranks 15.9 and 12.0.
-constexpr int64_t kOwnTBytes = 64 << 10;
+// 1024 (16 KB) 8.1 us this way, 10.6 the other; 3584 (56 KB) 9.9 and 11.4.  64
+// KB: one row, 32 ranks of 1024, 11.1 and 10.7; two rows of 16, 11.4 and 10.3.
+constexpr int64_t kOwnTBytes = 60 << 10;
 constexpr int kFewSetUp = 8;           // least: they share the table and x
 constexpr uint32_t kFewX = 64 << 10;   // LDS for a block's slice of x
 
@@ -879,35 +878,52 @@ __global__ __launch_bounds__(256) void combine_kernel(const float *__restrict__ 
 }
 
 // After few_kernel: y = the splits' partial sums in order (y itself where
-// there is one split) + the adapters' part.  A block: 16 columns, all rows;
-// its waves share the adapters, their sums added in wave order.
-constexpr int kExpandWaves = 16;
+// there is one split) + the adapters' part.  A block: 16 columns, all rows, a
+// result a thread: its row's t comes from LDS and its row of B, whose
+// neighbours lie beside it, from memory; fp32 throughout.  (On the matrix cores,
+// each adapter for all rows, 32 adapters of 16 ranks by 4096 columns took 10.3 us
+// and this 5.8.)
 template <int MT>
-__global__ __launch_bounds__(64 * kExpandWaves) void expand_kernel(const ProjArgs A) {
-  __shared__ __align__(16) float red[kExpandWaves * MT * 256];
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n0 = (int)blockIdx.x * 16;
-  // an output a thread: [16-row tile][row][column]
-  const int o = tid, mr = (o >> 4) & 15, m = 16 * (o >> 8) + mr, n = n0 + (o & 15);
-  const bool mine = o < MT * 256 && m < A.M && n < A.N;
+__global__ __launch_bounds__(256 * MT) void expand_kernel(const ProjArgs A) {
+  constexpr int kHeld = 4;                   // eights of ranks held in registers
+  __shared__ __align__(16) float t[16 * MT * 260];  // [row][R + 4]: rows in different banks
+  const int tid = threadIdx.x, m = tid >> 4, n = (int)blockIdx.x * 16 + (tid & 15), ld = A.R + 4;
+  const bool mine = m < A.M && n < A.N;
+  const int id = mine ? A.ids[m] : -1;
+  const bool has = id >= 0 && id < A.adapters;
+  const uint16_t *b = A.b + (has ? ((int64_t)id * A.N + n) * A.R : 0);
+  u32x4 held[kHeld];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i)
+    if (has && 8 * i < A.R) held[i] = *(const u32x4 *)(b + 8 * i);
+  const int MR = (int)A.M * A.R;
+  for (int o = tid; A.adapters > 0 && o < MR; o += 256 * MT) {
+    float v = A.t[o];
+    for (int s = 1; s < A.tsplits; ++s) v += A.t[(int64_t)s * MR + o];
+    t[o / A.R * ld + o % A.R] = v;
+  }
   float v = 0.f;
   if (mine) {
-    const float *p = A.splits > 1 ? A.partial : (const float *)A.out;
+    const float *p = (A.splits > 1 ? A.partial : (const float *)A.out) + (int64_t)m * A.N + n;
     const int64_t mn = A.M * A.N;
 #pragma unroll 8
-    for (int s = 0; s < A.splits; ++s) v += p[s * mn + (int64_t)m * A.N + n];
+    for (int s = 0; s < A.splits; ++s) v += p[s * mn];
   }
-  f32x4 acc[1][MT];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) acc[0][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-  add_adapters<false>(A, 0, n0, adapter_of(A, lane, lane < 16 * MT), kExpandWaves, wv, acc);
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) *(f32x4 *)(red + 4 * ((wv * MT + mt) * 64 + lane)) = acc[0][mt];
   __syncthreads();
   if (!mine) return;
-  const int at = ((o >> 8) * 64 + (mr >> 2) * 16 + (o & 15)) * 4 + (mr & 3);
-  for (int w = 0; w < kExpandWaves; ++w) v += red[w * MT * 256 + at];
+  if (has) {
+    float add = 0.f;
+    auto eight = [&](u32x4 w, int r) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        add = fmaf(t[m * ld + r + i], bf16_to_f32((uint16_t)(w[i / 2] >> (i & 1 ? 16 : 0))), add);
+    };
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (8 * i < A.R) eight(held[i], 8 * i);
+    for (int r = 8 * kHeld; r < A.R; r += 8) eight(*(const u32x4 *)(b + r), r);
+    v += add;
+  }
   ((float *)A.out)[(int64_t)m * A.N + n] = v;
 }
 
@@ -1399,8 +1415,7 @@ void launch_few(const Plan &p, const ProjArgs &a, const PreArgs &pre, hipStream_
     const dim3 grid((unsigned)(p.blocks + pre.shrink_blocks));
     auto kernel = shrink_tiles(a.R) == 1 ? few_kernel<G, NB, MT, ACT, 1> : few_kernel<G, NB, MT, ACT, kShrinkRanks>;
     hipLaunchKernelGGL(kernel, grid, dim3(kPreThreads), 0, stream, a, pre);
-    hipLaunchKernelGGL(expand_kernel<MT>, dim3((unsigned)ceil_div(a.N, 16)), dim3(64 * kExpandWaves), 0,
-                       stream, a);
+    hipLaunchKernelGGL(expand_kernel<MT>, dim3((unsigned)ceil_div(a.N, 16)), dim3(256 * MT), 0, stream, a);
   }
 }
 

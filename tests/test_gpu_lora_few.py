@@ -1,5 +1,5 @@
 """tq_lora_matmul for few rows and ranks, where one launch makes t and y (A of
-up to 64 KB a block) and just past that: ranks, rows, both group sizes, one
+up to 60 KB a block) and just past that: ranks, rows, both group sizes, one
 and several splits of K, ids absent, out of range and repeated."""
 import numpy as np
 import pytest
