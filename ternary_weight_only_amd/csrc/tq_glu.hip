@@ -40,7 +40,7 @@ __host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a
 
 // What the kernels read and write.
 struct ProjArgs {
-  const uint16_t *x;              // bf16 [M,K] (staged), or x in fragment order, or f16 rows
+  const uint16_t *x;              // bf16 [M,K], or as f16_role leaves it
   const uint8_t *packed[2];
   const uint16_t *scales[2];
   const int32_t *shift;           // wide: x of row m is stored times 2^shift[m]
@@ -234,7 +234,7 @@ struct PreArgs {
   const uint16_t *x, *a;
   const int32_t *ids;
   const float *scaling;
-  uint16_t *xo;     // fragments or f16 rows
+  uint16_t *xo;     // x as f16_role leaves it
   int32_t *shift;   // f16 rows
   float *t;
   int64_t M;
@@ -1237,7 +1237,8 @@ __device__ __forceinline__ void load_row(const PreArgs &A, int64_t first, u32x4 
 
 // Row m of x as f16 times 2^shift[m], for mid_kernel in its fragments
 // [chunk][quad][step][16-row tile][lane][8] (rows past M and groups past the
-// last are zeros), for wide_kernel in rows, in the order of its codes.
+// last are zeros), for wide_kernel as images of its LDS slots [256 rows][stage
+// of 32 k][slot], in the order of its codes.
 // Rows pass through LDS, from which their elements are picked; a block takes
 // `rpb` rows at a time (1, 2 or 4, so that they fit), threads / rpb each.  `v`
 // is load_row of these rows and, on return, of those `step` on, which are on
