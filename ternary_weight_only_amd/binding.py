@@ -11,6 +11,7 @@ import ctypes
 import os
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libtq.so")
@@ -1004,7 +1005,8 @@ def glu_backward(dh, x, wg, wu, g, u, act="silu", out=None, workspace=None):
 class GLU(torch.autograd.Function):
     """h = act(x wg^T) * (x wu^T) with gradients for x, wg and wu; after
     FakeQuantize the gradients of wg and wu reach the latent weights
-    unchanged.  Gradients that are not needed are still computed."""
+    unchanged.  Gradients that are not needed are still computed; gradients of
+    gradients are refused."""
 
     @staticmethod
     def forward(ctx, x, wg, wu, act="silu"):
@@ -1014,6 +1016,7 @@ class GLU(torch.autograd.Function):
         return h
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dh):
         x, wg, wu, g, u = ctx.saved_tensors
         return (*glu_backward(dh.contiguous(), x, wg, wu, g, u, ctx.act), None)

@@ -1,0 +1,46 @@
+"""GLU as autograd sees it, on the CPU: its two calls are replaced by the
+formulas in torch, so no kernel is launched."""
+import pytest
+import torch
+
+import ternary_weight_only_amd as tq
+from ternary_weight_only_amd import binding
+from tests import ffn_reference as ref
+
+
+@pytest.fixture
+def stand_ins(monkeypatch):
+    """glu_forward and glu_backward in float64; the list of the dh that the
+    backward call received."""
+    received = []
+
+    def forward(x, wg, wu, act="silu", save=True, out=None):
+        h, g, u, _, _, _ = ref.glu64(x, wg, wu, act)
+        return (h, g, u) if save else h
+
+    def backward(dh, x, wg, wu, g, u, act="silu", out=None, workspace=None):
+        received.append(dh)
+        return ref.backward64(dh, x, wg, wu, g, u, act)[0]
+
+    monkeypatch.setattr(binding, "glu_forward", forward)
+    monkeypatch.setattr(binding, "glu_backward", backward)
+    return received
+
+
+def _leaves():
+    return [ref.normal(3 + i, s, 1.0, torch.float64).requires_grad_() for i, s in enumerate(((5, 64), (8, 64), (8, 64)))]
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_first_gradients(stand_ins, act):
+    leaves = _leaves()
+    assert torch.autograd.gradcheck(lambda *t: tq.GLU.apply(*t, act), leaves)
+
+
+def test_a_second_gradient_raises(stand_ins):
+    """The backward call's results carry no graph: a gradient through them
+    would be dropped without a word."""
+    x, wg, wu = _leaves()
+    dx, = torch.autograd.grad(tq.GLU.apply(x, wg, wu).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dx.square().sum().backward()
