@@ -11,7 +11,6 @@ import ctypes
 import os
 
 import torch
-from torch.autograd.function import once_differentiable
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libtq.so")
@@ -1002,6 +1001,21 @@ def glu_backward(dh, x, wg, wu, g, u, act="silu", out=None, workspace=None):
     return dx, dwg, dwu
 
 
+class _FirstGradients(torch.autograd.Function):
+    """Gradients made from the first `n` arguments, passed through; a gradient
+    of them is refused, whichever of those it would be with respect to.  (A
+    backward marked once_differentiable refuses only where the incoming
+    gradient itself requires one.)"""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tensors[n:]
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise TQError("GLU has no gradients of gradients")
+
+
 class GLU(torch.autograd.Function):
     """h = act(x wg^T) * (x wu^T) with gradients for x, wg and wu; after
     FakeQuantize the gradients of wg and wu reach the latent weights
@@ -1016,7 +1030,10 @@ class GLU(torch.autograd.Function):
         return h
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, dh):
         x, wg, wu, g, u = ctx.saved_tensors
-        return (*glu_backward(dh.contiguous(), x, wg, wu, g, u, ctx.act), None)
+        with torch.no_grad():
+            grads = glu_backward(dh.contiguous(), x, wg, wu, g, u, ctx.act)
+        if torch.is_grad_enabled():  # create_graph
+            grads = _FirstGradients.apply(4, dh, x, wg, wu, *grads)
+        return (*grads, None)

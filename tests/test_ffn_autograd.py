@@ -37,10 +37,18 @@ def test_first_gradients(stand_ins, act):
     assert torch.autograd.gradcheck(lambda *t: tq.GLU.apply(*t, act), leaves)
 
 
-def test_a_second_gradient_raises(stand_ins):
+@pytest.mark.parametrize("of", [0, 1, 2, None])
+@pytest.mark.parametrize("to", [0, 1, 2])
+def test_a_second_gradient_raises(stand_ins, of, to):
     """The backward call's results carry no graph: a gradient through them
-    would be dropped without a word."""
-    x, wg, wu = _leaves()
-    dx, = torch.autograd.grad(tq.GLU.apply(x, wg, wu).sum(), x, create_graph=True)
-    with pytest.raises(RuntimeError, match="once_differentiable"):
-        dx.square().sum().backward()
+    would be dropped without a word.  First gradients with create_graph are
+    those without."""
+    leaves = _leaves()
+    dh = torch.ones(5, 8, dtype=torch.float64, requires_grad=of is None)
+    want = torch.autograd.grad(tq.GLU.apply(*leaves), leaves, dh.detach())
+    h = tq.GLU.apply(*leaves)
+    got = torch.autograd.grad(h, leaves, dh, create_graph=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    with pytest.raises(tq.TQError, match="gradients of gradients"):
+        second = got[of or 0].square().sum() + h.sum()
+        torch.autograd.grad(second, leaves[to] if of is not None else dh)
