@@ -1033,7 +1033,10 @@ class GLU(torch.autograd.Function):
     def backward(ctx, dh):
         x, wg, wu, g, u = ctx.saved_tensors
         with torch.no_grad():
-            grads = glu_backward(dh.contiguous(), x, wg, wu, g, u, ctx.act)
+            d = dh.contiguous()
+            if d.data_ptr() % 16:  # rows inside a larger tensor, as cat's backward makes them
+                d = d.clone()
+            grads = glu_backward(d, x, wg, wu, g, u, ctx.act)
         if torch.is_grad_enabled():  # create_graph
             grads = _FirstGradients.apply(4, dh, x, wg, wu, *grads)
         return (*grads, None)

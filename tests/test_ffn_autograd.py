@@ -52,3 +52,17 @@ def test_a_second_gradient_raises(stand_ins, of, to):
     with pytest.raises(tq.TQError, match="gradients of gradients"):
         second = got[of or 0].square().sum() + h.sum()
         torch.autograd.grad(second, leaves[to] if of is not None else dh)
+
+
+def test_a_gradient_that_starts_anywhere(stand_ins):
+    """h's gradient may be rows inside a larger tensor, as the backward of cat
+    makes it: the call gets it contiguous and on 16 bytes."""
+    x, (wg, wu) = ref.normal(3, (5, 64)), (ref.normal(i, (13, 64)).requires_grad_() for i in (4, 5))
+    whole = ref.normal(7, (8, 13))
+    for rows in (whole[3:], whole[::2][:3], whole.t()[:5, :]):
+        h = tq.GLU.apply(x[:rows.shape[0]], wg[:rows.shape[1]], wu[:rows.shape[1]])
+        h.backward(rows)
+    torch.cat([whole[:3], tq.GLU.apply(x, wg, wu)]).float().square().sum().backward()
+    assert len(stand_ins) == 4
+    for dh in stand_ins:
+        assert dh.is_contiguous() and dh.data_ptr() % 16 == 0
