@@ -8,6 +8,7 @@ the computation runs in the library's kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -158,6 +159,25 @@ def _stream() -> int:
     return torch.cuda.current_stream().cuda_stream
 
 
+_current_device = torch._C._cuda_getDevice
+
+
+def _on_device(fn):
+    """A call whose first argument is a tensor, or a list of them, made with
+    that tensor's device as the current one: the default stream is the same raw
+    0 on every device, and a launch goes to the current device's."""
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        t = args[0] if args else next(iter(kw.values()), None)
+        if isinstance(t, (list, tuple)) and t:
+            t = t[0]
+        if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != _current_device():
+            with torch.cuda.device(t.device):
+                return fn(*args, **kw)
+        return fn(*args, **kw)
+    return call
+
+
 # ---------------------------------------------------------------------------
 # validation: nothing reaches the library unless every tensor it will read
 # or write is a contiguous device tensor of the expected dtype and size on
@@ -262,6 +282,7 @@ def check(status: torch.Tensor) -> int:
 # quantize / QAT forward / unpack / decode
 # ---------------------------------------------------------------------------
 
+@_on_device
 def quantize_pack(w: torch.Tensor, G: int, status=None, out=None):
     """w: [N,K] bf16 -> (packed uint8 [N, (K/G)*ceil(G/5)], scales fp16 [N, K/G]).
     `out`, if given, is a (packed, scales) pair of that size."""
@@ -278,6 +299,7 @@ def quantize_pack(w: torch.Tensor, G: int, status=None, out=None):
     return packed, scales
 
 
+@_on_device
 def fake_quantize(w: torch.Tensor, G: int, status=None, out=None, scales_out=None):
     """QAT forward: w [N,K] bf16 -> w_hat bf16 [N,K] = bf16(c * s).
 
@@ -297,6 +319,7 @@ def fake_quantize(w: torch.Tensor, G: int, status=None, out=None, scales_out=Non
     return w_hat
 
 
+@_on_device
 def fake_quantize_f32(w: torch.Tensor, G: int, status=None, out=None, scales_out=None):
     """QAT forward from fp32 latent weights: w [N,K] fp32 -> w_hat fp32 [N,K]
     = c * s (exact).  scales_out as for fake_quantize."""
@@ -316,6 +339,7 @@ def fake_quantize_f32(w: torch.Tensor, G: int, status=None, out=None, scales_out
     return w_hat
 
 
+@_on_device
 def fake_quantize_f32_batched(ws, G: int, status=None, outs=None):
     """Same-shaped fp32 latent matrices -> list of w_hat fp32, one launch per 64."""
     if not ws:
@@ -344,6 +368,7 @@ def _same_shape(ws, name):
     return shapes.pop() if shapes else (0, 0)
 
 
+@_on_device
 def quantize_pack_batched(ws, G: int, status=None):
     """Same-shaped bf16 matrices -> list of (packed, scales), one launch per 64."""
     N, K = _same_shape(ws, "w")
@@ -360,6 +385,7 @@ def quantize_pack_batched(ws, G: int, status=None):
     return list(zip(pk, sc))
 
 
+@_on_device
 def fake_quantize_batched(ws, G: int, status=None, with_scales: bool = False):
     """Same-shaped bf16 matrices -> list of bf16 w_hat (and, with_scales, of
     (w_hat, scales)), one launch per 64."""
@@ -378,6 +404,7 @@ def fake_quantize_batched(ws, G: int, status=None, with_scales: bool = False):
     return list(zip(wh, sc)) if with_scales else wh
 
 
+@_on_device
 def unpack(packed: torch.Tensor, N: int, K: int, G: int, status=None, out=None):
     """packed -> codes int8 [N,K]."""
     _dev(packed, "packed", U8)
@@ -389,6 +416,7 @@ def unpack(packed: torch.Tensor, N: int, K: int, G: int, status=None, out=None):
     return codes
 
 
+@_on_device
 def unpack_batched(packeds, N: int, K: int, G: int, status=None):
     """Same-shaped packed matrices -> list of int8 codes [N,K], one launch per 64."""
     if not packeds:
@@ -404,6 +432,7 @@ def unpack_batched(packeds, N: int, K: int, G: int, status=None):
     return codes
 
 
+@_on_device
 def dequantize(packed: torch.Tensor, scales: torch.Tensor, N: int, K: int, G: int, status=None,
                out=None):
     """(packed, fp16 scales) -> w_hat bf16 [N,K] = bf16(c * s)."""
@@ -415,6 +444,7 @@ def dequantize(packed: torch.Tensor, scales: torch.Tensor, N: int, K: int, G: in
     return w_hat
 
 
+@_on_device
 def dequantize_batched(packeds, scales_list, N: int, K: int, G: int, status=None, outs=None):
     """Same-shaped (packed, scales) pairs -> list of bf16 [N,K], one launch per 64."""
     n = len(packeds)
@@ -464,11 +494,13 @@ def _mm(fn, name, x, packed, scales, N, K, G, status, out):
     return y
 
 
+@_on_device
 def gemv(x, packed, scales, N: int, K: int, G: int, status=None, out=None):
     """y[M,N] = x[M,K] * W_hat^T for 1 <= M <= 16 (decode path)."""
     return _mm(lib().tq_gemv, "tq_gemv", x, packed, scales, N, K, G, status, out)
 
 
+@_on_device
 def gemm(x, packed, scales, N: int, K: int, G: int, status=None, out=None):
     """y[M,N] = x[M,K] * W_hat^T for any M (prefill path)."""
     return _mm(lib().tq_gemm, "tq_gemm", x, packed, scales, N, K, G, status, out)
@@ -494,18 +526,21 @@ def _batched(fn, name, xs, packeds, scales_list, N, K, G, status, outs):
     return ys
 
 
+@_on_device
 def gemv_batched(xs, packeds, scales_list, N: int, K: int, G: int, status=None, outs=None):
     """[x_i] ([M,K] bf16 each, M <= 16), [packed_i], [scales_i] -> [y_i] ([M,N] fp32), one call."""
     return _batched(lib().tq_gemv_batched, "tq_gemv_batched", xs, packeds, scales_list, N, K, G,
                     status, outs)
 
 
+@_on_device
 def gemm_batched(xs, packeds, scales_list, N: int, K: int, G: int, status=None, outs=None):
     """[x_i] ([M,K] bf16 each), [packed_i], [scales_i] -> [y_i] ([M,N] fp32), one call."""
     return _batched(lib().tq_gemm_batched, "tq_gemm_batched", xs, packeds, scales_list, N, K, G,
                     status, outs)
 
 
+@_on_device
 def gemv_grouped(xs, packeds, scales_list, Ns, Ks, G: int, status=None, outs=None):
     """[x_i] ([1,K_i] bf16), [packed_i], [scales_i] of shapes (N_i, K_i) -> [y_i] ([1,N_i]
     fp32): M = 1 GEMVs of mixed shapes in as few launches as possible."""
@@ -529,6 +564,7 @@ def gemv_grouped(xs, packeds, scales_list, Ns, Ks, G: int, status=None, outs=Non
     return ys
 
 
+@_on_device
 def gemm_grouped(xs, packeds, scales_list, Ns, Ks, G: int, status=None, outs=None):
     """[x_i] ([M,K_i] bf16, one M), [packed_i], [scales_i] of shapes (N_i, K_i) -> [y_i]
     ([M,N_i] fp32): prefill matmuls of mixed shapes, one persistent launch where possible."""
@@ -565,6 +601,7 @@ def _check_packed2(packed, scales, N, K, G, device, what):
         raise TQError("%s: shapes do not match N=%d K=%d G=%d" % (what, N, K, G))
 
 
+@_on_device
 def quantize_pack2(w: torch.Tensor, G: int, status=None):
     """2-bit format: w [N,K] bf16 -> (packed2 uint8 [N, K/4], scales fp16 [N, K/G])."""
     _dev(w, "w", BF16, 2)
@@ -578,6 +615,7 @@ def quantize_pack2(w: torch.Tensor, G: int, status=None):
     return packed, scales
 
 
+@_on_device
 def quantize_pack2_batched(ws, G: int, status=None):
     """2-bit format, same-shaped bf16 matrices -> list of (packed2, scales),
     one launch per 64."""
@@ -594,6 +632,7 @@ def quantize_pack2_batched(ws, G: int, status=None):
     return list(zip(pk, sc))
 
 
+@_on_device
 def unpack2(packed: torch.Tensor, N: int, K: int, G: int, status=None):
     """2-bit packed [N, K/4] -> codes int8 [N,K]."""
     _dev(packed, "packed", U8)
@@ -605,6 +644,7 @@ def unpack2(packed: torch.Tensor, N: int, K: int, G: int, status=None):
     return codes
 
 
+@_on_device
 def gemv2(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, N: int, K: int, G: int,
           status=None, out=None):
     """2-bit format, M = 1: x [1,K] bf16 -> y fp32 [1,N]."""
@@ -619,6 +659,7 @@ def gemv2(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, N: int, K
     return y
 
 
+@_on_device
 def gemm2(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, N: int, K: int, G: int,
           status=None, out=None):
     """2-bit format, any M: x [M,K] bf16 -> y fp32 [M,N]."""
@@ -634,6 +675,7 @@ def gemm2(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, N: int, K
     return y
 
 
+@_on_device
 def gemm2_batched(xs, packeds, scales_list, N: int, K: int, G: int, status=None, outs=None):
     """2-bit format, same-shaped problems (every x [M,K] with the same M):
     list of y fp32 [M,N], one launch per 64."""
@@ -656,6 +698,7 @@ def gemm2_batched(xs, packeds, scales_list, N: int, K: int, G: int, status=None,
     return outs
 
 
+@_on_device
 def gemv2_batched(xs, packeds, scales_list, N: int, K: int, G: int, status=None, outs=None):
     """2-bit format, M = 1, same-shaped problems: list of y fp32 [1,N], one launch per 128."""
     n = len(xs)
@@ -676,6 +719,7 @@ def gemv2_batched(xs, packeds, scales_list, N: int, K: int, G: int, status=None,
     return outs
 
 
+@_on_device
 def gemv2_grouped(xs, packeds, scales_list, Ns, Ks, G: int, status=None, outs=None):
     """2-bit format, M = 1, problems of mixed shapes in one launch:
     list of y fp32 [1, Ns[i]]."""
@@ -715,6 +759,7 @@ def _w4_check(x, packed, scales, biases, N, K, G, device=None, any_m=False):
     return dev
 
 
+@_on_device
 def w4a16_gemm(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
                biases: torch.Tensor, N: int, K: int, G: int, out=None):
     """W4A16, any M: x [M,K] bf16, packed int32/uint32 [N, K/8], scales and
@@ -728,6 +773,7 @@ def w4a16_gemm(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
     return y
 
 
+@_on_device
 def w4a16_gemm_batched(xs, packeds, scales_list, biases_list, N: int, K: int, G: int,
                        outs=None):
     """Same-shaped W4A16 matmuls (every x [M,K] with the same M) -> list of
@@ -750,6 +796,7 @@ def w4a16_gemm_batched(xs, packeds, scales_list, biases_list, N: int, K: int, G:
     return outs
 
 
+@_on_device
 def w4a16_gemv(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
                biases: torch.Tensor, N: int, K: int, G: int, out=None):
     """W4A16, M = 1: x [1,K] bf16, packed int32/uint32 [N, K/8], scales and
@@ -762,6 +809,7 @@ def w4a16_gemv(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor,
     return y
 
 
+@_on_device
 def w4a16_gemv_batched(xs, packeds, scales_list, biases_list, N: int, K: int, G: int,
                        outs=None):
     """Same-shaped W4A16 problems -> list of y bf16 [1,N], one launch per 128."""
@@ -780,6 +828,7 @@ def w4a16_gemv_batched(xs, packeds, scales_list, biases_list, N: int, K: int, G:
     return outs
 
 
+@_on_device
 def w4a16_gemv_grouped(xs, packeds, scales_list, biases_list, Ns, Ks, G: int, outs=None):
     """W4A16 problems of mixed shapes in one launch -> list of y bf16 [1, Ns[i]]."""
     n = len(xs)
@@ -848,7 +897,9 @@ def _activations(x, K: int):
 
 
 def _stream_of(device) -> int:
-    """The raw current stream of `device`."""
+    """The raw current stream of `device`, which is the current one (as in
+    _on_device, spelled out in each call here: a small call is as long on the
+    host as on the GPU, and a wrapper is 0.3 us of it)."""
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
@@ -897,6 +948,9 @@ def glu(x, gate, up, N: int, K: int, G: int, act="silu", status=None, out=None, 
     form).  `workspace`, if given, is a uint8 tensor of at least
     glu_workspace(M, N, K, G) bytes that no other call in flight uses."""
     xp, M, dev = _activations(x, K)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return glu(x, gate, up, N, K, G, act, status, out, workspace)
     a = _act(act)
     nb, ns = _packed_sizes(N, K, G)
     gp, gs = _pair(*gate, nb, ns, dev, "tq_glu gate")
@@ -926,6 +980,9 @@ def lora_matmul(x, packed, scales, ids, a, b, scaling, N: int, K: int, G: int, s
     R is a multiple of 8 up to 256.  `workspace` as for glu, of
     lora_workspace(M, N, K, G, R) bytes."""
     xp, M, dev = _activations(x, K)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return lora_matmul(x, packed, scales, ids, a, b, scaling, N, K, G, status, out, workspace)
     nb, ns = _packed_sizes(N, K, G)
     wp_, sp = _pair(packed, scales, nb, ns, dev, "tq_lora_matmul")
     ip = _shaped(ids, "ids", (M,), I32, dev)
@@ -963,6 +1020,9 @@ def glu_forward(x, wg, wu, act="silu", save: bool = True, out=None):
     u = x wu^T; with save=False h alone (g and u are never written).
     `out`, if given, is (h, g, u) or, with save=False, h.  K % 64 == 0."""
     xp, gp, up, M, N, K, dev = _train_inputs(x, wg, wu)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return glu_forward(x, wg, wu, act, save, out)
     a = _act(act)
     h, g, u = (None, None, None) if out is None else out if save else (out, None, None)
     h, hp = _result(h, "h", (M, N), torch.bfloat16, BF16, dev)
@@ -986,6 +1046,9 @@ def glu_backward(dh, x, wg, wu, g, u, act="silu", out=None, workspace=None):
     dwu [N,K]) bf16.  `out`, if given, is that triple; `workspace` as for glu,
     of glu_backward_workspace(M, N, K) bytes."""
     xp, wgp, wup, M, N, K, dev = _train_inputs(x, wg, wu)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return glu_backward(dh, x, wg, wu, g, u, act, out, workspace)
     a = _act(act)
     dhp = _shaped(dh, "dh", (M, N), BF16, dev)
     gp, up = _shaped(g, "g", (M, N), BF16, dev), _shaped(u, "u", (M, N), BF16, dev)
