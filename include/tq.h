@@ -547,7 +547,8 @@ int tq_w4a16_gemv_grouped(int count, const uint16_t *const *xs, const uint32_t *
 /*
  * Gated feed-forward block on packed ternary weights (serving), any M >= 0:
  *   h[m,n] = bf16_rne(act(g[m,n]) * u[m,n]),
- *   g = x Wg_hat^T, u = x Wu_hat^T, both accumulated in fp32 and never stored
+ *   g = x Wg_hat^T, u = x Wu_hat^T, both accumulated in fp32 (whatever the
+ *   spread of a row of x) and never stored
  * -- the gate and up projections, the activation and the product of one
  * decoder feed-forward block; h is the x of the down projection.
  *   x                        [M,K] bf16, 16-byte aligned

@@ -43,7 +43,9 @@ struct ProjArgs {
   const uint16_t *x;              // bf16 [M,K], or as f16_role leaves it
   const uint8_t *packed[2];
   const uint16_t *scales[2];
-  const int32_t *shift;           // wide: x of row m is stored times 2^shift[m]
+  const uint16_t *x0;             // bf16 [M,K]
+  const u32x2 *rows;              // mid, wide: x of row m is stored times 2^rows[m].x, and the
+                                  // magnitudes that it lost by that are rows[m].y (fp32) in all
   const int32_t *ids;             // lora
   const float *t;                 // lora: [tsplits][M,R] fp32, scaled
   int tsplits;
@@ -59,6 +61,101 @@ struct ProjArgs {
   int tp, tq;                     // wide: tiles
   int32_t *status;
 };
+
+// ---------------------------------------------------------------------------
+// what x loses as f16
+// ---------------------------------------------------------------------------
+
+// A row whose elements spread over more than 2^32 loses some of its smallest
+// (tq_ternary.h): in a sum, at most the magnitudes lost times the largest
+// scale.  A sum at least 2^22 times that has it within an fp32 sum's own
+// roundings; one below -- where the row's largest elements meet codes 0, or
+// cancel -- gets the lost part added, a wave a sum.  Rows that lose something
+// are known when x is converted, so others cost a load and a ballot.  (One
+// element of 2^40 in every row of normal ones: a third of the sums get theirs.)
+constexpr float kLostCounts = 4194304.f;
+
+// The same value, known only here: what follows from it is not computed ahead
+// of a loop around, where it would hold registers that the loop needs.
+__device__ __forceinline__ int uniform_here(int v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+s"(v));
+#endif
+  return v;
+}
+// The lane, from no register that a loop before had to keep.
+__device__ __forceinline__ int lane_here() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  int lane = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  asm volatile("" : "+v"(lane));
+  return lane;
+#else
+  return 0;
+#endif
+}
+
+// Largest magnitude among the scales of `rows` weight rows from n0 on.
+__device__ __forceinline__ float scale_top(const ProjArgs &A, int i, int n0, int rows, int nG) {
+  const int lane = lane_here();
+  nG = uniform_here(nG);
+  const uint16_t *s = A.scales[i] + (int64_t)n0 * nG;
+  const int64_t count = (int64_t)max(0, min(rows, A.N - n0)) * nG;
+  uint32_t top = 0;
+  for (int64_t e = lane; e < count; e += 64) top = max(top, (uint32_t)s[e] & 0x7FFFu);
+#pragma unroll
+  for (int o = 32; o; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)top);
+}
+
+// The lost part (WHOLE: all) of the sum of x's row m (times 2^shift) and row n
+// of matrix i over groups g0 .. g1 - 1; by a whole wave, the same in every
+// lane.  A byte a lane at a time, decoded by division: few registers beside
+// those of the kernel around it, and no table need be there.
+template <int G, bool WHOLE>
+__device__ __forceinline__ float lost_part(const ProjArgs &A, int i, int64_t m, int64_t n, int g0, int g1,
+                                           int shift) {
+  constexpr int B = bytes_per_group(G);
+  const int nG = uniform_here(A.K / G);
+  const uint8_t *p = A.packed[i] + (n * nG + g0) * B;
+  const uint16_t *s = A.scales[i] + n * nG + g0;
+  const uint16_t *x = A.x0 + (m * nG + g0) * G;
+  float sum = 0.f;
+#pragma unroll 1
+  for (int e = lane_here(); e < (g1 - g0) * B; e += 64) {
+    const int g = e / B, k = 5 * (e - g * B);
+    uint32_t byte = p[e];
+    float part = 0.f;
+#pragma unroll
+    for (int d = 0; d < 5; ++d) {  // the last byte's codes past G are 0
+      const uint32_t b = x[g * G + min(k + d, G - 1)];
+      part = fmaf((float)(int)(byte % 3u) - 1.f, WHOLE ? bf16_to_f32(b) : lost_of(b, shift), part);
+      byte /= 3u;
+    }
+    sum = fmaf(part, (float)__builtin_bit_cast(_Float16, s[g]), sum);
+  }
+  return wave_sum(sum);
+}
+
+// The lost part added to what a split of groups g0 .. g1 - 1 stored for row m
+// of x and column n, by the lane that stored it (`mine`; in order for it).
+// Where that is the gated product, it is made anew, and any lane may write it.
+template <int G, int NB, int ACT>
+__device__ __forceinline__ void mend_result(const ProjArgs &A, int64_t m, int64_t n, int split, int g0, int g1,
+                                            bool mine) {
+  const int64_t o = m * A.N + n;
+  if (NB == 2 && A.splits == 1) {
+    const float g = lost_part<G, true>(A, 0, m, n, g0, g1, 0), u = lost_part<G, true>(A, 1, m, n, g0, g1, 0);
+    if (mine) ((uint16_t *)A.out)[o] = f32_to_bf16(act_value<ACT>(g) * u);
+    return;
+  }
+  const int shift = (int)A.rows[m].x;
+#pragma unroll 1
+  for (int i = 0; i < NB; ++i) {
+    const float add = lost_part<G, false>(A, i, m, n, g0, g1, shift);
+    float *y = (A.splits > 1 ? A.partial + ((int64_t)split * NB + i) * A.M * A.N : (float *)A.out) + o;
+    if (mine) *y += add;
+  }
+}
 
 // ---------------------------------------------------------------------------
 // adapters
@@ -214,6 +311,11 @@ __device__ __forceinline__ void add_own_adapters(const ProjArgs &A, int64_t m0, 
     }
 }
 
+// What the product's kernels need of row m; zeros past the last.
+__device__ __forceinline__ u32x2 row_scale(const ProjArgs &A, int64_t m) {
+  return m < A.M ? A.rows[m] : u32x2{0u, 0u};
+}
+
 // The id of row m as add_adapters takes it.
 __device__ __forceinline__ int adapter_of(const ProjArgs &A, int64_t m, bool in) {
   const int id = in && m < A.M ? A.ids[m] : -1;
@@ -235,7 +337,7 @@ struct PreArgs {
   const int32_t *ids;
   const float *scaling;
   uint16_t *xo;     // x as f16_role leaves it
-  int32_t *shift;   // f16 rows
+  u32x2 *rows;      // as in ProjArgs
   float *t;
   int64_t M;
   int K, adapters, R, rpb;
@@ -472,8 +574,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
   const int split = block % A.splits, b0 = block / A.splits;
   const int blocks = work_blocks / A.splits;
   const int nU = (nG + GU - 1) / GU, nQ = (nU + 3) / 4;  // units, and fours of them
-  const int u0 = 4 * (int)((int64_t)nQ * split / A.splits);
-  const int u1 = min(nU, 4 * (int)((int64_t)nQ * (split + 1) / A.splits));
+  // (at most 4096 fours and as many splits: the products fit)
+  const int u0 = 4 * (nQ * split / A.splits), u1 = min(nU, 4 * (nQ * (split + 1) / A.splits));
   const int wk = A.wk, wt = A.wt;        // waves of a tile, tiles of a set
   const int kw = wv % wk, tw = wv / wk;  // this wave's place (tw >= wt: it helps set up)
   const int tiles = (A.N + 15) / 16, sets = (tiles + wt - 1) / wt;
@@ -514,22 +616,23 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
   // the first bytes are requested before the table is built and x put in order
   fetch();
   L::build(smem, tid, threads);
-  // largest magnitudes, [wave][row], where the sums will be
-  auto top_at = [&](int w, int m) {
+  // spans of the rows, [wave][row], where the sums will be
+  auto span_at = [&](int w, int m) {
     return (__attribute__((address_space(3))) uint32_t *)(smem + kRedOff + 4u * (uint32_t)(w * kFewRows + m));
   };
   // rows are shared by the waves, `parts` waves a row
   const int parts = max(1, waves / M);
+  const uint16_t *xs = A.x + (int64_t)u0 * 128;
+  const int len = min(A.K - u0 * 128, (u1 - u0) * 128);
   {
-    const uint16_t *xs = A.x + (int64_t)u0 * 128;
-    const int len = min(A.K - u0 * 128, (u1 - u0) * 128), part = wv % parts;
+    const int part = wv % parts;
     for (int m = wv / parts; m < M; m += waves / parts) {
-      uint32_t top = 0;
+      SpanOf of;
 #pragma unroll 4
       for (int k = 8 * (64 * part + lane); k < len; k += 512 * parts)
-        top = top_of(top, *(const u32x4 *)(xs + (int64_t)m * A.K + k));
-      top = wave_max(top);
-      if (lane == 0) *top_at(part, m) = top;
+        of.take(*(const u32x4 *)(xs + (int64_t)m * A.K + k));
+      const uint32_t span = span_wave(of.word());
+      if (lane == 0) *span_at(part, m) = span;
     }
     if constexpr (RT == kOwnT) {
       if (block == 0 && tid < M && A.status) {
@@ -560,18 +663,32 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
     }
   }
   __syncthreads();
-  auto shift_of = [&](int m) {
-    uint32_t top = 0;
-    for (int w = 0; w < parts; ++w) top = max(top, *top_at(w, m));
-    return f16_shift(top);
+  auto span_of = [&](int m) {
+    uint32_t span = 0;
+    for (int w = 0; w < parts; ++w) span = span_join(span, *span_at(w, m));
+    return span;
   };
+  // of row `lane`: its power of two, and what it loses; and the rows that lose
+  // something, the same in every wave
+  const uint32_t span_own = span_of(min(lane, M - 1));
+  const int shift_own = f16_shift(span_top(span_own));
+  float lost = 0.f;
+  const uint32_t lossy = (uint32_t)__ballot(lane < M && span_loses(span_own));
+#pragma unroll 1
+  for (uint32_t todo = lossy; todo; todo &= todo - 1) {
+    const int m = __builtin_ctz(todo), shift = __builtin_amdgcn_readlane(shift_own, m);
+    float sum = 0.f;
+    for (int k = 8 * lane; k < len; k += 512) sum += lost_of(*(const u32x4 *)(xs + (int64_t)m * A.K + k), shift);
+    sum = wave_sum(sum);
+    lost = lane == m ? sum : lost;
+  }
   {
     // a piece: the five steps of 40 codes, or those that are left, of a group
     // of a row
     constexpr int U = (G + 39) / 40, kLast = G - 40 * (U - 1);
     const int pieces = quads * 4 * GU * U;
     for (int o = tid; o < pieces * M; o += threads) {
-      const int m = o / pieces, e = o - m * pieces, shift = shift_of(m);
+      const int m = o / pieces, e = o - m * pieces, shift = f16_shift(span_top(span_of(m)));
       const int slot = e / U, piece = e - slot * U;  // slot: a group's place
       // in a row's odd last unit the last group comes second
       int g = GU * u0 + slot;
@@ -600,11 +717,6 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
       }
     }
   }
-  int unshift[MT][4];  // of rows 16 mt + 4 q + c
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) unshift[mt][c] = -shift_of(min(16 * mt + 4 * q + c, M - 1));
   __syncthreads();
 
   const L lut(0, lane);
@@ -680,7 +792,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
           const int mt = c0 + ct;
           f32x4 v;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) v[c] = ldexpf(acc[i][mt][c], unshift[mt][c]);
+          for (int c = 0; c < 4; ++c) v[c] = ldexpf(acc[i][mt][c], -__shfl(shift_own, 16 * mt + 4 * q + c));
           *(__attribute__((address_space(3))) f32x4 *)(smem + kRedOff + 16u * (uint32_t)(((i * kOnce + ct) * waves + wv) * 64 + lane)) = v;
           acc[i][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
@@ -688,8 +800,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
       for (int o = tid; o < wt * kOnce * 256; o += threads) {  // [tile][16-row tile][row][column]
         const int ct = (o >> 8) % kOnce, ts = (o >> 8) / kOnce;
         const int mr = (o >> 4) & 15, m = 16 * (c0 + ct) + mr;
-        const int n = ((b0 + j * blocks) * wt + ts) * 16 + (o & 15);
-        if (m >= M || n >= A.N) continue;
+        const int n0 = ((b0 + j * blocks) * wt + ts) * 16, n = n0 + (o & 15);
+        const bool in = m < M && n < A.N;
+        if (!lossy && !in) continue;
         // row mr of column c is element mr % 4 of lane 16 (mr / 4) + c
         const uint32_t at = kRedOff + 16u * (uint32_t)(ts * wk * 64 + (mr >> 2) * 16 + (o & 15)) + 4u * (mr & 3);
         float v[NB];
@@ -698,6 +811,27 @@ __global__ __launch_bounds__(64 * kFewWaves) void few_kernel(const ProjArgs A, c
           v[i] = 0.f;
           for (int w = 0; w < wk; ++w)
             v[i] += *(__attribute__((address_space(3))) float *)(smem + at + 1024u * (uint32_t)((i * kOnce + ct) * waves + w));
+        }
+        if (lossy) {  // a wave's 64 results are of one tile
+          const float mine = __shfl(lost, m);
+          bool low = false;
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+            low = low || fabsf(v[i]) < kLostCounts * mine * scale_top(A, i, n0, 16, nG);
+          for (uint64_t todo = __ballot(in && low); todo; todo &= todo - 1) {
+            const int r = __builtin_ctzll(todo);
+            const int mm = __builtin_amdgcn_readlane(m, r), nn = __builtin_amdgcn_readlane(n, r);
+            const int sh = __builtin_amdgcn_readlane(shift_own, mm);
+            const int sp = uniform_here(split), g0 = GU * 4 * (nQ * sp / A.splits);
+            const int g1 = min(nG, GU * 4 * (nQ * (sp + 1) / A.splits));
+#pragma unroll 1
+            for (int i = 0; i < NB; ++i) {
+              const float add = lost_part<G, false>(A, i, mm, nn, g0, g1, sh);
+#pragma unroll
+              for (int k = 0; k < NB; ++k) v[k] += lane == r && k == i ? add : 0.f;
+            }
+          }
+          if (!in) continue;
         }
         if constexpr (RT == kOwnT) {
           const int id = A.ids[m];
@@ -801,13 +935,12 @@ void mid_kernel(const ProjArgs A) {
   for (int i = 0; i < NB; ++i)
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) acc[i][mt] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto shift_rows = [&](int sign) {
+  auto shift_rows = [&](int sign, u32x2 of_row, int q) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        const int64_t m = m0 + 16 * mt + 4 * q + c;
-        const int sh = m < A.M ? sign * A.shift[m] : 0;
+        const int sh = sign * __shfl((int)of_row.x, 16 * mt + 4 * q + c);
 #pragma unroll
         for (int i = 0; i < NB; ++i) acc[i][mt][c] = ldexpf(acc[i][mt][c], sh);
       }
@@ -824,7 +957,7 @@ void mid_kernel(const ProjArgs A) {
         add_own_adapters(A, m0, n, id, A.splits, split, acc[0]);
       else
         add_adapters<false>(A, m0, n0, id, A.splits, split, acc);
-      shift_rows(1);
+      shift_rows(1, row_scale(A, m0 + lane), q);
     }
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -881,24 +1014,53 @@ void mid_kernel(const ProjArgs A) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load may still write this block's LDS
   if ((flags & kBadFlag) && A.status) atomicOr(A.status, kDevInvalidByte);
 
-  shift_rows(-1);
-  if (n0 + l >= A.N) return;
+  {
+    static_assert(kMidRows == 64, "a row of x a lane");
+    // from here on: kept through the loop they would cost it registers
+    const int lane = lane_here(), l = lane & 15, q = lane >> 4;
+    const u32x2 of_row = row_scale(A, m0 + lane);
+    shift_rows(-1, of_row, q);
+    const float lost = __uint_as_float(of_row.y);
+    uint32_t low = 0;  // sums that may lack something: bit 4 mt + c, of either matrix
+    if (__ballot(lost > 0.f)) {
+      float most[NB];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+      for (int i = 0; i < NB; ++i) most[i] = kLostCounts * scale_top(A, i, n0, 16, nG);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int64_t m = m0 + 16 * mt + 4 * q + c;
-      if (m >= A.M) continue;
-      const int64_t o = m * A.N + n;
-      if (A.splits > 1) {
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int i = 0; i < NB; ++i) A.partial[((int64_t)split * NB + i) * A.M * A.N + o] = acc[i][mt][c];
-      } else if constexpr (NB == 2) {
-        ((uint16_t *)A.out)[o] = f32_to_bf16(act_value<ACT>(acc[0][mt][c]) * acc[1][mt][c]);
-      } else {
-        ((float *)A.out)[o] = acc[0][mt][c];
-      }
+        for (int c = 0; c < 4; ++c) {
+          const float mine = __shfl(lost, 16 * mt + 4 * q + c);
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+            if (m0 + 16 * mt + 4 * q + c < A.M && n0 + l < A.N && fabsf(acc[i][mt][c]) < most[i] * mine)
+              low |= 1u << (4 * mt + c);
+        }
     }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int64_t m = m0 + 16 * mt + 4 * q + c;
+        if (m >= A.M || n0 + l >= A.N) continue;
+        const int64_t o = m * A.N + n0 + l;
+        if (A.splits > 1) {
+#pragma unroll
+          for (int i = 0; i < NB; ++i) A.partial[((int64_t)split * NB + i) * A.M * A.N + o] = acc[i][mt][c];
+        } else if constexpr (NB == 2) {
+          ((uint16_t *)A.out)[o] = f32_to_bf16(act_value<ACT>(acc[0][mt][c]) * acc[1][mt][c]);
+        } else {
+          ((float *)A.out)[o] = acc[0][mt][c];
+        }
+      }
+    while (const uint64_t todo = __ballot(low != 0)) {
+      const int r = __builtin_ctzll(todo);
+      const int e = __builtin_ctz((uint32_t)__builtin_amdgcn_readlane((int)low, r));
+      low &= lane == r ? ~(1u << e) : ~0u;
+      mend_result<G, NB, ACT>(A, m0 + 16 * (e / 4) + 4 * (r / 16) + e % 4, n0 + r % 16, split, 4 * q0,
+                              min(nG, 4 * q1), lane == r);
+    }
+  }
 }
 
 // The splits' partial sums, in order, and the operator's last step.
@@ -999,7 +1161,7 @@ void wide_kernel(const ProjArgs A) {
   constexpr uint32_t kQOff = kWideC * kPSlot, kLutOff = kQOff + kWideX * kQSlot;
   __shared__ __align__(16) unsigned char smem_raw[kLutOff + L::kBytes];
   lds_bytes *smem = (lds_bytes *)smem_raw;
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wp = wv / WQ, wq = wv % WQ;
   const int nG = A.K / G, tiles = A.tp * A.tq, split = (int)blockIdx.x / tiles;
@@ -1037,7 +1199,7 @@ void wide_kernel(const ProjArgs A) {
       scale_next[J / S32] = values.load2(soff, g * 2);
     }
   };
-  const L lut(kLutOff, lane);
+  const L lut(kLutOff, tid & 63);
   const uint32_t put0 = rows_at((uint32_t)sr, 2u * hf), put1 = rows_at((uint32_t)sr, 2u * hf + 1u);
   // codes of the stage whose bytes are raw[J], J = its index % 4, -> slot: the
   // table's entries first, some work of others' between, then the rest
@@ -1087,8 +1249,8 @@ void wide_kernel(const ProjArgs A) {
 
   Frags<kRows, kWideP, TP> pf;
   Frags<kRows, kWideQ, TQ> qf;
-  pf.init(lane, wp * (kWideP / WP));
-  qf.init(lane, wq * (kWideQ / WQ));
+  pf.init(tid & 63, wp * (kWideP / WP));
+  qf.init(tid & 63, wq * (kWideQ / WQ));
   f32x4 acc[TP][TQ];
 #pragma unroll
   for (int a = 0; a < TP; ++a)
@@ -1150,12 +1312,23 @@ void wide_kernel(const ProjArgs A) {
 
   // ---- epilogue: lane holds rows n = 16 a + 4 (lane / 16) + r, column
   // m = 16 b + lane % 16 ----
-  const int l = lane & 15, q = lane >> 4;
+  const int lane = lane_here(), l = lane & 15, q = lane >> 4;
   const int64_t mq = q0 + wq * (kWideQ / WQ) + l;
+  const int64_t mw = q0 + wq * (kWideQ / WQ);  // the wave's 64 rows of x, one a lane
+  static_assert(kWideQ / WQ == 64 && 16 * TQ == 64, "");
+  // what x's row of column b needs: read by each lane, or one a lane and handed
+  // over (each way leaves the loop above without spills where it is used)
+  struct Rows {
+    u32x2 own;
+    __device__ __forceinline__ u32x2 of(const ProjArgs &A, int64_t mw, int l, int b) const {
+      if constexpr (NB == 2) return row_scale(A, mw + 16 * b + l);
+      return u32x2{(uint32_t)__shfl((int)own.x, 16 * b + l), (uint32_t)__shfl((int)own.y, 16 * b + l)};
+    }
+  };
+  const Rows for_shift{NB == 2 ? u32x2{} : row_scale(A, mw + lane)};
 #pragma unroll
   for (int b = 0; b < TQ; ++b) {
-    const int64_t m = mq + 16 * b;
-    const int sh = m < A.M ? -A.shift[m] : 0;
+    const int sh = -(int)for_shift.of(A, mw, l, b).x;
 #pragma unroll
     for (int a = 0; a < TP; ++a)
 #pragma unroll
@@ -1177,8 +1350,27 @@ void wide_kernel(const ProjArgs A) {
   if constexpr (NB == 1) {
     if (A.adapters > 0) {
       // the wave's 64 columns, one a lane; the splits share the adapters
-      const int64_t mw = q0 + wq * (kWideQ / WQ);
       add_adapters<true>(A, mw, nw, adapter_of(A, mw + lane, true), A.splits, split, acc);
+    }
+  }
+  const Rows for_lost{row_scale(A, mw + lane_here())};
+  uint32_t low[TQ] = {};  // sums that may lack something: bit 4 a + r, of either matrix
+  if (__ballot(__uint_as_float(for_lost.own.y) > 0.f)) {
+    float most[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) most[i] = kLostCounts * scale_top(A, i, nw, HP, nG);
+#pragma unroll
+    for (int b = 0; b < TQ; ++b) {
+      const float lost = __uint_as_float(for_lost.of(A, mw, l, b).y);
+#pragma unroll
+      for (int a = 0; a < TP; ++a)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int of = a % (TP / NB);
+          if (mq + 16 * b < A.M && nw + 16 * of + 4 * q + r < A.N &&
+              fabsf(acc[a][b][r]) < most[a / (TP / NB)] * lost)
+            low[b] |= 1u << (4 * of + r);
+        }
     }
   }
 #pragma unroll
@@ -1217,11 +1409,28 @@ void wide_kernel(const ProjArgs A) {
       for (int a = 0; a < TP; ++a) store_f32((float *)A.out, m, nw + 16 * a + 4 * q, acc[a][b], vec);
     }
   }
+  if (!__ballot((low[0] | low[1] | low[2] | low[3]) != 0)) return;
+  // a gated result may have been stored by a neighbour (pack8): it has to be there first
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll 1
+  for (int b = 0; b < TQ; ++b) {
+    while (const uint64_t todo = __ballot(low[0] != 0)) {
+      const int j = __builtin_ctzll(todo);
+      const int e = __builtin_ctz((uint32_t)__builtin_amdgcn_readlane((int)low[0], j));
+      low[0] &= lane == j ? ~(1u << e) : ~0u;
+      mend_result<G, NB, ACT>(A, mw + 16 * b + j % 16, nw + 16 * (e / 4) + 4 * (j / 16) + e % 4, split, g0, g1,
+                              lane == j);
+    }
+#pragma unroll
+    for (int k = 0; k + 1 < TQ; ++k) low[k] = low[k + 1];
+  }
 }
 
 // ---------------------------------------------------------------------------
 // before the product, in a launch of its own
 // ---------------------------------------------------------------------------
+
+constexpr int kPreHead = 2 * 4 * kPreWaves;  // LDS bytes before the rows
 
 // The first kRowLds / rpb elements of a row, 16 a thread; zeros past its end.
 __device__ __forceinline__ void load_row(const PreArgs &A, int64_t first, u32x4 (&v)[2]) {
@@ -1235,7 +1444,7 @@ __device__ __forceinline__ void load_row(const PreArgs &A, int64_t first, u32x4 
   }
 }
 
-// Row m of x as f16 times 2^shift[m], for mid_kernel in its fragments
+// Row m of x as f16 times a power of two, and what it loses by that, for mid_kernel in its fragments
 // [chunk][quad][step][16-row tile][lane][8] (rows past M and groups past the
 // last are zeros), for wide_kernel as images of its LDS slots [256 rows][stage
 // of 32 k][slot], in the order of its codes.
@@ -1246,29 +1455,50 @@ __device__ __forceinline__ void load_row(const PreArgs &A, int64_t first, u32x4 
 template <int G, bool FRAG>
 __device__ __forceinline__ void f16_role(const PreArgs &A, int64_t first, int64_t step, int64_t rows_in_all,
                                          u32x4 (&v)[2], unsigned char *smem_raw) {
-  uint32_t *tops = (uint32_t *)smem_raw;             // [16]
+  uint32_t *spans = (uint32_t *)smem_raw;            // [16] of the waves' parts of rows
+  float *losses = (float *)(spans + kPreWaves);      // [16]
   const int threads = kPreThreads / A.rpb, room = kRowLds / A.rpb;
   const int tid = threadIdx.x % threads, part = threadIdx.x / threads;
-  uint16_t *row = (uint16_t *)(smem_raw + 64) + part * room;
+  uint16_t *row = (uint16_t *)(smem_raw + kPreHead) + part * room;
   const int64_t m = first + part;
   const uint16_t *xr = A.x + m * A.K;
   const bool in = m < A.M;
   __syncthreads();  // the rows before have been read
-  uint32_t top = 0;
+  SpanOf mine;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    top = top_of(top, v[i]);
+    mine.take(v[i]);
     *(u32x4 *)(row + 8 * (tid + i * threads)) = v[i];
   }
   if (in)
-    for (int k = room + 8 * tid; k < A.K; k += 8 * threads) top = top_of(top, *(const u32x4 *)(xr + k));
+    for (int k = room + 8 * tid; k < A.K; k += 8 * threads) mine.take(*(const u32x4 *)(xr + k));
   if (first + step < rows_in_all) load_row(A, first + step, v);
-  top = wave_max(top);
-  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  const uint32_t of_wave = span_wave(mine.word());
+  if ((threadIdx.x & 63) == 0) spans[threadIdx.x >> 6] = of_wave;
   __syncthreads();
-  for (int w = 0; w < threads / 64; ++w) top = max(top, tops[part * (threads / 64) + w]);
-  const int shift = f16_shift(top);
-  if (in && tid == 0) A.shift[m] = shift;
+  // joined by four waves (rpb is 4, 2 or 1): of this row, and of all the block's
+  uint32_t four[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const u32x4 s = ((const u32x4 *)spans)[w];
+    four[w] = span_join(span_join(s[0], s[1]), span_join(s[2], s[3]));
+  }
+  const uint32_t lower = span_join(four[0], four[1]), upper = span_join(four[2], four[3]);
+  const uint32_t all = span_join(lower, upper);
+  const uint32_t span = A.rpb == 1 ? all : A.rpb == 2 ? (part ? upper : lower)
+                        : part < 2 ? (part ? four[1] : four[0]) : (part == 2 ? four[2] : four[3]);
+  const int shift = f16_shift(span_top(span));
+  float lost = 0.f;
+  if (span_loses(all)) {  // then a row of the block may; the same for all threads
+    if (in && span_loses(span))
+      for (int k = 8 * tid; k < A.K; k += 8 * threads) lost += lost_of(*(const u32x4 *)(xr + k), shift);
+    lost = wave_sum(lost);
+    if ((threadIdx.x & 63) == 0) losses[threadIdx.x >> 6] = lost;
+    __syncthreads();
+    lost = 0.f;
+    for (int w = 0; w < threads / 64; ++w) lost += losses[part * (threads / 64) + w];
+  }
+  if (in && tid == 0) A.rows[m] = u32x2{(uint32_t)shift, __float_as_uint(lost)};
   constexpr int T = G / 8;
   const int nG = A.K / G, nQ = (nG + 3) / 4, rows = kMidRows;
   const int64_t chunk = FRAG ? m / rows : 0;
@@ -1321,7 +1551,7 @@ constexpr int kPreFrag = 1, kPreRows = 2;
 template <int G, int MODE, int RT>
 __global__ __launch_bounds__(kPreThreads) __attribute__((amdgpu_waves_per_eu(8, 8)))
 void pre_kernel(const PreArgs A) {
-  constexpr int kShrinkLds = RT ? shrink_lds<RT, kPreTiles>() : 0, kRowBytes = 64 + 2 * kRowLds;
+  constexpr int kShrinkLds = RT ? shrink_lds<RT, kPreTiles>() : 0, kRowBytes = kPreHead + 2 * kRowLds;
   __shared__ __align__(16) unsigned char smem[kShrinkLds > kRowBytes ? kShrinkLds : kRowBytes];
   const int row_blocks = (int)gridDim.x - A.shrink_blocks;
   if constexpr (RT > 0) {
@@ -1351,8 +1581,8 @@ struct Plan {
   int kind, wk, wt, splits, tsplits;
   bool own_t;
   int64_t blocks, chunks;
-  int64_t x, shift, t, partial;  // workspace bytes, each a multiple of 16, in this order
-  int64_t total() const { return x + shift + t + partial; }
+  int64_t x, rows, t, partial;  // workspace bytes, each a multiple of 16, in this order
+  int64_t total() const { return x + rows + t + partial; }
 };
 
 // The number of splits of K that costs least, in us: blocks of `steps` steps,
@@ -1426,7 +1656,7 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
         split_of(ceil_div(N, 128) * chunks, quads, 2, 512, 4, G / 32, (NB == 1 ? 3.9 : 5.0) * G / 64, sums);
     // mid_kernel's results go out in runs of 32 bytes
     p.kind = wide.cost < mid.cost + 1.4e-6 * M * N ? kWide : kMid;
-    p.shift = round16(M * 4);
+    p.rows = round16(M * 8);
     if (p.kind == kWide) {
       p.splits = wide.splits;
       p.blocks = wide_tiles * p.splits;
@@ -1479,11 +1709,12 @@ void launch_proj(const Plan &p, ProjArgs a, PreArgs pre, void *workspace, hipStr
   char *ws = (char *)workspace;
   pre.x = a.x;
   pre.xo = (uint16_t *)ws;
-  pre.shift = (int32_t *)(ws + p.x);
-  pre.t = (float *)(ws + p.x + p.shift);
-  a.partial = (float *)(ws + p.x + p.shift + p.t);
+  pre.rows = (u32x2 *)(ws + p.x);
+  pre.t = (float *)(ws + p.x + p.rows);
+  a.partial = (float *)(ws + p.x + p.rows + p.t);
   a.t = pre.t;
-  a.shift = pre.shift;
+  a.x0 = a.x;
+  a.rows = pre.rows;
   a.tsplits = pre.tsplits = p.tsplits;
   a.splits = p.splits;
   a.wk = p.wk;

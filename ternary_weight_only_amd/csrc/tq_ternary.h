@@ -181,27 +181,72 @@ __device__ __forceinline__ _Float16 f16_of(uint32_t bf16, int shift) {
 
 // The power of two that brings the largest finite magnitude `top` (bf16 bits
 // without sign) to [2^14, 2^15): a bf16 value's eight bits fit f16's eleven,
-// so every element down to 2^-32 of the largest is exact in f16, and a smaller
-// one is off by at most 2^-40 of it.
+// so every element down to 2^-32 of the largest is exact in f16.  A smaller
+// one is off by at most 2^-40 of it; what the sums lose by that is added where
+// it counts (lost_part in tq_glu.hip).
 __device__ __forceinline__ int f16_shift(uint32_t top) {
   int exponent;  // top is in [2^(exponent - 1), 2^exponent)
   (void)frexpf(bf16_to_f32(top), &exponent);
   return top ? 15 - exponent : 0;
 }
 
-// The larger of `top` and the largest finite magnitude of eight bf16 values.
-__device__ __forceinline__ uint32_t top_of(uint32_t top, u32x4 v) {
+// Of some bf16 values, as bits without sign: the largest that is finite and
+// the smallest that is not 0, two values a step in packed 16-bit operations.
+// A span is one word, {largest, ~smallest}, and joins by its halves' maxima.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+struct SpanOf {
+  u16x2 top{0, 0};           // less 0x7F80 modulo 2^16: the finite ones from 0x8080 on, Inf and NaN below
+  u16x2 low{0xFFFF, 0xFFFF};  // less one: 0 is the largest
+
+  __device__ __forceinline__ void take(u32x4 v) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t b = (j & 1 ? v[j / 2] >> 16 : v[j / 2]) & 0x7FFFu;
-    top = b < 0x7F80u && b > top ? b : top;
+    for (int j = 0; j < 4; ++j) {
+      const u16x2 b = __builtin_bit_cast(u16x2, v[j] & 0x7FFF7FFFu);
+      top = __builtin_elementwise_max(top, b - (u16x2){0x7F80, 0x7F80});
+      low = __builtin_elementwise_min(low, b - (u16x2){1, 1});
+    }
   }
-  return top;
+  __device__ __forceinline__ uint32_t word() const {
+    const u16x2 t{top.x, (uint16_t)~low.x}, l{top.y, (uint16_t)~low.y};
+    return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(t, l));
+  }
+};
+__device__ __forceinline__ uint32_t span_join(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(
+      uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+__device__ __forceinline__ uint32_t span_wave(uint32_t s) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) s = span_join(s, (uint32_t)__shfl_xor((int)s, o));
+  return s;
+}
+__device__ __forceinline__ uint32_t span_top(uint32_t s) {
+  const uint32_t t = s & 0xFFFFu;
+  return t > 0x8080u ? t - 0x8080u : 0u;
+}
+// Whether some may be inexact in f16 times 2^f16_shift(top): the last bit of
+// one with exponent field f is worth 2^(f - top's field + 7), f16's 2^-24.
+__device__ __forceinline__ bool span_loses(uint32_t s) {
+  const uint32_t smallest = (~s >> 16) + 1u;  // 2^16: none
+  return max(smallest >> 7, 1u) + 31u < span_top(s) >> 7;
 }
 
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+// What a finite bf16 value has that f16_of leaves out (exact), and of eight the
+// magnitudes' sum; 0 of an Inf or NaN.
+__device__ __forceinline__ float lost_of(uint32_t bf16, int shift) {
+  const float v = bf16_to_f32(bf16);
+  return (bf16 & 0x7FFFu) < 0x7F80u ? v - ldexpf((float)f16_of(bf16, shift), -shift) : 0.f;
+}
+__device__ __forceinline__ float lost_of(u32x4 v, int shift) {
+  float sum = 0.f;
 #pragma unroll
-  for (int o = 32; o; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
+  for (int j = 0; j < 8; ++j) sum += fabsf(lost_of((j & 1 ? v[j / 2] >> 16 : v[j / 2]) & 0xFFFFu, shift));
+  return sum;
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
   return v;
 }
 
