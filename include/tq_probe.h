@@ -71,6 +71,25 @@ int tq_probe_lds_table(int iters, int grid, uint32_t *sink, unsigned long long *
 int tq_probe_valu(int kind, int iters, int grid, uint32_t *sink, unsigned long long *clocks,
                   void *stream);
 
+/*
+ * Which kernels a call of these sizes runs, by the rules its launch follows
+ * (host only, no device is touched); what tests at a kernel's sizes check.
+ *
+ * tq_probe_projection_plan: tq_glu (matrices = 2, R ignored) or
+ * tq_lora_matmul (matrices = 1).  plan[0] the kernel (0 few_kernel, 1
+ * mid_kernel, 2 wide_kernel), plan[1] the splits of K, plan[2] the splits of K
+ * that make t, plan[3] 1 where every block makes its own t.
+ *
+ * tq_probe_train_plan: plan[0] the tile of tq_glu_forward (256 or 128);
+ * tq_glu_backward: plan[1] its tile, plan[2] 1 where both products run side by
+ * side, plan[3] and plan[4] the splits of K of the weight gradients and of dx.
+ *
+ * TQ_ERR_NULL, or the error that the calls return for such sizes; M >= 1.
+ */
+int tq_probe_projection_plan(int64_t M, int64_t N, int64_t K, int G, int matrices, int64_t R,
+                             int64_t *plan);
+int tq_probe_train_plan(int64_t M, int64_t N, int64_t K, int64_t *plan);
+
 #ifdef __cplusplus
 }
 #endif

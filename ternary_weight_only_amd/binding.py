@@ -35,8 +35,8 @@ SYMBOLS = ("tq_status_string", "tq_packed_row_bytes", "tq_packed_bytes", "tq_qua
            "tq_glu", "tq_glu_workspace", "tq_lora_matmul", "tq_lora_workspace", "tq_glu_forward",
            "tq_glu_backward", "tq_glu_backward_workspace")
 # Every symbol include/tq_probe.h declares (measurement probes).
-PROBE_SYMBOLS = ("tq_probe_lds_table", "tq_probe_mfma_bf16", "tq_probe_read_stream",
-                 "tq_probe_valu")
+PROBE_SYMBOLS = ("tq_probe_lds_table", "tq_probe_mfma_bf16", "tq_probe_projection_plan",
+                 "tq_probe_read_stream", "tq_probe_train_plan", "tq_probe_valu")
 
 _lib = None
 
@@ -146,6 +146,10 @@ def lib() -> ctypes.CDLL:
         l.tq_probe_lds_table.restype = i32
         l.tq_probe_valu.argtypes = [i32, i32, i32, p, p, p]
         l.tq_probe_valu.restype = i32
+        l.tq_probe_projection_plan.argtypes = [i64, i64, i64, i32, i32, i64, p]
+        l.tq_probe_projection_plan.restype = i32
+        l.tq_probe_train_plan.argtypes = [i64, i64, i64, p]
+        l.tq_probe_train_plan.restype = i32
         _lib = l
     return _lib
 

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "../../include/tq.h"
+#include "../../include/tq_probe.h"
 #include "tq_internal.h"
 
 namespace {
@@ -112,6 +113,17 @@ int tq_lora_matmul(const uint16_t *x, const uint8_t *packed, const uint16_t *sca
   return finish_launch();
 }
 
+int tq_probe_projection_plan(int64_t M, int64_t N, int64_t K, int G, int matrices, int64_t R,
+                             int64_t *plan) {
+  int rc = check_packed_shape(M, N, K, G);
+  if (!rc && matrices == 1) rc = check_rank(M, N, K, 0, R);
+  if (rc) return rc;
+  if (M < 1 || matrices < 1 || matrices > 2) return TQ_ERR_SHAPE;
+  if (!plan) return TQ_ERR_NULL;
+  tq::projection_plan(M, N, K, G, matrices, (int)R, plan);
+  return TQ_OK;
+}
+
 int tq_glu_forward(const uint16_t *x, const uint16_t *wg, const uint16_t *wu, int64_t M,
                    int64_t N, int64_t K, int act, uint16_t *h, uint16_t *g, uint16_t *u,
                    void *stream) {
@@ -153,6 +165,15 @@ int tq_glu_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *wg,
   tq::launch_glu_backward(dh, x, wg, wu, g, u, M, N, K, act, dx, dwg, dwu, workspace,
                           (hipStream_t)stream);
   return finish_launch();
+}
+
+int tq_probe_train_plan(int64_t M, int64_t N, int64_t K, int64_t *plan) {
+  const int rc = check_train_shape(M, N, K);
+  if (rc) return rc;
+  if (M < 1) return TQ_ERR_SHAPE;
+  if (!plan) return TQ_ERR_NULL;
+  tq::train_plan(M, N, K, plan);
+  return TQ_OK;
 }
 
 }  // extern "C"

@@ -1783,6 +1783,11 @@ int64_t lora_workspace(int64_t M, int64_t N, int64_t K, int G, int R) {
   return plan_of(M, N, K, G, 1, R).total();
 }
 
+void projection_plan(int64_t M, int64_t N, int64_t K, int G, int matrices, int R, int64_t *plan) {
+  const Plan p = plan_of(M, N, K, G, matrices, matrices == 1 ? R : 0);
+  plan[0] = p.kind, plan[1] = p.splits, plan[2] = p.tsplits, plan[3] = p.own_t;
+}
+
 void launch_lora(const uint16_t *x, const uint8_t *packed, const uint16_t *scales, int64_t M,
                  int64_t N, int64_t K, int G, const int32_t *ids, const uint16_t *a,
                  const uint16_t *b, const float *scaling, int adapters, int R, float *y,

@@ -503,15 +503,26 @@ BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K) {
   return b;
 }
 
+// 256 x 256 tiles unless the smaller ones fill the chip better.
+bool forward_big(int64_t M, int64_t N, int stages) {
+  return product_us(kRates[0], 2 * N, M, stages, 1, kRates[0].slots) <=
+         product_us(kRates[1], 2 * N, M, stages, 1, kRates[1].slots);
+}
+
 }  // namespace
+
+void train_plan(int64_t M, int64_t N, int64_t K, int64_t *plan) {
+  const BackwardPlan b = plan_backward(M, N, K);
+  plan[0] = kRates[forward_big(M, N, (int)(K / kKS)) ? 0 : 1].size;
+  plan[1] = kRates[b.big ? 0 : 1].size, plan[2] = b.joint;
+  plan[3] = b.w.splits, plan[4] = b.x.splits;
+}
 
 void launch_glu_forward(const uint16_t *x, const uint16_t *wg, const uint16_t *wu, int64_t M,
                         int64_t N, int64_t K, int act, uint16_t *h, uint16_t *g, uint16_t *u,
                         hipStream_t stream) {
   const int stages = (int)(K / kKS);
-  // 256 x 256 tiles unless the smaller ones fill the chip better
-  const bool big = product_us(kRates[0], 2 * N, M, stages, 1, kRates[0].slots) <=
-                   product_us(kRates[1], 2 * N, M, stages, 1, kRates[1].slots);
+  const bool big = forward_big(M, N, stages);
   const Rates &r = kRates[big ? 0 : 1];
   TrainArgs a{};
   a.p0 = wg, a.p1 = wu, a.q = x, a.o0 = h, a.o1 = g, a.o2 = u;

@@ -169,6 +169,7 @@ void launch_lora(const uint16_t *x, const uint8_t *packed, const uint16_t *scale
                  const uint16_t *b, const float *scaling, int adapters, int R, float *y,
                  void *workspace, int32_t *d_status, hipStream_t stream);
 int64_t lora_workspace(int64_t M, int64_t N, int64_t K, int G, int R);
+void projection_plan(int64_t M, int64_t N, int64_t K, int G, int matrices, int R, int64_t *plan);
 
 // Gated feed-forward on bf16 weights, forward and backward (tq_glu_train.hip).
 void launch_glu_forward(const uint16_t *x, const uint16_t *wg, const uint16_t *wu, int64_t M,
@@ -179,5 +180,6 @@ void launch_glu_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *
                          int64_t N, int64_t K, int act, uint16_t *dx, uint16_t *dwg, uint16_t *dwu,
                          void *workspace, hipStream_t stream);
 int64_t glu_backward_workspace(int64_t M, int64_t N, int64_t K);
+void train_plan(int64_t M, int64_t N, int64_t K, int64_t *plan);
 
 }  // namespace tq

@@ -1,0 +1,43 @@
+"""Which kernels the sizes of the GPU tests run, by the library's own rules
+(host only): a rule that changes must not leave a kernel untested."""
+import ctypes
+
+import pytest
+
+from tests.test_ffn_args import _lib
+
+FEW, MID, WIDE = 0, 1, 2
+ONE, TWO = 1, 2                     # matrices: tq_lora_matmul, tq_glu
+
+
+def projection(M, N, K, G, matrices, R=8):
+    """(kernel, splits of K, splits of K for t, whether each block makes t)."""
+    plan = (ctypes.c_int64 * 4)()
+    assert _lib().tq_probe_projection_plan(M, N, K, G, matrices, R, plan) == 0
+    return tuple(plan)
+
+
+def train(M, N, K):
+    """(forward tile, backward tile, side by side, splits of dW, splits of dx)."""
+    plan = (ctypes.c_int64 * 5)()
+    assert _lib().tq_probe_train_plan(M, N, K, plan) == 0
+    return tuple(plan)
+
+
+def test_refusals():
+    lib, plan = _lib(), (ctypes.c_int64 * 5)()
+    for bad, rc in (((4, 8, 64, 32, 2, 8), -3), ((4, 8, 100, 64, 2, 8), -2), ((0, 8, 64, 64, 2, 8), -2),
+                    ((4, 8, 64, 64, 3, 8), -2), ((4, 8, 64, 64, 1, 12), -2)):
+        assert lib.tq_probe_projection_plan(*bad, plan) == rc, bad
+    assert lib.tq_probe_projection_plan(4, 8, 64, 64, 2, 8, None) == -1
+    assert lib.tq_probe_train_plan(4, 8, 96, plan) == -2 and lib.tq_probe_train_plan(0, 8, 64, plan) == -2
+    assert lib.tq_probe_train_plan(4, 8, 64, None) == -1
+
+
+def test_sizes_of_the_spread_tests():
+    from tests import test_gpu_ffn_spread as t
+    for matrices, wide in ((ONE, t.WIDE_ONE), (TWO, t.WIDE_TWO)):
+        plans = {s: projection(*s, matrices) for s in t.SHAPES + wide}
+        kinds = {(p[0], p[1] > 1) for p in plans.values()}
+        assert kinds == {(k, split) for k in (FEW, MID, WIDE) for split in (False, True)}, plans
+        assert all(plans[s][0] == WIDE for s in wide)
