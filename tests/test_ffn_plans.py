@@ -41,3 +41,10 @@ def test_sizes_of_the_spread_tests():
         kinds = {(p[0], p[1] > 1) for p in plans.values()}
         assert kinds == {(k, split) for k in (FEW, MID, WIDE) for split in (False, True)}, plans
         assert all(plans[s][0] == WIDE for s in wide)
+
+
+def test_sizes_of_the_training_tile_tests():
+    from tests import test_gpu_glu_train_tiles as t
+    assert all(train(*s[:3])[0] == 256 for s in t.FORWARD)
+    assert [train(*s[:3])[1:] for s in t.BACKWARD] == [
+        (256, 1, 1, 2), (256, 1, 1, 4), (256, 0, 1, 4), (256, 1, 4, 2), (256, 0, 8, 1), (256, 1, 1, 1)]
