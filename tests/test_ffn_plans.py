@@ -48,3 +48,17 @@ def test_sizes_of_the_training_tile_tests():
     assert all(train(*s[:3])[0] == 256 for s in t.FORWARD)
     assert [train(*s[:3])[1:] for s in t.BACKWARD] == [
         (256, 1, 1, 2), (256, 1, 1, 4), (256, 0, 1, 4), (256, 1, 4, 2), (256, 0, 8, 1), (256, 1, 1, 1)]
+
+
+def test_sizes_of_the_split_and_scale_tests():
+    from tests import test_gpu_lora_splits as s
+    from tests import test_gpu_wide_scales as w
+
+    def of(cases):
+        return [projection(*c[:4], ONE, c[5])[:3] for c in cases]
+
+    for cases, kernel in ((s.MANY, MID), (s.FEW, MID), (s.WIDE, WIDE), (s.LITTLE, FEW)):
+        assert all(p[0] == kernel and (p[1] > 1 or kernel == FEW) for p in of(cases)), of(cases)
+    assert {p[2] for p in of(s.MANY)} == {2, 4} and {p[2] for p in of(s.LITTLE)} == {1, 2}
+    assert all(projection(*c, TWO)[0] == WIDE for c in w.GLU) and all(projection(*c, ONE)[0] == WIDE for c in w.LORA)
+    assert {projection(*c, TWO)[0] for c in w.LONG} == {FEW, MID, WIDE}
