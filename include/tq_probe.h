@@ -78,7 +78,8 @@ int tq_probe_valu(int kind, int iters, int grid, uint32_t *sink, unsigned long l
  * tq_probe_projection_plan: tq_glu (matrices = 2, R ignored) or
  * tq_lora_matmul (matrices = 1).  plan[0] the kernel (0 few_kernel, 1
  * mid_kernel, 2 wide_kernel), plan[1] the splits of K, plan[2] the splits of K
- * that make t, plan[3] 1 where every block makes its own t.
+ * that make t, plan[3] 1 where every block makes its own t; of few_kernel
+ * plan[4] the waves of a tile and plan[5] the tiles of a set (else 0).
  *
  * tq_probe_train_plan: plan[0] the tile of tq_glu_forward (256 or 128);
  * tq_glu_backward: plan[1] its tile, plan[2] 1 where both products run side by

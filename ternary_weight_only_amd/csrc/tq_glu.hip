@@ -1611,6 +1611,25 @@ Split split_of(int64_t blocks, int64_t steps, int64_t least, int64_t places, dou
   return best;
 }
 
+// few_kernel's waves of a tile and tiles of a set: those that take least by
+// measured rates, in us.  A block works on its sets one after another; of a set,
+// each wave takes 1.5 for every four units, all of them together 0.25, and
+// gathering the sums 1.  With fewer waves a tile a set is larger and a block has
+// fewer: as few sets as its 16 waves allow, of equal size.  (M = 1, two matrices,
+// waves by tiles: [14336,4096] 8 x 1 21.4 us, 8 x 2 18.9, 4 x 4 18.1, 2 x 8 25.1,
+// 1 x 16 40.4; [11008,8192] 16 x 1 30.9, 8 x 2 33.9, 4 x 4 32.2, 4 x 3 25.7;
+// [512,4096] 8 x 1 9.8, 4 x 1 10.1, 2 x 1 12.5, 1 x 1 18.8, 8 x 2 12.8.)
+void set_waves(Plan &p, int64_t tiles, int64_t quads, int64_t blocks) {
+  double least = 1e30;
+  for (int64_t wk = std::min<int64_t>(quads, kFewWaves);; wk = ceil_div(wk, 2)) {
+    const int64_t sets = ceil_div(tiles, blocks * (kFewWaves / wk));  // of a block
+    const int64_t wt = ceil_div(tiles, blocks * sets);
+    const double cost = sets * (std::max(1.5 * ceil_div(quads, wk), 0.25 * wt * quads) + 1);
+    if (cost < least) least = cost, p.wk = (int)wk, p.wt = (int)wt;
+    if (wk == 1) break;
+  }
+}
+
 Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
   Plan p{};
   const int64_t nG = K / G;
@@ -1634,19 +1653,11 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
     p.own_t = R && M <= 16 && M * R * ceil_div(fours, p.splits) * 512 * 2 <= kOwnTBytes;
     // (the workspace has room for t either way: callers need not know which)
     const int64_t quads = ceil_div(fours, p.splits), tiles = ceil_div(N, 16);
-    // waves along K: four units each where that many waves are to be
-    // had; as many tiles a block as leave every CU one
-    p.wk = (int)std::min<int64_t>(quads, kFewWaves);
-    const int64_t spread = std::max<int64_t>(1, tiles * p.splits / 224);
-    p.wt = (int)std::min<int64_t>(kFewWaves / p.wk, spread);
-    if (p.wt == 1 && spread >= 4 && p.wk > 4) {
-      // many tiles: fewer sums to gather, more bytes a wave in flight
-      p.wk = 4;
-      p.wt = kFewWaves / p.wk;
-    }
     // a block a CU, beside those that make t
     const int64_t cus = 256 - (R && !p.own_t ? std::min<int64_t>(64, M * p.tsplits) : 0);
-    p.blocks = std::min(ceil_div(tiles, p.wt), std::max<int64_t>(1, cus / p.splits)) * p.splits;
+    const int64_t most = std::max<int64_t>(1, cus / p.splits);  // blocks of a split
+    set_waves(p, tiles, quads, most);
+    p.blocks = std::min(ceil_div(tiles, p.wt), most) * p.splits;
   } else {
     // the cheaper of the two by the model of split_of
     const int64_t quads = ceil_div(nG, 4), chunks = ceil_div(M, kMidRows);
@@ -1786,6 +1797,7 @@ int64_t lora_workspace(int64_t M, int64_t N, int64_t K, int G, int R) {
 void projection_plan(int64_t M, int64_t N, int64_t K, int G, int matrices, int R, int64_t *plan) {
   const Plan p = plan_of(M, N, K, G, matrices, matrices == 1 ? R : 0);
   plan[0] = p.kind, plan[1] = p.splits, plan[2] = p.tsplits, plan[3] = p.own_t;
+  plan[4] = p.wk, plan[5] = p.wt;
 }
 
 void launch_lora(const uint16_t *x, const uint8_t *packed, const uint16_t *scales, int64_t M,
