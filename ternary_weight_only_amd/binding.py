@@ -1086,8 +1086,15 @@ class _FirstGradients(torch.autograd.Function):
 class GLU(torch.autograd.Function):
     """h = act(x wg^T) * (x wu^T) with gradients for x, wg and wu; after
     FakeQuantize the gradients of wg and wu reach the latent weights
-    unchanged.  Gradients that are not needed are still computed; gradients of
-    gradients are refused."""
+    unchanged.  Where no gradient can be asked for, g and u are not written;
+    where one can, all three are computed.  Gradients of gradients are
+    refused."""
+
+    @classmethod
+    def apply(cls, x, wg, wu, act="silu"):
+        if torch.is_grad_enabled() and any(getattr(t, "requires_grad", False) for t in (x, wg, wu)):
+            return super().apply(x, wg, wu, act)
+        return glu_forward(x, wg, wu, act, save=False)
 
     @staticmethod
     def forward(ctx, x, wg, wu, act="silu"):

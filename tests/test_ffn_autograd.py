@@ -11,10 +11,15 @@ from tests import ffn_reference as ref
 @pytest.fixture
 def stand_ins(monkeypatch):
     """glu_forward and glu_backward in float64; the list of the dh that the
-    backward call received."""
-    received = []
+    backward call received, with the list `saved` of the forward calls' save."""
+    class Received(list):
+        pass
+
+    received = Received()
+    received.saved = []
 
     def forward(x, wg, wu, act="silu", save=True, out=None):
+        received.saved.append(save)
         h, g, u, _, _, _ = ref.glu64(x, wg, wu, act)
         return (h, g, u) if save else h
 
@@ -66,3 +71,15 @@ def test_a_gradient_that_starts_anywhere(stand_ins):
     assert len(stand_ins) == 4
     for dh in stand_ins:
         assert dh.is_contiguous() and dh.data_ptr() % 16 == 0
+
+
+def test_nothing_is_saved_where_no_gradient_can_be_asked_for(stand_ins):
+    x, wg, wu = _leaves()
+    want = tq.GLU.apply(x, wg, wu, "gelu")
+    with torch.no_grad():
+        a = tq.GLU.apply(x, wg, wu, "gelu")
+    b = tq.GLU.apply(x.detach(), wg.detach(), wu.detach(), act="gelu")
+    c = tq.GLU.apply(x.detach(), wg, wu.detach(), "gelu")
+    assert stand_ins.saved == [True, False, False, True]
+    assert want.requires_grad and c.requires_grad and not a.requires_grad and not b.requires_grad
+    assert all(torch.equal(t, want) for t in (a, b, c))
