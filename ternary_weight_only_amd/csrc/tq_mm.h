@@ -35,7 +35,6 @@ namespace tq {
 typedef __attribute__((address_space(3))) unsigned char lds_bytes;
 typedef __attribute__((address_space(3))) const bf16x8 lds_bf16x8_c;
 typedef __attribute__((address_space(3))) const u32x2 lds_u32x2_c;
-typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -46,16 +45,6 @@ constexpr uint32_t kNoRow = 0x80000000u;  // past every range: such a load write
 
 constexpr int kRows = 0, kCols = 1;  // operand storage
 
-// The same load for a kernel whose LDS reads the compiler can tell apart from
-// these writes; its own wait counts then include it.
-__device__ __forceinline__ void dma16_tracked(const void *base, lds_bytes *dst, uint32_t off) {
-#if defined(__HIP_DEVICE_COMPILE__)  // the host pass knows no 16-byte load into LDS
-  const __amdgpu_buffer_rsrc_t rs =
-      __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, 0x7FFFFFFF, 0x00020000);
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)dst, 16, off, 0, 0, 0);
-#endif
-}
-
 // Loads at a scalar address, plus a lane's offset, plus a scalar one: no lane
 // holds or adds 64-bit addresses.  Any alignment; zeros past `bytes`.
 struct Scalar {
@@ -63,9 +52,6 @@ struct Scalar {
   __amdgpu_buffer_rsrc_t rs;
   __device__ __forceinline__ explicit Scalar(const void *base, uint32_t bytes = 0x7FFFFFFFu)
       : rs(__builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000)) {}
-  __device__ __forceinline__ bf16x8 load16(uint32_t off, int at) const {
-    return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)off, at, 0));
-  }
   __device__ __forceinline__ uint32_t load4(uint32_t off, int at) const {
     return __builtin_amdgcn_raw_buffer_load_b32(rs, (int)off, at, 0);
   }
@@ -77,7 +63,6 @@ struct Scalar {
   }
 #else
   __device__ explicit Scalar(const void *, uint32_t = 0) {}
-  __device__ bf16x8 load16(uint32_t, int) const { return bf16x8{}; }
   __device__ uint32_t load4(uint32_t, int) const { return 0; }
   __device__ uint32_t load2(uint32_t, int) const { return 0; }
   __device__ uint32_t load1(uint32_t, int) const { return 0; }
@@ -112,6 +97,16 @@ __device__ __forceinline__ void dma16(const void *base, lds_bytes *dst, uint32_t
   const u32x4 rs{(uint32_t)b, (uint32_t)(b >> 32) & 0xFFFFu, 0x7FFFFFFFu, 0x00020000u};
   asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :: "{m0}"((uint32_t)dst), "v"(off), "s"(rs));
+#endif
+}
+
+// The same load for a kernel whose LDS reads the compiler can tell apart from
+// these writes; its own wait counts then include it.
+__device__ __forceinline__ void dma16_tracked(const void *base, lds_bytes *dst, uint32_t off) {
+#if defined(__HIP_DEVICE_COMPILE__)  // the host pass knows no 16-byte load into LDS
+  const __amdgpu_buffer_rsrc_t rs =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, 0x7FFFFFFF, 0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void *)dst, 16, off, 0, 0, 0);
 #endif
 }
 
