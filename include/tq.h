@@ -548,7 +548,8 @@ int tq_w4a16_gemv_grouped(int count, const uint16_t *const *xs, const uint32_t *
  * Gated feed-forward block on packed ternary weights (serving), any M >= 0:
  *   h[m,n] = bf16_rne(act(g[m,n]) * u[m,n]),
  *   g = x Wg_hat^T, u = x Wu_hat^T, both accumulated in fp32 (whatever the
- *   spread of a row of x) and never stored
+ *   spread of a row of x) and not rounded before the product (where K is
+ *   split between blocks, fp32 partial sums of both pass through the workspace)
  * -- the gate and up projections, the activation and the product of one
  * decoder feed-forward block; h is the x of the down projection.
  *   x                        [M,K] bf16, 16-byte aligned
@@ -565,7 +566,9 @@ int tq_w4a16_gemv_grouped(int count, const uint16_t *const *xs, const uint32_t *
  * holds an Inf or NaN gives unspecified (Inf or NaN where the formula has
  * them) values in that row of h and in no other.  Invalid packed bytes set
  * TQ_DEV_INVALID_BYTE; their contribution is then unspecified.
- * Deterministic: a fixed summation order for given shapes.
+ * Deterministic: equal inputs give equal bits.  The summation order follows
+ * from the shapes, and for sums that cancel far below the row's largest
+ * elements from x too.
  */
 int tq_glu(const uint16_t *x, const uint8_t *gate_packed, const uint16_t *gate_scales,
            const uint8_t *up_packed, const uint16_t *up_scales, int64_t M, int64_t N, int64_t K,
@@ -596,7 +599,9 @@ int64_t tq_glu_workspace(int64_t M, int64_t N, int64_t K, int G);
  *   workspace as tq_glu, at least tq_lora_workspace(M, N, K, G, R) bytes
  * An id below -1 or >= adapters sets TQ_DEV_BAD_ADAPTER and counts as -1.
  * M = 0 enqueues nothing.  K, Inf and NaN, invalid bytes and determinism as
- * tq_glu.  Only the adapters that rows name are read.
+ * tq_glu; the order also follows from which adapters a row's 64 neighbours
+ * name, so its last bits may change with them.  Only the adapters that rows
+ * name are read.
  */
 int tq_lora_matmul(const uint16_t *x, const uint8_t *packed, const uint16_t *scales,
                    const int32_t *ids, const uint16_t *A, const uint16_t *B,
@@ -624,7 +629,9 @@ int tq_glu_forward(const uint16_t *x, const uint16_t *wg, const uint16_t *wu, in
 
 /*
  * Gradients of tq_glu_forward given dh, the gradient of h:
- *   dg = dh * u * act'(g), du = dh * act(g)   (rounded to bf16 for the products)
+ *   dg = dh * u * act'(g), du = dh * act(g)   (rounded once to bf16, the type
+ *   the matrix cores multiply: a gradient's error is 0.0023 of it in root mean
+ *   square, where its own rounding alone is 0.0017)
  *   dx = dg Wg + du Wu, dwg = dg^T x, dwu = du^T x
  * accumulated in fp32, each rounded once to bf16.  dwg and dwu are also the
  * gradients of the latent weights (straight-through).

@@ -543,9 +543,11 @@ struct Raw {
 // ends of tiles, and the first before the table is built.  (Two or three ahead
 // cost 2 to 4 us more at M = 7, 2 x [14336,4096]: x's loads wait behind them.)
 // LDS: 64 KB table, 64 KB x, up to 32 KB for the sums of the waves.
-// Bound by the decode: 2 x [14336,4096], G = 64, takes 20 us at 7 rows (28 MB:
-// 1.4 TB/s; 5.4 us at copy rate), VALU issue 0.36 busy between waits for
-// weights.  2 x [3584,1024] at one row: 7.8 us, 4 to 5 of them any launch's.
+// 2 x [14336,4096], G = 64, takes 19.4 us at 7 rows (28 MB: 1.4 TB/s; 5.4 us at
+// copy rate): about 8 before the first sum (a launch's own 4 to 5, the table, x
+// put in order), then the decode, 0.25 us a CU for 16 rows by 512 codes of both
+// matrices, in which VALU issue is 0.7 busy (0.33 of the whole).  2 x [3584,1024]
+// at one row: 7.8 us.
 // lora: the projection alone; the first blocks make t meanwhile (RT as in
 // shrink_role, 0 for none), and expand_kernel adds the adapters.  Of few rows
 // and ranks (RT = kOwnT) every block makes the t of its split, in fp32 beside
@@ -1150,7 +1152,8 @@ constexpr int kWideX = 5, kWideC = 4;  // slots of x, and of codes
 // tiles are few.
 // A stage takes 0.85 us (1.26 PFLOP/s on all CUs; a library's bf16 product
 // reaches 1.45): LDS is busy 0.4 of it, the MFMAs 0.55 to 0.6.  2 x
-// [14336,4096] by 2048 rows: 440 us, 1.09 PFLOP/s, 3.5 tiles a CU.
+// [14336,4096] by 2048 rows: 442 us a call, 11 of them before it, 1.12 PFLOP/s,
+// 3.5 tiles a CU.
 template <int G, int NB, int ACT>
 __global__ __launch_bounds__(kWideThreads) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void wide_kernel(const ProjArgs A) {
@@ -1643,8 +1646,9 @@ Plan plan_of(int64_t M, int64_t N, int64_t K, int G, int NB, int R) {
     p.t = round16(p.tsplits * M * R * 4);
   }
   const int64_t wide_tiles = ceil_div(NB * N, kWideP) * ceil_div(M, kWideQ);
-  // few against mid_kernel at 32 rows: 33 us and 42 ([4096,14336]), 13 and 21
-  // ([1024,3584] of two); at 16 rows 24 and 39
+  // few against mid_kernel at 32 rows: 28.7 us and 36.4 ([4096,14336], 16 ranks),
+  // 31 and 40 (2 x [14336,4096]), 12.2 and 20.7 (2 x [3584,1024]); at 16 rows of
+  // the first 19.5 and 33.5
   if (M <= kFewRows && K >= 128) {
     p.kind = kFew;
     // a block's slice of x, in whole fours of units, fits its LDS

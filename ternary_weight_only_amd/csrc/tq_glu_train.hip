@@ -377,8 +377,13 @@ __global__ __launch_bounds__(256) void reduce_kernel(const TrainArgs W, const Tr
                         (int64_t)((int)gridDim.x - w_blocks) * 256);
 }
 
-// [dg | du], each rounded once to bf16 (the type the matrix cores take); the
-// columns past N of each half are zeros.  Eight columns a thread; VEC: N % 8
+// [dg | du], each rounded once to bf16, the type the matrix cores take: it is
+// all that a gradient loses beside its own rounding (error 0.0023 in root mean
+// square, where that rounding alone makes 0.0017).  With a second bf16 piece of
+// each multiplied too the error was 0.0017, and the matrix cores' work twice as
+// much: 4096 rows of [3584,1024] 269 us instead of 148, 2048 rows of
+// [14336,4096] 1631 instead of 842.
+// The columns past N of each half are zeros.  Eight columns a thread; VEC: N % 8
 // == 0, so the inputs' eight are one aligned load.
 template <int ACT, bool VEC>
 __global__ __launch_bounds__(256) void gate_grad_kernel(const uint16_t *__restrict__ dh,
