@@ -60,26 +60,41 @@ typedef enum {
     TQ_ERR_ALIGN = -4,   /* a pointer is not aligned as its call requires       */
     TQ_ERR_LAUNCH = -5,  /* the HIP runtime reported an error at launch         */
     TQ_ERR_WORKSPACE = -6, /* a workspace is smaller than its call asks for      */
-    TQ_ERR_ACT = -7      /* act is not a tq_act value                           */
+    TQ_ERR_ACT = -7,     /* act is not a tq_act value that the call takes       */
+    TQ_ERR_TYPE = -8,    /* a type is not a tq_type value                       */
+    TQ_ERR_VALUE = -9    /* eps is not a positive finite number                 */
 } tq_status;
 
 /* Device status bits. */
 enum {
-    TQ_DEV_NONFINITE = 1,      /* a weight (tq_quantize_pack) or a scale           */
-                               /* (tq_dequantize) is Inf or NaN                    */
+    TQ_DEV_NONFINITE = 1,      /* a weight (tq_quantize_pack), a scale             */
+                               /* (tq_dequantize) or a row (tq_rms_norm_*) has an  */
+                               /* Inf or NaN                                       */
     TQ_DEV_SCALE_OVERFLOW = 2, /* a group mean rounds to >= 65520 (tq_quantize_pack)*/
     TQ_DEV_INVALID_BYTE = 4,   /* a packed byte is >= 243 (unpack, gemv, gemm)     */
     TQ_DEV_BAD_PADDING = 8,    /* a padding trit is not code 0 (tq_unpack,         */
                                /* tq_dequantize)                                   */
-    TQ_DEV_BAD_ADAPTER = 16    /* an adapter id is below -1 or >= adapters         */
+    TQ_DEV_BAD_ADAPTER = 16,   /* an adapter id is below -1 or >= adapters         */
                                /* (tq_lora_matmul)                                 */
+    TQ_DEV_BAD_SEGMENT = 32,   /* offsets leave 0 .. T or fall (tq_expert_gemm_i8) */
+    TQ_DEV_BAD_ROW = 64        /* a row index is below 0 or >= sources             */
+                               /* (tq_expert_gemm_i8)                              */
 };
 
-/* Gate activations of the gated feed-forward calls. */
+/* Activations: the gated feed-forward calls take the first two, the 8-bit
+ * products all four. */
 typedef enum {
     TQ_ACT_SILU = 0, /* g / (1 + e^-g)                                          */
-    TQ_ACT_GELU = 1  /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2         */
+    TQ_ACT_GELU = 1, /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2         */
+    TQ_ACT_NONE = 2, /* g                                                       */
+    TQ_ACT_RELU2 = 3 /* max(g, 0)^2                                             */
 } tq_act;
+
+/* Element types of the calls that take several. */
+typedef enum {
+    TQ_BF16 = 0,
+    TQ_F32 = 1
+} tq_type;
 
 /* Human-readable name of a tq_status value. */
 const char *tq_status_string(int status);
@@ -648,6 +663,129 @@ int tq_glu_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *wg,
 
 /* Workspace bytes of tq_glu_backward; 0 also on bad arguments (host-only helper). */
 int64_t tq_glu_backward_workspace(int64_t M, int64_t N, int64_t K);
+
+/*
+ * Root-mean-square norm in front of a projection that reads 8-bit rows, with
+ * the residual's addition (serving):
+ *   y[m,k] = x[m,k] + residual[m,k], rounded once to residual_type (y is x
+ *            where residual is NULL)
+ *   rms    = sqrt(sum_k y[m,k]^2 / K + eps),  t = y[m,k] * weight[k]
+ *   q[m,k] = round_half_even(127 * t / max_k |t|)
+ *   scales[m] = max_k |t| / (127 * rms)
+ * so that q * scales is the normalized row times the weight to within half a
+ * step.  q is exact for the y that is stored (where y and weight are both fp32,
+ * to fp64); a row of zeros gets q = 0 and scale 0.
+ *   x         [M,K] of x_type;  residual [M,K] of residual_type, or NULL
+ *   weight    [K] of weight_type, or NULL for ones
+ *   eps       positive and finite
+ *   q         [M,K] int8, overwritten;  scales [M] fp32, overwritten
+ *   y         [M,K] of residual_type, overwritten; NULL where residual is.  It
+ *             may be the residual's own memory (or x's, if x_type is
+ *             residual_type), and then exactly that.
+ * Types are tq_type values; a type whose tensor is NULL is ignored.  Pointers
+ * are aligned as their elements are.  A row with an Inf or NaN in t sets
+ * TQ_DEV_NONFINITE and gets q = 0 and scale NaN; others are not affected.  K is at most
+ * 2097152 (2^21).  M = 0 enqueues nothing.  Bit-exact and deterministic but
+ * for the last bits of scales, and those do not depend on M.
+ */
+int tq_rms_norm_i8(const void *x, int x_type, const void *residual, int residual_type,
+                   const void *weight, int weight_type, int64_t M, int64_t K, double eps,
+                   int8_t *q, float *scales, void *y, int32_t *d_status, void *stream);
+
+/*
+ * The same with the values that q and scales stand for (training: what the
+ * projection's fake-quantized weights are multiplied by):
+ *   h[m,k] = bf16_rne(q[m,k] * scales[m])
+ *   rstd   [M] fp32, overwritten: 1 / rms, which the backward call reads; NULL
+ *          when no gradient is needed
+ * A row with an Inf or NaN gets h = NaN.  All else as tq_rms_norm_i8.
+ */
+int tq_rms_norm_forward(const void *x, int x_type, const void *residual, int residual_type,
+                        const void *weight, int weight_type, int64_t M, int64_t K, double eps,
+                        uint16_t *h, void *y, float *rstd, int32_t *d_status, void *stream);
+
+/*
+ * Gradients of tq_rms_norm_forward, straight through the rounding to 8 bits,
+ * given dh and dy, the gradients of h and y (n = y * rstd):
+ *   dx[m,k]    = rstd (dh w - n mean_k(dh w n)) + dy   (of x and of residual alike)
+ *   dweight[k] = sum_m dh[m,k] n[m,k]
+ * in fp32, each rounded once to its type.
+ *   dh        [M,K] bf16
+ *   y         [M,K] of y_type, as the forward call left it (x without residual)
+ *   rstd      [M] fp32;  weight as the forward call had it
+ *   dy        [M,K] of y_type, or NULL for zeros
+ *   dx        [M,K] of y_type, overwritten
+ *   dweight   [K] of weight_type, overwritten; NULL to leave it out, and where
+ *             weight is NULL
+ *   workspace device memory, 16-byte aligned, at least
+ *             tq_rms_norm_backward_workspace(M, K) bytes, as tq_glu's
+ * M = 0 sets dweight to 0.  Deterministic.
+ */
+int tq_rms_norm_backward(const uint16_t *dh, const void *y, int y_type, const float *rstd,
+                         const void *weight, int weight_type, const void *dy, int64_t M, int64_t K,
+                         void *dx, void *dweight, void *workspace, int64_t workspace_bytes,
+                         void *stream);
+
+/* Workspace bytes of tq_rms_norm_backward; 0 also on bad arguments (host-only helper). */
+int64_t tq_rms_norm_backward_workspace(int64_t M, int64_t K);
+
+/*
+ * 8-bit rows times packed ternary weights, with an epilogue (serving), any M >= 0:
+ *   v[m,n] = x_scales[m] * sum_g scales[n,g] * (sum_{j<G} x[m,gG+j] * c[n,gG+j])
+ *   out[m,n] = act(v[m,n] + bias[n]) + residual[m,n], rounded once to out_type
+ * The inner sums are whole numbers and exact; the sum over groups and the
+ * epilogue are fp32.
+ *   x         [M,K] int8 (any value), 16-byte aligned;  x_scales [M] fp32
+ *   packed    [N, K/G, ceil(G/5)] bytes (any alignment)
+ *   scales    [N, K/G] fp16
+ *   bias      [N] of bias_type, or NULL
+ *   act       a tq_act
+ *   residual  [M,N] of out_type, or NULL; it may be out itself
+ *   out       [M,N] of out_type, overwritten
+ *   workspace as tq_glu, at least tq_gemm_i8_workspace(M, N, K, G) bytes
+ * M = 0 enqueues nothing.  K is at most 2097152 (2^21).  Inf and NaN in scales,
+ * bias and residual reach the results that use them and no others (the scale
+ * of a row or group counts as used where its codes are 0).  Invalid packed bytes
+ * set TQ_DEV_INVALID_BYTE; their contribution is then unspecified.
+ * Deterministic; the summation order follows from the shapes.
+ */
+int tq_gemm_i8(const int8_t *x, const float *x_scales, const uint8_t *packed,
+               const uint16_t *scales, const void *bias, int bias_type, int act,
+               const void *residual, int64_t M, int64_t N, int64_t K, int G, void *out,
+               int out_type, void *workspace, int64_t workspace_bytes, int32_t *d_status,
+               void *stream);
+
+/* Workspace bytes of tq_gemm_i8; 0 also on bad arguments (host-only helper). */
+int64_t tq_gemm_i8_workspace(int64_t M, int64_t N, int64_t K, int G);
+
+/*
+ * The same grouped by expert: of T rows sorted by expert, rows offsets[e] ..
+ * offsets[e+1] - 1 (any number of them, none too) are multiplied by expert e's
+ * weights, and get its bias.  Row m's x and x_scales are those of row rows[m]
+ * where rows is given (a token's row for each of its experts, not copied), else
+ * of row m.
+ *   x         [sources,K] int8, 16-byte aligned;  x_scales [sources] fp32
+ *   rows      [T] int32, or NULL (then sources >= T)
+ *   packed    [experts, N, K/G, ceil(G/5)];  scales [experts, N, K/G]
+ *   offsets   [experts+1] int32 on the device, 1 <= experts <= 65536
+ *   bias      [experts,N], or NULL
+ *   residual, out   [T,N]
+ *   workspace at least tq_expert_gemm_i8_workspace(T, N, K, G, experts) bytes
+ * Rows before offsets[0] and from offsets[experts] on are of no expert: their
+ * out is left as it was.  Only the experts that have rows are read.  Offsets
+ * that leave 0 .. T or fall set TQ_DEV_BAD_SEGMENT; out is then unspecified.  A
+ * row index out of range sets TQ_DEV_BAD_ROW and counts as a row of zeros.
+ * All else as tq_gemm_i8.
+ */
+int tq_expert_gemm_i8(const int8_t *x, const float *x_scales, int64_t sources,
+                      const int32_t *rows, const uint8_t *packed, const uint16_t *scales,
+                      const int32_t *offsets, int64_t experts, const void *bias, int bias_type,
+                      int act, const void *residual, int64_t T, int64_t N, int64_t K, int G,
+                      void *out, int out_type, void *workspace, int64_t workspace_bytes,
+                      int32_t *d_status, void *stream);
+
+/* Workspace bytes of tq_expert_gemm_i8; 0 also on bad arguments (host-only helper). */
+int64_t tq_expert_gemm_i8_workspace(int64_t T, int64_t N, int64_t K, int G, int64_t experts);
 
 #ifdef __cplusplus
 }

@@ -26,6 +26,12 @@ package only marshals torch tensors to that ABI:
     h, g, u        = glu_forward(x_bf16, w_hat, w_hat)       # gated block on bf16 weights
     dx, dwg, dwu   = glu_backward(dh, x_bf16, w_hat, w_hat, g, u)
     h              = GLU.apply(x_bf16, w_hat, w_hat)         # both, for autograd
+    q, s, y        = rms_norm_i8(x, weight, residual)        # norm into 8-bit rows, y = x + residual
+    h, y, rstd     = rms_norm_forward(x, weight, residual)   # the values those stand for (training)
+    dx, dweight    = rms_norm_backward(dh, y, rstd, weight, dy)
+    h, y           = RMSNorm.apply(x, weight, residual)      # both, for autograd
+    y              = gemm_i8(q, s, packed, scales, N, K, G, bias, act, residual)  # 8-bit rows, any M
+    y              = expert_gemm_i8(q, s, packed, scales, offsets, N, K, G)  # grouped by expert
 
 `ternary_weight_only_amd.package` writes and reads the per-tensor package
 (codes + fp16 scales + sha256 hashes) and decodes it to bf16 on the device.
@@ -37,15 +43,20 @@ missing build raises immediately; there is no CPU fallback.
 from .binding import (  # noqa: F401
     FakeQuantize,
     GLU,
+    RMSNorm,
     TQError,
     DEV_BAD_ADAPTER,
     DEV_BAD_PADDING,
+    DEV_BAD_ROW,
+    DEV_BAD_SEGMENT,
     DEV_INVALID_BYTE,
     DEV_NONFINITE,
     DEV_SCALE_OVERFLOW,
     check,
     dequantize,
     dequantize_batched,
+    expert_gemm_i8,
+    expert_gemm_i8_workspace,
     fake_quantize,
     fake_quantize_batched,
     fake_quantize_f32,
@@ -53,6 +64,8 @@ from .binding import (  # noqa: F401
     gemm,
     gemm_batched,
     gemm_grouped,
+    gemm_i8,
+    gemm_i8_workspace,
     gemv,
     gemv_batched,
     gemv_grouped,
@@ -81,6 +94,10 @@ from .binding import (  # noqa: F401
     quantize_pack_batched,
     quantize_pack2,
     quantize_pack2_batched,
+    rms_norm_backward,
+    rms_norm_backward_workspace,
+    rms_norm_forward,
+    rms_norm_i8,
     unpack,
     unpack_batched,
     unpack2,

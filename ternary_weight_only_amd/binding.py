@@ -21,8 +21,11 @@ DEV_SCALE_OVERFLOW = 2
 DEV_INVALID_BYTE = 4
 DEV_BAD_PADDING = 8
 DEV_BAD_ADAPTER = 16
+DEV_BAD_SEGMENT = 32
+DEV_BAD_ROW = 64
 
 ACTS = {"silu": 0, "gelu": 1}
+ACTS_I8 = {None: 2, "silu": 0, "gelu": 1, "relu2": 3}
 
 # Every symbol include/tq.h declares.
 SYMBOLS = ("tq_status_string", "tq_packed_row_bytes", "tq_packed_bytes", "tq_quantize_pack",
@@ -33,7 +36,9 @@ SYMBOLS = ("tq_status_string", "tq_packed_row_bytes", "tq_packed_bytes", "tq_qua
            "tq_gemv2_grouped", "tq_gemm2", "tq_gemm2_batched", "tq_w4a16_gemv", "tq_w4a16_gemv_batched", "tq_w4a16_gemv_grouped",
            "tq_w4a16_gemm", "tq_w4a16_gemm_batched", "tq_gemv", "tq_gemv_batched", "tq_gemv_grouped", "tq_gemm", "tq_gemm_batched", "tq_gemm_grouped",
            "tq_glu", "tq_glu_workspace", "tq_lora_matmul", "tq_lora_workspace", "tq_glu_forward",
-           "tq_glu_backward", "tq_glu_backward_workspace")
+           "tq_glu_backward", "tq_glu_backward_workspace", "tq_rms_norm_i8", "tq_rms_norm_forward",
+           "tq_rms_norm_backward", "tq_rms_norm_backward_workspace", "tq_gemm_i8",
+           "tq_gemm_i8_workspace", "tq_expert_gemm_i8", "tq_expert_gemm_i8_workspace")
 # Every symbol include/tq_probe.h declares (measurement probes).
 PROBE_SYMBOLS = ("tq_probe_lds_table", "tq_probe_mfma_bf16", "tq_probe_projection_plan",
                  "tq_probe_read_stream", "tq_probe_train_plan", "tq_probe_valu")
@@ -137,6 +142,24 @@ def lib() -> ctypes.CDLL:
         l.tq_glu_backward.restype = i32
         l.tq_glu_backward_workspace.argtypes = [i64, i64, i64]
         l.tq_glu_backward_workspace.restype = i64
+        f64 = ctypes.c_double
+        l.tq_rms_norm_i8.argtypes = [p, i32, p, i32, p, i32, i64, i64, f64, p, p, p, p, p]
+        l.tq_rms_norm_i8.restype = i32
+        l.tq_rms_norm_forward.argtypes = [p, i32, p, i32, p, i32, i64, i64, f64, p, p, p, p, p]
+        l.tq_rms_norm_forward.restype = i32
+        l.tq_rms_norm_backward.argtypes = [p, p, i32, p, p, i32, p, i64, i64, p, p, p, i64, p]
+        l.tq_rms_norm_backward.restype = i32
+        l.tq_rms_norm_backward_workspace.argtypes = [i64, i64]
+        l.tq_rms_norm_backward_workspace.restype = i64
+        l.tq_gemm_i8.argtypes = [p, p, p, p, p, i32, i32, p, i64, i64, i64, i32, p, i32, p, i64, p, p]
+        l.tq_gemm_i8.restype = i32
+        l.tq_gemm_i8_workspace.argtypes = [i64, i64, i64, i32]
+        l.tq_gemm_i8_workspace.restype = i64
+        l.tq_expert_gemm_i8.argtypes = [p, p, i64, p, p, p, p, i64, p, i32, i32, p, i64, i64, i64, i32, p, i32,
+                                        p, i64, p, p]
+        l.tq_expert_gemm_i8.restype = i32
+        l.tq_expert_gemm_i8_workspace.argtypes = [i64, i64, i64, i32, i64]
+        l.tq_expert_gemm_i8_workspace.restype = i64
         # measurement probes (include/tq_probe.h)
         l.tq_probe_read_stream.argtypes = [p, i64, i32, p, p]
         l.tq_probe_read_stream.restype = i32
@@ -1114,3 +1137,263 @@ class GLU(torch.autograd.Function):
         if torch.is_grad_enabled():  # create_graph
             grads = _FirstGradients.apply(4, dh, x, wg, wu, *grads)
         return (*grads, None)
+
+
+# ---------------------------------------------------------------------------
+# rows in 8 bits: the norm that makes them, the products that read them
+# ---------------------------------------------------------------------------
+
+TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _typed(t, name: str, shape, device):
+    """(address, tq_type) of a bf16 or fp32 input of exactly `shape`; 0, 0 of None."""
+    if t is None:
+        return 0, 0
+    if (isinstance(t, torch.Tensor) and t.dtype in TYPES and t.shape == shape and t.is_contiguous()
+            and t.get_device() == device.index):
+        return t.data_ptr(), TYPES[t.dtype]
+    _dev(t, name, tuple(TYPES), None, device)
+    raise TQError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+
+
+def _rows_of(x, name: str):
+    """(M, K, device) of a 2-D device tensor."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        _dev(x, name, tuple(TYPES) + I8, 2)
+    return x.shape[0], x.shape[1], x.device
+
+
+def _exactly(t, name: str, shape, dtype, device):
+    """A call's output of `shape` and `dtype`, allocated or the caller's; (tensor, address)."""
+    if t is None:
+        t = torch.empty(*shape, dtype=dtype, device=device)
+        return t, t.data_ptr()
+    return t, _shaped(t, name, shape, (dtype,), device)
+
+
+def _eps(eps) -> float:
+    if not isinstance(eps, (int, float)):
+        raise TQError("eps must be a number, not %r" % (eps,))
+    return float(eps)
+
+
+def _norm_args(x, weight, residual, eps):
+    M, K, dev = _rows_of(x, "x")
+    xp, xt = _typed(x, "x", (M, K), dev)
+    rp, rt = _typed(residual, "residual", (M, K), dev)
+    wp, wt = _typed(weight, "weight", (K,), dev)
+    return (xp, xt, rp, rt, wp, wt, M, K, _eps(eps)), M, K, dev
+
+
+def _sum_out(y, x, residual, M, K, dev):
+    """(the sum, its address to write): x itself where nothing is added."""
+    if residual is None:
+        if y is not None:
+            raise TQError("y is written only with a residual")
+        return x, 0
+    return _exactly(y, "y", (M, K), residual.dtype, dev)
+
+
+def rms_norm_i8(x, weight=None, residual=None, eps: float = 1e-6, status=None, out=None):
+    """Root-mean-square norm into 8-bit rows, with the residual's addition:
+    x [M,K], residual [M,K] or None, weight [K] or None, each bf16 or fp32 ->
+    (q int8 [M,K], scales fp32 [M], y) with y = x + residual in residual's type
+    (x itself without one) and q * scales = y / sqrt(mean(y^2) + eps) * weight to
+    within half a step of each row's largest / 127.  `out`, if given, is that
+    triple (y None without a residual); y may be the residual."""
+    args, M, K, dev = _norm_args(x, weight, residual, eps)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return rms_norm_i8(x, weight, residual, eps, status, out)
+    q, s, y = (None, None, None) if out is None else out
+    q, qp = _exactly(q, "q", (M, K), torch.int8, dev)
+    s, sp = _exactly(s, "scales", (M,), torch.float32, dev)
+    y, yp = _sum_out(y, x, residual, M, K, dev)
+    rc = lib().tq_rms_norm_i8(*args, qp, sp, yp, _st(status, dev) if status is not None else 0, _stream_of(dev))
+    if rc:
+        _rc(rc, "tq_rms_norm_i8")
+    return q, s, y
+
+
+def rms_norm_forward(x, weight=None, residual=None, eps: float = 1e-6, status=None, out=None):
+    """rms_norm_i8 with the values that its 8-bit rows stand for (training):
+    (h bf16 [M,K], y, rstd fp32 [M]), h = bf16(q * scales), rstd =
+    1 / sqrt(mean(y^2) + eps), which rms_norm_backward reads.  `out`, if given,
+    is that triple (y None without a residual)."""
+    args, M, K, dev = _norm_args(x, weight, residual, eps)
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return rms_norm_forward(x, weight, residual, eps, status, out)
+    h, y, r = (None, None, None) if out is None else out
+    h, hp = _exactly(h, "h", (M, K), torch.bfloat16, dev)
+    y, yp = _sum_out(y, x, residual, M, K, dev)
+    r, rp = _exactly(r, "rstd", (M,), torch.float32, dev)
+    rc = lib().tq_rms_norm_forward(*args, hp, yp, rp, _st(status, dev) if status is not None else 0,
+                                   _stream_of(dev))
+    if rc:
+        _rc(rc, "tq_rms_norm_forward")
+    return h, y, r
+
+
+def rms_norm_backward_workspace(M: int, K: int) -> int:
+    """Workspace bytes of rms_norm_backward; 0 for invalid arguments."""
+    return int(lib().tq_rms_norm_backward_workspace(M, K))
+
+
+def rms_norm_backward(dh, y, rstd, weight=None, dy=None, out=None, workspace=None):
+    """Gradients of rms_norm_forward, straight through the rounding: dh [M,K]
+    bf16, y and rstd as it returned them, dy [M,K] of y's type or None ->
+    (dx [M,K] of y's type, for x and residual alike; dweight [K] of weight's
+    type, None without one).  `out`, if given, is that pair; `workspace` as for
+    glu, of rms_norm_backward_workspace(M, K) bytes."""
+    M, K, dev = _rows_of(y, "y")
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return rms_norm_backward(dh, y, rstd, weight, dy, out, workspace)
+    yp, yt = _typed(y, "y", (M, K), dev)
+    hp = _shaped(dh, "dh", (M, K), (torch.bfloat16,), dev)
+    rp = _shaped(rstd, "rstd", (M,), F32, dev)
+    wp, wt = _typed(weight, "weight", (K,), dev)
+    dyp = 0 if dy is None else _shaped(dy, "dy", (M, K), (y.dtype,), dev)
+    dx, dw = (None, None) if out is None else out
+    dx, dxp = _exactly(dx, "dx", (M, K), y.dtype, dev)
+    dwp = 0
+    if weight is not None:
+        dw, dwp = _exactly(dw, "dweight", (K,), weight.dtype, dev)
+    elif dw is not None:
+        raise TQError("dweight is written only with a weight")
+    l = lib()
+    ws, wsp, wsn = _workspace(workspace, l.tq_rms_norm_backward_workspace(M, K), dev)
+    rc = l.tq_rms_norm_backward(hp, yp, yt, rp, wp, wt, dyp, M, K, dxp, dwp, wsp, wsn, _stream_of(dev))
+    if rc:
+        _rc(rc, "tq_rms_norm_backward")
+    return dx, dw
+
+
+class RMSNorm(torch.autograd.Function):
+    """rms_norm_forward with gradients for x, weight and residual: h, or (h, y)
+    with a residual.  Gradients of gradients are refused."""
+
+    @classmethod
+    def apply(cls, x, weight=None, residual=None, eps: float = 1e-6):
+        return super().apply(x, weight, residual, eps)
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        h, y, rstd = rms_norm_forward(x, weight, residual, eps)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(y, rstd, weight)
+        ctx.x_type = x.dtype
+        return h if residual is None else (h, y)
+
+    @staticmethod
+    def backward(ctx, dh, dy=None):
+        y, rstd, weight = ctx.saved_tensors
+        with torch.no_grad():
+            if dh is None:  # only the sum is used
+                dx, dw = dy, None
+            else:
+                dx, dw = rms_norm_backward(dh.contiguous(), y, rstd, weight, None if dy is None else dy.contiguous())
+            grads = [None if not need else g for need, g in zip(
+                ctx.needs_input_grad, (None if dx is None else dx.to(ctx.x_type), dw, dx))]
+        if torch.is_grad_enabled():  # create_graph
+            given = [t for t in (dh, dy, y, weight) if t is not None]
+            some = [g for g in grads if g is not None]
+            made = iter(_FirstGradients.apply(len(given), *given, *some))
+            grads = [None if g is None else next(made) for g in grads]
+        return (*grads, None)
+
+
+def _out_type(dtype) -> int:
+    t = TYPES.get(dtype)
+    if t is None:
+        raise TQError("dtype must be torch.bfloat16 or torch.float32, not %r" % (dtype,))
+    return t
+
+
+def _act_i8(act) -> int:
+    a = ACTS_I8.get(act) if act is None or isinstance(act, str) else None
+    if a is None:
+        raise TQError("act must be None or one of %s, not %r" % (sorted(ACTS), act))
+    return a
+
+
+def gemm_i8_workspace(M: int, N: int, K: int, G: int) -> int:
+    """Workspace bytes of gemm_i8; 0 for invalid arguments."""
+    return int(lib().tq_gemm_i8_workspace(M, N, K, G))
+
+
+def gemm_i8(x, x_scales, packed, scales, N: int, K: int, G: int, bias=None, act=None, residual=None,
+            dtype=torch.bfloat16, status=None, out=None, workspace=None):
+    """8-bit rows times packed ternary weights, with an epilogue, any M:
+    x [M,K] int8, x_scales [M] fp32 (rms_norm_i8 makes both), [N,K] packed
+    weights -> [M,N] of `dtype` (bf16 or fp32) =
+    act(x_scales * (x W_hat^T) + bias) + residual.  act is None, "silu", "gelu"
+    (tanh form) or "relu2" (max(v, 0)^2); bias [N] is bf16 or fp32, residual
+    [M,N] of `dtype` (and may be `out`).  `workspace` as for glu, of
+    gemm_i8_workspace(M, N, K, G) bytes."""
+    M, _, dev = _rows_of(x, "x")
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return gemm_i8(x, x_scales, packed, scales, N, K, G, bias, act, residual, dtype, status, out, workspace)
+    xp = _shaped(x, "x", (M, K), I8, dev)
+    xs = _shaped(x_scales, "x_scales", (M,), F32, dev)
+    nb, ns = _packed_sizes(N, K, G)
+    wp_, sp = _pair(packed, scales, nb, ns, dev, "tq_gemm_i8")
+    bp, bt = _typed(bias, "bias", (N,), dev)
+    a, ot = _act_i8(act), _out_type(dtype)
+    rp = 0 if residual is None else _shaped(residual, "residual", (M, N), (dtype,), dev)
+    y, yp = _exactly(out, "out", (M, N), dtype, dev)
+    l = lib()
+    ws, wp, wn = _workspace(workspace, l.tq_gemm_i8_workspace(M, N, K, G), dev)
+    rc = l.tq_gemm_i8(xp, xs, wp_, sp, bp, bt, a, rp, M, N, K, G, yp, ot, wp, wn,
+                      _st(status, dev) if status is not None else 0, _stream_of(dev))
+    if rc:
+        _rc(rc, "tq_gemm_i8")
+    return y
+
+
+def expert_gemm_i8_workspace(T: int, N: int, K: int, G: int, experts: int) -> int:
+    """Workspace bytes of expert_gemm_i8; 0 for invalid arguments."""
+    return int(lib().tq_expert_gemm_i8_workspace(T, N, K, G, experts))
+
+
+def expert_gemm_i8(x, x_scales, packed, scales, offsets, N: int, K: int, G: int, rows=None, bias=None, act=None,
+                   residual=None, dtype=torch.bfloat16, status=None, out=None, workspace=None):
+    """gemm_i8 grouped by expert: of T rows sorted by expert, rows offsets[e] ..
+    offsets[e+1] - 1 meet expert e's weights and bias.  offsets is an int32
+    device tensor [experts+1]; packed and scales hold [experts,N,K] weights, bias
+    is [experts,N].  Row m reads row m of x [T,K], or, with rows (int32 [T]), row
+    rows[m] of x [sources,K].  -> [T,N]; rows outside every segment are left as
+    they were in `out` (and are not set where it is allocated here)."""
+    sources, _, dev = _rows_of(x, "x")
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return expert_gemm_i8(x, x_scales, packed, scales, offsets, N, K, G, rows, bias, act, residual, dtype,
+                                  status, out, workspace)
+    xp = _shaped(x, "x", (sources, K), I8, dev)
+    xs = _shaped(x_scales, "x_scales", (sources,), F32, dev)
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise TQError("offsets must be a 1-D tensor of experts + 1 elements")
+    E = offsets.shape[0] - 1
+    op = _shaped(offsets, "offsets", (E + 1,), I32, dev)
+    T, ip = sources, 0
+    if rows is not None:
+        if not isinstance(rows, torch.Tensor) or rows.dim() != 1:
+            raise TQError("rows must be a 1-D tensor")
+        T = rows.shape[0]
+        ip = _shaped(rows, "rows", (T,), I32, dev)
+    nb, ns = _packed_sizes(N, K, G)
+    wp_, sp = _pair(packed, scales, E * nb, E * ns, dev, "tq_expert_gemm_i8")
+    bp, bt = _typed(bias, "bias", (E, N), dev)
+    a, ot = _act_i8(act), _out_type(dtype)
+    rp = 0 if residual is None else _shaped(residual, "residual", (T, N), (dtype,), dev)
+    y, yp = _exactly(out, "out", (T, N), dtype, dev)
+    l = lib()
+    ws, wp, wn = _workspace(workspace, l.tq_expert_gemm_i8_workspace(T, N, K, G, E), dev)
+    rc = l.tq_expert_gemm_i8(xp, xs, sources, ip, wp_, sp, op, E, bp, bt, a, rp, T, N, K, G, yp, ot, wp, wn,
+                             _st(status, dev) if status is not None else 0, _stream_of(dev))
+    if rc:
+        _rc(rc, "tq_expert_gemm_i8")
+    return y

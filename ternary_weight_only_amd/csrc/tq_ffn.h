@@ -20,7 +20,7 @@ __device__ __forceinline__ uint16_t f32_to_bf16(float f) {
   return __builtin_bit_cast(uint16_t, (__bf16)f);
 }
 
-constexpr int kActSilu = 0, kActGelu = 1;
+constexpr int kActSilu = 0, kActGelu = 1, kActNone = 2, kActRelu2 = 3;  // the last two: tq_i8.hip alone
 
 // sigma(z) = 1 / (1 + e^-z); e^-z overflows to infinity and the quotient to 0.
 // v_rcp_f32 is within one unit of fp32; a correctly rounded division costs

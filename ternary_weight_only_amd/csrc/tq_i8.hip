@@ -1,0 +1,906 @@
+// tq_i8.hip -- 8-bit rows times packed ternary weights, by themselves and
+// grouped by expert.
+//
+//   v[m,n]   = s_x[m] sum_g s[n,g] sum_{j<G} q[m,gG+j] c[n,gG+j]
+//   out[m,n] = act(v[m,n] + bias[n]) + residual[m,n]
+// With experts, rows offsets[e] .. offsets[e+1] - 1 meet the weights (and
+// bias) of expert e; row m's q and s_x are those of row rows[m] where rows are
+// given.
+//
+// A group's inner sum is a whole number below 2^15, made exactly by the 8-bit
+// matrix cores, so the fp16 scale is never rounded into a code; the sum over
+// groups is fp32.  The five codes of a byte come from a table in LDS, four in a
+// dword and the fifth beside them, and dwords of four consecutive codes are put
+// together from them: q is read as it lies in memory.
+//
+// Two kernels multiply:
+//   few_kernel    few rows (of each expert): bound by the weights' bytes.  Each
+//                 lane decodes whole units of 128 codes in registers.
+//   tile_kernel   more: each block decodes its weight rows into LDS, where its
+//                 rows of q use them.
+#include <hip/hip_fp16.h>
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "tq_ffn.h"
+#include "tq_internal.h"
+#include "tq_mm.h"
+
+namespace tq {
+namespace {
+
+__host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) const u32x4 lds_u32x4_c;
+typedef __attribute__((address_space(3))) const f32x4 lds_f32x4_c;
+typedef __attribute__((address_space(3))) float lds_float;
+typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
+
+struct I8Args {
+  const int8_t *q;          // [sources,K]
+  const float *qs;          // [sources]
+  const uint8_t *packed;    // [E,N,K/G,B]
+  const uint16_t *scales;   // [E,N,K/G]
+  const void *bias;         // [E,N] or null
+  const void *residual;     // [T,N] or null, of out's type
+  void *out;                // [T,N]
+  const int32_t *offsets;   // [E+1], null without experts
+  const int32_t *rows;      // [T] or null
+  int64_t T, sources;
+  int N, K, E;
+  bool bias32, out32, vec;  // vec: four columns at a time are aligned
+  int act;
+  float *partial;           // [splits][T][N] where splits > 1
+  int splits;
+  int wk, wt, bpu;          // few: waves of a tile, tiles of a set, blocks of a unit
+  int tp;                   // tile: tiles of weight rows
+  int64_t units;            // few: of the launch
+  int32_t *status;
+};
+
+// ---------------------------------------------------------------------------
+// decoding
+// ---------------------------------------------------------------------------
+
+constexpr uint32_t kBad = 0x00FF0000u;  // in the second dword of invalid bytes' entries
+
+// 256 entries of 8 bytes, COPIES times, as tq_ternary.h lays its table out:
+// codes 0 .. 3 as bytes; code 4 in bytes 0 and 3 of the second dword, whose
+// byte 2 marks invalid bytes.
+template <uint32_t COPIES>
+struct Codes {
+  static constexpr uint32_t kStride = 8 * COPIES, kBytes = 256 * kStride;
+  uint32_t at;
+
+  __device__ __forceinline__ Codes(uint32_t base, int lane) : at(base + 8u * ((uint32_t)lane & (COPIES - 1u))) {}
+
+  __device__ static __forceinline__ void build(lds_bytes *table, int tid, int threads) {
+    constexpr uint32_t kParts = 2, kPer = COPIES / 2 / kParts;  // 16-byte stores a thread
+    const uint32_t part = (uint32_t)tid % kParts;
+    for (uint32_t e = (uint32_t)tid / kParts; e < 256u; e += (uint32_t)threads / kParts) {
+      uint32_t lo = 0, v = e;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        lo |= ((v % 3u - 1u) & 0xFFu) << (8 * i);
+        v /= 3u;
+      }
+      const uint32_t c4 = (v % 3u - 1u) & 0xFFu;
+      const u32x2 entry = e >= 243u ? u32x2{0u, kBad} : u32x2{lo, c4 | c4 << 24};
+      const u32x4 two{entry.x, entry.y, entry.x, entry.y};
+#pragma unroll
+      for (uint32_t k = 0; k < kPer; ++k)
+        *(lds_u32x4 *)(table + e * kStride + 16u * (part + kParts * ((k + (e >> 1)) % kPer))) = two;
+    }
+  }
+
+  __device__ __forceinline__ u32x2 read(lds_bytes *smem, uint32_t word, int i) const {
+    if constexpr (COPIES == 32)  // `at` is below 256: byte 0 the lane, byte 1 the byte
+      return *(lds_u32x2_c *)(smem + __builtin_amdgcn_perm(word, at, 0x0C0C0400u + 0x100u * (uint32_t)i));
+    else
+      return *(lds_u32x2_c *)(smem + (((word >> (8 * i)) & 0xFFu) * kStride + at));
+  }
+};
+
+// The dwords of codes that begin in the first, second, third and fourth of
+// four consecutive bytes a, b, c, d (the first byte's own codes 0 .. 3 are a.x).
+__device__ __forceinline__ uint32_t join_ab(u32x2 a, u32x2 b) { return __builtin_amdgcn_alignbyte(b.x, a.y, 3); }
+__device__ __forceinline__ uint32_t join_bc(u32x2 b, u32x2 c) {
+  return __builtin_amdgcn_perm(c.x, __builtin_amdgcn_alignbyte(b.y, b.x, 3), 0x05040100u);
+}
+__device__ __forceinline__ uint32_t join_cd(u32x2 c, u32x2 d) {
+  return __builtin_amdgcn_perm(d.x, __builtin_amdgcn_alignbyte(c.y, c.x, 2), 0x04020100u);
+}
+__device__ __forceinline__ uint32_t join_d(u32x2 d) { return __builtin_amdgcn_alignbyte(d.y, d.x, 1); }
+
+// Keeps the OR of entries' second dwords where it is written.
+__device__ __forceinline__ void settle(uint32_t &flags) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(flags));
+#endif
+}
+
+// The 26 bytes of a unit (128 codes, one group or two) as two loads bring
+// them: bytes 0 .. 15 and 10 .. 25.
+struct Unit {
+  u32x4 a, b;
+  uint32_t scale;  // fp16, or two
+};
+
+// Dwords 4 P .. of the codes of group `H` of a unit, P < G / 16: 16 codes.
+template <int G, int OFF, class L>
+__device__ __forceinline__ u32x2 unit_entry(lds_bytes *smem, const L &lut, const Unit &u, int i) {
+  const int at = OFF + i;
+  return at < 16 ? lut.read(smem, u.a[at >> 2], at & 3) : lut.read(smem, u.b[(at - 10) >> 2], (at - 10) & 3);
+}
+
+// All codes of the group that starts at byte OFF of a unit, in order.
+template <int G, int OFF, class L>
+__device__ __forceinline__ void decode_unit(lds_bytes *smem, const L &lut, const Unit &u, uint32_t (&d)[G / 4],
+                                            uint32_t &flags) {
+#pragma unroll
+  for (int p = 0; p < G / 20; ++p) {
+    const u32x2 a = unit_entry<G, OFF>(smem, lut, u, 4 * p), b = unit_entry<G, OFF>(smem, lut, u, 4 * p + 1);
+    const u32x2 c = unit_entry<G, OFF>(smem, lut, u, 4 * p + 2), e = unit_entry<G, OFF>(smem, lut, u, 4 * p + 3);
+    flags |= a.y | b.y | c.y | e.y;
+    d[5 * p] = a.x;
+    d[5 * p + 1] = join_ab(a, b);
+    d[5 * p + 2] = join_bc(b, c);
+    d[5 * p + 3] = join_cd(c, e);
+    d[5 * p + 4] = join_d(e);
+    settle(flags);
+  }
+  constexpr int P = G / 20;  // 8 codes are left of 128, 4 of 64
+  const u32x2 a = unit_entry<G, OFF>(smem, lut, u, 4 * P);
+  flags |= a.y;
+  d[5 * P] = a.x;
+  if constexpr (G == 128) {
+    const u32x2 b = unit_entry<G, OFF>(smem, lut, u, 4 * P + 1);
+    flags |= b.y;
+    d[5 * P + 1] = join_ab(a, b);
+  }
+  settle(flags);
+}
+
+__device__ __forceinline__ float f16_value(uint32_t bits) {
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+}
+
+__device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------------------
+// experts' rows
+// ---------------------------------------------------------------------------
+
+// Up to `rows` rows of one expert's segment.
+struct Segment {
+  int e;          // -1: no such unit
+  int64_t a, b;   // its rows
+  int64_t unit;   // which of its units
+};
+
+// Segment e, forced into 0 .. T and to follow its own start, so that offsets
+// of any value lead to no access out of range.
+__device__ __forceinline__ void bounds_of(const I8Args &A, int e, int64_t &a, int64_t &b) {
+  a = min(max((int64_t)A.offsets[e], (int64_t)0), A.T);
+  b = min(max((int64_t)A.offsets[e + 1], a), A.T);
+}
+
+// Units of `rows` rows in all segments before lane's of the 64 from e0 on, and
+// its own; returns those of the 64.
+__device__ __forceinline__ int64_t scan_units(const I8Args &A, int e0, int rows, int64_t &a, int64_t &b,
+                                              int64_t &before, int64_t &own) {
+  const int lane = threadIdx.x & 63, e = e0 + lane;
+  a = b = 0;
+  if (e < A.E) bounds_of(A, e, a, b);
+  own = (b - a + rows - 1) / rows;
+  int64_t sum = own;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t v = __shfl_up((long long)sum, o);
+    if (lane >= o) sum += v;
+  }
+  before = sum - own;
+  return __shfl((long long)sum, 63);
+}
+
+__device__ __forceinline__ int64_t count_units(const I8Args &A, int rows) {
+  if (!A.offsets) return (A.T + rows - 1) / rows;
+  int64_t a, b, before, own, total = 0;
+  for (int e0 = 0; e0 < A.E; e0 += 64) total += scan_units(A, e0, rows, a, b, before, own);
+  return total;
+}
+
+// Unit `u` in the order of the experts; by whole waves, the same in every lane.
+__device__ __forceinline__ Segment find_unit(const I8Args &A, int rows, int64_t u) {
+  if (!A.offsets) return Segment{u * rows < A.T ? 0 : -1, 0, A.T, u};
+  int64_t a, b, before, own;
+  for (int e0 = 0; e0 < A.E; e0 += 64) {
+    const int64_t total = scan_units(A, e0, rows, a, b, before, own);
+    if (u < total) {
+      const uint64_t mask = __ballot(before <= u && u < before + own);
+      const int j = __builtin_ctzll(mask);
+      return Segment{e0 + j, __shfl((long long)a, j), __shfl((long long)b, j), u - __shfl((long long)before, j)};
+    }
+    u -= total;
+  }
+  return Segment{-1, 0, 0, 0};
+}
+
+// Where row m of the product is read: -1 for a row index out of range.
+__device__ __forceinline__ int64_t source_of(const I8Args &A, int64_t m) {
+  if (!A.rows) return m;
+  const int r = A.rows[m];
+  return r >= 0 && r < A.sources ? r : -1;
+}
+
+// ---------------------------------------------------------------------------
+// the epilogue
+// ---------------------------------------------------------------------------
+
+__device__ __forceinline__ float activate(float v, int act) {
+  if (act == kActSilu) return act_value<kActSilu>(v);
+  if (act == kActGelu) return act_value<kActGelu>(v);
+  if (act == kActRelu2) return v > 0.f ? v * v : (v <= 0.f ? 0.f : v);  // NaN stays
+  return v;
+}
+
+// Columns n .. n + C - 1 of row m (all of them below N) of expert e: v is the
+// sum over groups.
+template <int C>
+__device__ __forceinline__ void finish(const I8Args &A, int e, int64_t m, int n, float scale, const float *v) {
+  float o[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) o[i] = v[i] * scale;
+  if (A.bias) {
+    const int64_t at = (int64_t)e * A.N + n;
+    if (A.bias32) {
+      float b[C];
+      __builtin_memcpy(b, (const float *)A.bias + at, sizeof(b));
+#pragma unroll
+      for (int i = 0; i < C; ++i) o[i] += b[i];
+    } else {
+      uint16_t b[C];
+      __builtin_memcpy(b, (const uint16_t *)A.bias + at, sizeof(b));
+#pragma unroll
+      for (int i = 0; i < C; ++i) o[i] += bf16_to_f32(b[i]);
+    }
+  }
+  if (A.act != kActNone)
+#pragma unroll
+    for (int i = 0; i < C; ++i) o[i] = activate(o[i], A.act);
+  const int64_t at = m * A.N + n;
+  if (A.out32) {
+    float *p = (float *)A.out + at;
+    if (A.residual) {
+      float r[C];
+      __builtin_memcpy(r, (const float *)A.residual + at, sizeof(r));
+#pragma unroll
+      for (int i = 0; i < C; ++i) o[i] += r[i];
+    }
+    if constexpr (C == 4)
+      *(f32x4 *)p = f32x4{o[0], o[1], o[2], o[3]};
+    else
+      for (int i = 0; i < C; ++i) p[i] = o[i];
+  } else {
+    uint16_t *p = (uint16_t *)A.out + at;
+    if (A.residual) {
+      uint16_t r[C];
+      __builtin_memcpy(r, (const uint16_t *)A.residual + at, sizeof(r));
+#pragma unroll
+      for (int i = 0; i < C; ++i) o[i] += bf16_to_f32(r[i]);
+    }
+    if constexpr (C == 4)
+      *(u32x2 *)p = u32x2{pack2(o[0], o[1]), pack2(o[2], o[3])};
+    else
+      for (int i = 0; i < C; ++i) p[i] = f32_to_bf16(o[i]);
+  }
+}
+
+// The splits' sums, in order, and the epilogue.  Blocks stride over the rows,
+// threads over the columns.
+__global__ __launch_bounds__(256) void join_kernel(const I8Args A) {
+  const int64_t tn = A.T * A.N;
+  for (int64_t m = blockIdx.y; m < A.T; m += gridDim.y) {
+    int e = 0;
+    if (A.offsets) {  // the expert whose segment has m: the last one that starts at or before it
+      int lo = -1, hi = A.E;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (A.offsets[mid] <= m)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      if (lo < 0 || m >= A.offsets[lo + 1]) continue;  // of no segment: left as it was
+      e = lo;
+    }
+    const int64_t src = source_of(A, m);
+    const float scale = src < 0 ? 0.f : A.qs[src];
+    for (int n = (int)blockIdx.x * 256 + threadIdx.x; n < A.N; n += (int)gridDim.x * 256) {
+      float v = 0.f;
+      const float *p = A.partial + m * A.N + n;
+#pragma unroll 4
+      for (int s = 0; s < A.splits; ++s) v += p[s * tn];
+      finish<1>(A, e, m, n, scale, &v);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// few rows
+// ---------------------------------------------------------------------------
+
+constexpr int few_waves(int copies) { return copies == 32 ? 16 : 8; }
+
+template <int MB, int COPIES>
+struct FewRoom {
+  static constexpr int kRows = 4 * MB, kWaves = few_waves(COPIES);
+  static constexpr uint32_t kTable = Codes<COPIES>::kBytes, kSums = kWaves * MB * 256;
+  static constexpr uint32_t kX = COPIES == 32 ? (159u << 10) - kTable - kSums : 32u << 10;
+};
+
+// A unit is up to 4 MB rows of q (of one expert); a block takes one split of K
+// and sets of wt tiles of 16 weight rows, wk waves a tile.  Lane (l, q) decodes
+// unit q of a quad (512 codes) of weight row l, so its bytes are two wide loads
+// and the four lanes of a row read 104 neighbouring ones.  The matrix cores sum
+// over the four lanes of a row, which have different groups here: so of the 16
+// columns, four are given to each row of q, column 4 i + j with row i's part of
+// unit j and zeros elsewhere, and a result is a row's sum over one unit, exact,
+// which is then scaled.  (Four rows of q a matrix instruction instead of 16;
+// the instructions are far from bounding it.)
+template <int G, int MB, int COPIES>
+__global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Args A) {
+  typedef Codes<COPIES> L;
+  typedef FewRoom<MB, COPIES> Room;
+  constexpr int B = bytes_per_group(G), GU = 128 / G;  // groups of a unit
+  constexpr uint32_t kXOff = Room::kTable, kSumOff = kXOff + Room::kX, kZeroOff = kSumOff + Room::kSums;
+  __shared__ __align__(16) unsigned char smem_raw[kZeroOff + 128];
+  __shared__ float row_scale[Room::kRows];
+  __shared__ int64_t row_source[Room::kRows];
+  lds_bytes *smem = (lds_bytes *)smem_raw;
+  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), waves = threads >> 6;
+  const int split = (int)(blockIdx.x % A.splits);
+  const int b0 = (int)(blockIdx.x / A.splits % A.bpu);
+  const int64_t unit = blockIdx.x / A.splits / A.bpu;
+  const Segment seg = find_unit(A, Room::kRows, unit);
+  if (A.offsets && blockIdx.x == 0 && A.status)
+    for (int e = tid; e < A.E; e += threads)
+      if (A.offsets[e] < 0 || A.offsets[e + 1] < A.offsets[e] || A.offsets[e + 1] > A.T)
+        atomicOr(A.status, kDevBadSegment);
+  if (seg.e < 0) return;
+  const int64_t m0 = seg.a + seg.unit * Room::kRows;
+  const int M = (int)min(seg.b - m0, (int64_t)Room::kRows);
+  const int nG = A.K / G, nU = (nG + GU - 1) / GU, nQ = (nU + 3) / 4;
+  const int u0 = 4 * (int)((int64_t)nQ * split / A.splits), u1 = min(nU, 4 * (int)((int64_t)nQ * (split + 1) / A.splits));
+  const int wk = A.wk, wt = A.wt, kw = wv % wk, tw = wv / wk;
+  const int tiles = (A.N + 15) / 16, sets = (tiles + wt - 1) / wt;
+  const int steps = b0 < sets ? (sets - b0 + A.bpu - 1) / A.bpu : 0;
+  const int quads = (u1 - u0 + 3) / 4, batches = (quads + wk - 1) / wk;
+  const uint8_t *packed = A.packed + (int64_t)seg.e * A.N * nG * B;
+  const uint16_t *scales = A.scales + (int64_t)seg.e * A.N * nG;
+
+  auto tile_row = [&](int j) { return ((b0 + j * A.bpu) * wt + tw) * 16; };
+  const bool active = tw < wt;
+  int fj = 0, fk = 0;  // step and batch of the next request
+  Unit f;
+  auto fetch = [&]() {
+    if (!active) return;
+    // rows past N read row N - 1, units past the last read it, with scales 0
+    const int64_t n = min(tile_row(fj) + l, A.N - 1);
+    const int u = u0 + 4 * (kw + wk * fk) + q, g = GU * min(u, u1 - 1);
+    uint32_t sc;
+    if constexpr (G == 128) {
+      const int64_t at = n * nG + g;
+      const uint8_t *p = packed + at * B;
+      __builtin_memcpy(&f.a, p, 16);
+      __builtin_memcpy(&f.b, p + 10, 16);
+      sc = scales[at];
+    } else if (nG > 1) {
+      // of an odd number of groups the last unit is the last two, the first of which belongs to the unit before
+      const int64_t at = n * nG + min(g, nG - 2);
+      const uint8_t *p = packed + at * B;
+      __builtin_memcpy(&f.a, p, 16);
+      __builtin_memcpy(&f.b, p + 10, 16);
+      __builtin_memcpy(&sc, scales + at, 4);
+      if (g + 1 == nG) sc &= 0xFFFF0000u;
+    } else {  // a row is one group: 13 bytes, the unit's first
+      const uint8_t *p = packed + n * B;
+      u32x2 v, w;
+      __builtin_memcpy(&v, p, 8);
+      __builtin_memcpy(&w, p + 5, 8);
+      f.a = u32x4{v.x, v.y, __builtin_amdgcn_alignbyte(w.y, w.x, 3), w.y >> 24};
+      f.b = u32x4{0u, 0u, 0u, 0u};
+      sc = scales[n];
+    }
+    f.scale = u < u1 ? sc : 0u;
+    if (++fk == batches) {
+      fk = 0;
+      ++fj;
+    }
+  };
+  fetch();
+  L::build(smem, tid, threads);
+  if (tid < 8) *(lds_u32x4 *)(smem + kZeroOff + 16 * tid) = u32x4{0u, 0u, 0u, 0u};
+  if (tid < Room::kRows) {
+    const int64_t src = tid < M ? source_of(A, m0 + tid) : -1;
+    if (src < 0 && tid < M && b0 == 0 && split == 0 && A.status) atomicOr(A.status, kDevBadRow);
+    row_source[tid] = src;
+    row_scale[tid] = src < 0 ? 0.f : A.qs[src];
+  }
+  __syncthreads();
+  // q of the split, a row after another; of the 16-byte chunks of a unit the
+  // halves are exchanged in units 2 and 3 of a quad, so that four rows' four
+  // units fall into different banks
+  const uint32_t ld = 512u * (uint32_t)quads + 16u;
+  {
+    const int chunks = (min(A.K, 128 * u1) - 128 * u0) / 16;
+    const bool odd = GU == 2 && (nG & 1) && nG > 1 && u1 == nU;  // the last unit: the last two groups
+    for (int o = tid; o < M * chunks; o += threads) {
+      const int r = o / chunks, c = o - r * chunks;
+      const int64_t src = row_source[r];
+      u32x4 v{0u, 0u, 0u, 0u};
+      if (src >= 0) v = *(const u32x4 *)(A.q + src * A.K + 128 * (int64_t)u0 + 16 * c);
+      uint32_t to = (uint32_t)c;
+      if (odd && c >= chunks - 4) to += 4;  // its second half
+      *(lds_u32x4 *)(smem + kXOff + r * ld + 16u * (to ^ ((to >> 2) & 4u))) = v;
+      if (odd && c >= chunks - 4)
+        *(lds_u32x4 *)(smem + kXOff + r * ld + 16u * ((uint32_t)c ^ (((uint32_t)c >> 2) & 4u))) = u32x4{0u, 0u, 0u, 0u};
+    }
+  }
+  __syncthreads();
+
+  const L lut(0, lane);
+  const int qc = l & 3, mi = l >> 2;  // this lane's column: unit, row
+  uint32_t flags = 0;
+  f32x4 acc[MB];
+#pragma unroll
+  for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  int j = 0, k = 0;
+  const int total = steps * batches;
+  for (int t = 0; t < total; ++t) {
+    const int quad = kw + wk * k;
+    if (active && tile_row(j) < A.N && quad < quads) {
+      uint32_t d[GU][G / 4];
+      decode_unit<G, 0>(smem, lut, f, d[0], flags);
+      if constexpr (GU == 2) decode_unit<G, 13>(smem, lut, f, d[1], flags);
+      // the scales of this lane's results: rows 4 q + r, unit qc
+      float s[GU][4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t sc = (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (16 * qc + 4 * q + r), (int)f.scale);
+        s[0][r] = f16_value(sc);
+        if constexpr (GU == 2) s[1][r] = f16_value(sc >> 16);
+      }
+      fetch();
+#pragma unroll
+      for (int b = 0; b < MB; ++b) {
+        if (4 * b >= M) break;
+        const uint32_t x0 = kXOff + (uint32_t)(4 * b + mi) * ld + 512u * (uint32_t)quad + 128u * (uint32_t)q;
+        const uint32_t swap = 64u * (uint32_t)(q >> 1);
+        const uint32_t xa = qc == q ? x0 + swap : kZeroOff, xb = qc == q ? x0 - swap : kZeroOff;
+#pragma unroll
+        for (int h = 0; h < GU; ++h) {
+          i32x4 sum{0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < G / 16; ++i) {
+            const int st = h * (G / 16) + i;  // of the unit's eight steps
+            const uint32_t *w = d[h] + 4 * i;
+            const u32x4 x = *(lds_u32x4_c *)(smem + (st < 4 ? xa : xb) + 16u * (uint32_t)st);
+            sum = mfma_i8(u32x4{w[0], w[1], w[2], w[3]}, x, sum);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[b][r] = fmaf(s[h][r], (float)sum[r], acc[b][r]);
+        }
+      }
+    } else {
+      fetch();
+    }
+    if (++k < batches) continue;
+    k = 0;
+    // the tile's last batch: the units' sums (four lanes), then the waves', in order
+    __syncthreads();  // the sums before have been read
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      float mine = 0.f;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        float v = acc[b][r];
+        v += __shfl_xor(v, 1);
+        v += __shfl_xor(v, 2);
+        mine = qc == r ? v : mine;
+        acc[b][r] = 0.f;
+      }
+      *(lds_float *)(smem + kSumOff + 4u * (uint32_t)((b * waves + wv) * 64 + lane)) = mine;
+    }
+    __syncthreads();
+    for (int o = tid; o < wt * MB * 64; o += threads) {  // [tile][row of q][column]
+      const int ts = o / (MB * 64), m = o / 16 % (4 * MB), c = o & 15;
+      const int n = ((b0 + j * A.bpu) * wt + ts) * 16 + c;
+      if (m >= M || n >= A.N) continue;
+      const uint32_t at = (uint32_t)((m >> 2) * waves + ts * wk) * 64 + (uint32_t)(16 * (c >> 2) + 4 * (m & 3) + (c & 3));
+      float v = 0.f;
+      for (int w = 0; w < wk; ++w) v += *(lds_float *)(smem + kSumOff + 4u * (at + 64u * (uint32_t)w));
+      if (A.splits > 1)
+        A.partial[((int64_t)split * A.T + m0 + m) * A.N + n] = v;
+      else
+        finish<1>(A, seg.e, m0 + m, n, row_scale[m], &v);
+    }
+    ++j;
+  }
+  if ((flags & kBad) && A.status) atomicOr(A.status, kDevInvalidByte);
+}
+
+// ---------------------------------------------------------------------------
+// more rows
+// ---------------------------------------------------------------------------
+
+constexpr int kTileThreads = 512;
+
+// 16 bytes a lane from its address straight into LDS at dst + 16 lane, counted
+// by no one but the waits written below (as dma16 in tq_mm.h).
+__device__ __forceinline__ void dma16_from(const void *p, lds_bytes *dst) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"((uint32_t)dst), "v"(p));
+#endif
+}
+
+// Slot rows are 128 bytes of k; chunk c of row r sits at c ^ this, so that the
+// 16 rows and four chunks of an operand read fall into different banks.
+__device__ __forceinline__ uint32_t swap_of(uint32_t r) { return (r >> 1) & 7u; }
+
+// P weight rows by Q rows of q, stages of 128 k; eight waves, WP by WQ, the
+// tile kept with weight rows along a lane's four results.  While stage s is
+// multiplied, q of s + 1 is on its way into LDS, the bytes of s + 2 into
+// registers, and the codes of s + 1 are decoded: two threads a weight row (P =
+// 128: four), 64 codes (32) each.
+template <int G, int P, int Q, int WP>
+__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(P == 256 && Q == 256 ? 2 : 4)))
+void tile_kernel(const I8Args A) {
+  typedef Codes<8> L;
+  constexpr int WQ = 8 / WP, TP = P / WP / 16, TQ = Q / WQ / 16, B = bytes_per_group(G), GS = 128 / G;
+  constexpr uint32_t kPSlot = P * 128, kQSlot = Q * 128, kSSlot = GS * P * 4;
+  constexpr uint32_t kQOff = 2 * kPSlot, kSOff = kQOff + 2 * kQSlot, kLutOff = kSOff + 2 * kSSlot;
+  constexpr int kLoads = Q * 8 / kTileThreads;
+  __shared__ __align__(16) unsigned char smem_raw[kLutOff + L::kBytes];
+  lds_bytes *smem = (lds_bytes *)smem_raw;
+  const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), wp = wv / WQ, wq = wv % WQ;
+  const int nG = A.K / G, S = (A.K + 127) / 128;
+  L::build(smem + kLutOff, tid, kTileThreads);
+  const L lut(kLutOff, lane);
+  const int64_t units = count_units(A, Q);
+  if (A.offsets && blockIdx.x == 0 && A.status)
+    for (int e = tid; e < A.E; e += kTileThreads)
+      if (A.offsets[e] < 0 || A.offsets[e + 1] < A.offsets[e] || A.offsets[e + 1] > A.T)
+        atomicOr(A.status, kDevBadSegment);
+  uint32_t flags = 0;
+  const int64_t tiles = units * A.tp, total = tiles * A.splits;
+  for (int64_t work = blockIdx.x; work < total; work += gridDim.x) {
+    const int split = (int)(work / tiles);
+    const int64_t t = work - split * tiles;
+    const int64_t unit = t / A.tp;
+    const int ip = (int)(t - unit * A.tp);
+    const Segment seg = find_unit(A, Q, unit);
+    if (seg.e < 0) break;
+    const int s0 = (int)((int64_t)S * split / A.splits), s1 = (int)((int64_t)S * (split + 1) / A.splits);
+    const int n0 = ip * P;
+    const int64_t m0 = seg.a + seg.unit * Q;
+    const int M = (int)min(seg.b - m0, (int64_t)Q);
+
+    // q: this thread's chunks of a slot; rows past the last read it
+    const int8_t *from[kLoads];
+    uint32_t upper = 0;  // which of them are in the second half of a stage
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t at = (uint32_t)(i * kTileThreads + tid), r = at >> 3, c = (at & 7u) ^ swap_of(r);
+      const int64_t src = source_of(A, m0 + min((int)r, M - 1));
+      from[i] = A.q + max(src, (int64_t)0) * A.K + 16 * c;
+      upper |= (c >> 2) << i;
+    }
+    auto request = [&](int s) {
+      const bool half = 128 * s + 128 > A.K;  // the second half is past the row: the first again, its codes are 0
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        dma16_from(from[i] + 128 * (int64_t)s - (half && (upper >> i & 1) ? 64 : 0),
+                   smem + kQOff + (uint32_t)(s & 1) * kQSlot + 16u * (uint32_t)(i * kTileThreads + 64 * wv));
+    };
+
+    // codes: waves 0 .. 3 the first 64 of a stage's 128, waves 4 .. 7 the rest,
+    // so that the place of a byte's codes is the same for a wave
+    static_assert(P == 256 || P == 128, "");
+    constexpr int kTurns = 256 / P;  // P = 128: half of the waves of each kind at a time
+    const int hf = wv >> 2, dr = (tid & 255) % P;
+    const bool decodes = (tid & 255) < P;
+    const int64_t wrow = ((int64_t)seg.e * A.N + min(n0 + dr, A.N - 1)) * nG;
+    const uint8_t *bytes = A.packed + wrow * B;
+    const uint16_t *values = A.scales + wrow;
+    (void)kTurns;
+    struct Raw {
+      u32x4 w;
+      uint32_t scale;
+    };
+    Raw raw;
+    auto load_raw = [&](int s) {
+      s = min(s, s1 - 1);
+      if constexpr (G == 128) {
+        __builtin_memcpy(&raw.w, bytes + s * B + 10 * hf, 16);  // bytes 0 .. 15, or 10 .. 25
+        raw.scale = values[s];
+      } else {
+        const int g = min(2 * s + hf, nG - 1);
+        u32x2 a, b;
+        __builtin_memcpy(&a, bytes + g * B, 8);
+        __builtin_memcpy(&b, bytes + g * B + 5, 8);
+        raw.w = u32x4{a.x, a.y, __builtin_amdgcn_alignbyte(b.y, b.x, 3), b.y >> 24};
+        const uint32_t sc = values[g];
+        raw.scale = 2 * s + hf < nG ? sc : 0u;
+      }
+    };
+    auto decode = [&](int s) {
+      if (!decodes) return;
+      uint32_t d[16];
+      auto entry = [&](int i) { return lut.read(smem, raw.w[i >> 2], i & 3); };
+      if (G == 64 || hf == 0) {
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          const u32x2 a = entry(4 * p), b = entry(4 * p + 1), c = entry(4 * p + 2), e = entry(4 * p + 3);
+          flags |= a.y | b.y | c.y | e.y;
+          d[5 * p] = a.x;
+          d[5 * p + 1] = join_ab(a, b);
+          d[5 * p + 2] = join_bc(b, c);
+          d[5 * p + 3] = join_cd(c, e);
+          d[5 * p + 4] = join_d(e);
+        }
+        const u32x2 a = entry(12);
+        flags |= a.y;
+        d[15] = a.x;
+      } else {  // bytes 12 .. 25 are 2 .. 15 here; codes 64 on, the fifth of byte 12 first
+        u32x2 a = entry(2);
+        flags |= a.y;
+#pragma unroll
+        for (int p = 0; p < 3; ++p) {
+          const u32x2 b = entry(4 * p + 3), c = entry(4 * p + 4), e = entry(4 * p + 5);
+          flags |= b.y | c.y | e.y;
+          d[5 * p] = join_ab(a, b);
+          d[5 * p + 1] = join_bc(b, c);
+          d[5 * p + 2] = join_cd(c, e);
+          d[5 * p + 3] = join_d(e);
+          a = entry(4 * p + 6);
+          flags |= a.y;
+          d[5 * p + 4] = a.x;
+        }
+        const u32x2 b = entry(15);
+        flags |= b.y;
+        d[15] = join_ab(a, b);
+      }
+      lds_bytes *slot = smem + (uint32_t)(s & 1) * kPSlot + 128u * (uint32_t)dr;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *(lds_u32x4 *)(slot + 16u * ((uint32_t)(4 * hf + i) ^ swap_of((uint32_t)dr))) =
+            u32x4{d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]};
+      if (GS == 2 || hf == 0)
+        *(lds_float *)(smem + kSOff + (uint32_t)(s & 1) * kSSlot + 4u * (uint32_t)((GS == 2 ? hf : 0) * P + dr)) =
+            f16_value(raw.scale);
+    };
+
+    f32x4 acc[TP][TQ];
+#pragma unroll
+    for (int a = 0; a < TP; ++a)
+#pragma unroll
+      for (int b = 0; b < TQ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    __syncthreads();  // the table is there, and the tile before is done with LDS
+    load_raw(s0);
+    request(s0);
+    decode(s0);
+    load_raw(s0 + 1);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+    const uint32_t pr = (uint32_t)(wp * (P / WP) + l), qr = (uint32_t)(wq * (Q / WQ) + l);
+    // rows 16 apart have the same exchange
+    const uint32_t pat[2] = {128u * pr + 16u * ((uint32_t)q ^ swap_of(pr)), 128u * pr + 16u * ((uint32_t)(4 + q) ^ swap_of(pr))};
+    const uint32_t qat[2] = {128u * qr + 16u * ((uint32_t)q ^ swap_of(qr)), 128u * qr + 16u * ((uint32_t)(4 + q) ^ swap_of(qr))};
+    for (int s = s0; s < s1; ++s) {
+      if (s + 1 < s1) {
+        decode(s + 1);
+        request(s + 1);
+        load_raw(s + 2);
+      }
+      lds_bytes *ps = smem + (uint32_t)(s & 1) * kPSlot, *qs = smem + kQOff + (uint32_t)(s & 1) * kQSlot;
+      lds_bytes *ss = smem + kSOff + (uint32_t)(s & 1) * kSSlot + 4u * (uint32_t)(wp * (P / WP) + 4 * q);
+      u32x4 qf[TQ][2];
+#pragma unroll
+      for (int b = 0; b < TQ; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) qf[b][h] = *(lds_u32x4_c *)(qs + qat[h] + 2048u * (uint32_t)b);
+#pragma unroll
+      for (int a = 0; a < TP; ++a) {
+        const u32x4 pf[2] = {*(lds_u32x4_c *)(ps + pat[0] + 2048u * (uint32_t)a),
+                             *(lds_u32x4_c *)(ps + pat[1] + 2048u * (uint32_t)a)};
+        f32x4 sc[GS];
+#pragma unroll
+        for (int h = 0; h < GS; ++h) sc[h] = *(lds_f32x4_c *)(ss + 4u * (uint32_t)(h * P + 16 * a));
+        i32x4 sum[GS][TQ];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int b = 0; b < TQ; ++b)
+            sum[h % GS][b] = mfma_i8(pf[h], qf[b][h], h < GS ? i32x4{0, 0, 0, 0} : sum[0][b]);
+#pragma unroll
+        for (int h = 0; h < GS; ++h)
+#pragma unroll
+          for (int b = 0; b < TQ; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[a][b][r] = fmaf(sc[h][r], (float)sum[h][b][r], acc[a][b][r]);
+      }
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    }
+
+#pragma unroll
+    for (int b = 0; b < TQ; ++b) {
+      const int r = wq * (Q / WQ) + 16 * b + l;
+      if (r >= M) continue;
+      const int64_t m = m0 + r, src = source_of(A, m);
+      if (src < 0 && ip == 0 && split == 0 && A.status) atomicOr(A.status, kDevBadRow);
+      const float scale = src < 0 ? 0.f : A.qs[src];
+#pragma unroll
+      for (int a = 0; a < TP; ++a) {
+        const int n = n0 + wp * (P / WP) + 16 * a + 4 * q;
+        if (n >= A.N) continue;
+        float v[4] = {acc[a][b][0], acc[a][b][1], acc[a][b][2], acc[a][b][3]};
+        if (A.splits > 1) {
+          float *p = A.partial + ((int64_t)split * A.T + m) * A.N + n;
+          if (A.N % 4 == 0) {
+            *(f32x4 *)p = acc[a][b];
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (n + i < A.N) p[i] = v[i];
+          }
+        } else if (A.vec) {
+          finish<4>(A, seg.e, m, n, scale, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (n + i < A.N) finish<1>(A, seg.e, m, n + i, scale, v + i);
+        }
+      }
+    }
+  }
+  if ((flags & kBad) && A.status) atomicOr(A.status, kDevInvalidByte);
+}
+
+// ---------------------------------------------------------------------------
+// which kernel, and the workspace
+// ---------------------------------------------------------------------------
+
+constexpr int kFew = 0, kTile = 1;
+
+struct Plan {
+  int kind, mb, copies, wk, wt, splits, bpu, p, q;
+  int64_t units, blocks;
+};
+
+uint32_t few_room(int mb, int copies) {
+  if (copies == 8) return 32u << 10;
+  return (159u << 10) - 65536u - (uint32_t)few_waves(copies) * mb * 256u;
+}
+
+Plan plan_of(int64_t T, int64_t N, int64_t K, int G, int64_t E, bool grouped) {
+  (void)G;
+  Plan p{};
+  const int64_t used = grouped ? std::min(E, T) : 1;  // experts that have rows, at most
+  const int64_t mean = ceil_div(T, std::max<int64_t>(used, 1));
+  p.splits = 1;
+  if (mean <= (grouped ? 16 : 32)) {
+    p.kind = kFew;
+    const int64_t want = grouped ? std::min<int64_t>(2 * mean, 32) : mean;
+    p.mb = want <= 4 ? 1 : want <= 8 ? 2 : want <= 16 ? 4 : 8;
+    const int64_t rows = 4 * p.mb, quads = ceil_div(K, 512), tiles = ceil_div(N, 16);
+    p.units = grouped ? T / rows + used : 1;
+    p.copies = rows * (512 * quads + 16) <= few_room(p.mb, 8) ? 8 : 32;
+    const int waves = few_waves(p.copies);
+    const int64_t most = (few_room(p.mb, p.copies) / rows - 16) / 512;  // quads that fit
+    p.splits = (int)ceil_div(quads, most);
+    const int64_t q = ceil_div(quads, p.splits);
+    p.wk = (int)std::min<int64_t>(q, waves);
+    p.wt = std::max(1, waves / p.wk);
+    const int64_t sets = ceil_div(tiles, p.wt);
+    p.bpu = (int)std::max<int64_t>(1, std::min<int64_t>(sets, 512 / std::max<int64_t>(1, used * p.splits)));
+    p.blocks = p.units * p.bpu * p.splits;
+  } else {
+    p.kind = kTile;
+    const bool big = mean >= 192;
+    p.p = big ? 256 : 128;
+    p.q = big ? 256 : 64;
+    p.units = grouped ? T / p.q + used : ceil_div(T, p.q);
+    const int64_t tiles = ceil_div(N, p.p) * p.units, stages = ceil_div(K, 128), places = big ? 256 : 512;
+    while (p.splits < 8 && tiles * (p.splits + 1) <= places && stages / (p.splits + 1) >= 4) ++p.splits;
+    p.blocks = std::min<int64_t>(tiles * p.splits, 1 << 20);
+  }
+  return p;
+}
+
+template <int G>
+void launch(const Plan &p, const I8Args &a, hipStream_t stream) {
+  const dim3 grid((unsigned)p.blocks);
+  if (p.kind == kFew) {
+    const dim3 block(64 * p.wk * p.wt);
+    auto go = [&](auto small, auto big) {
+      if (p.copies == 8)
+        hipLaunchKernelGGL(small, grid, block, 0, stream, a);
+      else
+        hipLaunchKernelGGL(big, grid, block, 0, stream, a);
+    };
+    switch (p.mb) {
+      case 1: go(few_kernel<G, 1, 8>, few_kernel<G, 1, 32>); break;
+      case 2: go(few_kernel<G, 2, 8>, few_kernel<G, 2, 32>); break;
+      case 4: go(few_kernel<G, 4, 8>, few_kernel<G, 4, 32>); break;
+      default: go(few_kernel<G, 8, 8>, few_kernel<G, 8, 32>); break;
+    }
+  } else if (p.q == 256) {
+    hipLaunchKernelGGL((tile_kernel<G, 256, 256, 2>), grid, dim3(kTileThreads), 0, stream, a);
+  } else {
+    hipLaunchKernelGGL((tile_kernel<G, 128, 64, 4>), grid, dim3(kTileThreads), 0, stream, a);
+  }
+  if (a.splits > 1)
+    hipLaunchKernelGGL(join_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(a.N, 256), 64), (unsigned)std::min<int64_t>(a.T, 65535)),
+                       dim3(256), 0, stream, a);
+}
+
+}  // namespace
+
+int64_t gemm_i8_workspace(int64_t T, int64_t N, int64_t K, int G, int64_t E, bool grouped) {
+  const Plan p = plan_of(T, N, K, G, E, grouped);
+  return p.splits > 1 ? (p.splits * T * N * 4 + 15) / 16 * 16 : 0;
+}
+
+void launch_gemm_i8(const int8_t *q, const float *qs, const uint8_t *packed, const uint16_t *scales,
+                    const int32_t *offsets, int64_t E, const int32_t *rows, int64_t sources, const void *bias,
+                    bool bias32, int act, const void *residual, int64_t T, int64_t N, int64_t K, int G, void *out,
+                    bool out32, void *workspace, int32_t *status, hipStream_t stream) {
+  const Plan p = plan_of(T, N, K, G, E, offsets != nullptr);
+  I8Args a{};
+  a.q = q;
+  a.qs = qs;
+  a.packed = packed;
+  a.scales = scales;
+  a.bias = bias;
+  a.residual = residual;
+  a.out = out;
+  a.offsets = offsets;
+  a.rows = rows;
+  a.T = T;
+  a.sources = sources;
+  a.N = (int)N;
+  a.K = (int)K;
+  a.E = (int)E;
+  a.bias32 = bias32;
+  a.out32 = out32;
+  auto at16 = [](const void *v) { return (uintptr_t)v % 16 == 0; };
+  a.vec = N % 4 == 0 && at16(out) && at16(residual) && at16(bias);
+  a.act = act;
+  a.partial = (float *)workspace;
+  a.splits = p.splits;
+  a.wk = p.wk;
+  a.wt = p.wt;
+  a.bpu = p.bpu;
+  a.tp = p.kind == kTile ? (int)ceil_div(N, p.p) : 0;
+  a.units = p.units;
+  a.status = status;
+  if (G == 64)
+    launch<64>(p, a, stream);
+  else
+    launch<128>(p, a, stream);
+}
+
+}  // namespace tq

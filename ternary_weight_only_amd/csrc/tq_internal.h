@@ -13,6 +13,8 @@ constexpr int kDevScaleOverflow = 2;
 constexpr int kDevInvalidByte = 4;
 constexpr int kDevBadPadding = 8;
 constexpr int kDevBadAdapter = 16;
+constexpr int kDevBadSegment = 32;
+constexpr int kDevBadRow = 64;
 
 constexpr int bytes_per_group(int G) { return (G + 4) / 5; }
 
@@ -181,5 +183,24 @@ void launch_glu_backward(const uint16_t *dh, const uint16_t *x, const uint16_t *
                          void *workspace, hipStream_t stream);
 int64_t glu_backward_workspace(int64_t M, int64_t N, int64_t K);
 void train_plan(int64_t M, int64_t N, int64_t K, int64_t *plan);
+
+// Root-mean-square norm with the residual's addition and rows in 8 bits, and
+// its gradients (tq_norm.hip).  q and scales, or h, are written.
+void launch_rms_norm(const void *x, bool x32, const void *r, bool r32, const void *w, bool w32,
+                     int64_t M, int64_t K, double eps, int8_t *q, float *scales, uint16_t *h,
+                     void *y, float *rstd, int32_t *status, hipStream_t stream);
+int64_t rms_norm_backward_workspace(int64_t M, int64_t K);
+void launch_rms_norm_backward(const uint16_t *dh, const void *y, bool y32, const float *rstd,
+                              const void *w, bool w32, const void *dy, int64_t M, int64_t K,
+                              void *dx, void *dw, void *workspace, hipStream_t stream);
+
+// 8-bit rows times packed ternary weights (tq_i8.hip); offsets null: one
+// matrix (E = 1), else grouped by expert.
+int64_t gemm_i8_workspace(int64_t T, int64_t N, int64_t K, int G, int64_t E, bool grouped);
+void launch_gemm_i8(const int8_t *q, const float *qs, const uint8_t *packed,
+                    const uint16_t *scales, const int32_t *offsets, int64_t E, const int32_t *rows,
+                    int64_t sources, const void *bias, bool bias32, int act, const void *residual,
+                    int64_t T, int64_t N, int64_t K, int G, void *out, bool out32, void *workspace,
+                    int32_t *status, hipStream_t stream);
 
 }  // namespace tq
