@@ -181,55 +181,55 @@ __device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c) {
 // experts' rows
 // ---------------------------------------------------------------------------
 
-// Up to `rows` rows of one expert's segment.
+// Up to `rows` rows of one expert's segment (at most 2^30 rows in all, so that
+// their numbers fit int, and in scalar registers).
 struct Segment {
-  int e;          // -1: no such unit
-  int64_t a, b;   // its rows
-  int64_t unit;   // which of its units
+  int e;      // -1: no such unit
+  int a, b;   // its rows
+  int unit;   // which of its units
 };
 
 // Segment e, forced into 0 .. T and to follow its own start, so that offsets
 // of any value lead to no access out of range.
-__device__ __forceinline__ void bounds_of(const I8Args &A, int e, int64_t &a, int64_t &b) {
-  a = min(max((int64_t)A.offsets[e], (int64_t)0), A.T);
-  b = min(max((int64_t)A.offsets[e + 1], a), A.T);
+__device__ __forceinline__ void bounds_of(const I8Args &A, int e, int &a, int &b) {
+  a = min(max(A.offsets[e], 0), (int)A.T);
+  b = min(max(A.offsets[e + 1], a), (int)A.T);
 }
 
 // Units of `rows` rows in all segments before lane's of the 64 from e0 on, and
 // its own; returns those of the 64.
-__device__ __forceinline__ int64_t scan_units(const I8Args &A, int e0, int rows, int64_t &a, int64_t &b,
-                                              int64_t &before, int64_t &own) {
+__device__ __forceinline__ int scan_units(const I8Args &A, int e0, int rows, int &a, int &b, int &before, int &own) {
   const int lane = threadIdx.x & 63, e = e0 + lane;
   a = b = 0;
   if (e < A.E) bounds_of(A, e, a, b);
   own = (b - a + rows - 1) / rows;
-  int64_t sum = own;
+  int sum = own;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const int64_t v = __shfl_up((long long)sum, o);
+    const int v = __shfl_up(sum, o);
     if (lane >= o) sum += v;
   }
   before = sum - own;
-  return __shfl((long long)sum, 63);
+  return __builtin_amdgcn_readlane(sum, 63);
 }
 
-__device__ __forceinline__ int64_t count_units(const I8Args &A, int rows) {
-  if (!A.offsets) return (A.T + rows - 1) / rows;
-  int64_t a, b, before, own, total = 0;
+__device__ __forceinline__ int count_units(const I8Args &A, int rows) {
+  if (!A.offsets) return ((int)A.T + rows - 1) / rows;
+  int a, b, before, own, total = 0;
   for (int e0 = 0; e0 < A.E; e0 += 64) total += scan_units(A, e0, rows, a, b, before, own);
   return total;
 }
 
 // Unit `u` in the order of the experts; by whole waves, the same in every lane.
-__device__ __forceinline__ Segment find_unit(const I8Args &A, int rows, int64_t u) {
-  if (!A.offsets) return Segment{u * rows < A.T ? 0 : -1, 0, A.T, u};
-  int64_t a, b, before, own;
+__device__ __forceinline__ Segment find_unit(const I8Args &A, int rows, int u) {
+  if (!A.offsets) return Segment{(int64_t)u * rows < A.T ? 0 : -1, 0, (int)A.T, u};
+  int a, b, before, own;
   for (int e0 = 0; e0 < A.E; e0 += 64) {
-    const int64_t total = scan_units(A, e0, rows, a, b, before, own);
+    const int total = scan_units(A, e0, rows, a, b, before, own);
     if (u < total) {
-      const uint64_t mask = __ballot(before <= u && u < before + own);
-      const int j = __builtin_ctzll(mask);
-      return Segment{e0 + j, __shfl((long long)a, j), __shfl((long long)b, j), u - __shfl((long long)before, j)};
+      const int j = __builtin_ctzll(__ballot(before <= u && u < before + own));
+      return Segment{e0 + j, __builtin_amdgcn_readlane(a, j), __builtin_amdgcn_readlane(b, j),
+                     u - __builtin_amdgcn_readlane(before, j)};
     }
     u -= total;
   }
@@ -373,14 +373,14 @@ __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Arg
   const int split = (int)(blockIdx.x % A.splits);
   const int b0 = (int)(blockIdx.x / A.splits % A.bpu);
   const int64_t unit = blockIdx.x / A.splits / A.bpu;
-  const Segment seg = find_unit(A, Room::kRows, unit);
+  const Segment seg = find_unit(A, Room::kRows, (int)unit);
   if (A.offsets && blockIdx.x == 0 && A.status)
     for (int e = tid; e < A.E; e += threads)
       if (A.offsets[e] < 0 || A.offsets[e + 1] < A.offsets[e] || A.offsets[e + 1] > A.T)
         atomicOr(A.status, kDevBadSegment);
   if (seg.e < 0) return;
   const int64_t m0 = seg.a + seg.unit * Room::kRows;
-  const int M = (int)min(seg.b - m0, (int64_t)Room::kRows);
+  const int M = min(seg.b - (int)m0, Room::kRows);
   const int nG = A.K / G, nU = (nG + GU - 1) / GU, nQ = (nU + 3) / 4;
   const int u0 = 4 * (int)((int64_t)nQ * split / A.splits), u1 = min(nU, 4 * (int)((int64_t)nQ * (split + 1) / A.splits));
   const int wk = A.wk, wt = A.wt, kw = wv % wk, tw = wv / wk;
@@ -545,152 +545,171 @@ __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Arg
 // more rows
 // ---------------------------------------------------------------------------
 
-constexpr int kTileThreads = 512;
-
-// 16 bytes a lane from its address straight into LDS at dst + 16 lane, counted
-// by no one but the waits written below (as dma16 in tq_mm.h).
-__device__ __forceinline__ void dma16_from(const void *p, lds_bytes *dst) {
+// The lane, from no register that a loop before had to keep.
+__device__ __forceinline__ int lane_here() {
 #if defined(__HIP_DEVICE_COMPILE__)
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"((uint32_t)dst), "v"(p));
+  int lane = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  asm volatile("" : "+v"(lane));
+  return lane;
+#else
+  return 0;
 #endif
+}
+
+// 16 bytes a lane from base + off (uniform, and a lane's) straight into LDS at
+// dst + 16 lane, counted by no one but the waits written below (as dma16 in
+// tq_mm.h, with 32 bits of offset).
+__device__ __forceinline__ void dma16_from(const void *base, uint32_t off, lds_bytes *dst) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"((uint32_t)dst), "v"(off), "s"(base));
+#endif
+}
+
+// The same value, known only here: what follows from it is computed here, not
+// ahead of a loop around, where it would hold registers.
+__device__ __forceinline__ uint32_t known_here(uint32_t v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  asm volatile("" : "+v"(v));
+#endif
+  return v;
 }
 
 // Slot rows are 128 bytes of k; chunk c of row r sits at c ^ this, so that the
 // 16 rows and four chunks of an operand read fall into different banks.
 __device__ __forceinline__ uint32_t swap_of(uint32_t r) { return (r >> 1) & 7u; }
 
-// P weight rows by Q rows of q, stages of 128 k; eight waves, WP by WQ, the
-// tile kept with weight rows along a lane's four results.  While stage s is
-// multiplied, q of s + 1 is on its way into LDS, the bytes of s + 2 into
-// registers, and the codes of s + 1 are decoded: two threads a weight row (P =
-// 128: four), 64 codes (32) each.
+// P weight rows by Q rows of q, stages of 128 k; 2 P threads, their waves WP by
+// WQ, the tile kept with weight rows along a lane's four results.  Two LDS slots
+// of q and two of codes.  While stage s is multiplied, a row of TQ matrix tiles
+// after another, a wave
+//   - reads the next row's weights, and behind the last row the q of stage
+//     s + 1, which landed before this stage began;
+//   - scales and adds the row before;
+//   - decodes its codes of s + 1, two threads a weight row, 64 codes each;
+//   - requests q of s + 2, whose slot this stage's q has left, and bytes of s + 2.
 template <int G, int P, int Q, int WP>
-__global__ __launch_bounds__(kTileThreads) __attribute__((amdgpu_waves_per_eu(P == 256 && Q == 256 ? 2 : 4)))
+__global__ __launch_bounds__(2 * P) __attribute__((amdgpu_waves_per_eu(2, P == 256 ? 2 : 4)))
 void tile_kernel(const I8Args A) {
   typedef Codes<8> L;
-  constexpr int WQ = 8 / WP, TP = P / WP / 16, TQ = Q / WQ / 16, B = bytes_per_group(G), GS = 128 / G;
+  constexpr int NT = 2 * P, WQ = NT / 64 / WP, TP = P / WP / 16, TQ = Q / WQ / 16;
+  constexpr int B = bytes_per_group(G), GS = 128 / G;
   constexpr uint32_t kPSlot = P * 128, kQSlot = Q * 128, kSSlot = GS * P * 4;
   constexpr uint32_t kQOff = 2 * kPSlot, kSOff = kQOff + 2 * kQSlot, kLutOff = kSOff + 2 * kSSlot;
-  constexpr int kLoads = Q * 8 / kTileThreads;
+  constexpr int kLoads = Q * 8 / NT;
+  static_assert(P % 64 == 0 && TP >= 4, "");
   __shared__ __align__(16) unsigned char smem_raw[kLutOff + L::kBytes];
   lds_bytes *smem = (lds_bytes *)smem_raw;
   const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), wp = wv / WQ, wq = wv % WQ;
   const int nG = A.K / G, S = (A.K + 127) / 128;
-  L::build(smem + kLutOff, tid, kTileThreads);
+  L::build(smem + kLutOff, tid, NT);
   const L lut(kLutOff, lane);
-  const int64_t units = count_units(A, Q);
+  const int units = count_units(A, Q);
   if (A.offsets && blockIdx.x == 0 && A.status)
-    for (int e = tid; e < A.E; e += kTileThreads)
+    for (int e = tid; e < A.E; e += NT)
       if (A.offsets[e] < 0 || A.offsets[e + 1] < A.offsets[e] || A.offsets[e + 1] > A.T)
         atomicOr(A.status, kDevBadSegment);
   uint32_t flags = 0;
-  const int64_t tiles = units * A.tp, total = tiles * A.splits;
-  for (int64_t work = blockIdx.x; work < total; work += gridDim.x) {
-    const int split = (int)(work / tiles);
-    const int64_t t = work - split * tiles;
-    const int64_t unit = t / A.tp;
-    const int ip = (int)(t - unit * A.tp);
+  // (T N is at most 2^40 and E N 2^34: the tiles' number fits)
+  const int tiles = units * A.tp, total = tiles * A.splits;
+  for (int work = (int)blockIdx.x; work < total; work += (int)gridDim.x) {
+    // the same for the block: kept in scalar registers
+    auto scalar = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    const int split = scalar((int)((uint32_t)work / (uint32_t)tiles)), t = work - split * tiles;
+    const int unit = scalar((int)((uint32_t)t / (uint32_t)A.tp)), ip = t - unit * A.tp;
     const Segment seg = find_unit(A, Q, unit);
     if (seg.e < 0) break;
-    const int s0 = (int)((int64_t)S * split / A.splits), s1 = (int)((int64_t)S * (split + 1) / A.splits);
-    const int n0 = ip * P;
-    const int64_t m0 = seg.a + seg.unit * Q;
-    const int M = (int)min(seg.b - m0, (int64_t)Q);
+    // stages are counted from the split's first
+    const int s0 = scalar(S * split / A.splits), S1 = scalar(S * (split + 1) / A.splits) - s0;  // S is at most 2^14
+    const int n0 = ip * P, m0 = seg.a + seg.unit * Q, M = min(seg.b - m0, Q);
 
-    // q: this thread's chunks of a slot; rows past the last read it
-    const int8_t *from[kLoads];
+    // q: this thread's chunks of a slot, as bytes from the first of A.q (where
+    // rows are given: 32 bits reach all of them) or of this tile; rows past the
+    // last read it
+    uint32_t from[kLoads];
     uint32_t upper = 0;  // which of them are in the second half of a stage
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const uint32_t at = (uint32_t)(i * kTileThreads + tid), r = at >> 3, c = (at & 7u) ^ swap_of(r);
-      const int64_t src = source_of(A, m0 + min((int)r, M - 1));
-      from[i] = A.q + max(src, (int64_t)0) * A.K + 16 * c;
+      const uint32_t at = (uint32_t)(i * NT + tid), r = at >> 3, c = (at & 7u) ^ swap_of(r);
+      const int row = min((int)r, M - 1);
+      from[i] = known_here((A.rows ? (uint32_t)max(source_of(A, m0 + row), (int64_t)0) : (uint32_t)row) * (uint32_t)A.K + 16u * c);
       upper |= (c >> 2) << i;
     }
-    auto request = [&](int s) {
-      const bool half = 128 * s + 128 > A.K;  // the second half is past the row: the first again, its codes are 0
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        dma16_from(from[i] + 128 * (int64_t)s - (half && (upper >> i & 1) ? 64 : 0),
-                   smem + kQOff + (uint32_t)(s & 1) * kQSlot + 16u * (uint32_t)(i * kTileThreads + 64 * wv));
+    const int8_t *qbase = A.q + (A.rows ? (int64_t)0 : (int64_t)m0 * A.K) + 128 * (int64_t)s0;
+    auto request = [&](int s, uint32_t slot, int i) __attribute__((always_inline)) {
+      s = min(s, S1 - 1);  // past the end the last one again, unused
+      // where the second half is past the row, the first again: its codes are 0
+      const uint32_t back = G == 64 && 128 * (s0 + s) + 128 > A.K && (upper >> i & 1) ? 64u : 0u;
+      dma16_from(qbase + 128 * s, from[i] - back,
+                 smem + kQOff + slot + 16u * (uint32_t)(i * NT + 64 * wv));
     };
 
-    // codes: waves 0 .. 3 the first 64 of a stage's 128, waves 4 .. 7 the rest,
-    // so that the place of a byte's codes is the same for a wave
-    static_assert(P == 256 || P == 128, "");
-    constexpr int kTurns = 256 / P;  // P = 128: half of the waves of each kind at a time
-    const int hf = wv >> 2, dr = (tid & 255) % P;
-    const bool decodes = (tid & 255) < P;
-    const int64_t wrow = ((int64_t)seg.e * A.N + min(n0 + dr, A.N - 1)) * nG;
-    const uint8_t *bytes = A.packed + wrow * B;
-    const uint16_t *values = A.scales + wrow;
-    (void)kTurns;
-    struct Raw {
-      u32x4 w;
-      uint32_t scale;
+    // codes: this thread's are 64 hf .. 64 hf + 63 of row dr; hf is a wave's.
+    // Their bytes as two loads bring them: 0 .. 7, and the last eight of 14 (of
+    // a 128-group: bytes 0 .. 13 or 12 .. 25, whose dwords of codes are those of
+    // 0 .. 16 but the last, or but the first) or of 13.
+    const int hf = wv / (NT / 128), dr = tid % P;
+    const int64_t first = ((int64_t)seg.e * A.N + n0) * nG;
+    const uint32_t row = (uint32_t)min(dr, A.N - 1 - n0) * (uint32_t)nG;  // rows past N read row N - 1
+    const uint32_t boff = known_here(row * B + (G == 128 ? 12u * (uint32_t)hf : 0u)), voff = known_here(2u * row);
+    u32x2 lo, hi;
+    uint32_t scale;
+    constexpr int kBytes = G == 128 ? 14 : 13;
+    auto load_raw = [&](int s) __attribute__((always_inline)) {
+      s = s0 + min(s, S1 - 1);
+      const int g = G == 128 ? s : min(2 * s + hf, nG - 1);
+      const uint8_t *bytes = A.packed + (first + g) * B;
+      const uint32_t sc = *(const uint16_t *)((const uint8_t *)(A.scales + first + g) + voff);
+      // after the scale: whoever has waited for hi has all three
+      __builtin_memcpy(&lo, bytes + boff, 8);
+      __builtin_memcpy(&hi, bytes + boff + (kBytes - 8), 8);
+      scale = G == 128 || 2 * s + hf < nG ? sc : 0u;
     };
-    Raw raw;
-    auto load_raw = [&](int s) {
-      s = min(s, s1 - 1);
-      if constexpr (G == 128) {
-        __builtin_memcpy(&raw.w, bytes + s * B + 10 * hf, 16);  // bytes 0 .. 15, or 10 .. 25
-        raw.scale = values[s];
+    u32x2 e[4];  // entries of a piece
+    uint32_t d[17];
+    auto look = [&](auto pc) __attribute__((always_inline)) {
+      constexpr int I = 4 * decltype(pc)::value;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = I + k;
+        if (i < kBytes) e[k] = i < 8 ? lut.read(smem, lo[i >> 2], i & 3) : lut.read(smem, hi[(i - kBytes + 8) >> 2], (i - kBytes + 8) & 3);
+      }
+    };
+    auto join = [&](auto pc) __attribute__((always_inline)) {
+      constexpr int p = decltype(pc)::value;
+      if constexpr (p < 3) {
+        flags |= e[0].y | e[1].y | e[2].y | e[3].y;
+        d[5 * p] = e[0].x;
+        d[5 * p + 1] = join_ab(e[0], e[1]);
+        d[5 * p + 2] = join_bc(e[1], e[2]);
+        d[5 * p + 3] = join_cd(e[2], e[3]);
+        d[5 * p + 4] = join_d(e[3]);
       } else {
-        const int g = min(2 * s + hf, nG - 1);
-        u32x2 a, b;
-        __builtin_memcpy(&a, bytes + g * B, 8);
-        __builtin_memcpy(&b, bytes + g * B + 5, 8);
-        raw.w = u32x4{a.x, a.y, __builtin_amdgcn_alignbyte(b.y, b.x, 3), b.y >> 24};
-        const uint32_t sc = values[g];
-        raw.scale = 2 * s + hf < nG ? sc : 0u;
+        flags |= e[0].y;
+        d[15] = e[0].x;
+        if constexpr (G == 128) {
+          flags |= e[1].y;
+          d[16] = join_ab(e[0], e[1]);
+        }
       }
+      settle(flags);
     };
-    auto decode = [&](int s) {
-      if (!decodes) return;
-      uint32_t d[16];
-      auto entry = [&](int i) { return lut.read(smem, raw.w[i >> 2], i & 3); };
-      if (G == 64 || hf == 0) {
+    // 16 codes (chunk c of this thread's four), once piece c is joined
+    // where they go; slots are changed by their bit
+    uint32_t put = known_here(128u * (uint32_t)dr + 16u * ((4u * (uint32_t)hf) ^ swap_of((uint32_t)dr)));
+    uint32_t sput = known_here(kSOff + 4u * (uint32_t)((GS == 2 ? hf : 0) * P + dr));
+    auto piece = [&](auto pc) __attribute__((always_inline)) {
+      constexpr int D = 4 * decltype(pc)::value;
+      join(pc);
+      u32x4 v{d[D], d[D + 1], d[D + 2], d[D + 3]};
+      if constexpr (G == 128)
 #pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          const u32x2 a = entry(4 * p), b = entry(4 * p + 1), c = entry(4 * p + 2), e = entry(4 * p + 3);
-          flags |= a.y | b.y | c.y | e.y;
-          d[5 * p] = a.x;
-          d[5 * p + 1] = join_ab(a, b);
-          d[5 * p + 2] = join_bc(b, c);
-          d[5 * p + 3] = join_cd(c, e);
-          d[5 * p + 4] = join_d(e);
-        }
-        const u32x2 a = entry(12);
-        flags |= a.y;
-        d[15] = a.x;
-      } else {  // bytes 12 .. 25 are 2 .. 15 here; codes 64 on, the fifth of byte 12 first
-        u32x2 a = entry(2);
-        flags |= a.y;
-#pragma unroll
-        for (int p = 0; p < 3; ++p) {
-          const u32x2 b = entry(4 * p + 3), c = entry(4 * p + 4), e = entry(4 * p + 5);
-          flags |= b.y | c.y | e.y;
-          d[5 * p] = join_ab(a, b);
-          d[5 * p + 1] = join_bc(b, c);
-          d[5 * p + 2] = join_cd(c, e);
-          d[5 * p + 3] = join_d(e);
-          a = entry(4 * p + 6);
-          flags |= a.y;
-          d[5 * p + 4] = a.x;
-        }
-        const u32x2 b = entry(15);
-        flags |= b.y;
-        d[15] = join_ab(a, b);
-      }
-      lds_bytes *slot = smem + (uint32_t)(s & 1) * kPSlot + 128u * (uint32_t)dr;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *(lds_u32x4 *)(slot + 16u * ((uint32_t)(4 * hf + i) ^ swap_of((uint32_t)dr))) =
-            u32x4{d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]};
-      if (GS == 2 || hf == 0)
-        *(lds_float *)(smem + kSOff + (uint32_t)(s & 1) * kSSlot + 4u * (uint32_t)((GS == 2 ? hf : 0) * P + dr)) =
-            f16_value(raw.scale);
+        for (int i = 0; i < 4; ++i) v[i] = hf ? d[D + i + 1] : v[i];
+      *(lds_u32x4 *)(smem + (put ^ 16u * decltype(pc)::value)) = v;
+    };
+    auto store_scale = [&]() __attribute__((always_inline)) {
+      // G = 128: the two threads of a row write the same
+      *(lds_float *)(smem + sput) = f16_value(scale);
     };
 
     f32x4 acc[TP][TQ];
@@ -699,81 +718,137 @@ void tile_kernel(const I8Args A) {
 #pragma unroll
       for (int b = 0; b < TQ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
     __syncthreads();  // the table is there, and the tile before is done with LDS
-    load_raw(s0);
-    request(s0);
-    decode(s0);
-    load_raw(s0 + 1);
+    load_raw(0);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) request(0, 0, i);
+    look(Int<0>{}), piece(Int<0>{}), look(Int<1>{}), piece(Int<1>{});
+    look(Int<2>{}), piece(Int<2>{}), look(Int<3>{}), piece(Int<3>{});
+    store_scale();
+    put ^= kPSlot;
+    sput ^= kSSlot;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) request(1, kQSlot, i);
+    load_raw(1);
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
     const uint32_t pr = (uint32_t)(wp * (P / WP) + l), qr = (uint32_t)(wq * (Q / WQ) + l);
-    // rows 16 apart have the same exchange
-    const uint32_t pat[2] = {128u * pr + 16u * ((uint32_t)q ^ swap_of(pr)), 128u * pr + 16u * ((uint32_t)(4 + q) ^ swap_of(pr))};
-    const uint32_t qat[2] = {128u * qr + 16u * ((uint32_t)q ^ swap_of(qr)), 128u * qr + 16u * ((uint32_t)(4 + q) ^ swap_of(qr))};
-    for (int s = s0; s < s1; ++s) {
-      if (s + 1 < s1) {
-        decode(s + 1);
-        request(s + 1);
-        load_raw(s + 2);
-      }
-      lds_bytes *ps = smem + (uint32_t)(s & 1) * kPSlot, *qs = smem + kQOff + (uint32_t)(s & 1) * kQSlot;
-      lds_bytes *ss = smem + kSOff + (uint32_t)(s & 1) * kSSlot + 4u * (uint32_t)(wp * (P / WP) + 4 * q);
-      u32x4 qf[TQ][2];
+    // rows 16 apart have the same exchange; the second half of a stage is 64 bytes
+    // on, exchanged or not
+    uint32_t pat = 128u * pr + 16u * ((uint32_t)q ^ swap_of(pr));
+    uint32_t qat = kQOff + 128u * qr + 16u * ((uint32_t)q ^ swap_of(qr));
+    uint32_t sat = kSOff + 4u * (uint32_t)(wp * (P / WP) + 4 * q);
+    static_assert(kQOff % (2 * kQSlot) == 0 && kSOff % (2 * kSSlot) == 0, "a slot's bit");
+    u32x4 qf[2][TQ], pf[2];
+    f32x4 sc[GS];
+    i32x4 sum[TQ];  // of a group: of both halves of a stage, or (G = 64) of one
+    auto read_q = [&](int h) __attribute__((always_inline)) {
+#pragma unroll
+      for (int b = 0; b < TQ; ++b) qf[h][b] = *(lds_u32x4_c *)(smem + (qat ^ 64u * h) + 2048u * (uint32_t)b);
+    };
+    auto read_p = [&](int a) __attribute__((always_inline)) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) pf[h] = *(lds_u32x4_c *)(smem + (pat ^ 64u * h) + 2048u * (uint32_t)a);
+    };
+    auto read_s = [&](int a) __attribute__((always_inline)) {
+#pragma unroll
+      for (int h = 0; h < GS; ++h) sc[h] = *(lds_f32x4_c *)(smem + sat + 4u * (uint32_t)(h * P + 16 * a));
+    };
+    auto multiply = [&](int h) __attribute__((always_inline)) {
+#pragma unroll
+      for (int b = 0; b < TQ; ++b) sum[b] = mfma_i8(pf[h], qf[h][b], h < GS ? i32x4{0, 0, 0, 0} : sum[b]);
+    };
+    auto add = [&](int a, int h) __attribute__((always_inline)) {
 #pragma unroll
       for (int b = 0; b < TQ; ++b)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) qf[b][h] = *(lds_u32x4_c *)(qs + qat[h] + 2048u * (uint32_t)b);
+        for (int r = 0; r < 4; ++r) acc[a][b][r] = fmaf(sc[h][r], (float)sum[b][r], acc[a][b][r]);
+    };
+    read_q(0);
+    read_q(1);
+    qat ^= kQSlot;
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // q of stage 0 has left its slot
+    read_p(0);
+    read_s(0);
+    uint32_t here = 0;  // the slot of this stage's q
+    for (int s = 0; s < S1; ++s) {
 #pragma unroll
       for (int a = 0; a < TP; ++a) {
-        const u32x4 pf[2] = {*(lds_u32x4_c *)(ps + pat[0] + 2048u * (uint32_t)a),
-                             *(lds_u32x4_c *)(ps + pat[1] + 2048u * (uint32_t)a)};
-        f32x4 sc[GS];
+        __builtin_amdgcn_sched_barrier(0);
+        if (a == 0) look(Int<0>{});  // waits for the bytes requested a stage ago, so before other requests
+        multiply(0);
+        if (a == TP - 1) read_q(0);  // of the next stage (past the end: what the slot happens to hold)
+        if constexpr (GS == 2) add(a, 0);
+        multiply(1);
+        if (a == TP - 1) read_q(1);
+        __builtin_amdgcn_sched_barrier(0);
+        if (a + 1 < TP) read_p(a + 1);
+        if (a == 0) {
+          piece(Int<0>{});
+          look(Int<1>{});
 #pragma unroll
-        for (int h = 0; h < GS; ++h) sc[h] = *(lds_f32x4_c *)(ss + 4u * (uint32_t)(h * P + 16 * a));
-        i32x4 sum[GS][TQ];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int b = 0; b < TQ; ++b)
-            sum[h % GS][b] = mfma_i8(pf[h], qf[b][h], h < GS ? i32x4{0, 0, 0, 0} : sum[0][b]);
-#pragma unroll
-        for (int h = 0; h < GS; ++h)
-#pragma unroll
-          for (int b = 0; b < TQ; ++b)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[a][b][r] = fmaf(sc[h][r], (float)sum[h][b][r], acc[a][b][r]);
+          for (int i = 0; i < kLoads; ++i) request(s + 2, here, i);
+        }
+        if (a == 1) piece(Int<1>{}), look(Int<2>{});
+        if (a == 2) piece(Int<2>{}), look(Int<3>{});
+        if (a == 3) {
+          piece(Int<3>{});
+          store_scale();
+          load_raw(s + 2);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (a + 1 < TP) add(a, GS - 1), read_s(a + 1);
       }
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      here ^= kQSlot;
+      qat ^= kQSlot;
+      pat ^= kPSlot;
+      put ^= kPSlot;
+      sat ^= kSSlot;
+      sput ^= kSSlot;
+      __builtin_amdgcn_sched_barrier(0);
+      // q of s + 2 has landed: only the bytes of s + 2 may still be on their way
+      asm volatile("s_waitcnt vmcnt(3) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      read_p(0);
+      add(TP - 1, GS - 1);
+      read_s(0);
     }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // nothing is on its way into LDS
 
+    // 16 rows of q at a time through this wave's part of LDS, [row][weight row]:
+    // results leave in runs of a wave's weight rows
+    constexpr int W = P / WP, kLd = W + 4, kLanes = W / 4, kEach = 64 / kLanes;  // lanes of a row, rows at once
+    static_assert(NT / 64 * 16 * kLd * 4 <= kSOff, "");
+    const int lane = lane_here(), l = lane & 15, q = lane >> 4;
+    lds_bytes *room = smem + (uint32_t)(wv * (16 * kLd * 4));
+    const int nw = n0 + wp * W + 4 * (lane % kLanes);
 #pragma unroll
     for (int b = 0; b < TQ; ++b) {
-      const int r = wq * (Q / WQ) + 16 * b + l;
-      if (r >= M) continue;
-      const int64_t m = m0 + r, src = source_of(A, m);
-      if (src < 0 && ip == 0 && split == 0 && A.status) atomicOr(A.status, kDevBadRow);
-      const float scale = src < 0 ? 0.f : A.qs[src];
 #pragma unroll
-      for (int a = 0; a < TP; ++a) {
-        const int n = n0 + wp * (P / WP) + 16 * a + 4 * q;
-        if (n >= A.N) continue;
-        float v[4] = {acc[a][b][0], acc[a][b][1], acc[a][b][2], acc[a][b][3]};
+      for (int a = 0; a < TP; ++a) *(lds_f32x4 *)(room + 4u * (uint32_t)(l * kLd + 16 * a + 4 * q)) = acc[a][b];
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      const int r0 = wq * (Q / WQ) + 16 * b + lane / kLanes;
+#pragma unroll 1
+      for (int i = 0; i < 16; i += kEach) {
+        if (r0 + i >= M || nw >= A.N) continue;
+        const f32x4 sums = *(lds_f32x4_c *)(room + 4u * (uint32_t)((i + lane / kLanes) * kLd + 4 * (lane % kLanes)));
+        const float v[4] = {sums[0], sums[1], sums[2], sums[3]};
+        const int64_t m = m0 + r0 + i;
         if (A.splits > 1) {
-          float *p = A.partial + ((int64_t)split * A.T + m) * A.N + n;
-          if (A.N % 4 == 0) {
-            *(f32x4 *)p = acc[a][b];
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (n + i < A.N) p[i] = v[i];
-          }
-        } else if (A.vec) {
-          finish<4>(A, seg.e, m, n, scale, v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (n + i < A.N) finish<1>(A, seg.e, m, n + i, scale, v + i);
+          float *p = A.partial + ((int64_t)split * A.T + m) * A.N + nw;
+          if (A.N % 4 == 0)
+            *(f32x4 *)p = sums;
+          else
+            for (int c = 0; c < 4 && nw + c < A.N; ++c) p[c] = v[c];
+          continue;
         }
+        const int64_t src = source_of(A, m);
+        if (src < 0 && ip == 0 && A.status) atomicOr(A.status, kDevBadRow);
+        const float scale = src < 0 ? 0.f : A.qs[src];
+        if (A.vec)
+          finish<4>(A, seg.e, m, nw, scale, v);
+        else
+          for (int c = 0; c < 4 && nw + c < A.N; ++c) finish<1>(A, seg.e, m, nw + c, scale, v + c);
       }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
   }
   if ((flags & kBad) && A.status) atomicOr(A.status, kDevInvalidByte);
@@ -848,9 +923,9 @@ void launch(const Plan &p, const I8Args &a, hipStream_t stream) {
       default: go(few_kernel<G, 8, 8>, few_kernel<G, 8, 32>); break;
     }
   } else if (p.q == 256) {
-    hipLaunchKernelGGL((tile_kernel<G, 256, 256, 2>), grid, dim3(kTileThreads), 0, stream, a);
+    hipLaunchKernelGGL((tile_kernel<G, 256, 256, 2>), grid, dim3(512), 0, stream, a);
   } else {
-    hipLaunchKernelGGL((tile_kernel<G, 128, 64, 4>), grid, dim3(kTileThreads), 0, stream, a);
+    hipLaunchKernelGGL((tile_kernel<G, 128, 64, 2>), grid, dim3(256), 0, stream, a);
   }
   if (a.splits > 1)
     hipLaunchKernelGGL(join_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(a.N, 256), 64), (unsigned)std::min<int64_t>(a.T, 65535)),
