@@ -56,7 +56,7 @@ struct I8Args {
   const int32_t *rows;      // [T] or null
   int64_t T, sources;
   int N, K, E;
-  bool bias32, out32, vec;  // vec: four columns at a time are aligned
+  bool bias32, out32, vec;  // vec: eight columns at a time are aligned
   int act;
   float *partial;           // [splits][T][N] where splits > 1
   int splits;
@@ -254,55 +254,104 @@ __device__ __forceinline__ float activate(float v, int act) {
   return v;
 }
 
-// Columns n .. n + C - 1 of row m (all of them below N) of expert e: v is the
-// sum over groups.
+__device__ __forceinline__ float bias_of(const I8Args &A, int e, int n) {
+  const int64_t at = (int64_t)e * A.N + n;
+  return A.bias32 ? ((const float *)A.bias)[at] : bf16_to_f32(((const uint16_t *)A.bias)[at]);
+}
+
 template <int C>
-__device__ __forceinline__ void finish(const I8Args &A, int e, int64_t m, int n, float scale, const float *v) {
-  float o[C];
+__device__ __forceinline__ void activate_all(float (&v)[C], int act) {
+  if (act == kActNone) return;
+  if (act == kActRelu2) {
 #pragma unroll
-  for (int i = 0; i < C; ++i) o[i] = v[i] * scale;
-  if (A.bias) {
-    const int64_t at = (int64_t)e * A.N + n;
-    if (A.bias32) {
-      float b[C];
-      __builtin_memcpy(b, (const float *)A.bias + at, sizeof(b));
+    for (int c = 0; c < C; ++c) v[c] = activate(v[c], kActRelu2);
+  } else if (act == kActSilu) {
 #pragma unroll
-      for (int i = 0; i < C; ++i) o[i] += b[i];
+    for (int c = 0; c < C; ++c) v[c] = activate(v[c], kActSilu);
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c) v[c] = activate(v[c], kActGelu);
+  }
+}
+
+// What results need, in scalar registers: left to itself the compiler loads the
+// kernel's arguments again for every row, one after another.
+struct Result {
+  typedef __attribute__((address_space(1))) char byte;
+  uint64_t residual, out;
+  int N, act, out32, vec;
+
+  __device__ __forceinline__ explicit Result(const I8Args &A)
+      : residual((uint64_t)A.residual), out((uint64_t)A.out), N(A.N), act(A.act), out32(A.out32), vec(A.vec) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    asm volatile("" : "+s"(residual), "+s"(out), "+s"(N), "+s"(act), "+s"(out32), "+s"(vec));
+#endif
+  }
+
+  template <class T>
+  __device__ __forceinline__ __attribute__((address_space(1))) T *at(uint64_t base, int64_t i) const {
+    return (__attribute__((address_space(1))) T *)(byte *)base + i;
+  }
+
+  // Column n of row m, scaled and with its bias.
+  __device__ __forceinline__ void put(int64_t m, int n, float v) const {
+    const int64_t i = m * N + n;
+    float w[1] = {v};
+    activate_all(w, act);
+    if (residual) w[0] += out32 ? *at<const float>(residual, i) : bf16_to_f32(*at<const uint16_t>(residual, i));
+    if (out32)
+      *at<float>(out, i) = w[0];
+    else
+      *at<uint16_t>(out, i) = f32_to_bf16(w[0]);
+  }
+
+  // Eight columns, all there and aligned to 16 bytes (vec), and their residual's
+  // eight.
+  struct Eight {
+    u32x4 a, b;
+  };
+  __device__ __forceinline__ Eight residual8(int64_t m, int n) const {
+    const int64_t i = m * N + n;
+    Eight r{};
+    if (out32) {
+      r.a = *at<const u32x4>(residual, i / 4);
+      r.b = *at<const u32x4>(residual, i / 4 + 1);
     } else {
-      uint16_t b[C];
-      __builtin_memcpy(b, (const uint16_t *)A.bias + at, sizeof(b));
+      r.a = *at<const u32x4>(residual, i / 8);
+    }
+    return r;
+  }
+  template <bool RES>
+  __device__ __forceinline__ void put8(int64_t m, int n, float scale, const float (&bias)[8], f32x4 lo, f32x4 hi,
+                                       const Eight &r) const {
+    float v[8];
 #pragma unroll
-      for (int i = 0; i < C; ++i) o[i] += bf16_to_f32(b[i]);
+    for (int c = 0; c < 8; ++c) v[c] = fmaf(c < 4 ? lo[c] : hi[c - 4], scale, bias[c]);
+    activate_all(v, act);
+    if constexpr (RES)
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        v[c] += __uint_as_float(out32 ? (c < 4 ? r.a[c & 3] : r.b[c & 3])
+                                      : c & 1 ? r.a[c >> 1] & 0xFFFF0000u : r.a[c >> 1] << 16);
+    const int64_t i = m * N + n;
+    if (out32) {
+      *at<f32x4>(out, i / 4) = f32x4{v[0], v[1], v[2], v[3]};
+      *at<f32x4>(out, i / 4 + 1) = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+      *at<u32x4>(out, i / 8) = u32x4{pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
     }
   }
-  if (A.act != kActNone)
-#pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = activate(o[i], A.act);
-  const int64_t at = m * A.N + n;
-  if (A.out32) {
-    float *p = (float *)A.out + at;
-    if (A.residual) {
-      float r[C];
-      __builtin_memcpy(r, (const float *)A.residual + at, sizeof(r));
-#pragma unroll
-      for (int i = 0; i < C; ++i) o[i] += r[i];
-    }
-    if constexpr (C == 4)
-      *(f32x4 *)p = f32x4{o[0], o[1], o[2], o[3]};
-    else
-      for (int i = 0; i < C; ++i) p[i] = o[i];
+};
+
+// A split's sums of columns n .. n + 7 of a row, those below N.
+__device__ __forceinline__ void store_sums(float *p, int n, int N, f32x4 lo, f32x4 hi) {
+  if (N % 8 == 0) {
+    *(f32x4 *)p = lo;
+    *(f32x4 *)(p + 4) = hi;
   } else {
-    uint16_t *p = (uint16_t *)A.out + at;
-    if (A.residual) {
-      uint16_t r[C];
-      __builtin_memcpy(r, (const uint16_t *)A.residual + at, sizeof(r));
 #pragma unroll
-      for (int i = 0; i < C; ++i) o[i] += bf16_to_f32(r[i]);
-    }
-    if constexpr (C == 4)
-      *(u32x2 *)p = u32x2{pack2(o[0], o[1]), pack2(o[2], o[3])};
-    else
-      for (int i = 0; i < C; ++i) p[i] = f32_to_bf16(o[i]);
+    for (int c = 0; c < 8; ++c)
+      if (n + c < N) p[c] = c < 4 ? lo[c] : hi[c - 4];
   }
 }
 
@@ -310,6 +359,7 @@ __device__ __forceinline__ void finish(const I8Args &A, int e, int64_t m, int n,
 // threads over the columns.
 __global__ __launch_bounds__(256) void join_kernel(const I8Args A) {
   const int64_t tn = A.T * A.N;
+  const Result result(A);
   for (int64_t m = blockIdx.y; m < A.T; m += gridDim.y) {
     int e = 0;
     if (A.offsets) {  // the expert whose segment has m: the last one that starts at or before it
@@ -331,7 +381,7 @@ __global__ __launch_bounds__(256) void join_kernel(const I8Args A) {
       const float *p = A.partial + m * A.N + n;
 #pragma unroll 4
       for (int s = 0; s < A.splits; ++s) v += p[s * tn];
-      finish<1>(A, e, m, n, scale, &v);
+      result.put(m, n, fmaf(v, scale, A.bias ? bias_of(A, e, n) : 0.f));
     }
   }
 }
@@ -524,6 +574,7 @@ __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Arg
       *(lds_float *)(smem + kSumOff + 4u * (uint32_t)((b * waves + wv) * 64 + lane)) = mine;
     }
     __syncthreads();
+    const Result result(A);
     for (int o = tid; o < wt * MB * 64; o += threads) {  // [tile][row of q][column]
       const int ts = o / (MB * 64), m = o / 16 % (4 * MB), c = o & 15;
       const int n = ((b0 + j * A.bpu) * wt + ts) * 16 + c;
@@ -534,7 +585,7 @@ __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Arg
       if (A.splits > 1)
         A.partial[((int64_t)split * A.T + m0 + m) * A.N + n] = v;
       else
-        finish<1>(A, seg.e, m0 + m, n, row_scale[m], &v);
+        result.put(m0 + m, n, fmaf(v, row_scale[m], A.bias ? bias_of(A, seg.e, n) : 0.f));
     }
     ++j;
   }
@@ -593,7 +644,7 @@ void tile_kernel(const I8Args A) {
   typedef Codes<8> L;
   constexpr int NT = 2 * P, WQ = NT / 64 / WP, TP = P / WP / 16, TQ = Q / WQ / 16;
   constexpr int B = bytes_per_group(G), GS = 128 / G;
-  constexpr uint32_t kPSlot = P * 128, kQSlot = Q * 128, kSSlot = GS * P * 4;
+  constexpr uint32_t kPSlot = P * 128, kQSlot = Q * 128, kSSlot = 2 * P * 4;
   constexpr uint32_t kQOff = 2 * kPSlot, kSOff = kQOff + 2 * kQSlot, kLutOff = kSOff + 2 * kSSlot;
   constexpr int kLoads = Q * 8 / NT;
   static_assert(P % 64 == 0 && TP >= 4, "");
@@ -645,35 +696,57 @@ void tile_kernel(const I8Args A) {
     };
 
     // codes: this thread's are 64 hf .. 64 hf + 63 of row dr; hf is a wave's.
-    // Their bytes as two loads bring them: 0 .. 7, and the last eight of 14 (of
-    // a 128-group: bytes 0 .. 13 or 12 .. 25, whose dwords of codes are those of
-    // 0 .. 16 but the last, or but the first) or of 13.
+    // Of a 128-group they are in bytes 0 .. 13 or 12 .. 25, whose 17 dwords of
+    // codes are this thread's but the last, or but the first.
     const int hf = wv / (NT / 128), dr = tid % P;
     const int64_t first = ((int64_t)seg.e * A.N + n0) * nG;
     const uint32_t row = (uint32_t)min(dr, A.N - 1 - n0) * (uint32_t)nG;  // rows past N read row N - 1
-    const uint32_t boff = known_here(row * B + (G == 128 ? 12u * (uint32_t)hf : 0u)), voff = known_here(2u * row);
-    u32x2 lo, hi;
+    const uint32_t boff = known_here(row * B + (G == 128 && hf ? 10u : 0u));
+    // G = 128: the second thread of a row has no use for the scale; its wave's
+    // lanes read one and put it where no one looks (a branch in the loop costs more)
+    const uint32_t voff = known_here(GS == 2 || hf == 0 ? 2u * row : 0u);
+    u32x4 raw;  // bytes as `byte_at` finds them
     uint32_t scale;
     constexpr int kBytes = G == 128 ? 14 : 13;
     auto load_raw = [&](int s) __attribute__((always_inline)) {
       s = s0 + min(s, S1 - 1);
       const int g = G == 128 ? s : min(2 * s + hf, nG - 1);
       const uint8_t *bytes = A.packed + (first + g) * B;
+      // the scale first: whoever has waited for the bytes has all
       const uint32_t sc = *(const uint16_t *)((const uint8_t *)(A.scales + first + g) + voff);
-      // after the scale: whoever has waited for hi has all three
-      __builtin_memcpy(&lo, bytes + boff, 8);
-      __builtin_memcpy(&hi, bytes + boff + (kBytes - 8), 8);
+      if constexpr (G == 128) {
+        __builtin_memcpy(&raw, bytes + boff, 16);
+      } else {
+        u32x2 lo, hi;
+        __builtin_memcpy(&lo, bytes + boff, 8);
+        __builtin_memcpy(&hi, bytes + boff + 5, 8);
+        raw = u32x4{lo.x, lo.y, hi.x, hi.y};
+      }
       scale = G == 128 || 2 * s + hf < nG ? sc : 0u;
+    };
+    // byte i of this thread's, as (dword, byte of it)
+    auto entry = [&](int i) __attribute__((always_inline)) {
+      if (G == 128) return lut.read(smem, raw[i >> 2], i & 3);
+      return i < 8 ? lut.read(smem, raw[i >> 2], i & 3) : lut.read(smem, raw[2 + ((i - 5) >> 2)], (i - 5) & 3);
+    };
+    // bytes 12 .. 25 of a group, to where 0 .. 13 are
+    auto align_raw = [&]() __attribute__((always_inline)) {
+      if constexpr (G == 128) {
+        const uint32_t by = hf ? 2u : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw[i] = known_here(raw[i]);  // not waited for earlier
+#pragma unroll
+        for (int i = 0; i < 3; ++i) raw[i] = __builtin_amdgcn_alignbyte(raw[i + 1], raw[i], by);
+        raw[3] = __builtin_amdgcn_alignbyte(0u, raw[3], by);
+      }
     };
     u32x2 e[4];  // entries of a piece
     uint32_t d[17];
     auto look = [&](auto pc) __attribute__((always_inline)) {
       constexpr int I = 4 * decltype(pc)::value;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int i = I + k;
-        if (i < kBytes) e[k] = i < 8 ? lut.read(smem, lo[i >> 2], i & 3) : lut.read(smem, hi[(i - kBytes + 8) >> 2], (i - kBytes + 8) & 3);
-      }
+      for (int k = 0; k < 4; ++k)
+        if (I + k < kBytes) e[k] = entry(I + k);
     };
     auto join = [&](auto pc) __attribute__((always_inline)) {
       constexpr int p = decltype(pc)::value;
@@ -697,7 +770,7 @@ void tile_kernel(const I8Args A) {
     // 16 codes (chunk c of this thread's four), once piece c is joined
     // where they go; slots are changed by their bit
     uint32_t put = known_here(128u * (uint32_t)dr + 16u * ((4u * (uint32_t)hf) ^ swap_of((uint32_t)dr)));
-    uint32_t sput = known_here(kSOff + 4u * (uint32_t)((GS == 2 ? hf : 0) * P + dr));
+    uint32_t sput = known_here(kSOff + 4u * (uint32_t)(hf * P + dr));
     auto piece = [&](auto pc) __attribute__((always_inline)) {
       constexpr int D = 4 * decltype(pc)::value;
       join(pc);
@@ -708,7 +781,6 @@ void tile_kernel(const I8Args A) {
       *(lds_u32x4 *)(smem + (put ^ 16u * decltype(pc)::value)) = v;
     };
     auto store_scale = [&]() __attribute__((always_inline)) {
-      // G = 128: the two threads of a row write the same
       *(lds_float *)(smem + sput) = f16_value(scale);
     };
 
@@ -721,6 +793,7 @@ void tile_kernel(const I8Args A) {
     load_raw(0);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) request(0, 0, i);
+    align_raw();
     look(Int<0>{}), piece(Int<0>{}), look(Int<1>{}), piece(Int<1>{});
     look(Int<2>{}), piece(Int<2>{}), look(Int<3>{}), piece(Int<3>{});
     store_scale();
@@ -745,9 +818,8 @@ void tile_kernel(const I8Args A) {
 #pragma unroll
       for (int b = 0; b < TQ; ++b) qf[h][b] = *(lds_u32x4_c *)(smem + (qat ^ 64u * h) + 2048u * (uint32_t)b);
     };
-    auto read_p = [&](int a) __attribute__((always_inline)) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) pf[h] = *(lds_u32x4_c *)(smem + (pat ^ 64u * h) + 2048u * (uint32_t)a);
+    auto read_p = [&](int a, int h) __attribute__((always_inline)) {
+      pf[h] = *(lds_u32x4_c *)(smem + (pat ^ 64u * h) + 2048u * (uint32_t)a);
     };
     auto read_s = [&](int a) __attribute__((always_inline)) {
 #pragma unroll
@@ -767,34 +839,42 @@ void tile_kernel(const I8Args A) {
     read_q(1);
     qat ^= kQSlot;
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // q of stage 0 has left its slot
-    read_p(0);
+    read_p(0, 0);
+    read_p(0, 1);
     read_s(0);
-    uint32_t here = 0;  // the slot of this stage's q
+    // of the two waves of a SIMD one goes first, so that they take turns at the
+    // matrix cores and the other units
+    if (wv < NT / 128) __builtin_amdgcn_s_setprio(1);
+    constexpr int kLate = TP > 4 ? 1 : 0;  // rows between a stage's begin and the first codes
+    uint32_t here = 0;                     // the slot of this stage's q
     for (int s = 0; s < S1; ++s) {
 #pragma unroll
       for (int a = 0; a < TP; ++a) {
         __builtin_amdgcn_sched_barrier(0);
-        if (a == 0) look(Int<0>{});  // waits for the bytes requested a stage ago, so before other requests
+        // waits for the bytes requested a stage ago, so before other requests
+        if (kLate == 0 && a == 0) align_raw(), look(Int<0>{});
+        // operands are read as soon as those that they replace have been used
         multiply(0);
+        if (a + 1 < TP) read_p(a + 1, 0);
         if (a == TP - 1) read_q(0);  // of the next stage (past the end: what the slot happens to hold)
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (GS == 2) add(a, 0);
         multiply(1);
+        if (a + 1 < TP) read_p(a + 1, 1);
         if (a == TP - 1) read_q(1);
         __builtin_amdgcn_sched_barrier(0);
-        if (a + 1 < TP) read_p(a + 1);
-        if (a == 0) {
-          piece(Int<0>{});
-          look(Int<1>{});
+        if (kLate == 1 && a == 0) align_raw(), look(Int<0>{});
+        if (a == kLate) piece(Int<0>{}), look(Int<1>{});
+        if (a == 0)
 #pragma unroll
           for (int i = 0; i < kLoads; ++i) request(s + 2, here, i);
-        }
-        if (a == 1) piece(Int<1>{}), look(Int<2>{});
-        if (a == 2) piece(Int<2>{}), look(Int<3>{});
-        if (a == 3) {
-          piece(Int<3>{});
+        if (a == kLate + 1) piece(Int<1>{}), look(Int<2>{});
+        if (a == kLate + 2) {
+          piece(Int<2>{}), look(Int<3>{});
           store_scale();
           load_raw(s + 2);
         }
+        if (a == kLate + 3) piece(Int<3>{});
         __builtin_amdgcn_sched_barrier(0);
         if (a + 1 < TP) add(a, GS - 1), read_s(a + 1);
       }
@@ -805,48 +885,100 @@ void tile_kernel(const I8Args A) {
       sat ^= kSSlot;
       sput ^= kSSlot;
       __builtin_amdgcn_sched_barrier(0);
-      // q of s + 2 has landed: only the bytes of s + 2 may still be on their way
-      asm volatile("s_waitcnt vmcnt(3) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      read_p(0);
+      // q of s + 2 has landed: only the bytes and the scale of s + 2, requested
+      // behind it, may still be on their way
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(G == 128 ? 2 : 3) : "memory");
+      read_p(0, 0);
+      read_p(0, 1);
       add(TP - 1, GS - 1);
       read_s(0);
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // nothing is on its way into LDS
+    __builtin_amdgcn_s_setprio(0);
 
-    // 16 rows of q at a time through this wave's part of LDS, [row][weight row]:
-    // results leave in runs of a wave's weight rows
-    constexpr int W = P / WP, kLd = W + 4, kLanes = W / 4, kEach = 64 / kLanes;  // lanes of a row, rows at once
-    static_assert(NT / 64 * 16 * kLd * 4 <= kSOff, "");
+    // Results go through this wave's part of LDS, kOnce tiles of 16 rows of q at
+    // a time, [row][weight row], and leave in runs of a wave's weight rows; chunk
+    // c of a row sits at c ^ row % 16.  (Loops that stay loops: unrolled, the
+    // epilogue was most of the kernel's code and its fetching took 10 us.)
+    constexpr int W = P / WP, kOnce = TQ < 2 ? TQ : 2, kLanes = W / 8, kEach = 64 / kLanes;  // lanes of a row, rows at once
+    static_assert(NT / 64 * kOnce * 16 * W * 4 <= kSOff && TQ % kOnce == 0 && W % 64 == 0, "");
     const int lane = lane_here(), l = lane & 15, q = lane >> 4;
-    lds_bytes *room = smem + (uint32_t)(wv * (16 * kLd * 4));
-    const int nw = n0 + wp * W + 4 * (lane % kLanes);
+    lds_bytes *room = smem + (uint32_t)(wv * (kOnce * 16 * W * 4));
+    const int nw = n0 + wp * W + 8 * (lane % kLanes);
+    // a lane's row's scale (handed over below), and its columns' bias
+    static_assert(Q / WQ <= 64, "a row a lane");
+    float own = 0.f;
+    if (lane < Q / WQ && wq * (Q / WQ) + lane < M) {
+      const int64_t src = source_of(A, m0 + wq * (Q / WQ) + lane);
+      if (src >= 0)
+        own = A.qs[src];
+      else if (ip == 0 && split == 0 && A.status)
+        atomicOr(A.status, kDevBadRow);
+    }
+    float bias[8] = {};
+    if (A.bias)
 #pragma unroll
-    for (int b = 0; b < TQ; ++b) {
-#pragma unroll
-      for (int a = 0; a < TP; ++a) *(lds_f32x4 *)(room + 4u * (uint32_t)(l * kLd + 16 * a + 4 * q)) = acc[a][b];
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      const int r0 = wq * (Q / WQ) + 16 * b + lane / kLanes;
+      for (int c = 0; c < 8; ++c)
+        if (nw + c < A.N) bias[c] = bias_of(A, seg.e, nw + c);
+    const Result result(A);
+    const int64_t mw = m0 + wq * (Q / WQ);
+    float *sums = A.splits > 1 ? A.partial + ((int64_t)split * A.T + mw) * A.N + nw : nullptr;
 #pragma unroll 1
-      for (int i = 0; i < 16; i += kEach) {
-        if (r0 + i >= M || nw >= A.N) continue;
-        const f32x4 sums = *(lds_f32x4_c *)(room + 4u * (uint32_t)((i + lane / kLanes) * kLd + 4 * (lane % kLanes)));
-        const float v[4] = {sums[0], sums[1], sums[2], sums[3]};
-        const int64_t m = m0 + r0 + i;
-        if (A.splits > 1) {
-          float *p = A.partial + ((int64_t)split * A.T + m) * A.N + nw;
-          if (A.N % 4 == 0)
-            *(f32x4 *)p = sums;
-          else
-            for (int c = 0; c < 4 && nw + c < A.N; ++c) p[c] = v[c];
-          continue;
+    for (int part = 0; part < TQ / kOnce; ++part) {
+#pragma unroll
+      for (int b = 0; b < TQ; ++b)
+        if (b / kOnce == part)
+#pragma unroll
+          for (int a = 0; a < TP; ++a)
+            *(lds_f32x4 *)(room + 4u * (uint32_t)((b % kOnce * 16 + l) * W) + 16u * (uint32_t)((4 * a + q) ^ l)) = acc[a][b];
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      const uint32_t c = 2u * (uint32_t)(lane % kLanes);
+      // rows k on of this part, this lane's; `each` gets (row of the wave, its sums)
+      auto rows_of = [&](int k, auto each) __attribute__((always_inline)) {
+        const int i = k + lane / kLanes, r = 16 * kOnce * part + i;
+        lds_bytes *from = room + 4u * (uint32_t)(i * W);
+        const f32x4 lo = *(lds_f32x4_c *)(from + 16u * (c ^ (uint32_t)(i & 15)));
+        const f32x4 hi = *(lds_f32x4_c *)(from + 16u * ((c + 1u) ^ (uint32_t)(i & 15)));
+        const float scale = __shfl(own, r);
+        if (wq * (Q / WQ) + r < M && nw < result.N) each(r, scale, lo, hi);
+      };
+      // loops by themselves: a load in one would make every pass wait for the
+      // stores of the pass before
+      if (sums) {
+#pragma unroll 1
+        for (int k = 0; k < 16 * kOnce; k += kEach)
+          rows_of(k, [&](int r, float, f32x4 lo, f32x4 hi) { store_sums(sums + (int64_t)r * result.N, nw, result.N, lo, hi); });
+      } else if (!result.vec) {
+#pragma unroll 1
+        for (int k = 0; k < 16 * kOnce; k += kEach)
+          rows_of(k, [&](int r, float scale, f32x4 lo, f32x4 hi) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (nw + j < result.N) result.put(mw + r, nw + j, fmaf(j < 4 ? lo[j] : hi[j - 4], scale, bias[j]));
+          });
+      } else if (!result.residual) {
+#pragma unroll 2
+        for (int k = 0; k < 16 * kOnce; k += kEach)
+          rows_of(k, [&](int r, float scale, f32x4 lo, f32x4 hi) {
+            result.put8<false>(mw + r, nw, scale, bias, lo, hi, Result::Eight{});
+          });
+      } else {
+        constexpr int kAhead = 4;  // rows whose residuals are requested together
+        static_assert(16 * kOnce % (kAhead * kEach) == 0, "");
+#pragma unroll 1
+        for (int k = 0; k < 16 * kOnce; k += kAhead * kEach) {
+          Result::Eight res[kAhead];
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) {
+            const int r = 16 * kOnce * part + k + j * kEach + lane / kLanes;
+            res[j] = wq * (Q / WQ) + r < M && nw < result.N ? result.residual8(mw + r, nw) : Result::Eight{};
+          }
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j)
+            rows_of(k + j * kEach, [&](int r, float scale, f32x4 lo, f32x4 hi) {
+              result.put8<true>(mw + r, nw, scale, bias, lo, hi, res[j]);
+            });
         }
-        const int64_t src = source_of(A, m);
-        if (src < 0 && ip == 0 && A.status) atomicOr(A.status, kDevBadRow);
-        const float scale = src < 0 ? 0.f : A.qs[src];
-        if (A.vec)
-          finish<4>(A, seg.e, m, nw, scale, v);
-        else
-          for (int c = 0; c < 4 && nw + c < A.N; ++c) finish<1>(A, seg.e, m, nw + c, scale, v + c);
       }
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
@@ -962,7 +1094,7 @@ void launch_gemm_i8(const int8_t *q, const float *qs, const uint8_t *packed, con
   a.bias32 = bias32;
   a.out32 = out32;
   auto at16 = [](const void *v) { return (uintptr_t)v % 16 == 0; };
-  a.vec = N % 4 == 0 && at16(out) && at16(residual) && at16(bias);
+  a.vec = N % 8 == 0 && at16(out) && at16(residual);
   a.act = act;
   a.partial = (float *)workspace;
   a.splits = p.splits;
