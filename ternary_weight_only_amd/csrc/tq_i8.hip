@@ -84,6 +84,7 @@ struct Codes {
 
   __device__ static __forceinline__ void build(lds_bytes *table, int tid, int threads) {
     constexpr uint32_t kParts = 2, kPer = COPIES / 2 / kParts;  // 16-byte stores a thread
+    static_assert(kPer >= 1, "");
     const uint32_t part = (uint32_t)tid % kParts;
     for (uint32_t e = (uint32_t)tid / kParts; e < 256u; e += (uint32_t)threads / kParts) {
       uint32_t lo = 0, v = e;
@@ -390,7 +391,7 @@ __global__ __launch_bounds__(256) void join_kernel(const I8Args A) {
 // few rows
 // ---------------------------------------------------------------------------
 
-constexpr int few_waves(int copies) { return copies == 32 ? 16 : 8; }
+constexpr int few_waves(int copies) { return copies == 32 ? 16 : 8; }  // of a block, at most
 
 template <int MB, int COPIES>
 struct FewRoom {
@@ -402,12 +403,13 @@ struct FewRoom {
 // A unit is up to 4 MB rows of q (of one expert); a block takes one split of K
 // and sets of wt tiles of 16 weight rows, wk waves a tile.  Lane (l, q) decodes
 // unit q of a quad (512 codes) of weight row l, so its bytes are two wide loads
-// and the four lanes of a row read 104 neighbouring ones.  The matrix cores sum
-// over the four lanes of a row, which have different groups here: so of the 16
-// columns, four are given to each row of q, column 4 i + j with row i's part of
-// unit j and zeros elsewhere, and a result is a row's sum over one unit, exact,
-// which is then scaled.  (Four rows of q a matrix instruction instead of 16;
-// the instructions are far from bounding it.)
+// and the four lanes of a row read 104 neighbouring ones; two quads are on their
+// way while one is decoded.  The matrix cores sum over the four lanes of a row,
+// which have different groups here: so of the 16 columns, four are given to
+// each row of q, column 4 i + j with row i's part of unit j and zeros elsewhere,
+// and a result is a row's sum over one unit, exact, which is then scaled.  (Four
+// rows of q a matrix instruction instead of 16; the instructions are far from
+// bounding it.)
 template <int G, int MB, int COPIES>
 __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Args A) {
   typedef Codes<COPIES> L;
@@ -422,17 +424,16 @@ __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Arg
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), waves = threads >> 6;
   const int split = (int)(blockIdx.x % A.splits);
   const int b0 = (int)(blockIdx.x / A.splits % A.bpu);
-  const int64_t unit = blockIdx.x / A.splits / A.bpu;
-  const Segment seg = find_unit(A, Room::kRows, (int)unit);
+  const Segment seg = find_unit(A, Room::kRows, (int)(blockIdx.x / A.splits / A.bpu));
   if (A.offsets && blockIdx.x == 0 && A.status)
     for (int e = tid; e < A.E; e += threads)
       if (A.offsets[e] < 0 || A.offsets[e + 1] < A.offsets[e] || A.offsets[e + 1] > A.T)
         atomicOr(A.status, kDevBadSegment);
   if (seg.e < 0) return;
-  const int64_t m0 = seg.a + seg.unit * Room::kRows;
-  const int M = min(seg.b - (int)m0, Room::kRows);
+  const int m0 = seg.a + seg.unit * Room::kRows, M = min(seg.b - m0, Room::kRows);
   const int nG = A.K / G, nU = (nG + GU - 1) / GU, nQ = (nU + 3) / 4;
-  const int u0 = 4 * (int)((int64_t)nQ * split / A.splits), u1 = min(nU, 4 * (int)((int64_t)nQ * (split + 1) / A.splits));
+  // (at most 4096 quads and as many splits: the products fit)
+  const int u0 = 4 * (nQ * split / A.splits), u1 = min(nU, 4 * (nQ * (split + 1) / A.splits));
   const int wk = A.wk, wt = A.wt, kw = wv % wk, tw = wv / wk;
   const int tiles = (A.N + 15) / 16, sets = (tiles + wt - 1) / wt;
   const int steps = b0 < sets ? (sets - b0 + A.bpu - 1) / A.bpu : 0;
@@ -441,11 +442,8 @@ __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Arg
   const uint16_t *scales = A.scales + (int64_t)seg.e * A.N * nG;
 
   auto tile_row = [&](int j) { return ((b0 + j * A.bpu) * wt + tw) * 16; };
-  const bool active = tw < wt;
   int fj = 0, fk = 0;  // step and batch of the next request
-  Unit f;
-  auto fetch = [&]() {
-    if (!active) return;
+  auto fetch = [&](Unit &f) {
     // rows past N read row N - 1, units past the last read it, with scales 0
     const int64_t n = min(tile_row(fj) + l, A.N - 1);
     const int u = u0 + 4 * (kw + wk * fk) + q, g = GU * min(u, u1 - 1);
@@ -479,7 +477,9 @@ __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Arg
       ++fj;
     }
   };
-  fetch();
+  Unit f0, f1;
+  fetch(f0);
+  fetch(f1);
   L::build(smem, tid, threads);
   if (tid < 8) *(lds_u32x4 *)(smem + kZeroOff + 16 * tid) = u32x4{0u, 0u, 0u, 0u};
   if (tid < Room::kRows) {
@@ -511,16 +511,23 @@ __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Arg
   __syncthreads();
 
   const L lut(0, lane);
+  const Result result(A);
   const int qc = l & 3, mi = l >> 2;  // this lane's column: unit, row
   uint32_t flags = 0;
   f32x4 acc[MB];
 #pragma unroll
   for (int b = 0; b < MB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
   int j = 0, k = 0;
-  const int total = steps * batches;
-  for (int t = 0; t < total; ++t) {
+  // row m of the unit, column n
+  auto put = [&](int m, int n, float v) {
+    if (A.splits > 1)
+      A.partial[((int64_t)split * A.T + m0 + m) * A.N + n] = v;
+    else
+      result.put(m0 + m, n, fmaf(v, row_scale[m], A.bias ? bias_of(A, seg.e, n) : 0.f));
+  };
+  auto work = [&](Unit &f) {
     const int quad = kw + wk * k;
-    if (active && tile_row(j) < A.N && quad < quads) {
+    if (tile_row(j) < A.N && quad < quads) {
       uint32_t d[GU][G / 4];
       decode_unit<G, 0>(smem, lut, f, d[0], flags);
       if constexpr (GU == 2) decode_unit<G, 13>(smem, lut, f, d[1], flags);
@@ -532,7 +539,7 @@ __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Arg
         s[0][r] = f16_value(sc);
         if constexpr (GU == 2) s[1][r] = f16_value(sc >> 16);
       }
-      fetch();
+      fetch(f);
 #pragma unroll
       for (int b = 0; b < MB; ++b) {
         if (4 * b >= M) break;
@@ -554,12 +561,13 @@ __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Arg
         }
       }
     } else {
-      fetch();
+      fetch(f);
     }
-    if (++k < batches) continue;
+    if (++k < batches) return;
     k = 0;
-    // the tile's last batch: the units' sums (four lanes), then the waves', in order
-    __syncthreads();  // the sums before have been read
+    // the tile's last batch: the units' sums (four lanes); lane (l, q) then has
+    // weight row 4 q + qc of row mi of each four
+    if (wk > 1) __syncthreads();  // the sums before have been read
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
       float mine = 0.f;
@@ -571,23 +579,31 @@ __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Arg
         mine = qc == r ? v : mine;
         acc[b][r] = 0.f;
       }
-      *(lds_float *)(smem + kSumOff + 4u * (uint32_t)((b * waves + wv) * 64 + lane)) = mine;
+      if (wk > 1) {
+        *(lds_float *)(smem + kSumOff + 4u * (uint32_t)((b * waves + wv) * 64 + lane)) = mine;
+      } else {
+        const int n = tile_row(j) + 4 * q + qc;
+        if (4 * b + mi < M && n < A.N) put(4 * b + mi, n, mine);
+      }
     }
-    __syncthreads();
-    const Result result(A);
-    for (int o = tid; o < wt * MB * 64; o += threads) {  // [tile][row of q][column]
-      const int ts = o / (MB * 64), m = o / 16 % (4 * MB), c = o & 15;
-      const int n = ((b0 + j * A.bpu) * wt + ts) * 16 + c;
-      if (m >= M || n >= A.N) continue;
-      const uint32_t at = (uint32_t)((m >> 2) * waves + ts * wk) * 64 + (uint32_t)(16 * (c >> 2) + 4 * (m & 3) + (c & 3));
-      float v = 0.f;
-      for (int w = 0; w < wk; ++w) v += *(lds_float *)(smem + kSumOff + 4u * (at + 64u * (uint32_t)w));
-      if (A.splits > 1)
-        A.partial[((int64_t)split * A.T + m0 + m) * A.N + n] = v;
-      else
-        result.put(m0 + m, n, fmaf(v, row_scale[m], A.bias ? bias_of(A, seg.e, n) : 0.f));
+    if (wk > 1) {  // the waves' sums, in order
+      __syncthreads();
+      for (int o = tid; o < wt * MB * 64; o += threads) {  // [tile][row of q][column]
+        const int ts = o / (MB * 64), m = o / 16 % (4 * MB), c = o & 15;
+        const int n = ((b0 + j * A.bpu) * wt + ts) * 16 + c;
+        if (m >= M || n >= A.N) continue;
+        const uint32_t at = (uint32_t)((m >> 2) * waves + ts * wk) * 64 + (uint32_t)(16 * (c >> 2) + 4 * (m & 3) + (c & 3));
+        float v = 0.f;
+        for (int w = 0; w < wk; ++w) v += *(lds_float *)(smem + kSumOff + 4u * (at + 64u * (uint32_t)w));
+        put(m, n, v);
+      }
     }
     ++j;
+  };
+  const int total = steps * batches;
+  for (int t = 0; t < total; t += 2) {
+    work(f0);
+    if (t + 1 < total) work(f1);
   }
   if ((flags & kBad) && A.status) atomicOr(A.status, kDevInvalidByte);
 }
@@ -638,10 +654,10 @@ __device__ __forceinline__ uint32_t swap_of(uint32_t r) { return (r >> 1) & 7u; 
 //   - scales and adds the row before;
 //   - decodes its codes of s + 1, two threads a weight row, 64 codes each;
 //   - requests q of s + 2, whose slot this stage's q has left, and bytes of s + 2.
-template <int G, int P, int Q, int WP>
-__global__ __launch_bounds__(2 * P) __attribute__((amdgpu_waves_per_eu(2, P == 256 ? 2 : 4)))
+template <int G, int P, int Q, int WP, int COPIES>
+__global__ __launch_bounds__(2 * P) __attribute__((amdgpu_waves_per_eu(2, P == 256 || Q > 64 ? 2 : 4)))
 void tile_kernel(const I8Args A) {
-  typedef Codes<8> L;
+  typedef Codes<COPIES> L;
   constexpr int NT = 2 * P, WQ = NT / 64 / WP, TP = P / WP / 16, TQ = Q / WQ / 16;
   constexpr int B = bytes_per_group(G), GS = 128 / G;
   constexpr uint32_t kPSlot = P * 128, kQSlot = Q * 128, kSSlot = 2 * P * 4;
@@ -653,7 +669,6 @@ void tile_kernel(const I8Args A) {
   const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), wp = wv / WQ, wq = wv % WQ;
   const int nG = A.K / G, S = (A.K + 127) / 128;
-  L::build(smem + kLutOff, tid, NT);
   const L lut(kLutOff, lane);
   const int units = count_units(A, Q);
   if (A.offsets && blockIdx.x == 0 && A.status)
@@ -666,12 +681,14 @@ void tile_kernel(const I8Args A) {
   for (int work = (int)blockIdx.x; work < total; work += (int)gridDim.x) {
     // the same for the block: kept in scalar registers
     auto scalar = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
-    const int split = scalar((int)((uint32_t)work / (uint32_t)tiles)), t = work - split * tiles;
+    const int split = A.splits == 1 ? 0 : scalar((int)((uint32_t)work / (uint32_t)tiles)), t = work - split * tiles;
     const int unit = scalar((int)((uint32_t)t / (uint32_t)A.tp)), ip = t - unit * A.tp;
     const Segment seg = find_unit(A, Q, unit);
     if (seg.e < 0) break;
     // stages are counted from the split's first
-    const int s0 = scalar(S * split / A.splits), S1 = scalar(S * (split + 1) / A.splits) - s0;  // S is at most 2^14
+    // (S is at most 2^14)
+    const int s0 = A.splits == 1 ? 0 : scalar(S * split / A.splits);
+    const int S1 = A.splits == 1 ? S : scalar(S * (split + 1) / A.splits) - s0;
     const int n0 = ip * P, m0 = seg.a + seg.unit * Q, M = min(seg.b - m0, Q);
 
     // q: this thread's chunks of a slot, as bytes from the first of A.q (where
@@ -789,18 +806,22 @@ void tile_kernel(const I8Args A) {
     for (int a = 0; a < TP; ++a)
 #pragma unroll
       for (int b = 0; b < TQ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    __syncthreads();  // the table is there, and the tile before is done with LDS
+    if (work != (int)blockIdx.x) __syncthreads();  // the tile before is done with LDS
     load_raw(0);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) request(0, 0, i);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) request(1, kQSlot, i);
+    if (work == (int)blockIdx.x) {  // the table, while those are on their way
+      L::build(smem + kLutOff, tid, NT);
+      __syncthreads();
+    }
     align_raw();
     look(Int<0>{}), piece(Int<0>{}), look(Int<1>{}), piece(Int<1>{});
     look(Int<2>{}), piece(Int<2>{}), look(Int<3>{}), piece(Int<3>{});
     store_scale();
     put ^= kPSlot;
     sput ^= kSSlot;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) request(1, kQSlot, i);
     load_raw(1);
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
@@ -1002,38 +1023,71 @@ uint32_t few_room(int mb, int copies) {
   return (159u << 10) - 65536u - (uint32_t)few_waves(copies) * mb * 256u;
 }
 
-Plan plan_of(int64_t T, int64_t N, int64_t K, int G, int64_t E, bool grouped) {
-  (void)G;
+// tile_kernel's tiles and what they take, in us: a tile before and behind its
+// stages, and a stage where it is alone on a CU and where all `places` are taken.
+// (Measured with G = 128; a stage with G = 64 takes a fourth more of all.)
+struct Shape {
+  int p, q, places;
+  double start, alone, full;
+};
+constexpr Shape kShapes[] = {{128, 64, 512, 6.4, 0.82, 1.10}, {128, 128, 512, 8.5, 1.05, 1.56}, {256, 256, 256, 15, 2.25, 2.25}};
+
+// Of the shapes and the splits of K the cheapest.  Splits keep two stages, and
+// their sums are written, read and joined in a launch more.
+void plan_tiles(Plan &p, int64_t T, int64_t N, int64_t K, int64_t used, bool grouped) {
+  const int64_t stages = ceil_div(K, 128);
+  double least = 1e30;
+  for (const Shape &c : kShapes) {
+    // units of an expert: on average its last is half full
+    const int64_t units = grouped ? std::max(used, T / c.q + used / 2) : ceil_div(T, c.q);
+    const int64_t tiles = units * ceil_div(N, c.p);
+    for (int s = 1; s <= 16 && (s == 1 || stages / s >= 2); ++s) {
+      const int64_t rounds = tiles * s / c.places, rest = tiles * s - rounds * c.places;
+      const double last = rest ? c.alone + (c.full - c.alone) * std::max<double>(0, 2.0 * rest / c.places - 1) : 0;
+      const double cost = c.start * (rounds + (rest > 0)) + ceil_div(stages, s) * (rounds * c.full + last) +
+                          (s > 1 ? 4.5 + (double)s * T * N * 8 / 5.2e6 : 0);
+      if (cost < least) least = cost, p.p = c.p, p.q = c.q, p.splits = s;
+    }
+  }
+  p.kind = kTile;
+  p.units = grouped ? T / p.q + used : ceil_div(T, p.q);
+  p.blocks = std::min<int64_t>(ceil_div(N, p.p) * p.units * p.splits, 1 << 20);
+}
+
+Plan plan_of(int64_t T, int64_t N, int64_t K, int64_t E, bool grouped) {
   Plan p{};
   const int64_t used = grouped ? std::min(E, T) : 1;  // experts that have rows, at most
   const int64_t mean = ceil_div(T, std::max<int64_t>(used, 1));
-  p.splits = 1;
-  if (mean <= (grouped ? 16 : 32)) {
-    p.kind = kFew;
-    const int64_t want = grouped ? std::min<int64_t>(2 * mean, 32) : mean;
-    p.mb = want <= 4 ? 1 : want <= 8 ? 2 : want <= 16 ? 4 : 8;
-    const int64_t rows = 4 * p.mb, quads = ceil_div(K, 512), tiles = ceil_div(N, 16);
-    p.units = grouped ? T / rows + used : 1;
-    p.copies = rows * (512 * quads + 16) <= few_room(p.mb, 8) ? 8 : 32;
-    const int waves = few_waves(p.copies);
-    const int64_t most = (few_room(p.mb, p.copies) / rows - 16) / 512;  // quads that fit
-    p.splits = (int)ceil_div(quads, most);
-    const int64_t q = ceil_div(quads, p.splits);
-    p.wk = (int)std::min<int64_t>(q, waves);
-    p.wt = std::max(1, waves / p.wk);
-    const int64_t sets = ceil_div(tiles, p.wt);
-    p.bpu = (int)std::max<int64_t>(1, std::min<int64_t>(sets, 512 / std::max<int64_t>(1, used * p.splits)));
-    p.blocks = p.units * p.bpu * p.splits;
-  } else {
-    p.kind = kTile;
-    const bool big = mean >= 192;
-    p.p = big ? 256 : 128;
-    p.q = big ? 256 : 64;
-    p.units = grouped ? T / p.q + used : ceil_div(T, p.q);
-    const int64_t tiles = ceil_div(N, p.p) * p.units, stages = ceil_div(K, 128), places = big ? 256 : 512;
-    while (p.splits < 8 && tiles * (p.splits + 1) <= places && stages / (p.splits + 1) >= 4) ++p.splits;
-    p.blocks = std::min<int64_t>(tiles * p.splits, 1 << 20);
+  // few_kernel against tile_kernel, us: one matrix, 16 rows: [14336,4096] 16 and
+  // 20, [3584,1024] 7.7 and 9.4; 24 rows: 25 and 22, 11 and 10.  16 experts of 8
+  // rows on average: [4096,4096] 41 and 46, [3584,1024] 15 and 17; of 16: 53 and
+  // 44, 25 and 18.
+  if (mean > (grouped ? 8 : 16)) {
+    plan_tiles(p, T, N, K, used, grouped);
+    return p;
   }
+  p.kind = kFew;
+  // rows of a unit: of experts a few more than their mean, since some have more
+  // (16 of [4096,4096], 4, 8 and 16 rows a unit: 2 on average 20, 22, 24 us; 4: 37, 28, 28)
+  p.mb = grouped ? (mean <= 2 ? 1 : mean <= 4 ? 2 : 4) : (mean <= 4 ? 1 : mean <= 8 ? 2 : 4);
+  const int64_t rows = 4 * p.mb, quads = ceil_div(K, 512), tiles = ceil_div(N, 16);
+  p.units = grouped ? T / rows + used : 1;
+  // the large table (no two lanes of a read in a bank; one block a CU) where a CU
+  // has many quads: one row, [14336,4096] 9.9 us, 10.8 with the small one;
+  // [3584,1024] 5.8 and 5.5
+  p.copies = used * tiles * quads >= 4096 || rows * (512 * quads + 16) > few_room(p.mb, 8) ? 32 : 8;
+  const int waves = few_waves(p.copies);
+  const int64_t most = (few_room(p.mb, p.copies) / rows - 16) / 512;  // quads whose q fits
+  p.splits = (int)ceil_div(quads, most);
+  const int64_t q = ceil_div(quads, p.splits), all = used * tiles * p.splits;
+  // as many waves a tile as fill the card once (16 a CU), and as many tiles a
+  // block as leave every CU one (one row, [14336,4096], waves by tiles: 4 x 4 9.9
+  // us, 8 x 2 10.8, 2 x 4 10.4, 4 x 1 23; [3584,1024]: 2 x 1 5.5, 1 x 1 12)
+  p.wk = (int)std::max<int64_t>(1, std::min<int64_t>({q, waves, 4096 / all}));
+  p.wt = (int)std::max<int64_t>(1, std::min<int64_t>(waves / p.wk, ceil_div(all, 256)));
+  const int64_t sets = ceil_div(tiles, p.wt);
+  p.bpu = (int)std::max<int64_t>(1, std::min<int64_t>(sets, 512 / std::max<int64_t>(1, used * p.splits)));
+  p.blocks = p.units * p.bpu * p.splits;
   return p;
 }
 
@@ -1051,13 +1105,14 @@ void launch(const Plan &p, const I8Args &a, hipStream_t stream) {
     switch (p.mb) {
       case 1: go(few_kernel<G, 1, 8>, few_kernel<G, 1, 32>); break;
       case 2: go(few_kernel<G, 2, 8>, few_kernel<G, 2, 32>); break;
-      case 4: go(few_kernel<G, 4, 8>, few_kernel<G, 4, 32>); break;
-      default: go(few_kernel<G, 8, 8>, few_kernel<G, 8, 32>); break;
+      default: go(few_kernel<G, 4, 8>, few_kernel<G, 4, 32>); break;
     }
-  } else if (p.q == 256) {
-    hipLaunchKernelGGL((tile_kernel<G, 256, 256, 2>), grid, dim3(512), 0, stream, a);
+  } else if (p.p == 256) {
+    hipLaunchKernelGGL((tile_kernel<G, 256, 256, 2, 8>), grid, dim3(512), 0, stream, a);
+  } else if (p.q == 128) {
+    hipLaunchKernelGGL((tile_kernel<G, 128, 128, 2, 4>), grid, dim3(256), 0, stream, a);
   } else {
-    hipLaunchKernelGGL((tile_kernel<G, 128, 64, 2>), grid, dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((tile_kernel<G, 128, 64, 2, 8>), grid, dim3(256), 0, stream, a);
   }
   if (a.splits > 1)
     hipLaunchKernelGGL(join_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(a.N, 256), 64), (unsigned)std::min<int64_t>(a.T, 65535)),
@@ -1066,8 +1121,8 @@ void launch(const Plan &p, const I8Args &a, hipStream_t stream) {
 
 }  // namespace
 
-int64_t gemm_i8_workspace(int64_t T, int64_t N, int64_t K, int G, int64_t E, bool grouped) {
-  const Plan p = plan_of(T, N, K, G, E, grouped);
+int64_t gemm_i8_workspace(int64_t T, int64_t N, int64_t K, int64_t E, bool grouped) {
+  const Plan p = plan_of(T, N, K, E, grouped);
   return p.splits > 1 ? (p.splits * T * N * 4 + 15) / 16 * 16 : 0;
 }
 
@@ -1075,7 +1130,7 @@ void launch_gemm_i8(const int8_t *q, const float *qs, const uint8_t *packed, con
                     const int32_t *offsets, int64_t E, const int32_t *rows, int64_t sources, const void *bias,
                     bool bias32, int act, const void *residual, int64_t T, int64_t N, int64_t K, int G, void *out,
                     bool out32, void *workspace, int32_t *status, hipStream_t stream) {
-  const Plan p = plan_of(T, N, K, G, E, offsets != nullptr);
+  const Plan p = plan_of(T, N, K, E, offsets != nullptr);
   I8Args a{};
   a.q = q;
   a.qs = qs;

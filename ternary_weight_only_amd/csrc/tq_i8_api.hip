@@ -82,7 +82,7 @@ int product(const int8_t *x, const float *x_scales, int64_t sources, const int32
       !aligned(rows, 4) || (bias && !aligned(bias, size_of(bias_type))) || !aligned(out, size_of(out_type)) ||
       !aligned(residual, size_of(out_type)) || !aligned(d_status, 4))
     return TQ_ERR_ALIGN;
-  rc = check_workspace(workspace, workspace_bytes, tq::gemm_i8_workspace(T, N, K, G, experts, grouped));
+  rc = check_workspace(workspace, workspace_bytes, tq::gemm_i8_workspace(T, N, K, experts, grouped));
   if (rc) return rc;
   (void)hipGetLastError();
   tq::launch_gemm_i8(x, x_scales, packed, scales, offsets, experts, rows, sources, bias, bias_type == TQ_F32, act,
@@ -146,7 +146,7 @@ int tq_rms_norm_backward(const uint16_t *dh, const void *y, int y_type, const fl
 }
 
 int64_t tq_gemm_i8_workspace(int64_t M, int64_t N, int64_t K, int G) {
-  return check_product(M, N, K, G, 1) || M == 0 ? 0 : tq::gemm_i8_workspace(M, N, K, G, 1, false);
+  return check_product(M, N, K, G, 1) || M == 0 ? 0 : tq::gemm_i8_workspace(M, N, K, 1, false);
 }
 
 int tq_gemm_i8(const int8_t *x, const float *x_scales, const uint8_t *packed, const uint16_t *scales,
@@ -158,7 +158,7 @@ int tq_gemm_i8(const int8_t *x, const float *x_scales, const uint8_t *packed, co
 }
 
 int64_t tq_expert_gemm_i8_workspace(int64_t T, int64_t N, int64_t K, int G, int64_t experts) {
-  return check_product(T, N, K, G, experts) || T == 0 ? 0 : tq::gemm_i8_workspace(T, N, K, G, experts, true);
+  return check_product(T, N, K, G, experts) || T == 0 ? 0 : tq::gemm_i8_workspace(T, N, K, experts, true);
 }
 
 int tq_expert_gemm_i8(const int8_t *x, const float *x_scales, int64_t sources, const int32_t *rows,
