@@ -1067,10 +1067,16 @@ Plan plan_of(int64_t T, int64_t N, int64_t K, int64_t E, bool grouped) {
     return p;
   }
   p.kind = kFew;
-  // rows of a unit: of experts a few more than their mean, since some have more
-  // (16 of [4096,4096], 4, 8 and 16 rows a unit: 2 on average 20, 22, 24 us; 4: 37, 28, 28)
-  p.mb = grouped ? (mean <= 2 ? 1 : mean <= 4 ? 2 : 4) : (mean <= 4 ? 1 : mean <= 8 ? 2 : 4);
-  const int64_t rows = 4 * p.mb, quads = ceil_div(K, 512), tiles = ceil_div(N, 16);
+  const int64_t quads = ceil_div(K, 512), tiles = ceil_div(N, 16);
+  // Rows of a unit.  Experts' numbers of rows differ, and one with more than a
+  // unit's has its weights decoded again, while larger units hold more registers:
+  // where there is much to decode four times the mean, else twice (us, 4, 8 and 16
+  // rows a unit: 16 experts of [4096,14336], 4 rows on average 107, 101, 81; 8 of
+  // them, 2 on average, 62, 43, 60; 32 of [3584,1024], 4 on average, 23, 20, 25; 8
+  // of those, 2 on average, 7.6, 8.2, 9.6)
+  const int64_t want = !grouped ? mean : (used * tiles * quads >= 50000 ? 4 : 2) * mean;
+  p.mb = want <= 4 ? 1 : want <= 8 ? 2 : 4;
+  const int64_t rows = 4 * p.mb;
   p.units = grouped ? T / rows + used : 1;
   // the large table (no two lanes of a read in a bank; one block a CU) where a CU
   // has many quads: one row, [14336,4096] 9.9 us, 10.8 with the small one;
@@ -1085,8 +1091,8 @@ Plan plan_of(int64_t T, int64_t N, int64_t K, int64_t E, bool grouped) {
   // us, 8 x 2 10.8, 2 x 4 10.4, 4 x 1 23; [3584,1024]: 2 x 1 5.5, 1 x 1 12)
   p.wk = (int)std::max<int64_t>(1, std::min<int64_t>({q, waves, 4096 / all}));
   p.wt = (int)std::max<int64_t>(1, std::min<int64_t>(waves / p.wk, ceil_div(all, 256)));
-  const int64_t sets = ceil_div(tiles, p.wt);
-  p.bpu = (int)std::max<int64_t>(1, std::min<int64_t>(sets, 512 / std::max<int64_t>(1, used * p.splits)));
+  const int64_t sets = ceil_div(tiles, p.wt), blocks = p.mb == 4 ? 256 : 1024;
+  p.bpu = (int)std::max<int64_t>(1, std::min<int64_t>(sets, blocks / std::max<int64_t>(1, used * p.splits)));
   p.blocks = p.units * p.bpu * p.splits;
   return p;
 }
