@@ -765,7 +765,8 @@ int64_t tq_gemm_i8_workspace(int64_t M, int64_t N, int64_t K, int G);
  * where rows is given (a token's row for each of its experts, not copied), else
  * of row m.
  *   x         [sources,K] int8, 16-byte aligned;  x_scales [sources] fp32
- *   rows      [T] int32, or NULL (then sources >= T)
+ *   rows      [T] int32, or NULL (then sources >= T); with rows, x has at most
+ *             2^32 elements (TQ_ERR_SHAPE)
  *   packed    [experts, N, K/G, ceil(G/5)];  scales [experts, N, K/G]
  *   offsets   [experts+1] int32 on the device, 1 <= experts <= 65536
  *   bias      [experts,N], or NULL

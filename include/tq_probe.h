@@ -85,11 +85,18 @@ int tq_probe_valu(int kind, int iters, int grid, uint32_t *sink, unsigned long l
  * tq_glu_backward: plan[1] its tile, plan[2] 1 where both products run side by
  * side, plan[3] and plan[4] the splits of K of the weight gradients and of dx.
  *
+ * tq_probe_i8_plan: tq_gemm_i8 (experts = 0) or tq_expert_gemm_i8.  plan[0] the
+ * kernel (0 few_kernel, 1 tile_kernel, 2 part_kernel), plan[1] the splits of K;
+ * of few_kernel plan[2] the rows of a unit, plan[3] the table's copies, plan[4]
+ * the waves of a tile, plan[5] the tiles of a set and plan[6] the blocks of a
+ * unit; of the others plan[2] and plan[3] the weight rows and rows of a tile.
+ *
  * TQ_ERR_NULL, or the error that the calls return for such sizes; M >= 1.
  */
 int tq_probe_projection_plan(int64_t M, int64_t N, int64_t K, int G, int matrices, int64_t R,
                              int64_t *plan);
 int tq_probe_train_plan(int64_t M, int64_t N, int64_t K, int64_t *plan);
+int tq_probe_i8_plan(int64_t M, int64_t N, int64_t K, int G, int64_t experts, int64_t *plan);
 
 #ifdef __cplusplus
 }

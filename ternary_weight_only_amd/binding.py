@@ -40,7 +40,7 @@ SYMBOLS = ("tq_status_string", "tq_packed_row_bytes", "tq_packed_bytes", "tq_qua
            "tq_rms_norm_backward", "tq_rms_norm_backward_workspace", "tq_gemm_i8",
            "tq_gemm_i8_workspace", "tq_expert_gemm_i8", "tq_expert_gemm_i8_workspace")
 # Every symbol include/tq_probe.h declares (measurement probes).
-PROBE_SYMBOLS = ("tq_probe_lds_table", "tq_probe_mfma_bf16", "tq_probe_projection_plan",
+PROBE_SYMBOLS = ("tq_probe_i8_plan", "tq_probe_lds_table", "tq_probe_mfma_bf16", "tq_probe_projection_plan",
                  "tq_probe_read_stream", "tq_probe_train_plan", "tq_probe_valu")
 
 _lib = None
@@ -173,6 +173,8 @@ def lib() -> ctypes.CDLL:
         l.tq_probe_projection_plan.restype = i32
         l.tq_probe_train_plan.argtypes = [i64, i64, i64, p]
         l.tq_probe_train_plan.restype = i32
+        l.tq_probe_i8_plan.argtypes = [i64, i64, i64, i32, i64, p]
+        l.tq_probe_i8_plan.restype = i32
         _lib = l
     return _lib
 

@@ -36,6 +36,7 @@ __host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) const u32x4 lds_u32x4_c;
 typedef __attribute__((address_space(3))) const f32x4 lds_f32x4_c;
+typedef __attribute__((address_space(3))) const uint32_t lds_u32_c;
 typedef __attribute__((address_space(3))) float lds_float;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 
@@ -59,10 +60,10 @@ struct I8Args {
   bool bias32, out32, vec;  // vec: eight columns at a time are aligned
   int act;
   float *partial;           // [splits][T][N] where splits > 1
+  uint8_t *parts;           // of q, where it is taken in parts
   int splits;
   int wk, wt, bpu;          // few: waves of a tile, tiles of a set, blocks of a unit
   int tp;                   // tile: tiles of weight rows
-  int64_t units;            // few: of the launch
   int32_t *status;
 };
 
@@ -645,6 +646,123 @@ __device__ __forceinline__ uint32_t known_here(uint32_t v) {
 // 16 rows and four chunks of an operand read fall into different banks.
 __device__ __forceinline__ uint32_t swap_of(uint32_t r) { return (r >> 1) & 7u; }
 
+// A tile of results: expert, first weight row, first row of q and how many, and
+// which tile and split (each row of q is looked at by one of them).
+struct Tile {
+  int e, n0, m0, M, ip, split;
+};
+
+// Matrix tiles of rows of q that finish_tile takes at once, and LDS that it uses.
+template <int P, int Q, int WP>
+__host__ __device__ constexpr int finish_once() {
+  return Q / (P / 32 / WP) / 16 < 2 || WP == 1 ? 1 : 2;
+}
+template <int P, int Q, int WP>
+__host__ __device__ constexpr uint32_t finish_room() {
+  return P / 32 * finish_once<P, Q, WP>() * 16 * (P / WP) * 4;
+}
+
+// Results go through this wave's part of LDS, kOnce tiles of 16 rows of q at
+// a time, [row][weight row], and leave in runs of a wave's weight rows; chunk
+// c of a row sits at c ^ row % 16.  (Loops that stay loops: unrolled, the
+// epilogue was most of the kernel's code and its fetching took 10 us.)
+template <int P, int Q, int WP>
+__device__ __forceinline__ void finish_tile(const I8Args &A, f32x4 (&acc)[P / WP / 16][Q / (P / 32 / WP) / 16],
+                                            lds_bytes *smem, int wv, const Tile t) {
+  constexpr int WQ = P / 32 / WP, TP = P / WP / 16, TQ = Q / WQ / 16;
+  const int wp = wv / WQ, wq = wv % WQ;
+  constexpr int W = P / WP, kOnce = finish_once<P, Q, WP>(), kLanes = W / 8, kEach = 64 / kLanes;  // lanes of a row, rows at once
+  static_assert(TQ % kOnce == 0 && W % 64 == 0 && TP % 4 == 0, "");
+  const int lane = lane_here(), l = lane & 15, q = lane >> 4;
+  lds_bytes *room = smem + (uint32_t)(wv * (kOnce * 16 * W * 4));
+  // where column l of row 4 q would be but for its chunk of four
+  const uint32_t mine = (uint32_t)(wv * (kOnce * 16 * W * 4)) + 16u * (uint32_t)(q * W) + 64u * (uint32_t)q + 4u * (uint32_t)(l & 3);
+  const int nw = t.n0 + wp * W + 8 * (lane % kLanes);
+  // a lane's row's scale (handed over below), and its columns' bias
+  static_assert(Q / WQ <= 64, "a row a lane");
+  float own = 0.f;
+  if (lane < Q / WQ && wq * (Q / WQ) + lane < t.M) {
+    const int64_t src = source_of(A, t.m0 + wq * (Q / WQ) + lane);
+    if (src >= 0)
+      own = A.qs[src];
+    else if (t.ip == 0 && t.split == 0 && A.status)
+      atomicOr(A.status, kDevBadRow);
+  }
+  float bias[8] = {};
+  if (A.bias)
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (nw + c < A.N) bias[c] = bias_of(A, t.e, nw + c);
+  const Result result(A);
+  const int64_t mw = t.m0 + wq * (Q / WQ);
+  float *sums = A.splits > 1 ? A.partial + ((int64_t)t.split * A.T + mw) * A.N + nw : nullptr;
+#pragma unroll 1
+  for (int part = 0; part < TQ / kOnce; ++part) {
+#pragma unroll
+    for (int b = 0; b < TQ; ++b)
+      if (b / kOnce == part)
+#pragma unroll
+        for (int a = 0; a < 4; ++a)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            lds_bytes *to = smem + ((mine + 16u * ((uint32_t)(l >> 2) ^ (uint32_t)r)) ^ 64u * (uint32_t)a) + 4u * (uint32_t)(r * W);
+#pragma unroll
+            for (int c = 0; c < TP / 4; ++c)
+              *(lds_float *)(to + 256u * (uint32_t)c + 64u * (uint32_t)(b % kOnce * W)) = acc[4 * c + a][b][r];
+          }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const uint32_t c = 2u * (uint32_t)(lane % kLanes);
+    // rows k on of this part, this lane's; `each` gets (row of the wave, its sums)
+    auto rows_of = [&](int k, auto each) __attribute__((always_inline)) {
+      const int i = k + lane / kLanes, r = 16 * kOnce * part + i;
+      lds_bytes *from = room + 4u * (uint32_t)(i * W);
+      const f32x4 lo = *(lds_f32x4_c *)(from + 16u * (c ^ (uint32_t)(i & 15)));
+      const f32x4 hi = *(lds_f32x4_c *)(from + 16u * ((c + 1u) ^ (uint32_t)(i & 15)));
+      const float scale = __shfl(own, r);
+      if (wq * (Q / WQ) + r < t.M && nw < result.N) each(r, scale, lo, hi);
+    };
+    // loops by themselves: a load in one would make every pass wait for the
+    // stores of the pass before
+    if (sums) {
+#pragma unroll 1
+      for (int k = 0; k < 16 * kOnce; k += kEach)
+        rows_of(k, [&](int r, float, f32x4 lo, f32x4 hi) { store_sums(sums + (int64_t)r * result.N, nw, result.N, lo, hi); });
+    } else if (!result.vec) {
+#pragma unroll 1
+      for (int k = 0; k < 16 * kOnce; k += kEach)
+        rows_of(k, [&](int r, float scale, f32x4 lo, f32x4 hi) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (nw + j < result.N) result.put(mw + r, nw + j, fmaf(j < 4 ? lo[j] : hi[j - 4], scale, bias[j]));
+        });
+    } else if (!result.residual) {
+#pragma unroll 2
+      for (int k = 0; k < 16 * kOnce; k += kEach)
+        rows_of(k, [&](int r, float scale, f32x4 lo, f32x4 hi) {
+          result.put8<false>(mw + r, nw, scale, bias, lo, hi, Result::Eight{});
+        });
+    } else {
+      constexpr int kAhead = 4;  // rows whose residuals are requested together
+      static_assert(16 * kOnce % (kAhead * kEach) == 0, "");
+#pragma unroll 1
+      for (int k = 0; k < 16 * kOnce; k += kAhead * kEach) {
+        Result::Eight res[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const int r = 16 * kOnce * part + k + j * kEach + lane / kLanes;
+          res[j] = wq * (Q / WQ) + r < t.M && nw < result.N ? result.residual8(mw + r, nw) : Result::Eight{};
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+          rows_of(k + j * kEach, [&](int r, float scale, f32x4 lo, f32x4 hi) {
+            result.put8<true>(mw + r, nw, scale, bias, lo, hi, res[j]);
+          });
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+}
+
 // P weight rows by Q rows of q, stages of 128 k; 2 P threads, their waves WP by
 // WQ, the tile kept with weight rows along a lane's four results.  Two LDS slots
 // of q and two of codes.  While stage s is multiplied, a row of TQ matrix tiles
@@ -663,7 +781,7 @@ void tile_kernel(const I8Args A) {
   constexpr uint32_t kPSlot = P * 128, kQSlot = Q * 128, kSSlot = 2 * P * 4;
   constexpr uint32_t kQOff = 2 * kPSlot, kSOff = kQOff + 2 * kQSlot, kLutOff = kSOff + 2 * kSSlot;
   constexpr int kLoads = Q * 8 / NT;
-  static_assert(P % 64 == 0 && TP >= 4, "");
+  static_assert(P % 64 == 0 && TP >= 4 && finish_room<P, Q, WP>() <= kSOff, "");
   __shared__ __align__(16) unsigned char smem_raw[kLutOff + L::kBytes];
   lds_bytes *smem = (lds_bytes *)smem_raw;
   const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
@@ -676,7 +794,8 @@ void tile_kernel(const I8Args A) {
       if (A.offsets[e] < 0 || A.offsets[e + 1] < A.offsets[e] || A.offsets[e + 1] > A.T)
         atomicOr(A.status, kDevBadSegment);
   uint32_t flags = 0;
-  // (T N is at most 2^40 and E N 2^34: the tiles' number fits)
+  // (T N is at most 2^40, E N 2^34 and a tile has 2^13 results or more: their number
+  // fits, and only fewer than 2^24 are split)
   const int tiles = units * A.tp, total = tiles * A.splits;
   for (int work = (int)blockIdx.x; work < total; work += (int)gridDim.x) {
     // the same for the block: kept in scalar registers
@@ -830,10 +949,10 @@ void tile_kernel(const I8Args A) {
     // on, exchanged or not
     uint32_t pat = 128u * pr + 16u * ((uint32_t)q ^ swap_of(pr));
     uint32_t qat = kQOff + 128u * qr + 16u * ((uint32_t)q ^ swap_of(qr));
-    uint32_t sat = kSOff + 4u * (uint32_t)(wp * (P / WP) + 4 * q);
+    uint32_t sat = kSOff + 4u * (uint32_t)(wp * (P / WP) + l);
     static_assert(kQOff % (2 * kQSlot) == 0 && kSOff % (2 * kSSlot) == 0, "a slot's bit");
     u32x4 qf[2][TQ], pf[2];
-    f32x4 sc[GS];
+    float sc[GS];
     i32x4 sum[TQ];  // of a group: of both halves of a stage, or (G = 64) of one
     auto read_q = [&](int h) __attribute__((always_inline)) {
 #pragma unroll
@@ -844,17 +963,17 @@ void tile_kernel(const I8Args A) {
     };
     auto read_s = [&](int a) __attribute__((always_inline)) {
 #pragma unroll
-      for (int h = 0; h < GS; ++h) sc[h] = *(lds_f32x4_c *)(smem + sat + 4u * (uint32_t)(h * P + 16 * a));
+      for (int h = 0; h < GS; ++h) sc[h] = *(lds_float *)(smem + sat + 4u * (uint32_t)(h * P + 16 * a));
     };
     auto multiply = [&](int h) __attribute__((always_inline)) {
 #pragma unroll
-      for (int b = 0; b < TQ; ++b) sum[b] = mfma_i8(pf[h], qf[h][b], h < GS ? i32x4{0, 0, 0, 0} : sum[b]);
+      for (int b = 0; b < TQ; ++b) sum[b] = mfma_i8(qf[h][b], pf[h], h < GS ? i32x4{0, 0, 0, 0} : sum[b]);
     };
     auto add = [&](int a, int h) __attribute__((always_inline)) {
 #pragma unroll
       for (int b = 0; b < TQ; ++b)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[a][b][r] = fmaf(sc[h][r], (float)sum[b][r], acc[a][b][r]);
+        for (int r = 0; r < 4; ++r) acc[a][b][r] = fmaf(sc[h], (float)sum[b][r], acc[a][b][r]);
     };
     read_q(0);
     read_q(1);
@@ -863,9 +982,6 @@ void tile_kernel(const I8Args A) {
     read_p(0, 0);
     read_p(0, 1);
     read_s(0);
-    // of the two waves of a SIMD one goes first, so that they take turns at the
-    // matrix cores and the other units
-    if (wv < NT / 128) __builtin_amdgcn_s_setprio(1);
     constexpr int kLate = TP > 4 ? 1 : 0;  // rows between a stage's begin and the first codes
     uint32_t here = 0;                     // the slot of this stage's q
     for (int s = 0; s < S1; ++s) {
@@ -915,96 +1031,349 @@ void tile_kernel(const I8Args A) {
       read_s(0);
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // nothing is on its way into LDS
-    __builtin_amdgcn_s_setprio(0);
 
-    // Results go through this wave's part of LDS, kOnce tiles of 16 rows of q at
-    // a time, [row][weight row], and leave in runs of a wave's weight rows; chunk
-    // c of a row sits at c ^ row % 16.  (Loops that stay loops: unrolled, the
-    // epilogue was most of the kernel's code and its fetching took 10 us.)
-    constexpr int W = P / WP, kOnce = TQ < 2 ? TQ : 2, kLanes = W / 8, kEach = 64 / kLanes;  // lanes of a row, rows at once
-    static_assert(NT / 64 * kOnce * 16 * W * 4 <= kSOff && TQ % kOnce == 0 && W % 64 == 0, "");
-    const int lane = lane_here(), l = lane & 15, q = lane >> 4;
-    lds_bytes *room = smem + (uint32_t)(wv * (kOnce * 16 * W * 4));
-    const int nw = n0 + wp * W + 8 * (lane % kLanes);
-    // a lane's row's scale (handed over below), and its columns' bias
-    static_assert(Q / WQ <= 64, "a row a lane");
-    float own = 0.f;
-    if (lane < Q / WQ && wq * (Q / WQ) + lane < M) {
-      const int64_t src = source_of(A, m0 + wq * (Q / WQ) + lane);
-      if (src >= 0)
-        own = A.qs[src];
-      else if (ip == 0 && split == 0 && A.status)
-        atomicOr(A.status, kDevBadRow);
-    }
-    float bias[8] = {};
-    if (A.bias)
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-        if (nw + c < A.N) bias[c] = bias_of(A, seg.e, nw + c);
-    const Result result(A);
-    const int64_t mw = m0 + wq * (Q / WQ);
-    float *sums = A.splits > 1 ? A.partial + ((int64_t)split * A.T + mw) * A.N + nw : nullptr;
-#pragma unroll 1
-    for (int part = 0; part < TQ / kOnce; ++part) {
-#pragma unroll
-      for (int b = 0; b < TQ; ++b)
-        if (b / kOnce == part)
-#pragma unroll
-          for (int a = 0; a < TP; ++a)
-            *(lds_f32x4 *)(room + 4u * (uint32_t)((b % kOnce * 16 + l) * W) + 16u * (uint32_t)((4 * a + q) ^ l)) = acc[a][b];
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      const uint32_t c = 2u * (uint32_t)(lane % kLanes);
-      // rows k on of this part, this lane's; `each` gets (row of the wave, its sums)
-      auto rows_of = [&](int k, auto each) __attribute__((always_inline)) {
-        const int i = k + lane / kLanes, r = 16 * kOnce * part + i;
-        lds_bytes *from = room + 4u * (uint32_t)(i * W);
-        const f32x4 lo = *(lds_f32x4_c *)(from + 16u * (c ^ (uint32_t)(i & 15)));
-        const f32x4 hi = *(lds_f32x4_c *)(from + 16u * ((c + 1u) ^ (uint32_t)(i & 15)));
-        const float scale = __shfl(own, r);
-        if (wq * (Q / WQ) + r < M && nw < result.N) each(r, scale, lo, hi);
-      };
-      // loops by themselves: a load in one would make every pass wait for the
-      // stores of the pass before
-      if (sums) {
-#pragma unroll 1
-        for (int k = 0; k < 16 * kOnce; k += kEach)
-          rows_of(k, [&](int r, float, f32x4 lo, f32x4 hi) { store_sums(sums + (int64_t)r * result.N, nw, result.N, lo, hi); });
-      } else if (!result.vec) {
-#pragma unroll 1
-        for (int k = 0; k < 16 * kOnce; k += kEach)
-          rows_of(k, [&](int r, float scale, f32x4 lo, f32x4 hi) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (nw + j < result.N) result.put(mw + r, nw + j, fmaf(j < 4 ? lo[j] : hi[j - 4], scale, bias[j]));
-          });
-      } else if (!result.residual) {
-#pragma unroll 2
-        for (int k = 0; k < 16 * kOnce; k += kEach)
-          rows_of(k, [&](int r, float scale, f32x4 lo, f32x4 hi) {
-            result.put8<false>(mw + r, nw, scale, bias, lo, hi, Result::Eight{});
-          });
-      } else {
-        constexpr int kAhead = 4;  // rows whose residuals are requested together
-        static_assert(16 * kOnce % (kAhead * kEach) == 0, "");
-#pragma unroll 1
-        for (int k = 0; k < 16 * kOnce; k += kAhead * kEach) {
-          Result::Eight res[kAhead];
-#pragma unroll
-          for (int j = 0; j < kAhead; ++j) {
-            const int r = 16 * kOnce * part + k + j * kEach + lane / kLanes;
-            res[j] = wq * (Q / WQ) + r < M && nw < result.N ? result.residual8(mw + r, nw) : Result::Eight{};
-          }
-#pragma unroll
-          for (int j = 0; j < kAhead; ++j)
-            rows_of(k + j * kEach, [&](int r, float scale, f32x4 lo, f32x4 hi) {
-              result.put8<true>(mw + r, nw, scale, bias, lo, hi, res[j]);
-            });
-        }
-      }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    }
+    finish_tile<P, Q, WP>(A, acc, smem, wv, Tile{seg.e, n0, m0, M, ip, split});
   }
   if ((flags & kBad) && A.status) atomicOr(A.status, kDevInvalidByte);
+}
+
+// ---------------------------------------------------------------------------
+// more rows, groups of 128
+// ---------------------------------------------------------------------------
+
+// |q| = 16 h + l with h <= 7 and l <= 15 (16 of -128): with q's sign, 2 h and
+// l / 8 are numbers of the 6-bit formats (3 exponent and 2 mantissa bits; 2 and
+// 3), codes -1, 0 and 1 of the 4-bit one, and a group's sum of products, an
+// eighth of a whole number below 2^15, is exact in the fp32 of the matrix cores.
+// They do 128 codes of both parts in the time of 128 8-bit ones, but leave a
+// float (no conversion, of 128 a thread and group, where the vector unit is what
+// bounds the kernel) and halve the codes' place and reading in LDS.
+//
+// Parts of q: [K/128][T + pad][192], a row's 128 codes as twelve 16-byte chunks:
+// chunk 4 p + (j ^ (row / 4 % 4)) is lane j's (k 32 j .. 32 j + 31) first 128 bits
+// of its 192 of 2 h (p = 0), of l / 8 (p = 1), and the last 64 of both (p = 2,
+// exchanged for odd j).  So the 16 rows and four chunks of an operand read fall
+// into different banks, and a tile's stage is one run of memory.
+constexpr int kPartBytes = 192, kPartPad = 256;  // of a row and group; rows behind the last
+
+__host__ __device__ constexpr int64_t part_bytes(int64_t T, int64_t K) { return (K / 128 * T + kPartPad) * kPartBytes; }
+
+// Four bytes of six bits each, together: sums of products with 1 and 64.
+__device__ __forceinline__ uint32_t six_bits(uint32_t v) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return __builtin_amdgcn_udot4(v, 0x00004001u, __builtin_amdgcn_udot4(v, 0x40010000u, 0u, false) << 12, false);
+#else
+  return 0;
+#endif
+}
+
+// A thread a lane's 32 codes of a row: rows given by index are gathered here.
+// Bound by memory (read once, written 1.5 times).
+__global__ __launch_bounds__(256) void parts_kernel(const I8Args A) {
+  const int nG = A.K / 128, j = threadIdx.x & 3;
+  for (int64_t m = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2); m < A.T; m += (int64_t)gridDim.x * 64) {
+    const int64_t src = source_of(A, m);
+    for (int g = blockIdx.y; g < nG; g += gridDim.y) {
+      u32x4 in[2] = {};
+      if (src >= 0) {
+        const u32x4 *from = (const u32x4 *)(A.q + src * A.K + 128 * g + 32 * j);
+        in[0] = from[0];
+        in[1] = from[1];
+      }
+      uint32_t hi[6], lo[6], h24[4], l24[4];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x = in[half][i], sign = x & 0x80808080u, one = sign >> 7;
+          const uint32_t mag = (x ^ ((one << 8) - one)) + one;  // by bytes: 0 .. 128
+          const uint32_t top = mag >> 7 & 0x01010101u;          // of 128
+          const uint32_t l = (mag & 0x0F0F0F0Fu) + (top << 4), h = (mag >> 4 & 0x0F0F0F0Fu) - top;
+          // 2 h, h = 0 .. 7: the formats' bits, bytes chosen by h
+          const uint32_t code = __builtin_amdgcn_perm(0x1B1A1918u, 0x16141000u, h);
+          h24[i] = six_bits(code | sign >> 2);
+          l24[i] = six_bits(l | sign >> 2);
+        }
+#pragma unroll
+        for (int w = 0; w < 3; ++w) {
+          hi[3 * half + w] = h24[w] >> (8 * w) | h24[w + 1] << (24 - 8 * w);
+          lo[3 * half + w] = l24[w] >> (8 * w) | l24[w + 1] << (24 - 8 * w);
+        }
+      }
+      u32x4 *to = (u32x4 *)(A.parts + ((int64_t)g * A.T + m) * kPartBytes) + (j ^ (int)(m >> 2 & 3));
+      to[0] = u32x4{hi[0], hi[1], hi[2], hi[3]};
+      to[4] = u32x4{lo[0], lo[1], lo[2], lo[3]};
+      to[8] = j & 1 ? u32x4{lo[4], lo[5], hi[4], hi[5]} : u32x4{hi[4], hi[5], lo[4], lo[5]};
+    }
+  }
+}
+
+constexpr uint32_t kBadNibbles = 0x80000000u;
+
+// 256 entries of a dword, COPIES times: a byte's five codes in four bits each,
+// and the mark of invalid bytes.
+template <uint32_t COPIES>
+struct Nibbles {
+  static constexpr uint32_t kStride = 4 * COPIES, kBytes = 256 * kStride;
+  uint32_t at;
+
+  __device__ __forceinline__ Nibbles(uint32_t base, int lane) : at(base + 4u * ((uint32_t)lane & (COPIES - 1u))) {}
+
+  __device__ static __forceinline__ void build(lds_bytes *table, int tid, int threads) {
+    for (uint32_t e = (uint32_t)tid; e < 256u; e += (uint32_t)threads) {
+      uint32_t codes = 0, v = e;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        codes |= (0x20Au >> (4 * (v % 3u)) & 0xFu) << (4 * i);  // -1, 0, 1
+        v /= 3u;
+      }
+      const uint32_t w = e >= 243u ? kBadNibbles : codes;
+#pragma unroll
+      for (uint32_t k = 0; k < COPIES / 4; ++k)
+        *(lds_u32x4 *)(table + e * kStride + 16u * ((k + e) % (COPIES / 4))) = u32x4{w, w, w, w};
+    }
+  }
+
+  __device__ __forceinline__ uint32_t read(lds_bytes *smem, uint32_t word, int i) const {
+    return *(lds_u32_c *)(smem + (((word >> (8 * i)) & 0xFFu) * kStride + at));
+  }
+};
+
+struct Part {  // a lane's 32 numbers of six bits
+  u32x4 a;
+  u32x2 b;
+};
+
+// FORMAT of the part: 3 (2 h), 2 (l / 8)
+template <int FORMAT>
+__device__ __forceinline__ f32x4 mfma_parts(const Part &x, u32x4 codes, f32x4 c) {
+  typedef int i32x8 __attribute__((ext_vector_type(8)));
+  const i32x8 w{(int)codes.x, (int)codes.y, (int)codes.z, (int)codes.w, 0, 0, 0, 0};
+  const i32x8 v{(int)x.a.x, (int)x.a.y, (int)x.a.z, (int)x.a.w, (int)x.b.x, (int)x.b.y, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, w, c, FORMAT, 4, 0, 0, 0, 0);
+}
+
+// As tile_kernel, from the parts of q, a stage a group.
+template <int P, int Q, int COPIES>
+__global__ __launch_bounds__(2 * P) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void part_kernel(const I8Args A) {
+  typedef Nibbles<COPIES> L;
+  constexpr int NT = 2 * P, TP = P / 16, TQ = Q / (NT / 64) / 16, B = bytes_per_group(128);
+  constexpr uint32_t kPSlot = P * 64, kQSlot = Q * kPartBytes, kSSlot = P * 4;
+  constexpr uint32_t kSOff = 2 * kPSlot, kQOff = kSOff + 2 * kSSlot, kLutOff = kQOff + 2 * kQSlot;
+  constexpr uint32_t kRoom = kLutOff + L::kBytes;
+  constexpr int kLoads = kQSlot / 16 / NT, kStep = 2;  // rows of matrix tiles between pieces of the codes
+  static_assert(P % 64 == 0 && TP % 4 == 0 && 5 * kStep < TP && 4 * TQ <= TP && kQSlot % (16 * NT) == 0 && Q <= kPartPad, "");
+  static_assert(finish_room<P, Q, 1>() <= kLutOff && kRoom <= 160 << 10, "");
+  __shared__ __align__(16) unsigned char smem_raw[kRoom];
+  lds_bytes *smem = (lds_bytes *)smem_raw;
+  const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int S = A.K / 128;
+  const L lut(kLutOff, lane);
+  const int units = count_units(A, Q);
+  if (A.offsets && blockIdx.x == 0 && A.status)
+    for (int e = tid; e < A.E; e += NT)
+      if (A.offsets[e] < 0 || A.offsets[e + 1] < A.offsets[e] || A.offsets[e + 1] > A.T)
+        atomicOr(A.status, kDevBadSegment);
+  uint32_t flags = 0;
+  const int tiles = units * A.tp, total = tiles * A.splits;
+  for (int work = (int)blockIdx.x; work < total; work += (int)gridDim.x) {
+    auto scalar = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    const int split = A.splits == 1 ? 0 : scalar((int)((uint32_t)work / (uint32_t)tiles)), t = work - split * tiles;
+    const int unit = scalar((int)((uint32_t)t / (uint32_t)A.tp)), ip = t - unit * A.tp;
+    const Segment seg = find_unit(A, Q, unit);
+    if (seg.e < 0) break;
+    const int s0 = A.splits == 1 ? 0 : scalar(S * split / A.splits);
+    const int S1 = A.splits == 1 ? S : scalar(S * (split + 1) / A.splits) - s0;
+    const int n0 = ip * P, m0 = seg.a + seg.unit * Q, M = min(seg.b - m0, Q);
+
+    // the stage's rows, those behind the tile's last too (the next group's or the
+    // pad: all bits are numbers, and their results go nowhere)
+    const uint8_t *qbase = A.parts + ((int64_t)s0 * A.T + m0) * kPartBytes;
+    const int64_t qstep = A.T * kPartBytes;
+    auto request = [&](const uint8_t *from, uint32_t slot, int i) __attribute__((always_inline)) {
+      dma16_from(from + i * (16 * NT), 16u * (uint32_t)tid, smem + kQOff + slot + 16u * (uint32_t)(i * NT + 64 * wv));
+    };
+    // past the end the last stage again, unused
+    auto stage_of = [&](int s) __attribute__((always_inline)) { return qbase + qstep * min(s, S1 - 1); };
+
+    // codes: this thread's are 64 hf .. 64 hf + 63 of row dr, in bytes 0 .. 12 or
+    // 12 .. 25 of the group; hf is a wave's
+    const int hf = wv / (NT / 128), dr = tid % P;
+    const int64_t first = ((int64_t)seg.e * A.N + n0) * S + s0;
+    const uint32_t row = (uint32_t)min(dr, A.N - 1 - n0) * (uint32_t)S;  // rows past N read row N - 1
+    const uint32_t boff = known_here(row * B + (hf ? 10u : 0u));
+    // the second thread of a row has no use for the scale and puts it where the
+    // first does (a branch in the loop costs more)
+    const uint32_t voff = known_here(2u * row);
+    u32x4 raw;
+    uint32_t scale;
+    auto load_raw = [&](int s) __attribute__((always_inline)) {
+      s = min(s, S1 - 1);
+      // the scale first: whoever has waited for the bytes has both
+      scale = *(const uint16_t *)((const uint8_t *)(A.scales + first + s) + voff);
+      __builtin_memcpy(&raw, A.packed + (first + s) * B + boff, 16);
+    };
+    auto align_raw = [&]() __attribute__((always_inline)) {  // bytes 12 .. 25 to where 0 .. 13 are
+      const uint32_t by = hf ? 2u : 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) raw[i] = known_here(raw[i]);  // not waited for earlier
+#pragma unroll
+      for (int i = 0; i < 3; ++i) raw[i] = __builtin_amdgcn_alignbyte(raw[i + 1], raw[i], by);
+      raw[3] = __builtin_amdgcn_alignbyte(0u, raw[3], by);
+    };
+    uint32_t e[4];  // entries of a piece
+    uint32_t w[9];  // all codes, 20 bits a byte
+    auto look = [&](auto pc) __attribute__((always_inline)) {
+      constexpr int I = 4 * decltype(pc)::value;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (I + k < 14) e[k] = lut.read(smem, raw[(I + k) >> 2], (I + k) & 3);
+    };
+    uint32_t put = known_here(64u * (uint32_t)dr + 16u * ((2u * (uint32_t)hf) ^ ((uint32_t)dr >> 2 & 3u)));
+    uint32_t sput = known_here(kSOff + 4u * (uint32_t)dr);
+    auto store = [&](int c) __attribute__((always_inline)) {  // 32 codes
+      u32x4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = __builtin_amdgcn_alignbit(w[4 * c + i + 1], w[4 * c + i], 16 * hf);
+      *(lds_u32x4 *)(smem + (put ^ 16u * (uint32_t)c)) = v;
+    };
+    // entries 4 p .. of the bytes, and 32 codes once all of theirs are there
+    auto piece = [&](auto pc) __attribute__((always_inline)) {
+      constexpr int p = decltype(pc)::value, W = 5 * (p / 2);
+      flags |= p < 3 ? e[0] | e[1] | e[2] | e[3] : e[0] | e[1];
+      if constexpr (p == 0 || p == 2) {  // (the mark is in none of the bits taken)
+        w[W] = (e[0] & 0xFFFFFu) | e[1] << 20;
+        w[W + 1] = (e[1] >> 12 & 0xFFu) | e[2] << 8 | e[3] << 28;
+        w[W + 2] = e[3] >> 4 & 0xFFFFu;
+      } else {
+        w[W + 2] |= e[0] << 16;
+        w[W + 3] = (e[0] >> 16 & 0xFu) | e[1] << 4;
+        if constexpr (p == 1) {
+          w[W + 3] |= e[2] << 24;
+          w[W + 4] = (e[2] >> 8 & 0xFFFu) | e[3] << 12;
+        }
+      }
+      settle(flags);
+      if constexpr (p == 1) {
+        // the first 32 end in the fifth dword
+        store(0);
+      }
+      if constexpr (p == 3) store(1);
+    };
+    auto store_scale = [&](int s) __attribute__((always_inline)) {
+      *(lds_float *)(smem + sput) = s < S1 ? 8.f * f16_value(scale) : 0.f;  // sums are eighths
+    };
+
+    f32x4 acc[TP][TQ];
+#pragma unroll
+    for (int a = 0; a < TP; ++a)
+#pragma unroll
+      for (int b = 0; b < TQ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (work != (int)blockIdx.x) __syncthreads();  // the tile before is done with LDS
+    load_raw(0);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) request(stage_of(0), 0, i);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) request(stage_of(1), kQSlot, i);
+    if (work == (int)blockIdx.x) {  // the table, while those are on their way
+      L::build(smem + kLutOff, tid, NT);
+      __syncthreads();
+    }
+    align_raw();
+    look(Int<0>{}), piece(Int<0>{}), look(Int<1>{}), piece(Int<1>{});
+    look(Int<2>{}), piece(Int<2>{}), look(Int<3>{}), piece(Int<3>{});
+    store_scale(0);
+    put ^= kPSlot;
+    sput ^= kSSlot;
+    load_raw(1);
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+    // operand reads: all weight rows, and this wave's of q
+    const uint32_t qr = (uint32_t)(wv * (16 * TQ) + l);
+    uint32_t pat = 64u * (uint32_t)l + 16u * ((uint32_t)q ^ ((uint32_t)l >> 2 & 3u));
+    const uint32_t qat = kQOff + kPartBytes * qr + 16u * ((uint32_t)q ^ (((uint32_t)m0 + qr) >> 2 & 3u));
+    const uint32_t qrest[2] = {qat + 128u + 8u * (uint32_t)(q & 1), qat + 128u + 8u * (uint32_t)(~q & 1)};
+    uint32_t sat = kSOff + 4u * (uint32_t)l;
+    static_assert(kPSlot % 1024 == 0 && kSOff % (2 * kSSlot) == 0, "a slot's bit");
+    Part qf[2][2][TQ];  // of a stage and the next
+    u32x4 pf[2];
+    float sc[2];
+    f32x4 sum[2][TQ];
+    auto read_q = [&](int slot, int h, int b) __attribute__((always_inline)) {
+      const uint32_t on = (uint32_t)slot * kQSlot + 16u * kPartBytes * (uint32_t)b;
+      qf[slot][h][b].a = *(lds_u32x4_c *)(smem + qat + 64u * (uint32_t)h + on);
+      qf[slot][h][b].b = *(lds_u32x2_c *)(smem + qrest[h] + on);
+    };
+    auto read_p = [&](int a) __attribute__((always_inline)) {
+      pf[a & 1] = *(lds_u32x4_c *)(smem + pat + 1024u * (uint32_t)a);
+      sc[a & 1] = *(lds_float *)(smem + sat + 64u * (uint32_t)a);
+    };
+    auto add = [&](int a) __attribute__((always_inline)) {
+#pragma unroll
+      for (int b = 0; b < TQ; ++b)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[a][b][r] = fmaf(sc[a & 1], sum[a & 1][b][r], acc[a][b][r]);
+    };
+#pragma unroll
+    for (int b = 0; b < TQ; ++b) read_q(0, 0, b), read_q(0, 1, b);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // q of stage 0 has left its slot
+    read_p(0);
+    auto stage = [&](auto slot_c, int s) __attribute__((always_inline)) {
+      constexpr int slot = decltype(slot_c)::value;
+      const uint8_t *from = stage_of(s + 2);
+#pragma unroll
+      for (int a = 0; a < TP; ++a) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int b = 0; b < TQ; ++b) sum[a & 1][b] = mfma_parts<3>(qf[slot][0][b], pf[a & 1], f32x4{0.f, 0.f, 0.f, 0.f});
+        __builtin_amdgcn_sched_barrier(0);
+        if (a > 0) add(a - 1);
+        if (a + 1 < TP) read_p(a + 1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int b = 0; b < TQ; ++b) sum[a & 1][b] = mfma_parts<2>(qf[slot][1][b], pf[a & 1], sum[a & 1][b]);
+        __builtin_amdgcn_sched_barrier(0);
+        // q of the next stage, which landed before this one began
+        if (a % 2 == 1 && a / 2 < 2 * TQ) read_q(1 - slot, a / 2 & 1, a / 4);
+        if (a == 0) align_raw();
+        if (a == 0)
+#pragma unroll
+          for (int i = 0; i < kLoads; ++i) request(from, slot * kQSlot, i);
+        if (a == kStep) look(Int<0>{});
+        if (a == 2 * kStep) piece(Int<0>{}), look(Int<1>{});
+        if (a == 3 * kStep) piece(Int<1>{}), look(Int<2>{});
+        if (a == 4 * kStep) {
+          piece(Int<2>{}), look(Int<3>{});
+          store_scale(s + 1);
+          load_raw(s + 2);
+        }
+        if (a == 5 * kStep) piece(Int<3>{});
+      }
+      pat ^= kPSlot;
+      put ^= kPSlot;
+      sat ^= kSSlot;
+      sput ^= kSSlot;
+      __builtin_amdgcn_sched_barrier(0);
+      // q of s + 2 has landed: only the bytes and the scale of s + 2, requested
+      // behind it, may still be on their way
+      asm volatile("s_waitcnt vmcnt(2) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      pf[0] = *(lds_u32x4_c *)(smem + pat);
+      const float next = *(lds_float *)(smem + sat);
+      add(TP - 1);
+      sc[0] = next;
+    };
+    // of an odd number the last stage has scales of 0
+    for (int s = 0; s < S1; s += 2) {
+      stage(Int<0>{}, s);
+      stage(Int<1>{}, s + 1);
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // nothing is on its way into LDS
+
+    finish_tile<P, Q, 1>(A, acc, smem, wv, Tile{seg.e, n0, m0, M, ip, split});
+  }
+  if ((flags & kBadNibbles) && A.status) atomicOr(A.status, kDevInvalidByte);
 }
 
 // ---------------------------------------------------------------------------
@@ -1015,6 +1384,7 @@ constexpr int kFew = 0, kTile = 1;
 
 struct Plan {
   int kind, mb, copies, wk, wt, splits, bpu, p, q;
+  bool parts;  // tile: q in parts
   int64_t units, blocks;
 };
 
@@ -1025,36 +1395,41 @@ uint32_t few_room(int mb, int copies) {
 
 // tile_kernel's tiles and what they take, in us: a tile before and behind its
 // stages, and a stage where it is alone on a CU and where all `places` are taken.
-// (Measured with G = 128; a stage with G = 64 takes a fourth more of all.)
+// (Measured with G = 128, the largest of part_kernel; a stage with G = 64 takes a
+// fourth more of all.)
 struct Shape {
   int p, q, places;
   double start, alone, full;
 };
-constexpr Shape kShapes[] = {{128, 64, 512, 6.4, 0.82, 1.10}, {128, 128, 512, 8.5, 1.05, 1.56}, {256, 256, 256, 15, 2.25, 2.25}};
+constexpr Shape kShapes[] = {{128, 64, 512, 6.4, 0.82, 1.10}, {128, 128, 512, 8.5, 1.05, 1.56}, {256, 256, 256, 13, 2.2, 2.2}};
 
 // Of the shapes and the splits of K the cheapest.  Splits keep two stages, and
-// their sums are written, read and joined in a launch more.
-void plan_tiles(Plan &p, int64_t T, int64_t N, int64_t K, int64_t used, bool grouped) {
+// their sums are written, read and joined in a launch more; so are q's parts.
+void plan_tiles(Plan &p, int64_t T, int64_t N, int64_t K, int G, int64_t used, bool grouped) {
   const int64_t stages = ceil_div(K, 128);
   double least = 1e30;
   for (const Shape &c : kShapes) {
     // units of an expert: on average its last is half full
     const int64_t units = grouped ? std::max(used, T / c.q + used / 2) : ceil_div(T, c.q);
     const int64_t tiles = units * ceil_div(N, c.p);
-    for (int s = 1; s <= 16 && (s == 1 || stages / s >= 2); ++s) {
+    for (int s = 1; s <= 16 && (s == 1 || (stages / s >= 2 && tiles * s < 1 << 24)); ++s) {
       const int64_t rounds = tiles * s / c.places, rest = tiles * s - rounds * c.places;
       const double last = rest ? c.alone + (c.full - c.alone) * std::max<double>(0, 2.0 * rest / c.places - 1) : 0;
       const double cost = c.start * (rounds + (rest > 0)) + ceil_div(stages, s) * (rounds * c.full + last) +
-                          (s > 1 ? 4.5 + (double)s * T * N * 8 / 5.2e6 : 0);
+                          (s > 1 ? 4.5 + (double)s * T * N * 8 / 5.2e6 : 0) +
+                          (c.p == 256 && G == 128 ? 4 + (double)T * K * 2.5 / 5.2e6 : 0);
       if (cost < least) least = cost, p.p = c.p, p.q = c.q, p.splits = s;
     }
   }
   p.kind = kTile;
+  // 2048 rows of [14336,4096] 160 us, 170 with 8-bit matrix instructions; 333 rows
+  // of [1024,3584], in small tiles, 26 and 21
+  p.parts = G == 128 && p.p == 256;
   p.units = grouped ? T / p.q + used : ceil_div(T, p.q);
   p.blocks = std::min<int64_t>(ceil_div(N, p.p) * p.units * p.splits, 1 << 20);
 }
 
-Plan plan_of(int64_t T, int64_t N, int64_t K, int64_t E, bool grouped) {
+Plan plan_of(int64_t T, int64_t N, int64_t K, int G, int64_t E, bool grouped) {
   Plan p{};
   const int64_t used = grouped ? std::min(E, T) : 1;  // experts that have rows, at most
   const int64_t mean = ceil_div(T, std::max<int64_t>(used, 1));
@@ -1063,7 +1438,7 @@ Plan plan_of(int64_t T, int64_t N, int64_t K, int64_t E, bool grouped) {
   // rows on average: [4096,4096] 41 and 46, [3584,1024] 15 and 17; of 16: 53 and
   // 44, 25 and 18.
   if (mean > (grouped ? 8 : 16)) {
-    plan_tiles(p, T, N, K, used, grouped);
+    plan_tiles(p, T, N, K, G, used, grouped);
     return p;
   }
   p.kind = kFew;
@@ -1094,6 +1469,9 @@ Plan plan_of(int64_t T, int64_t N, int64_t K, int64_t E, bool grouped) {
   const int64_t sets = ceil_div(tiles, p.wt), blocks = p.mb == 4 ? 256 : 1024;
   p.bpu = (int)std::max<int64_t>(1, std::min<int64_t>(sets, blocks / std::max<int64_t>(1, used * p.splits)));
   p.blocks = p.units * p.bpu * p.splits;
+  // (many experts of rows so long that q's take many splits: more blocks than a
+  // launch has; tiles go round)
+  if (p.blocks >= int64_t(1) << 22) plan_tiles(p, T, N, K, G, used, grouped);
   return p;
 }
 
@@ -1113,8 +1491,13 @@ void launch(const Plan &p, const I8Args &a, hipStream_t stream) {
       case 2: go(few_kernel<G, 2, 8>, few_kernel<G, 2, 32>); break;
       default: go(few_kernel<G, 4, 8>, few_kernel<G, 4, 32>); break;
     }
+  } else if (p.parts) {
+    const int64_t rows = ceil_div(a.T, 64), groups = a.K / 128;
+    const unsigned y = (unsigned)std::min<int64_t>(groups, 1024);
+    hipLaunchKernelGGL(parts_kernel, dim3((unsigned)std::min<int64_t>(rows, 64), y), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((part_kernel<256, 256, 16>), grid, dim3(512), 0, stream, a);
   } else if (p.p == 256) {
-    hipLaunchKernelGGL((tile_kernel<G, 256, 256, 2, 8>), grid, dim3(512), 0, stream, a);
+    if constexpr (G == 64) hipLaunchKernelGGL((tile_kernel<64, 256, 256, 2, 8>), grid, dim3(512), 0, stream, a);
   } else if (p.q == 128) {
     hipLaunchKernelGGL((tile_kernel<G, 128, 128, 2, 4>), grid, dim3(256), 0, stream, a);
   } else {
@@ -1127,16 +1510,28 @@ void launch(const Plan &p, const I8Args &a, hipStream_t stream) {
 
 }  // namespace
 
-int64_t gemm_i8_workspace(int64_t T, int64_t N, int64_t K, int64_t E, bool grouped) {
-  const Plan p = plan_of(T, N, K, E, grouped);
-  return p.splits > 1 ? (p.splits * T * N * 4 + 15) / 16 * 16 : 0;
+void i8_plan(int64_t T, int64_t N, int64_t K, int G, int64_t E, int64_t *plan) {
+  const Plan p = plan_of(T, N, K, G, E ? E : 1, E > 0);
+  const bool few = p.kind == kFew;
+  plan[0] = few ? 0 : p.parts ? 2 : 1;
+  plan[1] = p.splits;
+  plan[2] = few ? 4 * p.mb : p.p;
+  plan[3] = few ? p.copies : p.q;
+  plan[4] = few ? p.wk : 0;
+  plan[5] = few ? p.wt : 0;
+  plan[6] = few ? p.bpu : 0;
+}
+
+int64_t gemm_i8_workspace(int64_t T, int64_t N, int64_t K, int G, int64_t E, bool grouped) {
+  const Plan p = plan_of(T, N, K, G, E, grouped);
+  return (p.parts ? part_bytes(T, K) : 0) + (p.splits > 1 ? (p.splits * T * N * 4 + 15) / 16 * 16 : 0);
 }
 
 void launch_gemm_i8(const int8_t *q, const float *qs, const uint8_t *packed, const uint16_t *scales,
                     const int32_t *offsets, int64_t E, const int32_t *rows, int64_t sources, const void *bias,
                     bool bias32, int act, const void *residual, int64_t T, int64_t N, int64_t K, int G, void *out,
                     bool out32, void *workspace, int32_t *status, hipStream_t stream) {
-  const Plan p = plan_of(T, N, K, E, offsets != nullptr);
+  const Plan p = plan_of(T, N, K, G, E, offsets != nullptr);
   I8Args a{};
   a.q = q;
   a.qs = qs;
@@ -1157,13 +1552,13 @@ void launch_gemm_i8(const int8_t *q, const float *qs, const uint8_t *packed, con
   auto at16 = [](const void *v) { return (uintptr_t)v % 16 == 0; };
   a.vec = N % 8 == 0 && at16(out) && at16(residual);
   a.act = act;
-  a.partial = (float *)workspace;
+  a.parts = (uint8_t *)workspace;
+  a.partial = (float *)(a.parts + (p.parts ? part_bytes(T, K) : 0));
   a.splits = p.splits;
   a.wk = p.wk;
   a.wt = p.wt;
   a.bpu = p.bpu;
   a.tp = p.kind == kTile ? (int)ceil_div(N, p.p) : 0;
-  a.units = p.units;
   a.status = status;
   if (G == 64)
     launch<64>(p, a, stream);

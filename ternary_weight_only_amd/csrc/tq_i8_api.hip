@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/tq.h"
+#include "../../include/tq_probe.h"
 #include "tq_internal.h"
 
 namespace {
@@ -16,6 +17,7 @@ constexpr int64_t kMaxK = int64_t(1) << 21;
 constexpr int64_t kMaxRows = int64_t(1) << 30;
 constexpr int64_t kMaxElems = int64_t(1) << 40;  // every byte count stays below 2^62
 constexpr int64_t kMaxExperts = 65536;
+constexpr int64_t kMaxGather = int64_t(1) << 32;  // bytes of x, read by 32-bit offsets where rows are given by index
 
 bool product_ok(int64_t a, int64_t b) { return a == 0 || b <= kMaxElems / a; }
 
@@ -73,6 +75,7 @@ int product(const int8_t *x, const float *x_scales, int64_t sources, const int32
   int rc = check_product(T, N, K, G, experts);
   if (rc) return rc;
   if (sources < 0 || sources > kMaxRows || !product_ok(sources, K) || (!rows && sources < T)) return TQ_ERR_SHAPE;
+  if (rows && sources * K > kMaxGather) return TQ_ERR_SHAPE;
   if (act != TQ_ACT_SILU && act != TQ_ACT_GELU && act != TQ_ACT_NONE && act != TQ_ACT_RELU2) return TQ_ERR_ACT;
   if (!type_ok(out_type) || (bias && !type_ok(bias_type))) return TQ_ERR_TYPE;
   if (T == 0) return TQ_OK;
@@ -82,7 +85,7 @@ int product(const int8_t *x, const float *x_scales, int64_t sources, const int32
       !aligned(rows, 4) || (bias && !aligned(bias, size_of(bias_type))) || !aligned(out, size_of(out_type)) ||
       !aligned(residual, size_of(out_type)) || !aligned(d_status, 4))
     return TQ_ERR_ALIGN;
-  rc = check_workspace(workspace, workspace_bytes, tq::gemm_i8_workspace(T, N, K, experts, grouped));
+  rc = check_workspace(workspace, workspace_bytes, tq::gemm_i8_workspace(T, N, K, G, experts, grouped));
   if (rc) return rc;
   (void)hipGetLastError();
   tq::launch_gemm_i8(x, x_scales, packed, scales, offsets, experts, rows, sources, bias, bias_type == TQ_F32, act,
@@ -146,7 +149,7 @@ int tq_rms_norm_backward(const uint16_t *dh, const void *y, int y_type, const fl
 }
 
 int64_t tq_gemm_i8_workspace(int64_t M, int64_t N, int64_t K, int G) {
-  return check_product(M, N, K, G, 1) || M == 0 ? 0 : tq::gemm_i8_workspace(M, N, K, 1, false);
+  return check_product(M, N, K, G, 1) || M == 0 ? 0 : tq::gemm_i8_workspace(M, N, K, G, 1, false);
 }
 
 int tq_gemm_i8(const int8_t *x, const float *x_scales, const uint8_t *packed, const uint16_t *scales,
@@ -158,7 +161,7 @@ int tq_gemm_i8(const int8_t *x, const float *x_scales, const uint8_t *packed, co
 }
 
 int64_t tq_expert_gemm_i8_workspace(int64_t T, int64_t N, int64_t K, int G, int64_t experts) {
-  return check_product(T, N, K, G, experts) || T == 0 ? 0 : tq::gemm_i8_workspace(T, N, K, experts, true);
+  return check_product(T, N, K, G, experts) || T == 0 ? 0 : tq::gemm_i8_workspace(T, N, K, G, experts, true);
 }
 
 int tq_expert_gemm_i8(const int8_t *x, const float *x_scales, int64_t sources, const int32_t *rows,
@@ -168,6 +171,15 @@ int tq_expert_gemm_i8(const int8_t *x, const float *x_scales, int64_t sources, c
                       int32_t *d_status, void *stream) {
   return product(x, x_scales, sources, rows, packed, scales, offsets, true, experts, bias, bias_type, act, residual,
                  T, N, K, G, out, out_type, workspace, workspace_bytes, d_status, stream);
+}
+
+int tq_probe_i8_plan(int64_t M, int64_t N, int64_t K, int G, int64_t experts, int64_t *plan) {
+  const int rc = check_product(M, N, K, G, experts ? experts : 1);
+  if (rc) return rc;
+  if (M < 1) return TQ_ERR_SHAPE;
+  if (!plan) return TQ_ERR_NULL;
+  tq::i8_plan(M, N, K, G, experts, plan);
+  return TQ_OK;
 }
 
 }  // extern "C"

@@ -196,7 +196,8 @@ void launch_rms_norm_backward(const uint16_t *dh, const void *y, bool y32, const
 
 // 8-bit rows times packed ternary weights (tq_i8.hip); offsets null: one
 // matrix (E = 1), else grouped by expert.
-int64_t gemm_i8_workspace(int64_t T, int64_t N, int64_t K, int64_t E, bool grouped);
+void i8_plan(int64_t T, int64_t N, int64_t K, int G, int64_t E, int64_t *plan);
+int64_t gemm_i8_workspace(int64_t T, int64_t N, int64_t K, int G, int64_t E, bool grouped);
 void launch_gemm_i8(const int8_t *q, const float *qs, const uint8_t *packed,
                     const uint16_t *scales, const int32_t *offsets, int64_t E, const int32_t *rows,
                     int64_t sources, const void *bias, bool bias32, int act, const void *residual,

@@ -86,3 +86,23 @@ def within(got, want, bound, what):
     assert not bad.any(), "%s: %d of %d off; first at %s: %r, not %r, bound %.3g" % (
         what, int(bad.sum()), bad.numel(), bad.nonzero()[0].tolist(), got.cpu()[bad][0].item(),
         want[bad][0].item(), (bound if torch.is_tensor(bound) else torch.full_like(want, bound))[bad][0].item())
+
+
+# (rows, N, K, G, experts or 0): together they reach every kernel of the products,
+# with and without splits of K (tests/test_i8_plans.py sees to it)
+MIDDLE = [(3, 40, 192, 64, 0), (2, 9000, 4096, 64, 0), (4, 3000, 2048, 64, 0), (7, 40, 128, 64, 0), (6, 80, 14336, 64, 0), (14, 70, 448, 64, 0),
+          (15, 300, 4032, 64, 0), (2, 33, 384, 128, 0), (1, 2000, 8192, 128, 0), (8, 50, 640, 128, 0),
+          (5, 17, 7168, 128, 0), (13, 200, 1024, 128, 0), (16, 130, 5760, 128, 0), (30, 77, 192, 64, 0),
+          (40, 140, 1088, 64, 0), (50, 260, 128, 128, 0), (65, 130, 2176, 128, 0), (20, 48, 320, 64, 9),
+          (40, 600, 2048, 64, 16), (9, 40, 256, 128, 3), (64, 1000, 2048, 128, 16), (70, 90, 640, 128, 3)]
+LARGE = [(771, 5000, 64, 64, 0), (986, 2600, 192, 64, 20), (2286, 513, 4224, 64, 0), (1608, 513, 5504, 64, 20),
+         (3113, 2600, 64, 64, 0), (2694, 2600, 320, 64, 20), (1677, 5000, 3520, 64, 1),
+         (778, 5000, 128, 128, 0), (976, 2600, 384, 128, 20), (1350, 1024, 4992, 128, 0), (963, 1500, 4224, 128, 1),
+         (3099, 2600, 128, 128, 0), (3113, 2597, 384, 128, 0), (2628, 2600, 1024, 128, 20),
+         (3093, 2600, 9600, 128, 0), (1721, 5000, 3840, 128, 1)]
+
+
+def segments(rng, E, T):
+    """Uneven segments, some empty, with rows of none before and behind."""
+    cuts = np.sort(rng.integers(T // 20, T - T // 20 + 1, E + 1)) if E > 1 else np.array([T // 50, T - T // 70])
+    return cuts.astype(np.int32)

@@ -61,8 +61,15 @@ def test_shapes():
         for G in (0, 32, 96, 256, -64):
             assert _call(fn, spec, G=G) == GROUP
     for bad in (dict(E=0), dict(E=-1), dict(E=65537), dict(E=65536, N=1 << 20), dict(sources=-1),
-                dict(sources=0), dict(rows=None, sources=299)):
+                dict(sources=0), dict(rows=None, sources=299), dict(sources=(1 << 24) + 1)):
         assert _call("tq_expert_gemm_i8", EXPERT, **bad) == SHAPE, bad
+
+
+def test_rows_by_index_reach_32_bits():
+    """Offsets into x have 32 bits where rows are given, and only there."""
+    assert _call("tq_expert_gemm_i8", EXPERT, sources=(1 << 24) + 1, rows=FAKE) == SHAPE
+    assert _call("tq_expert_gemm_i8", EXPERT, sources=1 << 24, x=None) == NULL
+    assert _call("tq_expert_gemm_i8", EXPERT, sources=(1 << 24) + 1, rows=None, x=None) == NULL
 
 
 def test_types_and_numbers():
