@@ -662,13 +662,36 @@ __host__ __device__ constexpr uint32_t finish_room() {
   return P / 32 * finish_once<P, Q, WP>() * 16 * (P / WP) * 4;
 }
 
+// What a tile's end needs, the scales of its rows of q and the bias of its weight
+// rows, on their way since its beginning: a value a thread.
+template <int P, int Q>
+__device__ __forceinline__ float end_value(const I8Args &A, const Tile t, int tid) {
+  static_assert(Q <= P, "");
+  float v = 0.f;
+  if (tid >= P) {
+    if (A.bias && t.n0 + tid - P < A.N) v = bias_of(A, t.e, t.n0 + tid - P);
+  } else if (tid < min(Q, t.M)) {
+    const int64_t src = source_of(A, t.m0 + tid);
+    if (src >= 0)
+      v = A.qs[src];
+    else if (t.ip == 0 && t.split == 0 && A.status)
+      atomicOr(A.status, kDevBadRow);
+  }
+  return v;
+}
+
+template <int P, int Q>
+__device__ __forceinline__ void put_end(lds_bytes *ends, int tid, float v) {
+  if (tid < Q || tid >= P) *(lds_float *)(ends + 4u * (uint32_t)(tid < Q ? tid : tid - P + Q)) = v;
+}
+
 // Results go through this wave's part of LDS, kOnce tiles of 16 rows of q at
 // a time, [row][weight row], and leave in runs of a wave's weight rows; chunk
 // c of a row sits at c ^ row % 16.  (Loops that stay loops: unrolled, the
 // epilogue was most of the kernel's code and its fetching took 10 us.)
 template <int P, int Q, int WP>
 __device__ __forceinline__ void finish_tile(const I8Args &A, f32x4 (&acc)[P / WP / 16][Q / (P / 32 / WP) / 16],
-                                            lds_bytes *smem, int wv, const Tile t) {
+                                            lds_bytes *smem, uint32_t ends_off, int wv, const Tile t) {
   constexpr int WQ = P / 32 / WP, TP = P / WP / 16, TQ = Q / WQ / 16;
   const int wp = wv / WQ, wq = wv % WQ;
   constexpr int W = P / WP, kOnce = finish_once<P, Q, WP>(), kLanes = W / 8, kEach = 64 / kLanes;  // lanes of a row, rows at once
@@ -680,19 +703,12 @@ __device__ __forceinline__ void finish_tile(const I8Args &A, f32x4 (&acc)[P / WP
   const int nw = t.n0 + wp * W + 8 * (lane % kLanes);
   // a lane's row's scale (handed over below), and its columns' bias
   static_assert(Q / WQ <= 64, "a row a lane");
-  float own = 0.f;
-  if (lane < Q / WQ && wq * (Q / WQ) + lane < t.M) {
-    const int64_t src = source_of(A, t.m0 + wq * (Q / WQ) + lane);
-    if (src >= 0)
-      own = A.qs[src];
-    else if (t.ip == 0 && t.split == 0 && A.status)
-      atomicOr(A.status, kDevBadRow);
-  }
-  float bias[8] = {};
-  if (A.bias)
+  lds_bytes *ends = smem + ends_off;
+  const float own = *(lds_float *)(ends + 4u * (uint32_t)(wq * (Q / WQ) + min(lane, Q / WQ - 1)));
+  float bias[8];
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      if (nw + c < A.N) bias[c] = bias_of(A, t.e, nw + c);
+  for (int c = 0; c < 8; ++c)
+    bias[c] = *(lds_float *)(ends + 4u * (uint32_t)(Q + wp * W + 8 * (lane % kLanes) + c));
   const Result result(A);
   const int64_t mw = t.m0 + wq * (Q / WQ);
   float *sums = A.splits > 1 ? A.partial + ((int64_t)t.split * A.T + mw) * A.N + nw : nullptr;
@@ -782,13 +798,13 @@ void tile_kernel(const I8Args A) {
   constexpr uint32_t kQOff = 2 * kPSlot, kSOff = kQOff + 2 * kQSlot, kLutOff = kSOff + 2 * kSSlot;
   constexpr int kLoads = Q * 8 / NT;
   static_assert(P % 64 == 0 && TP >= 4 && finish_room<P, Q, WP>() <= kSOff, "");
-  __shared__ __align__(16) unsigned char smem_raw[kLutOff + L::kBytes];
+  constexpr uint32_t kEndOff = kLutOff + L::kBytes;
+  __shared__ __align__(16) unsigned char smem_raw[kEndOff + 4 * (P + Q)];
   lds_bytes *smem = (lds_bytes *)smem_raw;
   const int tid = threadIdx.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), wp = wv / WQ, wq = wv % WQ;
   const int nG = A.K / G, S = (A.K + 127) / 128;
   const L lut(kLutOff, lane);
-  const int units = count_units(A, Q);
   if (A.offsets && blockIdx.x == 0 && A.status)
     for (int e = tid; e < A.E; e += NT)
       if (A.offsets[e] < 0 || A.offsets[e + 1] < A.offsets[e] || A.offsets[e + 1] > A.T)
@@ -796,11 +812,12 @@ void tile_kernel(const I8Args A) {
   uint32_t flags = 0;
   // (T N is at most 2^40, E N 2^34 and a tile has 2^13 results or more: their number
   // fits, and only fewer than 2^24 are split)
-  const int tiles = units * A.tp, total = tiles * A.splits;
-  for (int work = (int)blockIdx.x; work < total; work += (int)gridDim.x) {
+  const int tiles = A.splits == 1 ? 0 : count_units(A, Q) * A.tp;
+  for (int work = (int)blockIdx.x;; work += (int)gridDim.x) {
     // the same for the block: kept in scalar registers
     auto scalar = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
-    const int split = A.splits == 1 ? 0 : scalar((int)((uint32_t)work / (uint32_t)tiles)), t = work - split * tiles;
+    const int split = A.splits == 1 || tiles == 0 ? 0 : scalar((int)((uint32_t)work / (uint32_t)tiles)), t = work - split * tiles;
+    if (split >= A.splits) break;
     const int unit = scalar((int)((uint32_t)t / (uint32_t)A.tp)), ip = t - unit * A.tp;
     const Segment seg = find_unit(A, Q, unit);
     if (seg.e < 0) break;
@@ -809,6 +826,7 @@ void tile_kernel(const I8Args A) {
     const int s0 = A.splits == 1 ? 0 : scalar(S * split / A.splits);
     const int S1 = A.splits == 1 ? S : scalar(S * (split + 1) / A.splits) - s0;
     const int n0 = ip * P, m0 = seg.a + seg.unit * Q, M = min(seg.b - m0, Q);
+    const Tile tile{seg.e, n0, m0, M, ip, split};
 
     // q: this thread's chunks of a slot, as bytes from the first of A.q (where
     // rows are given: 32 bits reach all of them) or of this tile; rows past the
@@ -931,6 +949,7 @@ void tile_kernel(const I8Args A) {
     for (int i = 0; i < kLoads; ++i) request(0, 0, i);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) request(1, kQSlot, i);
+    const float end = end_value<P, Q>(A, tile, tid);
     if (work == (int)blockIdx.x) {  // the table, while those are on their way
       L::build(smem + kLutOff, tid, NT);
       __syncthreads();
@@ -939,6 +958,7 @@ void tile_kernel(const I8Args A) {
     look(Int<0>{}), piece(Int<0>{}), look(Int<1>{}), piece(Int<1>{});
     look(Int<2>{}), piece(Int<2>{}), look(Int<3>{}), piece(Int<3>{});
     store_scale();
+    put_end<P, Q>(smem + kEndOff, tid, end);
     put ^= kPSlot;
     sput ^= kSSlot;
     load_raw(1);
@@ -1032,7 +1052,7 @@ void tile_kernel(const I8Args A) {
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // nothing is on its way into LDS
 
-    finish_tile<P, Q, WP>(A, acc, smem, wv, Tile{seg.e, n0, m0, M, ip, split});
+    finish_tile<P, Q, WP>(A, acc, smem, kEndOff, wv, tile);
   }
   if ((flags & kBad) && A.status) atomicOr(A.status, kDevInvalidByte);
 }
@@ -1161,7 +1181,7 @@ void part_kernel(const I8Args A) {
   constexpr int NT = 2 * P, TP = P / 16, TQ = Q / (NT / 64) / 16, B = bytes_per_group(128);
   constexpr uint32_t kPSlot = P * 64, kQSlot = Q * kPartBytes, kSSlot = P * 4;
   constexpr uint32_t kSOff = 2 * kPSlot, kQOff = kSOff + 2 * kSSlot, kLutOff = kQOff + 2 * kQSlot;
-  constexpr uint32_t kRoom = kLutOff + L::kBytes;
+  constexpr uint32_t kEndOff = kLutOff + L::kBytes, kRoom = kEndOff + 4 * (P + Q);
   constexpr int kLoads = kQSlot / 16 / NT, kStep = 2;  // rows of matrix tiles between pieces of the codes
   static_assert(P % 64 == 0 && TP % 4 == 0 && 5 * kStep < TP && 4 * TQ <= TP && kQSlot % (16 * NT) == 0 && Q <= kPartPad, "");
   static_assert(finish_room<P, Q, 1>() <= kLutOff && kRoom <= 160 << 10, "");
@@ -1171,22 +1191,23 @@ void part_kernel(const I8Args A) {
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int S = A.K / 128;
   const L lut(kLutOff, lane);
-  const int units = count_units(A, Q);
   if (A.offsets && blockIdx.x == 0 && A.status)
     for (int e = tid; e < A.E; e += NT)
       if (A.offsets[e] < 0 || A.offsets[e + 1] < A.offsets[e] || A.offsets[e + 1] > A.T)
         atomicOr(A.status, kDevBadSegment);
   uint32_t flags = 0;
-  const int tiles = units * A.tp, total = tiles * A.splits;
-  for (int work = (int)blockIdx.x; work < total; work += (int)gridDim.x) {
+  const int tiles = A.splits == 1 ? 0 : count_units(A, Q) * A.tp;
+  for (int work = (int)blockIdx.x;; work += (int)gridDim.x) {
     auto scalar = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
-    const int split = A.splits == 1 ? 0 : scalar((int)((uint32_t)work / (uint32_t)tiles)), t = work - split * tiles;
+    const int split = A.splits == 1 || tiles == 0 ? 0 : scalar((int)((uint32_t)work / (uint32_t)tiles)), t = work - split * tiles;
+    if (split >= A.splits) break;
     const int unit = scalar((int)((uint32_t)t / (uint32_t)A.tp)), ip = t - unit * A.tp;
     const Segment seg = find_unit(A, Q, unit);
     if (seg.e < 0) break;
     const int s0 = A.splits == 1 ? 0 : scalar(S * split / A.splits);
     const int S1 = A.splits == 1 ? S : scalar(S * (split + 1) / A.splits) - s0;
     const int n0 = ip * P, m0 = seg.a + seg.unit * Q, M = min(seg.b - m0, Q);
+    const Tile tile{seg.e, n0, m0, M, ip, split};
 
     // the stage's rows, those behind the tile's last too (the next group's or the
     // pad: all bits are numbers, and their results go nowhere)
@@ -1277,6 +1298,7 @@ void part_kernel(const I8Args A) {
     for (int i = 0; i < kLoads; ++i) request(stage_of(0), 0, i);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) request(stage_of(1), kQSlot, i);
+    const float end = end_value<P, Q>(A, tile, tid);
     if (work == (int)blockIdx.x) {  // the table, while those are on their way
       L::build(smem + kLutOff, tid, NT);
       __syncthreads();
@@ -1285,6 +1307,7 @@ void part_kernel(const I8Args A) {
     look(Int<0>{}), piece(Int<0>{}), look(Int<1>{}), piece(Int<1>{});
     look(Int<2>{}), piece(Int<2>{}), look(Int<3>{}), piece(Int<3>{});
     store_scale(0);
+    put_end<P, Q>(smem + kEndOff, tid, end);
     put ^= kPSlot;
     sput ^= kSSlot;
     load_raw(1);
@@ -1371,7 +1394,7 @@ void part_kernel(const I8Args A) {
     }
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // nothing is on its way into LDS
 
-    finish_tile<P, Q, 1>(A, acc, smem, wv, Tile{seg.e, n0, m0, M, ip, split});
+    finish_tile<P, Q, 1>(A, acc, smem, kEndOff, wv, tile);
   }
   if ((flags & kBadNibbles) && A.status) atomicOr(A.status, kDevInvalidByte);
 }
