@@ -1161,8 +1161,9 @@ def _typed(t, name: str, shape, device):
 
 def _rows_of(x, name: str):
     """(M, K, device) of a 2-D device tensor."""
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+    if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.get_device() < 0:
         _dev(x, name, tuple(TYPES) + I8, 2)
+        raise TQError("%s must be on a GPU" % name)
     return x.shape[0], x.shape[1], x.device
 
 
@@ -1275,7 +1276,9 @@ def rms_norm_backward(dh, y, rstd, weight=None, dy=None, out=None, workspace=Non
 
 class RMSNorm(torch.autograd.Function):
     """rms_norm_forward with gradients for x, weight and residual: h, or (h, y)
-    with a residual.  Gradients of gradients are refused."""
+    with a residual.  Gradients of gradients are refused.  A backward pass may be
+    captured in a graph as any of torch's may: with its forward pass, and while no
+    eager graph of the same leaves lives."""
 
     @classmethod
     def apply(cls, x, weight=None, residual=None, eps: float = 1e-6):
