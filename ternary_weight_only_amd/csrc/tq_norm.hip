@@ -565,14 +565,21 @@ __global__ __launch_bounds__(kColumns / 8) void norm_back_columns_kernel(const B
   if (A.partial) store8(A.partial + (int64_t)part * A.K, true, k, A.K, dw);
 }
 
+constexpr int kShare = kBackParts / 32;
+
 // dw[k]: the blocks' sums, in order within each of 32 shares, then the shares'.
 __global__ __launch_bounds__(1024) void norm_back_sum_kernel(const float *partial, int parts, int K, void *dw,
                                                             bool w32) {
   __shared__ float sums[32][33];
   const int c = threadIdx.x & 31, p0 = threadIdx.x >> 5, k = (int)blockIdx.x * 32 + c;
   float sum = 0.f;
-  if (k < K)
-    for (int p = p0; p < parts; p += 32) sum += partial[(int64_t)p * K + k];
+  for (int p = p0; p < parts; p += 32 * kShare) {  // their loads together: the kernel is their latency
+    float v[kShare];
+#pragma unroll
+    for (int i = 0; i < kShare; ++i) v[i] = k < K && p + 32 * i < parts ? partial[(int64_t)(p + 32 * i) * K + k] : 0.f;
+#pragma unroll
+    for (int i = 0; i < kShare; ++i) sum += v[i];
+  }
   sums[p0][c] = sum;
   __syncthreads();
   if (p0 || k >= K) return;
