@@ -1152,9 +1152,9 @@ def _typed(t, name: str, shape, device):
     """(address, tq_type) of a bf16 or fp32 input of exactly `shape`; 0, 0 of None."""
     if t is None:
         return 0, 0
-    if (isinstance(t, torch.Tensor) and t.dtype in TYPES and t.shape == shape and t.is_contiguous()
-            and t.get_device() == device.index):
-        return t.data_ptr(), TYPES[t.dtype]
+    if (isinstance(t, torch.Tensor) and (c := TYPES.get(t.dtype)) is not None and t.shape == shape
+            and t.is_contiguous() and t.get_device() == device.index):
+        return t.data_ptr(), c
     _dev(t, name, tuple(TYPES), None, device)
     raise TQError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
 
@@ -1189,6 +1189,14 @@ def _norm_args(x, weight, residual, eps):
     return (xp, xt, rp, rt, wp, wt, M, K, _eps(eps)), M, K, dev
 
 
+def _new_sum(x, residual):
+    """(the sum, its address to write), allocated here: x itself where nothing is added."""
+    if residual is None:
+        return x, 0
+    y = torch.empty_like(residual)
+    return y, y.data_ptr()
+
+
 def _sum_out(y, x, residual, M, K, dev):
     """(the sum, its address to write): x itself where nothing is added."""
     if residual is None:
@@ -1209,11 +1217,16 @@ def rms_norm_i8(x, weight=None, residual=None, eps: float = 1e-6, status=None, o
     if dev.index != _current_device():
         with torch.cuda.device(dev):
             return rms_norm_i8(x, weight, residual, eps, status, out)
-    q, s, y = (None, None, None) if out is None else out
-    q, qp = _exactly(q, "q", (M, K), torch.int8, dev)
-    s, sp = _exactly(s, "scales", (M,), torch.float32, dev)
-    y, yp = _sum_out(y, x, residual, M, K, dev)
-    rc = lib().tq_rms_norm_i8(*args, qp, sp, yp, _st(status, dev) if status is not None else 0, _stream_of(dev))
+    if out is None:
+        q, s = torch.empty(M, K, dtype=torch.int8, device=dev), torch.empty(M, dtype=torch.float32, device=dev)
+        y, yp = _new_sum(x, residual)
+        qp, sp = q.data_ptr(), s.data_ptr()
+    else:
+        q, s, y = out
+        q, qp = _exactly(q, "q", (M, K), torch.int8, dev)
+        s, sp = _exactly(s, "scales", (M,), torch.float32, dev)
+        y, yp = _sum_out(y, x, residual, M, K, dev)
+    rc = lib().tq_rms_norm_i8(*args, qp, sp, yp, 0 if status is None else _st(status, dev), _stream_of(dev))
     if rc:
         _rc(rc, "tq_rms_norm_i8")
     return q, s, y
@@ -1228,12 +1241,16 @@ def rms_norm_forward(x, weight=None, residual=None, eps: float = 1e-6, status=No
     if dev.index != _current_device():
         with torch.cuda.device(dev):
             return rms_norm_forward(x, weight, residual, eps, status, out)
-    h, y, r = (None, None, None) if out is None else out
-    h, hp = _exactly(h, "h", (M, K), torch.bfloat16, dev)
-    y, yp = _sum_out(y, x, residual, M, K, dev)
-    r, rp = _exactly(r, "rstd", (M,), torch.float32, dev)
-    rc = lib().tq_rms_norm_forward(*args, hp, yp, rp, _st(status, dev) if status is not None else 0,
-                                   _stream_of(dev))
+    if out is None:
+        h, r = torch.empty(M, K, dtype=torch.bfloat16, device=dev), torch.empty(M, dtype=torch.float32, device=dev)
+        y, yp = _new_sum(x, residual)
+        hp, rp = h.data_ptr(), r.data_ptr()
+    else:
+        h, y, r = out
+        h, hp = _exactly(h, "h", (M, K), torch.bfloat16, dev)
+        y, yp = _sum_out(y, x, residual, M, K, dev)
+        r, rp = _exactly(r, "rstd", (M,), torch.float32, dev)
+    rc = lib().tq_rms_norm_forward(*args, hp, yp, rp, 0 if status is None else _st(status, dev), _stream_of(dev))
     if rc:
         _rc(rc, "tq_rms_norm_forward")
     return h, y, r
