@@ -13,11 +13,14 @@
 // dword and the fifth beside them, and dwords of four consecutive codes are put
 // together from them: q is read as it lies in memory.
 //
-// Two kernels multiply:
-//   few_kernel    few rows (of each expert): bound by the weights' bytes.  Each
-//                 lane decodes whole units of 128 codes in registers.
+// Three kernels multiply:
+//   few_kernel    few rows (of each expert).  Each lane decodes whole units of 128
+//                 codes in registers.
 //   tile_kernel   more: each block decodes its weight rows into LDS, where its
 //                 rows of q use them.
+//   part_kernel   many, of 128-groups: the same with q in two parts of six bits
+//                 (made by parts_kernel), whose matrix instructions leave floats.
+// Where K is split, join_kernel adds the splits' sums and applies the epilogue.
 #include <hip/hip_fp16.h>
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -136,7 +139,7 @@ struct Unit {
   uint32_t scale;  // fp16, or two
 };
 
-// Dwords 4 P .. of the codes of group `H` of a unit, P < G / 16: 16 codes.
+// The entry of byte i of the group that starts at byte OFF of a unit.
 template <int G, int OFF, class L>
 __device__ __forceinline__ u32x2 unit_entry(lds_bytes *smem, const L &lut, const Unit &u, int i) {
   const int at = OFF + i;
@@ -411,6 +414,12 @@ struct FewRoom {
 // and a result is a row's sum over one unit, exact, which is then scaled.  (Four
 // rows of q a matrix instruction instead of 16; the instructions are far from
 // bounding it.)
+//
+// What bounds it: with few matrices the chain before the first sum, launch, q and
+// the table into LDS, about 6 us (8 tokens, eight experts of [3584,1024], 10.8 us;
+// 7 rows of [14336,4096] 12.0 us where the bytes alone take 2.6); with many the
+// decode in LDS, 26 table reads of 8 bytes a unit, beside the bytes: 32 tokens,
+// sixteen experts of [4096,14336], 80 us, 2.5 TB/s of packed bytes (of copy's 5.2).
 template <int G, int MB, int COPIES>
 __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Args A) {
   typedef Codes<COPIES> L;
@@ -788,6 +797,13 @@ __device__ __forceinline__ void finish_tile(const I8Args &A, f32x4 (&acc)[P / WP
 //   - scales and adds the row before;
 //   - decodes its codes of s + 1, two threads a weight row, 64 codes each;
 //   - requests q of s + 2, whose slot this stage's q has left, and bytes of s + 2.
+//
+// What bounds it: short K.  A tile takes 5 to 8 us beside its stages (offsets, row
+// indices, first bytes and decode, results), a stage of 128 x 64 0.8 us alone on
+// its CU and 1.1 with another: 2000 rows of 32 experts of [3584,1024] 54 to 58 us,
+// about half of it in stages; 333 rows of [1024,3584], K in five, 18.2 us.  In a
+// stage the vector unit (two instructions a result and group, and the decode) has
+// the longest part, which is why larger tiles of 128-groups go to part_kernel.
 template <int G, int P, int Q, int WP, int COPIES>
 __global__ __launch_bounds__(2 * P) __attribute__((amdgpu_waves_per_eu(2, P == 256 || Q > 64 ? 2 : 4)))
 void tile_kernel(const I8Args A) {
@@ -1065,9 +1081,9 @@ void tile_kernel(const I8Args A) {
 // l / 8 are numbers of the 6-bit formats (3 exponent and 2 mantissa bits; 2 and
 // 3), codes -1, 0 and 1 of the 4-bit one, and a group's sum of products, an
 // eighth of a whole number below 2^15, is exact in the fp32 of the matrix cores.
-// They do 128 codes of both parts in the time of 128 8-bit ones, but leave a
-// float (no conversion, of 128 a thread and group, where the vector unit is what
-// bounds the kernel) and halve the codes' place and reading in LDS.
+// They do 128 codes of both parts in the time of 128 8-bit ones (7.5 ns a SIMD for
+// each of the two instructions), but leave a float (no conversion, of 128 a thread
+// and group) and halve the codes' place and reading in LDS.
 //
 // Parts of q: [K/128][T + pad][192], a row's 128 codes as twelve 16-byte chunks:
 // chunk 4 p + (j ^ (row / 4 % 4)) is lane j's (k 32 j .. 32 j + 31) first 128 bits
@@ -1088,7 +1104,7 @@ __device__ __forceinline__ uint32_t six_bits(uint32_t v) {
 }
 
 // A thread a lane's 32 codes of a row: rows given by index are gathered here.
-// Bound by memory (read once, written 1.5 times).
+// Bound by memory (read once, written 1.5 times): 2048 rows of 4096 7.7 us.
 __global__ __launch_bounds__(256) void parts_kernel(const I8Args A) {
   const int nG = A.K / 128, j = threadIdx.x & 3;
   for (int64_t m = (int64_t)blockIdx.x * 64 + (threadIdx.x >> 2); m < A.T; m += (int64_t)gridDim.x * 64) {
@@ -1173,7 +1189,17 @@ __device__ __forceinline__ f32x4 mfma_parts(const Part &x, u32x4 codes, f32x4 c)
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, w, c, FORMAT, 4, 0, 0, 0, 0);
 }
 
-// As tile_kernel, from the parts of q, a stage a group.
+// As tile_kernel, from the parts of q, a stage a group.  Here a wave has all the
+// tile's weight rows and 32 rows of q, so that q is read from LDS once; its parts
+// of the next stage are read along the way, not at the stage's end by all waves at
+// once.
+//
+// What bounds it: a stage takes 2.0 to 2.2 us, 4770 cycles, of which the matrix
+// cores have 2050, the vector unit 1800 and LDS 2400: two waves a SIMD (there are
+// registers for no more) do not hide each other's waits.  Power holds the clock at
+// 2.1 GHz (2.4 with zeros as q, in the same cycles).  2048 rows of [14336,4096]
+// 159 us, 1.51 Pop/s (a library's plain 8-bit product of 8192^3 reaches 2.1, with
+// nothing to decode or scale); eight experts of them, two a token, 393 to 405 us.
 template <int P, int Q, int COPIES>
 __global__ __launch_bounds__(2 * P) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void part_kernel(const I8Args A) {
@@ -1427,7 +1453,8 @@ struct Shape {
 constexpr Shape kShapes[] = {{128, 64, 512, 6.4, 0.82, 1.10}, {128, 128, 512, 8.5, 1.05, 1.56}, {256, 256, 256, 13, 2.2, 2.2}};
 
 // Of the shapes and the splits of K the cheapest.  Splits keep two stages, and
-// their sums are written, read and joined in a launch more; so are q's parts.
+// their sums are written, read and joined in a launch more; parts of q are made in
+// one more.
 void plan_tiles(Plan &p, int64_t T, int64_t N, int64_t K, int G, int64_t used, bool grouped) {
   const int64_t stages = ceil_div(K, 128);
   double least = 1e30;

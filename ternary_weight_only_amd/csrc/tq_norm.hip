@@ -244,7 +244,9 @@ __device__ __forceinline__ int64_t stride_of(bool f32, int K) { return (int64_t)
 // eights v T + t of it a thread (T = 64 W threads), V of them.  Four rows a
 // block where a wave has one.  NARROW: all of bf16; a row whose sums leave what
 // fp32 is good for, and every row otherwise, is summed and rounded in fp64.
-// Bound by HBM at many rows, by latency at few.
+// Bound by HBM at many rows (4096 rows of 4096 bf16 with a residual 23.9 us on the
+// device, 134 MB at 5.6 TB/s, copy's rate), by latency at few (a row of 1024: 3.5
+// us, of a call's 10.4 on the host).
 template <int V, int W, bool NARROW>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(const NormArgs A) {
   __shared__ __align__(16) unsigned char room[2][W * 16];
@@ -420,7 +422,9 @@ constexpr int kRegisterK = 16384;   // longest row that registers hold
 
 // A block: G rows at a time (kBackWaves waves, W a row), rows strided over the
 // blocks; a thread keeps its columns' share of dw over all its rows, and the
-// block's G groups add theirs in order.
+// block's G groups add theirs in order.  4096 rows of 4096 bf16: 29.9 us, 4.5 TB/s
+// (copy 5.2; a row loaded ahead, 30.7), and norm_back_sum_kernel 4.2; 333 rows of
+// 3584 with fp32 7.9 and 2.7, both latency.
 template <int V, int W, bool NARROW>
 __global__ __launch_bounds__(64 * kBackWaves) void norm_back_kernel(const BackArgs A) {
   constexpr int T = 64 * W, G = kBackWaves / W;

@@ -99,7 +99,8 @@ LARGE = [(771, 5000, 64, 64, 0), (986, 2600, 192, 64, 20), (2286, 513, 4224, 64,
          (3113, 2600, 64, 64, 0), (2694, 2600, 320, 64, 20), (1677, 5000, 3520, 64, 1),
          (778, 5000, 128, 128, 0), (976, 2600, 384, 128, 20), (1350, 1024, 4992, 128, 0), (963, 1500, 4224, 128, 1),
          (3099, 2600, 128, 128, 0), (3113, 2597, 384, 128, 0), (2628, 2600, 1024, 128, 20),
-         (3093, 2600, 9600, 128, 0), (1721, 5000, 3840, 128, 1)]
+         (3093, 2600, 9600, 128, 0), (1721, 5000, 3840, 128, 1),
+         (964, 4100, 5376, 128, 0), (1476, 2600, 5632, 128, 5), (2061, 2000, 6016, 128, 2)]
 
 
 def segments(rng, E, T):
