@@ -1458,6 +1458,7 @@ constexpr Shape kShapes[] = {{128, 64, 512, 6.4, 0.82, 1.10}, {128, 128, 512, 8.
 void plan_tiles(Plan &p, int64_t T, int64_t N, int64_t K, int G, int64_t used, bool grouped) {
   const int64_t stages = ceil_div(K, 128);
   double least = 1e30;
+  int places = 0;
   for (const Shape &c : kShapes) {
     // units of an expert: on average its last is half full
     const int64_t units = grouped ? std::max(used, T / c.q + used / 2) : ceil_div(T, c.q);
@@ -1469,7 +1470,7 @@ void plan_tiles(Plan &p, int64_t T, int64_t N, int64_t K, int G, int64_t used, b
       const double cost = c.start * (rounds + (rest > 0)) + ceil_div(stages, s) * (rounds * c.full + last) +
                           (s > 1 ? 4.5 + (double)s * T * N * 8 / 5.2e6 : 0) +
                           (c.p == 256 && G == 128 ? 4 + (double)T * K * 2.5 / 5.2e6 : 0);
-      if (cost < least) least = cost, p.p = c.p, p.q = c.q, p.splits = s;
+      if (cost < least) least = cost, p.p = c.p, p.q = c.q, p.splits = s, places = c.places;
     }
   }
   p.kind = kTile;
@@ -1477,7 +1478,10 @@ void plan_tiles(Plan &p, int64_t T, int64_t N, int64_t K, int G, int64_t used, b
   // of [1024,3584], in small tiles, 26 and 21
   p.parts = G == 128 && p.p == 256;
   p.units = grouped ? T / p.q + used : ceil_div(T, p.q);
-  p.blocks = std::min<int64_t>(ceil_div(N, p.p) * p.units * p.splits, 1 << 20);
+  // blocks stay for more tiles, and keep their table: 2000 rows of 32 experts of
+  // [3584,1024] 58 us with a block a tile, 56 so; eight experts of 2048 rows of
+  // [14336,4096] 416 and 408
+  p.blocks = std::min<int64_t>(ceil_div(N, p.p) * p.units * p.splits, places);
 }
 
 Plan plan_of(int64_t T, int64_t N, int64_t K, int G, int64_t E, bool grouped) {

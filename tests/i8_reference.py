@@ -89,7 +89,8 @@ def within(got, want, bound, what):
 
 
 # (rows, N, K, G, experts or 0): together they reach every kernel of the products,
-# with and without splits of K (tests/test_i8_plans.py sees to it)
+# with and without splits of K, in one round of tiles and more (tests/test_i8_plans.py
+# sees to it)
 MIDDLE = [(3, 40, 192, 64, 0), (2, 9000, 4096, 64, 0), (4, 3000, 2048, 64, 0), (7, 40, 128, 64, 0), (6, 80, 14336, 64, 0), (14, 70, 448, 64, 0),
           (15, 300, 4032, 64, 0), (2, 33, 384, 128, 0), (1, 2000, 8192, 128, 0), (8, 50, 640, 128, 0),
           (5, 17, 7168, 128, 0), (13, 200, 1024, 128, 0), (16, 130, 5760, 128, 0), (30, 77, 192, 64, 0),
@@ -100,7 +101,9 @@ LARGE = [(771, 5000, 64, 64, 0), (986, 2600, 192, 64, 20), (2286, 513, 4224, 64,
          (778, 5000, 128, 128, 0), (976, 2600, 384, 128, 20), (1350, 1024, 4992, 128, 0), (963, 1500, 4224, 128, 1),
          (3099, 2600, 128, 128, 0), (3113, 2597, 384, 128, 0), (2628, 2600, 1024, 128, 20),
          (3093, 2600, 9600, 128, 0), (1721, 5000, 3840, 128, 1),
-         (964, 4100, 5376, 128, 0), (1476, 2600, 5632, 128, 5), (2061, 2000, 6016, 128, 2)]
+         (964, 4100, 5376, 128, 0), (1476, 2600, 5632, 128, 5), (2061, 2000, 6016, 128, 2),
+         (700, 6000, 192, 64, 20), (700, 6000, 128, 128, 20), (3099, 8200, 256, 128, 0),
+         (1500, 6000, 128, 128, 20), (1500, 6000, 192, 64, 20), (3000, 6000, 192, 64, 10)]
 
 
 def segments(rng, E, T):

@@ -32,6 +32,18 @@ def test_the_gpu_tests_sizes_reach_every_kernel():
     assert tiles == {t + (split,) for t in both for split in (False, True)}
 
 
+def test_the_gpu_tests_sizes_take_more_than_one_round():
+    """Blocks that go on to a second tile, of every shape, and with splits."""
+    again = set()
+    for M, N, K, G, E in LARGE:
+        p = plan(M, N, K, G, E)
+        units = M // p[3] + E // 2 if E else -(-M // p[3])
+        if units * -(-N // p[2]) * p[1] > (256 if p[2] == 256 else 512):
+            again.add((G, p[2], p[3], p[1] > 1))
+    assert {(G, *shape, False) for G in (64, 128) for shape in ((128, 64), (128, 128), (256, 256))} <= again
+    assert (128, 256, 256, True) in again
+
+
 def test_few_rows_in_many_shapes_of_blocks():
     """Waves of a tile and tiles of a set both vary; q's rows fit at any K."""
     shapes = {tuple(plan(M, N, K, 128, E)[4:6]) for M in (1, 7, 16) for N in (16, 700, 14336)
