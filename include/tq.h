@@ -714,11 +714,12 @@ int tq_rms_norm_forward(const void *x, int x_type, const void *residual, int res
  *   y         [M,K] of y_type, as the forward call left it (x without residual)
  *   rstd      [M] fp32;  weight as the forward call had it
  *   dy        [M,K] of y_type, or NULL for zeros
- *   dx        [M,K] of y_type, overwritten
+ *   dx        [M,K] of y_type, overwritten; no input's memory
  *   dweight   [K] of weight_type, overwritten; NULL to leave it out, and where
  *             weight is NULL
  *   workspace device memory, 16-byte aligned, at least
- *             tq_rms_norm_backward_workspace(M, K) bytes, as tq_glu's
+ *             tq_rms_norm_backward_workspace(M, K) bytes, as tq_glu's (none at few
+ *             rows)
  * M = 0 sets dweight to 0.  Deterministic.
  */
 int tq_rms_norm_backward(const uint16_t *dh, const void *y, int y_type, const float *rstd,

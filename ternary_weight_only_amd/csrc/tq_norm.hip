@@ -412,62 +412,112 @@ struct BackArgs {
   int64_t M;
   int K;
   void *dx;
-  float *partial;            // [parts][K], null where no dw is wanted
+  float *partial;            // [parts][K], null where no dw is wanted or blocks of columns make it
   float *mean;               // long rows: [M]
+  int row_blocks;            // those behind them: blocks of columns
+  void *dw;                  // theirs
 };
 
 constexpr int kBackWaves = 16;
 constexpr int kBackParts = 256;     // most partial sums of dw a column
 constexpr int kRegisterK = 16384;   // longest row that registers hold
 
+constexpr int kBackColumns = 64;  // of a block of them
+
+// dw of 64 columns over all rows: eight threads a row, eight columns each, 128 rows
+// at a time; the threads of a wave, then the waves are added in order.
+__device__ __forceinline__ void back_columns(const BackArgs &A, int block, float (&sums)[kBackWaves][kBackColumns]) {
+  const int c = threadIdx.x & 7, wave = threadIdx.x >> 6, k = block * kBackColumns + 8 * c;
+  float dw[8] = {};
+  for (int64_t m = threadIdx.x >> 3; m < A.M && k < A.K; m += 8 * kBackWaves) {
+    const Raw8 hr = load8(A.dh + m * A.K, false, k, A.K);
+    const Raw8 yr = load8((const char *)A.y + m * stride_of(A.y32, A.K), A.y32, k, A.K);
+    const float rstd = A.rstd[m];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[i] = fmaf(value8(hr, false, i), value8(yr, A.y32, i) * rstd, dw[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+#pragma unroll
+    for (int o = 8; o < 64; o <<= 1) dw[i] += __shfl_xor(dw[i], o);
+    if ((threadIdx.x & 56) == 0) sums[wave][8 * c + i] = dw[i];
+  }
+  __syncthreads();
+  const int n = block * kBackColumns + (int)threadIdx.x;
+  if (threadIdx.x >= kBackColumns || n >= A.K) return;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kBackWaves; ++i) sum += sums[i][threadIdx.x];
+  if (A.w32)
+    ((float *)A.dw)[n] = sum;
+  else
+    ((uint16_t *)A.dw)[n] = f32_to_bf16(sum);
+}
+
 // A block: G rows at a time (kBackWaves waves, W a row), rows strided over the
 // blocks; a thread keeps its columns' share of dw over all its rows, and the
 // block's G groups add theirs in order.  4096 rows of 4096 bf16: 29.9 us, 4.5 TB/s
-// (copy 5.2; a row loaded ahead, 30.7), and norm_back_sum_kernel 4.2; 333 rows of
-// 3584 with fp32 7.9 and 2.7, both latency.
+// (copy 5.2; a row loaded ahead, 30.7), and norm_back_sum_kernel 4.2.  At few rows
+// (by_columns) blocks behind those of rows make dw: 333 rows of 3584 with fp32 5.5,
+// latency.
 template <int V, int W, bool NARROW>
 __global__ __launch_bounds__(64 * kBackWaves) void norm_back_kernel(const BackArgs A) {
   constexpr int T = 64 * W, G = kBackWaves / W;
   __shared__ float dots[2][kBackWaves];
+  __shared__ float sums[kBackWaves][kBackColumns];
   extern __shared__ float total[];  // [K], for dw where G > 1
+  if ((int)blockIdx.x >= A.row_blocks) return back_columns(A, (int)blockIdx.x - A.row_blocks, sums);
   const int g = threadIdx.x / T, t = threadIdx.x % T, wave = threadIdx.x >> 6;
   const bool y32 = !NARROW && A.y32, w32 = !NARROW && A.w32;
+  // The weight and a row stay in registers, but where there is no room for them
+  // (two eights of fp32 a thread): then both are read again behind the mean.
+  // (Without room the compiler moved a lane's values over the masked stores below
+  // and put one back where no lane was on: wrong from a block's second row on.)
+  constexpr bool kHold = NARROW || V == 1;
+  auto weight = [&](int v) { return A.w ? load8(A.w, w32, 8 * (v * T + t), A.K) : Raw8{}; };
   Raw8 wr[V];
-  if (A.w)
+  if (kHold)
 #pragma unroll
-    for (int v = 0; v < V; ++v) wr[v] = load8(A.w, w32, 8 * (v * T + t), A.K);
+    for (int v = 0; v < V; ++v) wr[v] = weight(v);
   float dw[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[v][i] = 0.f;
-  const int64_t step = (int64_t)gridDim.x * G;
+  const int64_t step = (int64_t)A.row_blocks * G;
   int turn = 0;
   // every group takes as many turns: the barrier below is the block's
   for (int64_t m0 = (int64_t)blockIdx.x * G; m0 < A.M; m0 += step, turn ^= 1) {
     const int64_t m = m0 + g;
     const bool in = m < A.M;
     const int64_t ms = in ? m : A.M - 1;
+    const char *const dh = (const char *)(A.dh + ms * A.K);
+    const char *const y = (const char *)A.y + ms * stride_of(y32, A.K);
     Raw8 hr[V], yr[V], dr[V];
+    auto addend = [&](int v) { return load8((const char *)A.dy + ms * stride_of(y32, A.K), y32, 8 * (v * T + t), A.K); };
+    if (kHold) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int k = 8 * (v * T + t);
-      hr[v] = load8(A.dh + ms * A.K, false, k, A.K);
-      yr[v] = load8((const char *)A.y + ms * stride_of(y32, A.K), y32, k, A.K);
+      for (int v = 0; v < V; ++v) {
+        hr[v] = load8(dh, false, 8 * (v * T + t), A.K);
+        yr[v] = load8(y, y32, 8 * (v * T + t), A.K);
+      }
+      if (A.dy)
+#pragma unroll
+        for (int v = 0; v < V; ++v) dr[v] = addend(v);
     }
-    if (A.dy)
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        dr[v] = load8((const char *)A.dy + ms * stride_of(y32, A.K), y32, 8 * (v * T + t), A.K);
     const float rstd = A.rstd[ms];
     float dot = 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+      const int k = 8 * (v * T + t);
+      const Raw8 h = kHold ? hr[v] : load8(dh, false, k, A.K), yv = kHold ? yr[v] : load8(y, y32, k, A.K);
+      const Raw8 wv = kHold ? wr[v] : weight(v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d = value8(hr[v], false, i);
-        dot = fmaf(A.w ? d * value8(wr[v], w32, i) : d, value8(yr[v], y32, i) * rstd, dot);
+        const float d = value8(h, false, i);
+        dot = fmaf(A.w ? d * value8(wv, w32, i) : d, value8(yv, y32, i) * rstd, dot);
       }
+    }
     dot = wave_add(dot);
     if constexpr (W > 1) {
       if ((threadIdx.x & 63) == 0) dots[turn][wave] = dot;
@@ -481,12 +531,15 @@ __global__ __launch_bounds__(64 * kBackWaves) void norm_back_kernel(const BackAr
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int k = 8 * (v * T + t);
+      const Raw8 h = kHold ? hr[v] : load8(dh, false, k, A.K), yv = kHold ? yr[v] : load8(y, y32, k, A.K);
+      const Raw8 wv = kHold ? wr[v] : weight(v);
+      if (!kHold && A.dy) dr[v] = addend(v);
       float dx[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float d = value8(hr[v], false, i), n = value8(yr[v], y32, i) * rstd;
+        const float d = value8(h, false, i), n = value8(yv, y32, i) * rstd;
         dw[v][i] = fmaf(d, n, dw[v][i]);
-        dx[i] = rstd * fmaf(-n, mean, A.w ? d * value8(wr[v], w32, i) : d);
+        dx[i] = rstd * fmaf(-n, mean, A.w ? d * value8(wv, w32, i) : d);
         if (A.dy) dx[i] += value8(dr[v], y32, i);
       }
       if (k < A.K) store8((char *)A.dx + m * stride_of(y32, A.K), y32, k, A.K, dx);
@@ -603,8 +656,18 @@ int back_parts(int64_t M, int K) {
   return (int)std::min<int64_t>(kBackParts, ceil_div(M, kBackWaves / waves_of_row(K)));
 }
 
+// Whether blocks of columns make dw beside the blocks of rows, reading dh and y
+// again, in place of partial sums that a second launch adds.  On the device, us,
+// so and with partial sums: 333 rows of 3584 5.5 and 9.3, 700 10.8 and 12.5, 1500
+// 20.6 and 17.2; 700 rows of 14336 20.5 and 24.1, 1500 39 and 35; 1500 rows of 1024
+// 7.6 and 10.7, 3000 16.2 and 12.8; a row of 4096 3.3 and 6.9.
+bool by_columns(int64_t M, int64_t K) {
+  return K <= kRegisterK && (M <= 1024 || (M <= 2048 && M * K <= 1 << 21));
+}
+
 template <int V, int W>
 void launch_back(const BackArgs &A, bool narrow, int parts, hipStream_t stream) {
+  parts += A.dw ? (int)ceil_div(A.K, kBackColumns) : 0;
   const size_t lds = A.partial && W < kBackWaves ? (size_t)A.K * 4 : 0;  // 16 KB at most
   if (narrow)
     norm_back_kernel<V, W, true><<<parts, 64 * kBackWaves, lds, stream>>>(A);
@@ -640,6 +703,7 @@ void launch_rms_norm(const void *x, bool x32, const void *r, bool r32, const voi
 }
 
 int64_t rms_norm_backward_workspace(int64_t M, int64_t K) {
+  if (by_columns(M, K)) return 0;
   const int64_t sums = (int64_t)back_parts(M, (int)K) * K * 4;
   return (sums + (K > kRegisterK ? M * 4 : 0) + 15) / 16 * 16;
 }
@@ -648,8 +712,9 @@ void launch_rms_norm_backward(const uint16_t *dh, const void *y, bool y32, const
                               bool w32, const void *dy, int64_t M, int64_t K, void *dx, void *dw,
                               void *workspace, hipStream_t stream) {
   const int parts = M > 0 ? back_parts(M, (int)K) : 0;
-  const BackArgs A{dh, y, w, dy, y32, w32, rstd, M, (int)K, dx, dw ? (float *)workspace : nullptr,
-                   (float *)workspace + (int64_t)parts * K};
+  const bool columns = M > 0 && by_columns(M, K);
+  const BackArgs A{dh, y, w, dy, y32, w32, rstd, M, (int)K, dx, dw && !columns ? (float *)workspace : nullptr,
+                   (float *)workspace + (int64_t)parts * K, parts, columns ? dw : nullptr};
   const bool narrow = !y32 && !(w && w32);
   if (M > 0) {
     if (K <= 512)
@@ -670,7 +735,7 @@ void launch_rms_norm_backward(const uint16_t *dh, const void *y, bool y32, const
                                  stream>>>(A, parts);
     }
   }
-  if (dw) norm_back_sum_kernel<<<(unsigned)ceil_div(K, 32), 1024, 0, stream>>>((const float *)workspace, parts,
+  if (dw && !columns) norm_back_sum_kernel<<<(unsigned)ceil_div(K, 32), 1024, 0, stream>>>((const float *)workspace, parts,
                                                                               (int)K, dw, w32);
 }
 

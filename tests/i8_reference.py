@@ -95,7 +95,9 @@ MIDDLE = [(3, 40, 192, 64, 0), (2, 9000, 4096, 64, 0), (4, 3000, 2048, 64, 0), (
           (15, 300, 4032, 64, 0), (2, 33, 384, 128, 0), (1, 2000, 8192, 128, 0), (8, 50, 640, 128, 0),
           (5, 17, 7168, 128, 0), (13, 200, 1024, 128, 0), (16, 130, 5760, 128, 0), (30, 77, 192, 64, 0),
           (40, 140, 1088, 64, 0), (50, 260, 128, 128, 0), (65, 130, 2176, 128, 0), (20, 48, 320, 64, 9),
-          (40, 600, 2048, 64, 16), (9, 40, 256, 128, 3), (64, 1000, 2048, 128, 16), (70, 90, 640, 128, 3)]
+          (40, 600, 2048, 64, 16), (9, 40, 256, 128, 3), (64, 1000, 2048, 128, 16), (70, 90, 640, 128, 3),
+          (16, 70000, 576, 64, 0), (16, 70000, 640, 128, 0), (7, 280000, 128, 128, 0), (6, 280000, 64, 64, 0),
+          (3, 280000, 128, 64, 0), (4, 280000, 128, 128, 0), (16, 60000, 64, 64, 0), (16, 60000, 128, 128, 0)]
 LARGE = [(771, 5000, 64, 64, 0), (986, 2600, 192, 64, 20), (2286, 513, 4224, 64, 0), (1608, 513, 5504, 64, 20),
          (3113, 2600, 64, 64, 0), (2694, 2600, 320, 64, 20), (1677, 5000, 3520, 64, 1),
          (778, 5000, 128, 128, 0), (976, 2600, 384, 128, 20), (1350, 1024, 4992, 128, 0), (963, 1500, 4224, 128, 1),

@@ -51,7 +51,7 @@ def test_norm_refusals():
     _refused(lambda: tq.rms_norm_backward(h, x, rstd, w, x.float()))
     _refused(lambda: tq.rms_norm_backward(h, x, rstd, None, out=(None, w)))
     _refused(lambda: tq.rms_norm_backward(h, x, rstd, w, out=(y.float(), None)))
-    _refused(lambda: tq.rms_norm_backward(h, x, rstd, w, workspace=torch.zeros(8, dtype=torch.uint8, device="cuda")))
+    _refused(lambda: tq.rms_norm_backward(h, x, rstd, w, workspace=torch.zeros(8, device="cuda")))
     torch.cuda.synchronize()
     assert (q == 5).all() and (s == 5).all() and (y == 5).all()
 

@@ -17,6 +17,10 @@ SIZES = [(1, 1), (3, 7), (5, 64), (2, 509), (1, 1024), (9, 1000), (4, 2048), (7,
          (1, 8192), (2, 14336), (3, 16381), (2, 16392), (1, 40003)]
 
 
+# enough rows that dw is the sum of the blocks' parts, at every layout
+SUMS = [(4200, 64), (2100, 1000), (1100, 2000), (1100, 3001), (1100, 5001), (1100, 9001), (1100, 17000)]
+
+
 def _case(seed, M, K, xt, rt, wt):
     x = ref.normal(seed, (M, K), 1.0, r8.TYPES[xt])
     r = None if rt is None else ref.normal(seed + 1, (M, K), 3.0, r8.TYPES[rt])
@@ -118,7 +122,7 @@ def test_sum_in_place_of_the_residual():
         assert got[2] is rd and all(torch.equal(a, b) for a, b in zip(got, want))
 
 
-@pytest.mark.parametrize("M,K", SIZES + [(300, 513), (70, 17000)])
+@pytest.mark.parametrize("M,K", SIZES + [(300, 513), (70, 17000)] + SUMS)
 @pytest.mark.parametrize("types", ["bf16 bf16 1", "fp32 bf16 1", "bf16 fp32 0", "fp32 None 1", "bf16 None 0"])
 def test_backward(M, K, types):
     yt, wt, add = types.split()

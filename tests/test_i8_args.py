@@ -91,7 +91,7 @@ def test_alignment():
     for fn, spec, by2, by4, by16 in (
             ("tq_rms_norm_i8", NORM, ["x", "r", "y", "w"], ["s", "st"], []),
             ("tq_rms_norm_forward", FWD, ["x", "h", "w"], ["r", "y", "rstd", "st"], []),
-            ("tq_rms_norm_backward", BWD, ["dh", "y", "dy", "dx"], ["rstd", "w", "dw"], ["ws"]),
+            ("tq_rms_norm_backward", {**BWD, "M": 30000}, ["dh", "y", "dy", "dx"], ["rstd", "w", "dw"], ["ws"]),
             ("tq_gemm_i8", GEMM, ["s", "b", "r", "out"], ["xs", "st"], ["x"]),
             ("tq_expert_gemm_i8", EXPERT, ["s", "b", "r", "out"], ["xs", "st", "rows", "off"], ["x"])):
         for names, off in ((by2, 1), (by4, 2), (by16, 8)):
@@ -101,10 +101,10 @@ def test_alignment():
 
 def test_workspaces():
     lib = _lib()
-    need = lib.tq_rms_norm_backward_workspace(30, 100)
-    assert need > 0
-    assert _call("tq_rms_norm_backward", BWD, wn=need - 1) == WORKSPACE
-    assert _call("tq_rms_norm_backward", BWD, ws=None) == NULL
+    need = lib.tq_rms_norm_backward_workspace(30000, 100)
+    assert need > 0 and lib.tq_rms_norm_backward_workspace(30, 100) == 0
+    assert _call("tq_rms_norm_backward", BWD, M=30000, wn=need - 1) == WORKSPACE
+    assert _call("tq_rms_norm_backward", BWD, M=30000, ws=None) == NULL
     shapes = [(M, N, K, G) for M in (1, 5, 20, 33, 100, 300, 5000) for N, K in ((50, 256), (1024, 14336), (9000, 8192))
               for G in (64, 128)]
     some = 0

@@ -44,6 +44,17 @@ def test_the_gpu_tests_sizes_take_more_than_one_round():
     assert (128, 256, 256, True) in again
 
 
+def test_the_gpu_tests_sizes_take_many_sets_of_a_block():
+    """Blocks that go on to a second set of tiles, at every number of rows of a unit."""
+    again = set()
+    for M, N, K, G, E in MIDDLE:
+        p = plan(M, N, K, G, E)
+        if p[0] == 0 and -(-N // (16 * p[5])) > p[6]:
+            again.add((G, p[2], p[3]))
+    assert {(G, rows, 32) for G in (64, 128) for rows in (4, 8, 16)} <= again
+    assert (64, 16, 8) in again and (128, 16, 8) in again
+
+
 def test_few_rows_in_many_shapes_of_blocks():
     """Waves of a tile and tiles of a set both vary; q's rows fit at any K."""
     shapes = {tuple(plan(M, N, K, 128, E)[4:6]) for M in (1, 7, 16) for N in (16, 700, 14336)
