@@ -65,8 +65,9 @@ struct I8Args {
   float *partial;           // [splits][T][N] where splits > 1
   uint8_t *parts;           // of q, where it is taken in parts
   int splits;
-  int wk, wt, bpu;          // few: waves of a tile, tiles of a set, blocks of a unit
+  int wk, wt;               // few: waves of a tile, tiles of a set
   int tp;                   // tile: tiles of weight rows
+  int units;                // at most, of offsets that rise within 0 .. T
   int32_t *status;
 };
 
@@ -221,8 +222,8 @@ __device__ __forceinline__ int scan_units(const I8Args &A, int e0, int rows, int
 __device__ __forceinline__ int count_units(const I8Args &A, int rows) {
   if (!A.offsets) return ((int)A.T + rows - 1) / rows;
   int a, b, before, own, total = 0;
-  for (int e0 = 0; e0 < A.E; e0 += 64) total += scan_units(A, e0, rows, a, b, before, own);
-  return total;
+  for (int e0 = 0; e0 < A.E && total < A.units; e0 += 64) total += scan_units(A, e0, rows, a, b, before, own);
+  return min(total, A.units);
 }
 
 // Unit `u` in the order of the experts; by whole waves, the same in every lane.
@@ -432,9 +433,15 @@ __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Arg
   lds_bytes *smem = (lds_bytes *)smem_raw;
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 63, l = lane & 15, q = lane >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6), waves = threads >> 6;
+  // the blocks are shared among the units that there are (whose number the host,
+  // which gives every one that may be a block, does not know)
+  const int wk = A.wk, wt = A.wt, kw = wv % wk, tw = wv / wk;
+  const int tiles = (A.N + 15) / 16, sets = (tiles + wt - 1) / wt;
+  const int units = count_units(A, Room::kRows);
+  const int bpu = max(1, min(sets, (int)gridDim.x / max(1, units * A.splits)));
   const int split = (int)(blockIdx.x % A.splits);
-  const int b0 = (int)(blockIdx.x / A.splits % A.bpu);
-  const Segment seg = find_unit(A, Room::kRows, (int)(blockIdx.x / A.splits / A.bpu));
+  const int b0 = (int)(blockIdx.x / A.splits % bpu);
+  const Segment seg = find_unit(A, Room::kRows, (int)(blockIdx.x / A.splits / bpu));
   if (A.offsets && blockIdx.x == 0 && A.status)
     for (int e = tid; e < A.E; e += threads)
       if (A.offsets[e] < 0 || A.offsets[e + 1] < A.offsets[e] || A.offsets[e + 1] > A.T)
@@ -444,14 +451,12 @@ __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Arg
   const int nG = A.K / G, nU = (nG + GU - 1) / GU, nQ = (nU + 3) / 4;
   // (at most 4096 quads and as many splits: the products fit)
   const int u0 = 4 * (nQ * split / A.splits), u1 = min(nU, 4 * (nQ * (split + 1) / A.splits));
-  const int wk = A.wk, wt = A.wt, kw = wv % wk, tw = wv / wk;
-  const int tiles = (A.N + 15) / 16, sets = (tiles + wt - 1) / wt;
-  const int steps = b0 < sets ? (sets - b0 + A.bpu - 1) / A.bpu : 0;
+  const int steps = b0 < sets ? (sets - b0 + bpu - 1) / bpu : 0;
   const int quads = (u1 - u0 + 3) / 4, batches = (quads + wk - 1) / wk;
   const uint8_t *packed = A.packed + (int64_t)seg.e * A.N * nG * B;
   const uint16_t *scales = A.scales + (int64_t)seg.e * A.N * nG;
 
-  auto tile_row = [&](int j) { return ((b0 + j * A.bpu) * wt + tw) * 16; };
+  auto tile_row = [&](int j) { return ((b0 + j * bpu) * wt + tw) * 16; };
   int fj = 0, fk = 0;  // step and batch of the next request
   auto fetch = [&](Unit &f) {
     // rows past N read row N - 1, units past the last read it, with scales 0
@@ -600,7 +605,7 @@ __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Arg
       __syncthreads();
       for (int o = tid; o < wt * MB * 64; o += threads) {  // [tile][row of q][column]
         const int ts = o / (MB * 64), m = o / 16 % (4 * MB), c = o & 15;
-        const int n = ((b0 + j * A.bpu) * wt + ts) * 16 + c;
+        const int n = ((b0 + j * bpu) * wt + ts) * 16 + c;
         if (m >= M || n >= A.N) continue;
         const uint32_t at = (uint32_t)((m >> 2) * waves + ts * wk) * 64 + (uint32_t)(16 * (c >> 2) + 4 * (m & 3) + (c & 3));
         float v = 0.f;
@@ -835,6 +840,7 @@ void tile_kernel(const I8Args A) {
     const int split = A.splits == 1 || tiles == 0 ? 0 : scalar((int)((uint32_t)work / (uint32_t)tiles)), t = work - split * tiles;
     if (split >= A.splits) break;
     const int unit = scalar((int)((uint32_t)t / (uint32_t)A.tp)), ip = t - unit * A.tp;
+    if (unit >= A.units) break;  // (offsets that overlap make more)
     const Segment seg = find_unit(A, Q, unit);
     if (seg.e < 0) break;
     // stages are counted from the split's first
@@ -1228,6 +1234,7 @@ void part_kernel(const I8Args A) {
     const int split = A.splits == 1 || tiles == 0 ? 0 : scalar((int)((uint32_t)work / (uint32_t)tiles)), t = work - split * tiles;
     if (split >= A.splits) break;
     const int unit = scalar((int)((uint32_t)t / (uint32_t)A.tp)), ip = t - unit * A.tp;
+    if (unit >= A.units) break;  // (offsets that overlap make more)
     const Segment seg = find_unit(A, Q, unit);
     if (seg.e < 0) break;
     const int s0 = A.splits == 1 ? 0 : scalar(S * split / A.splits);
@@ -1432,7 +1439,7 @@ void part_kernel(const I8Args A) {
 constexpr int kFew = 0, kTile = 1;
 
 struct Plan {
-  int kind, mb, copies, wk, wt, splits, bpu, p, q;
+  int kind, mb, copies, wk, wt, splits, p, q;
   bool parts;  // tile: q in parts
   int64_t units, blocks;
 };
@@ -1522,8 +1529,8 @@ Plan plan_of(int64_t T, int64_t N, int64_t K, int G, int64_t E, bool grouped) {
   p.wk = (int)std::max<int64_t>(1, std::min<int64_t>({q, waves, 4096 / all}));
   p.wt = (int)std::max<int64_t>(1, std::min<int64_t>(waves / p.wk, ceil_div(all, 256)));
   const int64_t sets = ceil_div(tiles, p.wt), blocks = p.mb == 4 ? 256 : 1024;
-  p.bpu = (int)std::max<int64_t>(1, std::min<int64_t>(sets, blocks / std::max<int64_t>(1, used * p.splits)));
-  p.blocks = p.units * p.bpu * p.splits;
+  p.blocks = p.units * p.splits * std::max<int64_t>(1, std::min<int64_t>(sets, blocks / (p.units * p.splits)));
+  if (grouped) p.blocks = std::max(p.blocks, std::min(p.units * p.splits * sets, blocks));
   // (many experts of rows so long that q's take many splits: more blocks than a
   // launch has; tiles go round)
   if (p.blocks >= int64_t(1) << 22) plan_tiles(p, T, N, K, G, used, grouped);
@@ -1574,7 +1581,7 @@ void i8_plan(int64_t T, int64_t N, int64_t K, int G, int64_t E, int64_t *plan) {
   plan[3] = few ? p.copies : p.q;
   plan[4] = few ? p.wk : 0;
   plan[5] = few ? p.wt : 0;
-  plan[6] = few ? p.bpu : 0;
+  plan[6] = few ? p.blocks : 0;
 }
 
 int64_t gemm_i8_workspace(int64_t T, int64_t N, int64_t K, int G, int64_t E, bool grouped) {
@@ -1612,8 +1619,8 @@ void launch_gemm_i8(const int8_t *q, const float *qs, const uint8_t *packed, con
   a.splits = p.splits;
   a.wk = p.wk;
   a.wt = p.wt;
-  a.bpu = p.bpu;
   a.tp = p.kind == kTile ? (int)ceil_div(N, p.p) : 0;
+  a.units = (int)p.units;
   a.status = status;
   if (G == 64)
     launch<64>(p, a, stream);

@@ -49,7 +49,7 @@ def test_the_gpu_tests_sizes_take_many_sets_of_a_block():
     again = set()
     for M, N, K, G, E in MIDDLE:
         p = plan(M, N, K, G, E)
-        if p[0] == 0 and -(-N // (16 * p[5])) > p[6]:
+        if p[0] == 0 and -(-N // (16 * p[5])) * p[1] > p[6]:
             again.add((G, p[2], p[3]))
     assert {(G, rows, 32) for G in (64, 128) for rows in (4, 8, 16)} <= again
     assert (64, 16, 8) in again and (128, 16, 8) in again
@@ -73,7 +73,7 @@ def test_launches_stay_within_a_launch():
         p = plan(M, N, K, 64, E)
         if p[0] == 0:
             units = M // p[2] + min(E, M) if E else 1
-            assert units * p[6] * p[1] * 64 * p[4] * p[5] < 1 << 32, (M, N, K, E)
+            assert units * p[1] <= p[6] and p[6] * 64 * p[4] * p[5] < 1 << 32, (M, N, K, E)
 
 
 def test_refusals():
