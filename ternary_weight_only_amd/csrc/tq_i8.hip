@@ -420,7 +420,8 @@ struct FewRoom {
 // the table into LDS, about 6 us (8 tokens, eight experts of [3584,1024], 10.8 us;
 // 7 rows of [14336,4096] 12.0 us where the bytes alone take 2.6); with many the
 // decode in LDS, 26 table reads of 8 bytes a unit, beside the bytes: 32 tokens,
-// sixteen experts of [4096,14336], 80 us, 2.5 TB/s of packed bytes (of copy's 5.2).
+// sixteen experts of [4096,14336], 72 to 82 us, 2.5 to 2.8 TB/s of packed bytes (of
+// copy's 5.2; 76 us without decode and products).
 template <int G, int MB, int COPIES>
 __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Args A) {
   typedef Codes<COPIES> L;
@@ -805,7 +806,7 @@ __device__ __forceinline__ void finish_tile(const I8Args &A, f32x4 (&acc)[P / WP
 //
 // What bounds it: short K.  A tile takes 5 to 8 us beside its stages (offsets, row
 // indices, first bytes and decode, results), a stage of 128 x 64 0.8 us alone on
-// its CU and 1.1 with another: 2000 rows of 32 experts of [3584,1024] 54 to 58 us,
+// its CU and 1.1 with another: 2000 rows of 32 experts of [3584,1024] 52 to 58 us,
 // about half of it in stages; 333 rows of [1024,3584], K in five, 18.2 us.  In a
 // stage the vector unit (two instructions a result and group, and the decode) has
 // the longest part, which is why larger tiles of 128-groups go to part_kernel.
@@ -1205,7 +1206,7 @@ __device__ __forceinline__ f32x4 mfma_parts(const Part &x, u32x4 codes, f32x4 c)
 // registers for no more) do not hide each other's waits.  Power holds the clock at
 // 2.1 GHz (2.4 with zeros as q, in the same cycles).  2048 rows of [14336,4096]
 // 159 us, 1.51 Pop/s (a library's plain 8-bit product of 8192^3 reaches 2.1, with
-// nothing to decode or scale); eight experts of them, two a token, 393 to 405 us.
+// nothing to decode or scale); eight experts of them, two a token, 386 to 405 us.
 template <int P, int Q, int COPIES>
 __global__ __launch_bounds__(2 * P) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void part_kernel(const I8Args A) {
