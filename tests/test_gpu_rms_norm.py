@@ -111,6 +111,17 @@ def test_zero_rows_and_rows_that_are_not_finite():
         assert (h.cpu()[1] == 0).all() and h.cpu()[2:4].isnan().all() and h.cpu()[keep].isfinite().all()
 
 
+def test_sum_in_place_of_x():
+    for K, t in ((333, "bf16"), (4096, "fp32"), (20000, "bf16")):
+        x, r, w = _case(23, 6, K, t, t, "bf16")
+        want = tq.rms_norm_i8(x.cuda(), w.cuda(), r.cuda())
+        xd = x.cuda()
+        q, s = torch.empty_like(want[0]), torch.empty_like(want[1])
+        got = tq.rms_norm_i8(xd, w.cuda(), r.cuda(), out=(q, s, xd))
+        torch.cuda.synchronize()
+        assert got[2] is xd and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_sum_in_place_of_the_residual():
     for K in (333, 4096, 20000):
         x, r, w = _case(21, 6, K, "bf16", "bf16", "bf16")
