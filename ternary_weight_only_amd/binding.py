@@ -1094,18 +1094,19 @@ def glu_backward(dh, x, wg, wu, g, u, act="silu", out=None, workspace=None):
 
 
 class _FirstGradients(torch.autograd.Function):
-    """Gradients made from the first `n` arguments, passed through; a gradient
-    of them is refused, whichever of those it would be with respect to.  (A
-    backward marked once_differentiable refuses only where the incoming
-    gradient itself requires one.)"""
+    """Gradients that operator `of` made from the first `n` tensors, passed
+    through; a gradient of them is refused, whichever of those it would be with
+    respect to.  (A backward marked once_differentiable refuses only where the
+    incoming gradient itself requires one.)"""
 
     @staticmethod
-    def forward(ctx, n, *tensors):
+    def forward(ctx, of, n, *tensors):
+        ctx.of = of
         return tensors[n:]
 
     @staticmethod
     def backward(ctx, *_):
-        raise TQError("GLU has no gradients of gradients")
+        raise TQError("%s has no gradients of gradients" % ctx.of)
 
 
 class GLU(torch.autograd.Function):
@@ -1137,7 +1138,7 @@ class GLU(torch.autograd.Function):
                 d = d.clone()
             grads = glu_backward(d, x, wg, wu, g, u, ctx.act)
         if torch.is_grad_enabled():  # create_graph
-            grads = _FirstGradients.apply(4, dh, x, wg, wu, *grads)
+            grads = _FirstGradients.apply("GLU", 4, dh, x, wg, wu, *grads)
         return (*grads, None)
 
 
@@ -1322,7 +1323,7 @@ class RMSNorm(torch.autograd.Function):
         if torch.is_grad_enabled():  # create_graph
             given = [t for t in (dh, dy, y, weight) if t is not None]
             some = [g for g in grads if g is not None]
-            made = iter(_FirstGradients.apply(len(given), *given, *some))
+            made = iter(_FirstGradients.apply("RMSNorm", len(given), *given, *some))
             grads = [None if g is None else next(made) for g in grads]
         return (*grads, None)
 
