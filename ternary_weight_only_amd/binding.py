@@ -1338,7 +1338,7 @@ def _out_type(dtype) -> int:
 def _act_i8(act) -> int:
     a = ACTS_I8.get(act) if act is None or isinstance(act, str) else None
     if a is None:
-        raise TQError("act must be None or one of %s, not %r" % (sorted(ACTS), act))
+        raise TQError("act must be one of %s, not %r" % (list(ACTS_I8), act))
     return a
 
 
