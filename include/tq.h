@@ -571,7 +571,7 @@ int tq_w4a16_gemv_grouped(int count, const uint16_t *const *xs, const uint32_t *
  *   gate_packed, up_packed   [N, K/G, ceil(G/5)] bytes (any alignment)
  *   gate_scales, up_scales   [N, K/G] fp16, 2-byte aligned
  *   h                        [M,N] bf16, 2-byte aligned, overwritten
- *   act                      a tq_act
+ *   act                      TQ_ACT_SILU or TQ_ACT_GELU
  *   workspace                device memory, 16-byte aligned, at least
  *                            tq_glu_workspace(M, N, K, G) bytes (may be NULL
  *                            when that is 0); its contents on entry are

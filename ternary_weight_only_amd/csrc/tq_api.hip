@@ -45,7 +45,7 @@ const char *tq_status_string(int status) {
     case TQ_ERR_ALIGN: return "TQ_ERR_ALIGN: pointer not aligned as required";
     case TQ_ERR_LAUNCH: return "TQ_ERR_LAUNCH: HIP launch failed";
     case TQ_ERR_WORKSPACE: return "TQ_ERR_WORKSPACE: workspace too small";
-    case TQ_ERR_ACT: return "TQ_ERR_ACT: act is not a tq_act value";
+    case TQ_ERR_ACT: return "TQ_ERR_ACT: act is not a tq_act value that the call takes";
     case TQ_ERR_TYPE: return "TQ_ERR_TYPE: a type is not a tq_type value";
     case TQ_ERR_VALUE: return "TQ_ERR_VALUE: eps must be positive and finite";
     default: return "unknown tq status";

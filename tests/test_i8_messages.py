@@ -12,3 +12,13 @@ def test_every_activation_is_named(bad):
         binding._act_i8(bad)
     for name in binding.ACTS_I8:
         assert repr(name) in str(e.value), name
+
+
+def test_an_act_that_another_call_takes():
+    """The gated calls refuse two values that are activations: the text of the
+    status does not say that they are none."""
+    lib = tq.lib()
+    fake, big = 0x100000, 1 << 40  # never dereferenced
+    rc = lib.tq_glu(fake, fake, fake, fake, fake, 3, 5, 128, 64, binding.ACTS_I8["relu2"], fake, fake, big, None, None)
+    text = lib.tq_status_string(rc).decode()
+    assert text.startswith("TQ_ERR_ACT") and "not a tq_act value that the call takes" in text
