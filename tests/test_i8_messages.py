@@ -3,6 +3,7 @@ import pytest
 
 import ternary_weight_only_amd as tq
 from ternary_weight_only_amd import binding
+from tests.test_i8_args import _lib
 
 
 @pytest.mark.parametrize("bad", ["tanh", 2, True, ["silu"]])
@@ -17,7 +18,7 @@ def test_every_activation_is_named(bad):
 def test_an_act_that_another_call_takes():
     """The gated calls refuse two values that are activations: the text of the
     status does not say that they are none."""
-    lib = tq.lib()
+    lib = _lib()
     fake, big = 0x100000, 1 << 40  # never dereferenced
     rc = lib.tq_glu(fake, fake, fake, fake, fake, 3, 5, 128, 64, binding.ACTS_I8["relu2"], fake, fake, big, None, None)
     text = lib.tq_status_string(rc).decode()
