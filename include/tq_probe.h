@@ -88,8 +88,10 @@ int tq_probe_valu(int kind, int iters, int grid, uint32_t *sink, unsigned long l
  * tq_probe_i8_plan: tq_gemm_i8 (experts = 0) or tq_expert_gemm_i8.  plan[0] the
  * kernel (0 few_kernel, 1 tile_kernel, 2 part_kernel), plan[1] the splits of K;
  * of few_kernel plan[2] the rows of a unit, plan[3] the table's copies, plan[4]
- * the waves of a tile, plan[5] the tiles of a set and plan[6] the blocks, which
- * the units that there are share; of the others plan[2] and plan[3] the weight rows and rows of a tile.
+ * the waves of a tile and plan[5] the tiles of a set; of the others plan[2] and
+ * plan[3] the weight rows and rows of a tile (2 plan[2] threads a block).
+ * plan[6] the blocks, which the units that there are share, or which go on from
+ * one tile to another.
  *
  * TQ_ERR_NULL, or the error that the calls return for such sizes; M >= 1.
  */

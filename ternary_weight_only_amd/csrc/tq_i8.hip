@@ -1582,7 +1582,7 @@ void i8_plan(int64_t T, int64_t N, int64_t K, int G, int64_t E, int64_t *plan) {
   plan[3] = few ? p.copies : p.q;
   plan[4] = few ? p.wk : 0;
   plan[5] = few ? p.wt : 0;
-  plan[6] = few ? p.blocks : 0;
+  plan[6] = p.blocks;
 }
 
 int64_t gemm_i8_workspace(int64_t T, int64_t N, int64_t K, int G, int64_t E, bool grouped) {
