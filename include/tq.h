@@ -62,7 +62,7 @@ typedef enum {
     TQ_ERR_WORKSPACE = -6, /* a workspace is smaller than its call asks for      */
     TQ_ERR_ACT = -7,     /* act is not a tq_act value that the call takes       */
     TQ_ERR_TYPE = -8,    /* a type is not a tq_type value                       */
-    TQ_ERR_VALUE = -9    /* eps is not a positive finite number                 */
+    TQ_ERR_VALUE = -9    /* eps is not positive and finite, or too small for rstd */
 } tq_status;
 
 /* Device status bits. */
@@ -697,7 +697,9 @@ int tq_rms_norm_i8(const void *x, int x_type, const void *residual, int residual
  * projection's fake-quantized weights are multiplied by):
  *   h[m,k] = bf16_rne(q[m,k] * scales[m])
  *   rstd   [M] fp32, overwritten: 1 / rms, which the backward call reads; NULL
- *          when no gradient is needed
+ *          when no gradient is needed.  With it eps is at least 2^-252
+ *          (TQ_ERR_VALUE): a row of zeros has eps^-1/2 there, and its gradients
+ *          are multiplied by that
  * A row with an Inf or NaN gets h = NaN.  All else as tq_rms_norm_i8.
  */
 int tq_rms_norm_forward(const void *x, int x_type, const void *residual, int residual_type,

@@ -1236,8 +1236,8 @@ def rms_norm_i8(x, weight=None, residual=None, eps: float = 1e-6, status=None, o
 def rms_norm_forward(x, weight=None, residual=None, eps: float = 1e-6, status=None, out=None):
     """rms_norm_i8 with the values that its 8-bit rows stand for (training):
     (h bf16 [M,K], y, rstd fp32 [M]), h = bf16(q * scales), rstd =
-    1 / sqrt(mean(y^2) + eps), which rms_norm_backward reads.  `out`, if given,
-    is that triple (y None without a residual)."""
+    1 / sqrt(mean(y^2) + eps), which rms_norm_backward reads (so eps is 2^-252 at
+    least).  `out`, if given, is that triple (y None without a residual)."""
     args, M, K, dev = _norm_args(x, weight, residual, eps)
     if dev.index != _current_device():
         with torch.cuda.device(dev):

@@ -47,7 +47,7 @@ const char *tq_status_string(int status) {
     case TQ_ERR_WORKSPACE: return "TQ_ERR_WORKSPACE: workspace too small";
     case TQ_ERR_ACT: return "TQ_ERR_ACT: act is not a tq_act value that the call takes";
     case TQ_ERR_TYPE: return "TQ_ERR_TYPE: a type is not a tq_type value";
-    case TQ_ERR_VALUE: return "TQ_ERR_VALUE: eps must be positive and finite";
+    case TQ_ERR_VALUE: return "TQ_ERR_VALUE: eps must be positive and finite, and 2^-252 at least where rstd is written";
     default: return "unknown tq status";
   }
 }

@@ -17,6 +17,7 @@ constexpr int64_t kMaxK = int64_t(1) << 21;
 constexpr int64_t kMaxRows = int64_t(1) << 30;
 constexpr int64_t kMaxElems = int64_t(1) << 40;  // every byte count stays below 2^62
 constexpr int64_t kMaxExperts = 65536;
+constexpr double kMinEps = 0x1p-252;  // where rstd is written: a row of zeros has 2^126 there, which fp32 holds
 constexpr int64_t kMaxGather = int64_t(1) << 32;  // bytes of x, read by 32-bit offsets where rows are given by index
 
 bool product_ok(int64_t a, int64_t b) { return a == 0 || b <= kMaxElems / a; }
@@ -51,13 +52,13 @@ int finish_launch() {
 
 // The arguments that both forms of the norm have; `out` is q or h.
 int check_norm(const void *x, int x_type, const void *residual, int residual_type, const void *weight,
-               int weight_type, int64_t M, int64_t K, double eps, const void *out, const void *y,
+               int weight_type, int64_t M, int64_t K, double eps, double least, const void *out, const void *y,
                const int32_t *d_status) {
   const int rc = check_norm_shape(M, K);
   if (rc) return rc;
   if (!type_ok(x_type) || (residual && !type_ok(residual_type)) || (weight && !type_ok(weight_type)))
     return TQ_ERR_TYPE;
-  if (!(eps > 0.0) || !isfinite(eps)) return TQ_ERR_VALUE;
+  if (!(eps > 0.0) || !isfinite(eps) || eps < least) return TQ_ERR_VALUE;
   if (M == 0) return TQ_OK;
   if (!x || !out || !residual != !y) return TQ_ERR_NULL;
   if (!aligned(x, size_of(x_type)) || !aligned(d_status, 4) ||
@@ -100,7 +101,7 @@ extern "C" {
 int tq_rms_norm_i8(const void *x, int x_type, const void *residual, int residual_type, const void *weight,
                    int weight_type, int64_t M, int64_t K, double eps, int8_t *q, float *scales, void *y,
                    int32_t *d_status, void *stream) {
-  const int rc = check_norm(x, x_type, residual, residual_type, weight, weight_type, M, K, eps, q, y, d_status);
+  const int rc = check_norm(x, x_type, residual, residual_type, weight, weight_type, M, K, eps, 0.0, q, y, d_status);
   if (rc || M == 0) return rc;
   if (!scales) return TQ_ERR_NULL;
   if (!aligned(scales, 4)) return TQ_ERR_ALIGN;
@@ -113,7 +114,8 @@ int tq_rms_norm_i8(const void *x, int x_type, const void *residual, int residual
 int tq_rms_norm_forward(const void *x, int x_type, const void *residual, int residual_type, const void *weight,
                         int weight_type, int64_t M, int64_t K, double eps, uint16_t *h, void *y, float *rstd,
                         int32_t *d_status, void *stream) {
-  const int rc = check_norm(x, x_type, residual, residual_type, weight, weight_type, M, K, eps, h, y, d_status);
+  const int rc = check_norm(x, x_type, residual, residual_type, weight, weight_type, M, K, eps, rstd ? kMinEps : 0.0, h,
+                            y, d_status);
   if (rc || M == 0) return rc;
   if (!aligned(h, 2) || !aligned(rstd, 4)) return TQ_ERR_ALIGN;
   (void)hipGetLastError();
