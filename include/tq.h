@@ -779,6 +779,9 @@ int64_t tq_gemm_i8_workspace(int64_t M, int64_t N, int64_t K, int G);
  * out is left as it was.  Only the experts that have rows are read.  Offsets
  * that leave 0 .. T or fall set TQ_DEV_BAD_SEGMENT; out is then unspecified.  A
  * row index out of range sets TQ_DEV_BAD_ROW and counts as a row of zeros.
+ * The kernel is chosen by the rows an expert has on average: up to 8, an expert's
+ * weights are read and decoded once for every 4 to 16 of its rows, so that one with
+ * far more rows than the others costs the more.
  * All else as tq_gemm_i8.
  */
 int tq_expert_gemm_i8(const int8_t *x, const float *x_scales, int64_t sources,

@@ -1266,8 +1266,8 @@ def rms_norm_backward(dh, y, rstd, weight=None, dy=None, out=None, workspace=Non
     """Gradients of rms_norm_forward, straight through the rounding: dh [M,K]
     bf16, y and rstd as it returned them, dy [M,K] of y's type or None ->
     (dx [M,K] of y's type, for x and residual alike; dweight [K] of weight's
-    type, None without one).  `out`, if given, is that pair; `workspace` as for
-    glu, of rms_norm_backward_workspace(M, K) bytes."""
+    type, None without one).  `out`, if given, is that pair, in no input's
+    memory; `workspace` as for glu, of rms_norm_backward_workspace(M, K) bytes."""
     M, K, dev = _rows_of(y, "y")
     if dev.index != _current_device():
         with torch.cuda.device(dev):
@@ -1294,7 +1294,8 @@ def rms_norm_backward(dh, y, rstd, weight=None, dy=None, out=None, workspace=Non
 
 class RMSNorm(torch.autograd.Function):
     """rms_norm_forward with gradients for x, weight and residual: h, or (h, y)
-    with a residual.  Gradients of gradients are refused.  A backward pass may be
+    with a residual, whose type x's gradient is rounded to before its own.
+    Gradients of gradients are refused.  A backward pass may be
     captured in a graph as any of torch's may: with its forward pass, and while no
     eager graph of the same leaves lives."""
 
@@ -1389,7 +1390,8 @@ def expert_gemm_i8(x, x_scales, packed, scales, offsets, N: int, K: int, G: int,
     device tensor [experts+1]; packed and scales hold [experts,N,K] weights, bias
     is [experts,N].  Row m reads row m of x [T,K], or, with rows (int32 [T]), row
     rows[m] of x [sources,K].  -> [T,N]; rows outside every segment are left as
-    they were in `out` (and are not set where it is allocated here)."""
+    they were in `out` (and are not set where it is allocated here: a padded
+    batch whose other rows are read gives its own)."""
     sources, _, dev = _rows_of(x, "x")
     if dev.index != _current_device():
         with torch.cuda.device(dev):

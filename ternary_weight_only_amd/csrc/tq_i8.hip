@@ -408,8 +408,12 @@ struct FewRoom {
 // A unit is up to 4 MB rows of q (of one expert); a block takes one split of K
 // and sets of wt tiles of 16 weight rows, wk waves a tile.  Lane (l, q) decodes
 // unit q of a quad (512 codes) of weight row l, so its bytes are two wide loads
-// and the four lanes of a row read 104 neighbouring ones; two quads are on their
-// way while one is decoded.  The matrix cores sum over the four lanes of a row,
+// and the four lanes of a row read 104 neighbouring ones; a unit's loads are
+// asked for when the one before it has been decoded, two units in turn.  (As
+// compiled they do not stay on their way: `fetch` selects on the scale that it has
+// just asked for and so waits for all of it, with G = 64 right behind the loads,
+// with G = 128 in one half of a pair or both.)  The matrix cores sum over the four
+// lanes of a row,
 // which have different groups here: so of the 16 columns, four are given to
 // each row of q, column 4 i + j with row i's part of unit j and zeros elsewhere,
 // and a result is a row's sum over one unit, exact, which is then scaled.  (Four
@@ -418,10 +422,11 @@ struct FewRoom {
 //
 // What bounds it: with few matrices the chain before the first sum, launch, q and
 // the table into LDS, about 6 us (8 tokens, eight experts of [3584,1024], 10.8 us;
-// 7 rows of [14336,4096] 12.0 us where the bytes alone take 2.6); with many the
-// decode in LDS, 26 table reads of 8 bytes a unit, beside the bytes: 32 tokens,
-// sixteen experts of [4096,14336], 72 to 82 us, 2.5 to 2.8 TB/s of packed bytes (of
-// copy's 5.2; 76 us without decode and products).
+// 7 rows of [14336,4096] 12.0 us where the bytes alone take 2.7); with many a
+// load's latency in every quad: 32 tokens, sixteen experts of [4096,14336], 72 to
+// 82 us, 2.5 to 2.8 TB/s of packed bytes (of copy's 5.2; 76 us without decode and
+// products, 70 without loads).  16 rows of [14336,4096] 15.5 us, with G = 64 19.4
+// (few_kernel<64, 4, 32> spills 21 registers).
 template <int G, int MB, int COPIES>
 __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Args A) {
   typedef Codes<COPIES> L;
@@ -460,7 +465,8 @@ __global__ __launch_bounds__(64 * few_waves(COPIES)) void few_kernel(const I8Arg
   auto tile_row = [&](int j) { return ((b0 + j * bpu) * wt + tw) * 16; };
   int fj = 0, fk = 0;  // step and batch of the next request
   auto fetch = [&](Unit &f) {
-    // rows past N read row N - 1, units past the last read it, with scales 0
+    // rows past N read row N - 1 (their results go nowhere), units past the last
+    // read it with scales 0
     const int64_t n = min(tile_row(fj) + l, A.N - 1);
     const int u = u0 + 4 * (kw + wk * fk) + q, g = GU * min(u, u1 - 1);
     uint32_t sc;
@@ -753,7 +759,9 @@ __device__ __forceinline__ void finish_tile(const I8Args &A, f32x4 (&acc)[P / WP
       if (wq * (Q / WQ) + r < t.M && nw < result.N) each(r, scale, lo, hi);
     };
     // loops by themselves: a load in one would make every pass wait for the
-    // stores of the pass before
+    // stores of the pass before, as the second one's residual does, column after
+    // column (2048 rows of [14337,4096] in bf16 184 us, 242 with a residual; of
+    // [14336,4096], in the others, 170 and 173)
     if (sums) {
 #pragma unroll 1
       for (int k = 0; k < 16 * kOnce; k += kEach)
@@ -773,7 +781,7 @@ __device__ __forceinline__ void finish_tile(const I8Args &A, f32x4 (&acc)[P / WP
           result.put8<false>(mw + r, nw, scale, bias, lo, hi, Result::Eight{});
         });
     } else {
-      constexpr int kAhead = 4;  // rows whose residuals are requested together
+      constexpr int kAhead = 4;  // rows whose residuals are requested together (in bf16 one after another, as compiled)
       static_assert(16 * kOnce % (kAhead * kEach) == 0, "");
 #pragma unroll 1
       for (int k = 0; k < 16 * kOnce; k += kAhead * kEach) {
@@ -803,12 +811,16 @@ __device__ __forceinline__ void finish_tile(const I8Args &A, f32x4 (&acc)[P / WP
 //   - scales and adds the row before;
 //   - decodes its codes of s + 1, two threads a weight row, 64 codes each;
 //   - requests q of s + 2, whose slot this stage's q has left, and bytes of s + 2.
+// (With G = 64 the requests of a stage are waited for within it: load_raw selects
+// on the scale that it asks for, and of the bytes that a thread holds the second
+// eight are first looked at behind the requests of q, which drains those.)
 //
 // What bounds it: short K.  A tile takes 5 to 8 us beside its stages (offsets, row
 // indices, first bytes and decode, results), a stage of 128 x 64 0.8 us alone on
-// its CU and 1.1 with another: 2000 rows of 32 experts of [3584,1024] 52 to 58 us,
-// about half of it in stages; 333 rows of [1024,3584], K in five, 18.2 us.  In a
-// stage the vector unit (two instructions a result and group, and the decode) has
+// its CU and 1.1 with another, with G = 64 1.5 and 1.7 (the waits above, and twice
+// the sums): 2000 rows of 32 experts of [3584,1024] with G = 64 52 to 58 us (46 with
+// 128), about half of it in stages; 333 rows of [1024,3584], K in five, 18.2 us.  In
+// a stage the vector unit (two instructions a result and group, and the decode) has
 // the longest part, which is why larger tiles of 128-groups go to part_kernel.
 template <int G, int P, int Q, int WP, int COPIES>
 __global__ __launch_bounds__(2 * P) __attribute__((amdgpu_waves_per_eu(2, P == 256 || Q > 64 ? 2 : 4)))
@@ -1031,7 +1043,8 @@ void tile_kernel(const I8Args A) {
 #pragma unroll
       for (int a = 0; a < TP; ++a) {
         __builtin_amdgcn_sched_barrier(0);
-        // waits for the bytes requested a stage ago, so before other requests
+        // waits for the bytes requested a stage ago, so before other requests (with
+        // G = 64 for the first eight)
         if (kLate == 0 && a == 0) align_raw(), look(Int<0>{});
         // operands are read as soon as those that they replace have been used
         multiply(0);
@@ -1452,8 +1465,13 @@ uint32_t few_room(int mb, int copies) {
 
 // tile_kernel's tiles and what they take, in us: a tile before and behind its
 // stages, and a stage where it is alone on a CU and where all `places` are taken.
-// (Measured with G = 128, the largest of part_kernel; a stage with G = 64 takes a
-// fourth more of all.)
+// Measured with G = 128, the largest of part_kernel.  With G = 64 a stage takes
+// 1.52 and 1.74, 1.78 and 2.08, 2.98 us, which the table leaves out: it chooses
+// the same.  Of thirteen sizes with G = 64 its choice was the fastest to 2 % but
+// for one (us, this choice, then each shape without splits in the table's order;
+// [14336,4096]: 64 rows 32, of 49, 60, 109; 512 rows 75, of 104, 75, 110; 1024 rows
+// 111, of 192, 143, 114; 2048 rows 238, of 368, 266, 242; 2000 rows of 32 experts
+// of [3584,1024] 57, of 58, 56, 84; 8000 of them 127, of 145, 115, 128).
 struct Shape {
   int p, q, places;
   double start, alone, full;

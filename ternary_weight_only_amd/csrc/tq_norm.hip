@@ -244,9 +244,12 @@ __device__ __forceinline__ int64_t stride_of(bool f32, int K) { return (int64_t)
 // eights v T + t of it a thread (T = 64 W threads), V of them.  Four rows a
 // block where a wave has one.  NARROW: all of bf16; a row whose sums leave what
 // fp32 is good for, and every row otherwise, is summed and rounded in fp64.
-// Bound by HBM at many rows (4096 rows of 4096 bf16 with a residual 23.9 us on the
-// device, 134 MB at 5.6 TB/s, copy's rate), by latency at few (a row of 1024: 3.5
-// us, of a call's 10.4 on the host).
+// Bound by HBM at many rows: 4096 rows of 4096 bf16 with a residual, 134 MB, 23.9 us
+// on the device (a copy that moves as much takes 25.9, other buffers each time: a
+// part of either is still in the last cache); all in fp32, 235 MB, 44.3 a call
+// (45.5 at a large copy's 5.16 TB/s).  Without a residual 24.1 of fp32 rows, whose
+// sums and codes are fp64 (the bytes 19.5), and 15.2 of bf16 ones (13.0).  By latency
+// at few (a row of 1024: 3.5 us, of a call's 10.4 on the host).
 template <int V, int W, bool NARROW>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void norm_kernel(const NormArgs A) {
   __shared__ __align__(16) unsigned char room[2][W * 16];
@@ -459,7 +462,8 @@ __device__ __forceinline__ void back_columns(const BackArgs &A, int block, float
 // block's G groups add theirs in order.  4096 rows of 4096 bf16: 29.9 us, 4.5 TB/s
 // (copy 5.2; a row loaded ahead, 30.7), and norm_back_sum_kernel 4.2.  At few rows
 // (by_columns) blocks behind those of rows make dw: 333 rows of 3584 with fp32 5.5,
-// latency.
+// latency.  Rows that are read twice (below): 1100 of 8193 in fp32 49.2 us a call, of
+// 8192 33.2 (24.5 at a large copy's rate); 1024 of 14336 59.2 of 39.8.
 template <int V, int W, bool NARROW>
 __global__ __launch_bounds__(64 * kBackWaves) void norm_back_kernel(const BackArgs A) {
   constexpr int T = 64 * W, G = kBackWaves / W;
